@@ -192,7 +192,7 @@ def prepare(c, seed):
         else:
             s["ws"] = A.AttnWorkspace(T, R, H, Hk, D)
             if op == "paged":
-                s["sched"] = A.lora_attn_schedule(s["cu"], s["kv_len"], T, H, Hk, D, s["ws"])
+                s["sched"] = A.lora_attn_schedule(s["cu"], s["kv_len"], T, width * P, H, Hk, D, s["ws"])
     return s
 
 
