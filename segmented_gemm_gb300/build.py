@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(PKG, "liblora.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "liblora_debug.so")
 
 SOURCES = ["lora_api.cu", "seg_build.cu", "fused_tc.cu", "fused_splitk.cu", "fused_cluster.cu",
-           "lora_noalloc.cu", "moe.cu", "widen.cu", "seg_check.cu", "stage.cu", "moe_pair.cu"]
+           "lora_noalloc.cu", "moe.cu", "widen.cu", "seg_check.cu", "stage.cu", "moe_pair.cu", "attn_api.cu",
+           "attn_schedule.cu", "attn.cu", "kv.cu"]
 VARIANTS = ((LIB_PATH, "", []), (DEBUG_LIB_PATH, "debug", ["-DLORA_DEBUG"]))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -39,7 +40,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "lora.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return files
 
 

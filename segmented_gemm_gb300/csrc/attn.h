@@ -1,0 +1,130 @@
+// Internal declarations of the attention operators (include/lora_attn.h).
+//
+// Workspace (offsets 256-byte aligned):
+//   counters   status word, work-list counters, arrival counters of split
+//              groups                                   (zero at rest but the status)
+//   hdr        schedule header (AttnHdr)
+//   blocks     query blocks of the step (AttnBlock), in request order
+//   order      the blocks, longest first
+//   part       partial results of split groups: fp32 O rows, then (m, l) pairs
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "lora_attn.h"
+
+namespace lora {
+
+constexpr int kAttnTileQ = 128;     // rows of one query tile (UMMA M): tokens x the group's heads
+constexpr int kAttnTileK = 128;     // keys of one key tile (UMMA N)
+constexpr int kAttnMaxCtas = 160;   // upper bound on the persistent grid
+
+// counter block entries (int32); the status word is lora.h's CNT_STATUS (0)
+enum AttnCounters {
+    ACNT_NEXT = 2,      // units taken beyond each CTA's first
+    ACNT_DONE = 3,      // CTAs finished
+    ACNT_GROUP = 32,    // [kAttnMaxCtas] partial results stored of the group that starts in a unit
+    ACNT_WORDS = ACNT_GROUP + kAttnMaxCtas
+};
+
+// A query block: up to two query tiles of one request, for every kv head.
+struct AttnBlock {
+    int64_t pre;      // key tiles of the blocks before it (one head)
+    int32_t req;
+    int32_t tok0;     // first packed row
+    int32_t ntok;
+    int32_t qpos0;    // row tok0 sees keys [0, qpos0 + 1) (none when that is <= 0)
+    int32_t kv_len;
+    int32_t tiles;    // key tiles its last row reaches, at least 1
+};
+
+struct AttnHdr {
+    int32_t nblocks;
+    int32_t units;      // pieces of work
+    int32_t cut;        // 0: a unit is one (block, head); 1: a unit is unit_tiles consecutive key tiles
+    int32_t sec_heads;  // heads whose blocks run together (cut 0)
+    int64_t unit_tiles;
+    int64_t tiles;      // key tiles of all blocks and heads
+};
+
+struct AttnLayout {
+    int32_t tq;          // tokens of one query tile
+    int64_t max_blocks;
+    int32_t part_rows;   // rows of a partial slot
+    size_t counters, hdr, blocks, order, part, part_ml, total;
+};
+
+struct AttnSchedParams {
+    const int32_t *cu, *kv_len;
+    int32_t R, tq, kv_heads, head_dim, ctas;
+    int64_t T, max_kv, max_blocks;
+    AttnHdr *hdr;
+    AttnBlock *blocks;
+    int32_t *order;
+    int32_t *counters;
+};
+
+struct AttnParams {
+    const uint16_t *q;
+    uint16_t *o;
+    float *lse;
+    int64_t q_tok, q_head, o_tok, o_head;   // element strides
+    int32_t heads, kv_heads, group, head_dim, tq;
+    float scale;
+    const AttnHdr *hdr;
+    const AttnBlock *blocks;
+    const int32_t *order;
+    int32_t *counters;
+    // keys and values: paged (block_table set) or packed rows
+    const uint16_t *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;   // packed: element strides
+    const int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_width, num_pages, page_shift;
+    int64_t page_stride, head_stride, slot_stride;
+    const int32_t *cu;
+};
+
+struct KvPlanParams {
+    lora_kv_plan_t a;
+    int32_t *status;
+};
+
+struct KvStoreParams {
+    const uint16_t *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;
+    uint16_t *kc, *vc;
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t slots;
+    int32_t page_shift, kv_heads, vecs;   // vecs: 16-byte units of one head
+    int64_t T;
+    const int32_t *slot_map;
+    int32_t *status;
+};
+
+cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
+cudaError_t launch_kv_store(const KvStoreParams &p, cudaStream_t stream);
+cudaError_t launch_attn_schedule(const AttnSchedParams &p, cudaStream_t stream);
+cudaError_t launch_attn(const AttnParams &p, cudaStream_t stream);
+
+// Launch attribute of a programmatic dependent launch: the kernel may start
+// its prologue while the one ahead finishes (every kernel here waits for it
+// with griddepcontrol.wait before it touches memory).
+inline void pdl_attribute(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[1])
+{
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+}
+
+// defined in lora_api.cu
+bool device_supported();
+int num_sms_current_device();
+bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box, CUtensorMapSwizzle sw);
+
+}  // namespace lora

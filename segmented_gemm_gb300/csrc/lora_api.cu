@@ -32,7 +32,7 @@ int num_sms_current_device()
     return n;
 }
 
-static bool device_supported()
+bool device_supported()
 {
     static int cache[64] = {0};   // 0 unknown, 1 yes, 2 no
     int dev = 0;
@@ -95,6 +95,24 @@ static bool encode_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1
     cuuint32_t es[3] = {1, 1, 1};
     return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 map of 2 to 5 dimensions; strides: bytes, of dimensions 1 and up.
+bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box, CUtensorMapSwizzle sw)
+{
+    EncodeTiledFn fn = encoder();
+    if (!fn || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i] < 1 ? 1 : dims[i];
+        b[i] = box[i];
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, b,
+              es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
