@@ -1,112 +1,783 @@
-// Attention over packed rows or a paged cache (include/lora_attn.h).
+// Attention over packed rows or a paged cache (include/lora_attn.h):
+//   o_i = sum_j p_ij v_j / l_i,   p_ij = 2^(c q_i.k_j - c m_i),   l_i = sum_j p_ij,   c = scale log2(e)
+// over the keys j that row i sees, m_i a running maximum of the scores.
 //
-// A first kernel that is right for every case: a warp per (row, head), 32 keys
-// at a time, a lane per key for the scores and a lane per column for p v, with
-// the running maximum and sum of a softmax.
+// A query tile is 128 rows: tq tokens times the group's query heads, which
+// share the key/value head, so a key tile is loaded once for the group.  A
+// CTA works on two score streams at once, so that one's softmax runs under the
+// other's matrix products:
+//   pair     two query tiles against the same key tiles (long chunks, prompts)
+//   single   one query tile, the key tiles dealt to the streams in turn
+//            (decode and short chunks, where the cache's bytes bound the call)
+// Per stream and key tile of 128 keys, all on the tensor cores:
+//   S = Q K^T   both from shared memory, S [128 x 128] fp32 in tensor memory
+//   softmax     a thread per row: S to registers, p = 2^(..), P as bf16 back
+//               over S's cells (half of them)
+//   O += P V    P from tensor memory, V from shared memory as it was loaded
+//               (its head dimension contiguous: an N-major operand)
+// O stays in tensor memory.  m_i moves only when the maximum has grown by more
+// than 2^8 in p (so p <= 256, well inside fp32 and bf16): O is rescaled then,
+// by the softmax threads themselves, and the division by l_i at the end makes
+// any m_i as good as the true maximum.
+//
+// Roles (320 threads): warps 0..3 and 4..7 the softmax and the results of
+// stream 0 and 1, warp 8 loads (TMA), warp 9 issues the matrix products.
+// Shared memory: two query tiles and a ring of key and value tiles.
+// Persistent, one CTA per SM; work comes from the schedule (attn_schedule.cu).
+// A group (block, kv head) cut into pieces leaves partial (O, m, l) in the
+// workspace; the piece that finishes last joins them in their order, so
+// results do not depend on timing.  Every wait is bounded.
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_ptx.cuh"
 #include "internal.h"
-#include "ptx.cuh"
 
 namespace lora {
 
-constexpr int kAttnThreads = 128;
+constexpr int kAttnThreads = 320;
+constexpr int kItems = 4;             // work items in flight between the loader and the others
+constexpr float kRescaleBits = 8.f;   // m_i may lag the maximum by this many powers of two
 
-__global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnParams p)
+// tensor memory columns (512 in all): S of stream s at s * 128 (P over its
+// first 64), O of stream s at 256 + s * DP
+constexpr uint32_t kColS = 128, kColO = 256;
+
+// a piece of one (block, kv head): key tiles [t0, t1)
+struct AttnItem {
+    int32_t valid, pair, req, tok0, ntok, qpos0, kv_len, kvh;
+    int32_t t0, t1;
+    int32_t end0;     // pair: tiles that stream 0's rows reach
+    int32_t parts;    // pieces of the group
+    int32_t slot;     // this piece's partial results (parts > 1)
+    int32_t unit0;    // the unit that the group starts in (its counter; parts > 1)
+};
+
+template <int DP>
+struct AttnSmem {
+    static constexpr int kHalves = DP / 64;                    // 128-byte column blocks of a tile
+    static constexpr int kTile = 128 * DP * 2;                 // bytes of a query, key or value tile
+    static constexpr int kStages = 5 * 128 / DP + (DP == 64 ? 2 : 0);
+    static constexpr int kStats = 2 * kTile + kStages * kTile; // offsets
+    static constexpr int kItem = kStats + 128 * 8;
+    static constexpr int kBars = kItem + kItems * static_cast<int>(sizeof(AttnItem));
+    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2;
+    static constexpr int kEnd = kBars + kNumBars * 8 + 32;
+    static constexpr int kBytes = kEnd + 1024;                 // room to align the base
+    static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
+};
+
+struct AttnMaps {
+    CUtensorMap q, q1, k, v;   // q: tq tokens of a group's heads; q1: one token's
+};
+
+template <int DP, bool kPaged>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    __shared__ float qs[kAttnThreads / 32][LORA_MAX_HEAD_DIM];
+    using Sm = AttnSmem<DP>;
+    constexpr int kStages = Sm::kStages, kTile = Sm::kTile, kHalves = Sm::kHalves;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = smem, *ring = smem + 2 * kTile;
+    float2 *stats = reinterpret_cast<float2 *>(smem + Sm::kStats);   // stream 1's (m, l), single items
+    AttnItem *items = reinterpret_cast<AttnItem *>(smem + Sm::kItem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Sm::kBars), *empty = full + kStages;
+    uint64_t *item_full = empty + kStages, *item_empty = item_full + kItems;
+    uint64_t *q_full = item_empty + kItems;   // [2]
+    uint64_t *q_empty = q_full + 2;
+    uint64_t *s_full = q_empty + 1;           // [2]
+    uint64_t *p_full = s_full + 2;            // [2]
+    uint64_t *o_full = p_full + 2;            // [2]
+    uint64_t *xbar = o_full + 2;              // the 256 softmax threads meet here
+    uint64_t *end_bar = xbar + 1;             // after a wait gave up: the matrix products issued so far
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(end_bar + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *drain = reinterpret_cast<int *>(tmem_slot + 2);   // [0] ring loads issued, [1], [2] query loads issued
+    int *join_flag = drain + 3;
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nb = p.hdr->nblocks, D = p.head_dim;
-    for (int64_t u = blockIdx.x; u < static_cast<int64_t>(nb) * p.kv_heads; u += gridDim.x) {
-        const AttnBlock b = p.blocks[p.order[u / p.kv_heads]];
-        const int kvh = static_cast<int>(u % p.kv_heads);
-        const int base = p.cu[b.req];
-        for (int row = warp; row < b.ntok * p.group; row += kAttnThreads / 32) {
-            const int i = row / p.group, h = kvh * p.group + row % p.group;
-            const int64_t t = b.tok0 + i;
-            const int limit = max(0, min(b.kv_len, b.qpos0 + i + 1));
-            __syncwarp();
-            for (int d = lane; d < D; d += 32)
-                qs[warp][d] = __uint_as_float(static_cast<uint32_t>(p.q[t * p.q_tok + h * p.q_head + d]) << 16);
-            __syncwarp();
-            float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int j0 = 0; j0 < limit; j0 += 32) {
-                const int j = j0 + lane;
-                int64_t ko = -1, vo = -1;
-                bool zero = false;
-                if (j < limit) {
-                    if (p.block_table) {
-                        const int pg = j >> p.page_shift;
-                        const int page = pg < p.table_width ? p.block_table[b.req * p.table_stride + pg] : -1;
-                        if (page < 0 || page >= p.num_pages) {
-                            zero = true;
-                            atomicOr(p.counters + CNT_STATUS, LORA_DEV_BAD_PAGE);
-                        } else {
-                            ko = vo = page * p.page_stride + kvh * p.head_stride +
-                                      (j & ((1 << p.page_shift) - 1)) * p.slot_stride;
-                        }
-                    } else {
-                        ko = (static_cast<int64_t>(base) + j) * p.k_tok + kvh * p.k_head;
-                        vo = (static_cast<int64_t>(base) + j) * p.v_tok + kvh * p.v_head;
+    int32_t *status = p.counters + CNT_STATUS;
+    const long long budget = p.wait_cycles;
+    // called by whole warps; the answer is the same for all lanes, so a wait
+    // that gives up takes its warp out together
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
+    pdl_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 9);   // 8 softmax warps, the MMA warp
+        }
+        mbar_init(&q_full[0], 1);
+        mbar_init(&q_full[1], 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+            mbar_init(&o_full[s], 1);
+        }
+        mbar_init(xbar, 8);
+        mbar_init(end_bar, 1);
+        *abort_flag = 0;
+        drain[0] = drain[1] = drain[2] = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.q1);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    const AttnHdr hdr = *p.hdr;
+
+    if (warp == 8) {
+        // ===================== loader =========================================
+        uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0;
+        // one (block, head) piece: hand it to the other roles, then load it
+        auto emit = [&](const AttnBlock &b, int kvh, int t0, int t1, int parts, int slot, int unit0) {
+            AttnItem w;
+            w.valid = 1;
+            w.pair = b.ntok > p.tq;
+            w.req = b.req;
+            w.tok0 = b.tok0;
+            w.ntok = b.ntok;
+            w.qpos0 = b.qpos0;
+            w.kv_len = b.kv_len;
+            w.kvh = kvh;
+            w.t0 = t0;
+            w.t1 = t1;
+            w.end0 = max(1, (min(b.kv_len, b.qpos0 + min(b.ntok, p.tq)) + kAttnTileK - 1) / kAttnTileK);
+            w.parts = parts;
+            w.slot = slot;
+            w.unit0 = unit0;
+            const int is = nitem % kItems;
+            if (nitem >= kItems) wait(&item_empty[is], (nitem / kItems - 1) & 1);
+            if (lane == 0) {
+                items[is] = w;
+                mbar_arrive(&item_full[is]);
+            }
+            ++nitem;
+            const int n = t1 - t0;
+            const int seen = min(b.kv_len, b.qpos0 + b.ntok);   // keys past this no row sees
+            const int box = p.box_rows;
+            const int mybox = lane / kHalves, myhalf = lane % kHalves;
+            // load i of the piece: its key and value tiles in the order in which the MMA warp needs them
+            auto what = [&](int i, bool &is_v) {
+                if (w.pair) {
+                    is_v = i & 1;
+                    return i >> 1;
+                }
+                if (n == 1 || i < 2) {
+                    is_v = n == 1 && i == 1;
+                    return n == 1 ? 0 : i;
+                }
+                is_v = (i & 1) == 0 || i == 2 * n - 1;
+                return i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) >> 1 : (i - 2) >> 1;
+            };
+            // my box's page (paged), fetched one load ahead
+            auto page_of = [&](int i) {
+                bool v;
+                const int64_t key = static_cast<int64_t>(t0 + what(i, v)) * kAttnTileK + mybox * box;
+                const int64_t col = key >> p.page_shift;
+                int32_t page = -1;
+                if (key < seen && mybox * box < kAttnTileK) {
+                    if (col < p.table_width) page = p.block_table[b.req * p.table_stride + col];
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(status, LORA_DEV_BAD_PAGE);
+                        page = p.num_pages;   // outside the map: reads as zeros
                     }
                 }
-                float s = -INFINITY;
-                if (ko >= 0) {
-                    s = 0.f;
-                    for (int d = 0; d < D; d += 8) {
-                        const uint4 k8 = *reinterpret_cast<const uint4 *>(p.k + ko + d);
-                        const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s += qs[warp][d + 2 * e] * bf16_lo(w[e]) + qs[warp][d + 2 * e + 1] * bf16_hi(w[e]);
-                    }
-                    s *= p.scale;
-                } else if (zero) {
-                    s = 0.f;
+                return page;
+            };
+            int32_t next_page = kPaged ? page_of(0) : 0;
+            auto load = [&](int i) {
+                bool is_v;
+                const int tile = t0 + what(i, is_v);
+                const int32_t page = next_page;
+                if (kPaged && i + 1 < 2 * n) next_page = page_of(i + 1);
+                const int valid = max(0, min(kAttnTileK, seen - tile * kAttnTileK));
+                const int boxes = (valid + box - 1) / box;
+                const int s = it % kStages;
+                if (it >= kStages) wait(&empty[s], (it / kStages - 1) & 1);
+                ++it;
+                if (lane == 0) mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
+                __syncwarp();
+                if (mybox < boxes) {
+                    uint8_t *dst = ring + s * kTile + myhalf * (kAttnTileK * 128) + mybox * box * 128;
+                    const CUtensorMap *m = is_v ? &maps.v : &maps.k;
+                    if (kPaged)
+                        tma_load_4d(dst, m, &full[s], myhalf * 64,
+                                    (tile * kAttnTileK + mybox * box) & ((1 << p.page_shift) - 1), kvh, page);
+                    else
+                        tma_load_3d(dst, m, &full[s], myhalf * 64, kvh, b.tok0 - b.qpos0 + tile * kAttnTileK + mybox * box);
                 }
-                float mx = s;
-                for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : expf(m - mn);
-                const float pr = s == -INFINITY ? 0.f : expf(s - mn);
-                m = mn;
-                l = l * f + pr;
-                const float pb = __uint_as_float(pack_bf16x2(pr, 0.f) << 16);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] *= f;
-                for (int e = 0; e < 32 && j0 + e < limit; ++e) {
-                    const float pe = __shfl_sync(0xffffffffu, pb, e);
-                    const int64_t ve = __shfl_sync(0xffffffffu, vo, e);
-                    if (ve < 0) continue;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c * 32 + lane < D)
-                            acc[c] += pe * __uint_as_float(static_cast<uint32_t>(p.v[ve + c * 32 + lane]) << 16);
+            };
+            // a few tiles go ahead of the queries, whose buffers the previous piece may still hold
+            const int ahead = min(3, 2 * n);
+            for (int i = 0; i < ahead; ++i) load(i);
+            if (nitem > 1) wait(q_empty, (nitem - 2) & 1);
+            const int g = p.group, few = 4;
+            for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
+                const int first = s * p.tq, ntok = min(p.tq, b.ntok - first);
+                uint8_t *dst = qbuf + s * kTile;
+                if (ntok <= few) {   // single tokens: their rows only, not the whole tile's
+                    if (lane == 0) mbar_expect_tx(&q_full[s], ntok * g * 128 * kHalves);
+                    __syncwarp();
+                    const int i = lane / kHalves;
+                    if (i < ntok)
+                        tma_load_3d(dst + myhalf * (kAttnTileQ * 128) + i * g * 128, &maps.q1, &q_full[s], myhalf * 64,
+                                    kvh * g, b.tok0 + first + i);
+                } else {
+                    if (lane == 0) mbar_expect_tx(&q_full[s], p.tq * g * 128 * kHalves);
+                    __syncwarp();
+                    if (lane < kHalves)
+                        tma_load_3d(dst + lane * (kAttnTileQ * 128), &maps.q, &q_full[s], lane * 64, kvh * g,
+                                    b.tok0 + first);
+                }
+                if (s) ++nq1;
+                else ++nq0;
+            }
+            for (int i = ahead; i < 2 * n && !aborted(); ++i) load(i);
+        };
+        int64_t unit = blockIdx.x;
+        while (unit < hdr.units && !aborted()) {
+            if (!hdr.cut) {
+                // whole groups, longest first; the heads of a section together
+                const int64_t per = static_cast<int64_t>(hdr.nblocks) * hdr.sec_heads;
+                const int sec = static_cast<int>(unit / per);
+                const int64_t rem = unit - sec * per;
+                const int hs = min(hdr.sec_heads, p.kv_heads - sec * hdr.sec_heads);
+                const AttnBlock b = p.blocks[p.order[rem / hs]];
+                emit(b, sec * hdr.sec_heads + static_cast<int>(rem % hs), 0, b.tiles, 1, 0, 0);
+                int next = 0;
+                if (lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
+                unit = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
+            } else {
+                const int64_t c = hdr.unit_tiles;
+                int64_t pos = unit * c;
+                const int64_t end = min(pos + c, hdr.tiles);
+                // the block that tile `pos` is in: the last one whose tiles start at or before it
+                int lo = 0, hi = hdr.nblocks;
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 31) / 32;
+                    const int at = lo + step * lane;
+                    const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
+                    const unsigned m = __ballot_sync(0xffffffffu, le);   // lanes 0..k: lane 0 always
+                    const int k = 31 - __clz(m);
+                    const int nlo = lo + step * k;
+                    hi = min(hi, nlo + step);
+                    lo = nlo;
+                }
+                AttnBlock b = p.blocks[lo];
+                int kvh = static_cast<int>((pos - b.pre * p.kv_heads) / b.tiles);
+                while (pos < end && !aborted()) {
+                    const int64_t g0 = b.pre * p.kv_heads + static_cast<int64_t>(kvh) * b.tiles;
+                    const int t0 = static_cast<int>(pos - g0);
+                    const int t1 = static_cast<int>(min(static_cast<int64_t>(b.tiles), t0 + (end - pos)));
+                    const int64_t u0 = g0 / c, u1 = (g0 + b.tiles - 1) / c;
+                    emit(b, kvh, t0, t1, static_cast<int>(u1 - u0 + 1),
+                         static_cast<int>(unit == u0 ? 2 * unit + 1 : 2 * unit), static_cast<int>(u0));
+                    pos += t1 - t0;
+                    if (++kvh == p.kv_heads) {
+                        kvh = 0;
+                        if (++lo < hdr.nblocks) b = p.blocks[lo];
+                    }
+                }
+                break;   // one unit a CTA
+            }
+        }
+        const int is = nitem % kItems;
+        if (nitem >= kItems) wait(&item_empty[is], (nitem / kItems - 1) & 1);
+        if (lane == 0) {
+            items[is].valid = 0;
+            mbar_arrive(&item_full[is]);
+            drain[0] = static_cast<int>(it);
+            drain[1] = static_cast<int>(nq0);
+            drain[2] = static_cast<int>(nq1);
+        }
+    } else if (warp == 9) {
+        // ===================== MMA issuer =====================================
+        uint32_t it = 0, nitem = 0;
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+        const uint64_t qdesc = umma_sdesc(smem_u32(qbuf), 1024, kSwizzle128);
+        const uint64_t kdesc = umma_sdesc(smem_u32(ring), 1024, kSwizzle128);
+        const uint64_t vdesc = umma_sdesc_nmajor(smem_u32(ring), kAttnTileK * 128, 1024);
+        const int dsteps = (p.head_dim + 15) / 16;
+        const uint32_t idesc_pv = umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
+        while (true) {
+            const int is = nitem % kItems;
+            if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
+            const AttnItem w = items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[is]);
+            ++nitem;
+            if (!w.valid) break;
+            const int n = w.t1 - w.t0;
+            const int seen = min(w.kv_len, w.qpos0 + w.ntok);
+            const int n0 = max(0, min(w.t1, w.end0) - w.t0);   // pair: stream 0's tiles
+            auto valid_of = [&](int t) { return max(0, min(kAttnTileK, seen - (w.t0 + t) * kAttnTileK)); };
+            auto stage_of = [&](uint32_t i) { return static_cast<int>((it + i) % kStages); };
+            auto wait_stage = [&](uint32_t i) {
+                wait(&full[stage_of(i)], ((it + i) / kStages) & 1);
+                tc_fence_after();
+            };
+            auto qk = [&](int s, int slot, uint32_t i, int t) {
+                const int nk = max(16, (valid_of(t) + 15) & ~15);
+                if (lane == 0) {
+                    const uint64_t qd = qdesc + static_cast<uint64_t>((slot * kTile) >> 4);
+                    const uint64_t kd = kdesc + static_cast<uint64_t>((stage_of(i) * kTile) >> 4);
+                    const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, nk);
+                    for (int kk = 0; kk < dsteps; ++kk) {
+                        const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
+                        umma_bf16(tmem + s * kColS, qd + o, kd + o, idesc, kk > 0);
+                    }
+                    umma_commit(&s_full[s]);
+                }
+                __syncwarp();
+            };
+            // keys past the last one that a row sees: their p is 0, but 0 times what the
+            // tile holds there (another request's rows, stale pages) may be NaN
+            auto clean = [&](uint32_t i, int t) {
+                const int valid = valid_of(t), up = (valid + 15) & ~15;
+                if (valid == up) return;
+                uint8_t *v = ring + stage_of(i) * kTile;
+                for (int e = lane; e < (up - valid) * 8 * kHalves; e += 32) {
+                    const int r = valid + e / (8 * kHalves), c = e % (8 * kHalves);
+                    *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            auto pv = [&](int s, uint32_t i, int t, bool first) {
+                wait(&p_full[s], np[s]++ & 1);
+                tc_fence_after();
+                const int ksteps = (valid_of(t) + 15) / 16;
+                if (lane == 0) {
+                    const uint64_t vd = vdesc + static_cast<uint64_t>((stage_of(i) * kTile) >> 4);
+                    for (int kk = 0; kk < ksteps; ++kk)
+                        umma_bf16_ts(tmem + kColO + s * DP, tmem + s * kColS + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
+                                     !first || kk > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (lane == 0) umma_commit(bar);
+                __syncwarp();
+            };
+            wait(&q_full[0], nq[0]++ & 1);
+            if (w.pair) {
+                wait(&q_full[1], nq[1]++ & 1);
+                // loads: K0 V0 K1 V1 ...
+                wait_stage(0);
+                if (n0 > 0) qk(0, 0, 0, 0);
+                qk(1, 1, 0, 0);
+                commit(&empty[stage_of(0)]);
+                if (n == 1) commit(q_empty);
+                for (int t = 0; t < n && !aborted(); ++t) {
+                    const uint32_t vi = 2 * t + 1, ki = 2 * t + 2;
+                    wait_stage(vi);
+                    clean(vi, t);
+                    if (t < n0) {
+                        pv(0, vi, t, t == 0);
+                        if (t == n0 - 1) commit(&o_full[0]);
+                    }
+                    if (t + 1 < n) {
+                        wait_stage(ki);
+                        if (t + 1 < n0) qk(0, 0, ki, t + 1);
+                    }
+                    pv(1, vi, t, t == 0);
+                    commit(&empty[stage_of(vi)]);
+                    if (t == n - 1) commit(&o_full[1]);
+                    if (t + 1 < n) {
+                        qk(1, 1, ki, t + 1);
+                        commit(&empty[stage_of(ki)]);
+                        if (t + 2 == n) commit(q_empty);
+                    }
+                }
+            } else {
+                // loads: K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1)
+                wait_stage(0);
+                qk(0, 0, 0, 0);
+                commit(&empty[stage_of(0)]);
+                if (n > 1) {
+                    wait_stage(1);
+                    qk(1, 0, 1, 1);
+                    commit(&empty[stage_of(1)]);
+                }
+                if (n <= 2) commit(q_empty);
+                for (int t = 0; t < n && !aborted(); ++t) {
+                    const int s = t & 1;
+                    const uint32_t vi = min(2 * t + 2, n + t), ki = 2 * t + 3;
+                    wait_stage(vi);
+                    clean(vi, t);
+                    pv(s, vi, t, t < 2);
+                    commit(&empty[stage_of(vi)]);
+                    if (t + 2 >= n) commit(&o_full[s]);
+                    if (t + 2 < n) {
+                        wait_stage(ki);
+                        qk(s, 0, ki, t + 2);
+                        commit(&empty[stage_of(ki)]);
+                        if (t + 3 == n) commit(q_empty);
+                    }
                 }
             }
-            for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            it += 2 * n;
+            if (aborted()) break;
+        }
+    } else {
+        // ===================== softmax and results ============================
+        const int s = warp >> 2, quad = warp & 3;
+        const int r = quad * 32 + lane;   // my row of the query tile
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t t_s = tmem + lanes + s * kColS, t_o = tmem + lanes + kColO + s * DP;
+        const int G = p.group, D = p.head_dim;
+        const float c = p.scale * 1.4426950408889634f;
+        uint32_t nitem = 0, ns = 0, no[2] = {0, 0}, nx = 0;
+        auto meet = [&] {   // all 256 threads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(xbar);
+            wait(xbar, nx++ & 1);
+        };
+        while (true) {
+            const int is = nitem % kItems;
+            if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
+            const AttnItem w = items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[is]);
+            ++nitem;
+            if (!w.valid) break;
+            const int n = w.t1 - w.t0;
+            int cnt[2];
+            if (w.pair) {
+                cnt[0] = max(0, min(w.t1, w.end0) - w.t0);
+                cnt[1] = n;
+            } else {
+                cnt[0] = (n + 1) / 2;
+                cnt[1] = n / 2;
+            }
+            const int i = r / G, tok = (w.pair && s ? p.tq : 0) + i;   // my token of the block
+            const bool row_ok = i < p.tq && tok < w.ntok;
+            const int limit = row_ok ? max(0, min(w.kv_len, w.qpos0 + tok + 1)) : 0;
+            const bool live = __any_sync(0xffffffffu, limit > 0);
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < cnt[s] && !aborted(); ++k) {
+                const int tile = w.pair ? w.t0 + k : w.t0 + s + 2 * k;
+                const int rem = limit - tile * kAttnTileK;   // my visible columns of this tile
+                wait(&s_full[s], ns++ & 1);
+                tc_fence_after();
+                if (live) {
+                    if (!__any_sync(0xffffffffu, rem > 0)) {   // no row of this warp sees the tile
+                        uint32_t z[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c * 32 + lane < D)
-                    p.o[t * p.o_tok + h * p.o_head + c * 32 + lane] =
-                        static_cast<uint16_t>(pack_bf16x2(limit ? acc[c] * inv : 0.f, 0.f) & 0xFFFFu);
-            if (p.lse && lane == 0) p.lse[t * p.heads + h] = limit ? m + logf(l) : -INFINITY;
+                        for (int e = 0; e < 16; ++e) z[e] = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_st16(t_s + 16 * q, z);
+                    } else {
+                        float x[128];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, x + 32 * q);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_use32(x + 32 * q);
+                        if (__any_sync(0xffffffffu, rem < kAttnTileK)) {
+#pragma unroll
+                            for (int e = 0; e < 128; ++e) x[e] = e < rem ? x[e] : -INFINITY;
+                        }
+                        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int e = 4; e < 128; e += 8) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mx[q] = e + 4 + q < 128 ? fmaxf(fmaxf(mx[q], x[e + q]), x[e + 4 + q])
+                                                        : fmaxf(mx[q], x[e + q]);
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        // the running maximum follows when it lags too far (always from -infinity)
+                        const bool grow = (top - m) * c > kRescaleBits;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float mn = grow ? top : m;
+                            const float f = grow ? ex2((m - mn) * c) : 1.f;   // 0 from -infinity
+                            m = mn;
+                            l *= f;
+                            if (k > 0) {   // O holds the earlier tiles' sums: S of this tile came after them
+                                float o[32];
+#pragma unroll
+                                for (int q = 0; q < DP / 32; ++q) {
+                                    tmem_ld32(t_o + 32 * q, o);
+                                    tmem_ld_wait();
+                                    tmem_use32(o);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                                    tmem_st32(t_o + 32 * q, o);
+                                }
+                            }
+                        }
+                        const float off = m == -INFINITY ? 0.f : -m * c;
+                        const uint64_t c2 = pack_f2(c, c), off2 = pack_f2(off, off);
+                        uint64_t sum[2] = {0, 0};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float a, b;
+                                unpack_f2(fma_f2(pack_f2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), c2, off2), a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
+                                pk[e] = pack_bf16x2(a, b);
+                            }
+                            tmem_st16(t_s + 16 * q, pk);
+                        }
+                        float a0, a1;
+                        unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
+                        l += a0 + a1;
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[s]);
+            }
+
+            // ---- results ----------------------------------------------------
+            const int g = r - i * G;
+            float f0 = 1.f, f1 = 0.f;   // single: factors of the two streams' sums
+            bool use0 = true, use1 = false;
+            if (w.pair) {
+                if (cnt[s] > 0) wait(&o_full[s], no[s] & 1);
+            } else {
+                // both streams worked on the same rows: stream 0's threads join them
+                if (s == 1) stats[r] = make_float2(m, l);
+                wait(&o_full[0], no[0] & 1);
+                if (cnt[1] > 0) wait(&o_full[1], no[1] & 1);
+                meet();
+                if (s == 0) {
+                    const float2 st = stats[r];
+                    const float mm = fmaxf(m, st.x);
+                    // a stream without keys for the row has nothing defined in O
+                    use0 = l != 0.f;
+                    use1 = st.y != 0.f;
+                    f0 = use0 ? ex2((m - mm) * c) : 0.f;
+                    f1 = use1 ? ex2((st.x - mm) * c) : 0.f;
+                    m = mm;
+                    l = l * f0 + st.y * f1;
+                }
+            }
+            tc_fence_after();
+            if (cnt[0] > 0) ++no[0];
+            if (cnt[1] > 0) ++no[1];
+            const bool mine = w.pair || s == 0;
+            const int rho = tok * G + g;   // my row of the block
+            if (mine && __any_sync(0xffffffffu, row_ok)) {
+                const bool whole = w.parts == 1;
+                const float inv = whole && l != 0.f ? 1.f / l : 1.f;
+                const int64_t row = static_cast<int64_t>(w.tok0) + tok;
+                const int head = w.kvh * G + g;
+                uint16_t *out = p.o + row * p.o_tok + head * p.o_head;
+                float *part = p.part + (static_cast<int64_t>(w.slot) * p.part_rows + rho) * D;
+#pragma unroll
+                for (int q = 0; q < DP / 32; ++q) {
+                    if (32 * q >= D) break;
+                    float o[32];
+                    tmem_ld32(t_o + 32 * q, o);
+                    tmem_ld_wait();
+                    tmem_use32(o);
+                    if (!w.pair) {
+                        float o1[32];
+                        tmem_ld32(t_o + DP + 32 * q, o1);
+                        tmem_ld_wait();
+                        tmem_use32(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = (use0 ? o[e] * f0 : 0.f) + (use1 ? o1[e] * f1 : 0.f);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+                    if (!row_ok) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (32 * q + e < D)
+                                *reinterpret_cast<uint4 *>(out + 32 * q + e) =
+                                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                               pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (32 * q + e < D)
+                                *reinterpret_cast<float4 *>(part + 32 * q + e) =
+                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (row_ok) {
+                    if (!whole)
+                        p.part_ml[static_cast<int64_t>(w.slot) * p.part_rows + rho] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+                }
+            }
+            if (w.parts > 1) {
+                // the piece that finishes last joins the group's pieces, in their order
+                __threadfence();
+                meet();
+                if (threadIdx.x == 0)
+                    *join_flag = atom_acq_rel_gpu_add(p.counters + ACNT_GROUP + w.unit0, 1) == w.parts - 1;
+                meet();
+                if (*join_flag) {
+                    const int rows = w.ntok * G, d4 = D / 4;
+                    auto slot_of = [&](int k) {
+                        return static_cast<int64_t>(k == 0 ? 2 * w.unit0 + 1 : 2 * (w.unit0 + k)) * p.part_rows;
+                    };
+                    for (int u = threadIdx.x; u < rows * d4; u += 256) {
+                        const int rr = u / d4, col = (u - rr * d4) * 4;
+                        float mm = -INFINITY;
+                        for (int k = 0; k < w.parts; ++k) mm = fmaxf(mm, __ldcg(&p.part_ml[slot_of(k) + rr].x));
+                        float ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int k = 0; k < w.parts; ++k) {
+                            const float2 ml = __ldcg(p.part_ml + slot_of(k) + rr);
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(k) + rr) * D + col));
+                            const float f = ml.y == 0.f ? 0.f : ex2((ml.x - mm) * c);
+                            ll += f * ml.y;
+                            a[0] += f * v.x;
+                            a[1] += f * v.y;
+                            a[2] += f * v.z;
+                            a[3] += f * v.w;
+                        }
+                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                        const int tk = rr / G, hd = w.kvh * G + (rr - tk * G);
+                        const int64_t row = static_cast<int64_t>(w.tok0) + tk;
+                        *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col) =
+                            make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
+                        if (p.lse && col == 0)
+                            p.lse[row * p.heads + hd] = ll == 0.f ? -INFINITY : (mm * c + log2f(ll)) * 0.6931471805599453f;
+                    }
+                    if (threadIdx.x == 0) p.counters[ACNT_GROUP + w.unit0] = 0;
+                }
+            } else if (!w.pair) {
+                tc_fence_before();
+                meet();   // O of stream 1 and its stats have been read
+            }
+            tc_fence_before();
+            if (aborted()) break;
+        }
+    }
+
+    // ---- teardown -----------------------------------------------------------
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) {
+        // loads in flight are waited for (bounded) before the shared memory goes,
+        // matrix products before the tensor memory does
+        auto settle = [&](uint64_t *bar, uint32_t parity) {
+            mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
+        };
+        if (warp == 8 && lane == 0) {
+            const uint32_t n = static_cast<uint32_t>(drain[0]);
+            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) settle(&full[i % kStages], (i / kStages) & 1);
+            for (int s = 0; s < 2; ++s)
+                if (drain[1 + s] > 0) settle(&q_full[s], (drain[1 + s] - 1) & 1);
+        }
+        if (warp == 9 && lane == 0) {
+            umma_commit(end_bar);
+            settle(end_bar, 0);
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    // the work-list counters go back to zero with the last CTA
+    if (threadIdx.x == 0 && !hdr.cut) {
+        if (atom_acq_rel_gpu_add(p.counters + ACNT_DONE, 1) == static_cast<int>(gridDim.x) - 1) {
+            p.counters[ACNT_NEXT] = 0;
+            p.counters[ACNT_DONE] = 0;
         }
     }
 }
 
-cudaError_t launch_attn(const AttnParams &p, cudaStream_t stream)
+template <int DP, bool kPaged>
+static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_t stream)
 {
+    static int configured[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    constexpr int bytes = AttnSmem<DP>::kBytes;
+    if (dev >= 64 || !configured[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(attn_kernel<DP, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = 1;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(8 * num_sms_current_device());
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
     cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     pdl_attribute(cfg, at);
-    return cudaLaunchKernelEx(&cfg, attn_kernel, p);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<DP, kPaged>, maps, p);
+}
+
+cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
+{
+    AttnMaps m;
+    const uint64_t D = p.head_dim, row = D * 2;
+    // a stride over an extent of 1 is never used; the map wants a valid one
+    auto bytes = [&](int64_t stride, int64_t extent) {
+        return extent > 1 ? static_cast<uint64_t>(stride) * 2 : row;
+    };
+    const uint32_t G = static_cast<uint32_t>(p.group);
+    {
+        const uint64_t dims[3] = {D, static_cast<uint64_t>(p.heads), static_cast<uint64_t>(p.T)};
+        const uint64_t st[2] = {bytes(p.q_head, p.heads), bytes(p.q_tok, p.T)};
+        const uint32_t box[3] = {64, G, static_cast<uint32_t>(p.tq)}, box1[3] = {64, G, 1};
+        if (!encode_map(&m.q, p.q, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_map(&m.q1, p.q, 3, dims, st, box1, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    if (p.paged) {
+        const int page = 1 << p.page_shift;
+        p.box_rows = page < kAttnTileK ? page : kAttnTileK;
+        const uint64_t dims[4] = {D, static_cast<uint64_t>(page), static_cast<uint64_t>(p.kv_heads),
+                                  static_cast<uint64_t>(p.num_pages)};
+        const uint64_t st[3] = {bytes(p.slot_stride, page), bytes(p.head_stride, p.kv_heads),
+                                bytes(p.page_stride, p.num_pages)};
+        const uint32_t box[4] = {64, static_cast<uint32_t>(p.box_rows), 1, 1};
+        if (!encode_map(&m.k, p.k, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_map(&m.v, p.v, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    } else {
+        p.box_rows = 32;   // a short prompt's tile reads at most 31 rows too many
+        const uint64_t dims[3] = {D, static_cast<uint64_t>(p.kv_heads), static_cast<uint64_t>(p.T)};
+        const uint64_t ks[2] = {bytes(p.k_head, p.kv_heads), bytes(p.k_tok, p.T)};
+        const uint64_t vs[2] = {bytes(p.v_head, p.kv_heads), bytes(p.v_tok, p.T)};
+        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(p.box_rows)};
+        if (!encode_map(&m.k, p.k, 3, dims, ks, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_map(&m.v, p.v, 3, dims, vs, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    if (p.head_dim <= 64) return p.paged ? launch<64, true>(m, p, stream) : launch<64, false>(m, p, stream);
+    return p.paged ? launch<128, true>(m, p, stream) : launch<128, false>(m, p, stream);
 }
 
 }  // namespace lora

@@ -78,14 +78,21 @@ struct AttnParams {
     const AttnBlock *blocks;
     const int32_t *order;
     int32_t *counters;
-    // keys and values: paged (block_table set) or packed rows
+    // keys and values: paged or packed rows
     const uint16_t *k, *v;
     int64_t k_tok, k_head, v_tok, v_head;   // packed: element strides
     const int32_t *block_table;
     int64_t table_stride;
     int32_t table_width, num_pages, page_shift;
     int64_t page_stride, head_stride, slot_stride;
-    const int32_t *cu;
+    int32_t paged;
+    int32_t box_rows;        // keys of one TMA box
+    int64_t T;
+    int32_t ctas;
+    float *part;             // [2 * kAttnMaxCtas][part_rows][head_dim] partial O
+    float2 *part_ml;         // [2 * kAttnMaxCtas][part_rows] partial (m, l)
+    int32_t part_rows;
+    int64_t wait_cycles;     // long budget of the bounded waits, in SM clock cycles
 };
 
 struct KvPlanParams {
@@ -108,7 +115,7 @@ struct KvStoreParams {
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
 cudaError_t launch_kv_store(const KvStoreParams &p, cudaStream_t stream);
 cudaError_t launch_attn_schedule(const AttnSchedParams &p, cudaStream_t stream);
-cudaError_t launch_attn(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn(AttnParams &p, cudaStream_t stream);   // fills in box_rows
 
 // Launch attribute of a programmatic dependent launch: the kernel may start
 // its prologue while the one ahead finishes (every kernel here waits for it

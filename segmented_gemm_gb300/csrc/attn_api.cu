@@ -162,7 +162,12 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->blocks = at<AttnBlock>(ws, L.blocks);
     p->order = at<int32_t>(ws, L.order);
     p->counters = at<int32_t>(ws, L.counters);
-    p->cu = a->cu;
+    p->T = a->num_tokens;
+    p->ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
+    p->part = at<float>(ws, L.part);
+    p->part_ml = at<float2>(ws, L.part_ml);
+    p->part_rows = L.part_rows;
+    p->wait_cycles = tc_wait_cycles();
     return LORA_OK;
 }
 
@@ -286,6 +291,7 @@ extern "C" int lora_attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *c
     if (rc) return rc;
     p.k = cache->k;
     p.v = cache->v;
+    p.paged = 1;
     p.block_table = block_table;
     p.table_stride = table_stride;
     p.table_width = table_width;

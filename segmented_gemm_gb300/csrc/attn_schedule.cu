@@ -25,6 +25,8 @@ namespace lora {
 
 constexpr int kSchedThreads = 1024;
 constexpr int kSchedBuckets = 1024;          // block costs told apart by the sort
+constexpr int kMinPiece = 2;                 // key tiles of a piece, at least
+constexpr int kJoinSingle = 2, kJoinPair = 6; // what joining partial results costs, in key tiles
 constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads that run together (L2 holds 126 MB)
 
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const AttnSchedParams p)
@@ -42,6 +44,9 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     }
     hist[tid] = 0;
     pdl_wait();
+    // a call whose waits gave up may have left counters behind
+    for (int i = tid; i < ACNT_WORDS; i += kSchedThreads)
+        if (i != CNT_STATUS) p.counters[i] = 0;
 
     // query rows and keys of request r, clamped
     int bad = 0;
@@ -130,9 +135,14 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
         AttnHdr h;
         h.nblocks = nb;
         h.tiles = W;
-        h.cut = 0;
-        h.unit_tiles = 0;
-        h.units = static_cast<int32_t>(min(static_cast<int64_t>(nb) * p.kv_heads, static_cast<int64_t>(INT32_MAX)));
+        // key tiles a CTA runs, on average, and what each way adds to that
+        const int64_t each = (W + p.ctas - 1) / p.ctas;
+        const int64_t whole = max(each + (s_max + 1) / 2, static_cast<int64_t>(s_max));
+        const int64_t piece = max(each, static_cast<int64_t>(kMinPiece)) + (s_pair ? kJoinPair : kJoinSingle);
+        h.cut = piece < whole;
+        h.unit_tiles = max(each, static_cast<int64_t>(kMinPiece));
+        h.units = static_cast<int32_t>(h.cut ? (W + h.unit_tiles - 1) / h.unit_tiles
+                                             : min(static_cast<int64_t>(nb) * p.kv_heads, static_cast<int64_t>(INT32_MAX)));
         const int64_t head_bytes = max(static_cast<int64_t>(1), all_keys * p.head_dim * 4);
         h.sec_heads = static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
         *p.hdr = h;
