@@ -20,8 +20,9 @@
 // by the softmax threads themselves, and the division by l_i at the end makes
 // any m_i as good as the true maximum.
 //
-// Roles (320 threads): warps 0..3 and 4..7 the softmax and the results of
-// stream 0 and 1, warp 8 loads (TMA), warp 9 issues the matrix products.
+// Roles (384 threads): warps 0..3 and 4..7 the softmax and the results of
+// stream 0 and 1, warp 8 loads (TMA), warp 9 issues the matrix products (10 and
+// 11 fill the warpgroup up: registers move between warpgroups).
 // Shared memory: two query tiles and a ring of key and value tiles.
 // Persistent, one CTA per SM; work comes from the schedule (attn_schedule.cu).
 // A group (block, kv head) cut into pieces leaves partial (O, m, l) in the
@@ -35,7 +36,10 @@
 
 namespace lora {
 
-constexpr int kAttnThreads = 320;
+constexpr int kAttnThreads = 384;
+// registers a thread: 168 at launch; a softmax thread holds a row's 128 scores
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the split draws on the launch's registers");
 constexpr int kItems = 4;             // work items in flight between the loader and the others
 constexpr float kRescaleBits = 8.f;   // m_i may lag the maximum by this many powers of two
 
@@ -66,6 +70,36 @@ struct AttnSmem {
     static constexpr int kBytes = kEnd + 1024;                 // room to align the base
     static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
 };
+
+// Each lane holds 64 bytes (four 16-byte chunks) of its own row at byte `at`;
+// four lanes exchange theirs so that a store instruction writes 64 bytes of
+// each of eight rows instead of 16 bytes of thirty-two.  dst: the lane's row,
+// or 0; bytes: the row's length.
+__device__ __forceinline__ void store_rows(uint32_t (&v)[16], uint64_t dst, int at, int bytes, int lane)
+{
+#pragma unroll
+    for (int step = 1; step <= 2; step <<= 1) {
+        const bool hi = lane & step;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (a & step) continue;
+            const int b = a | step;   // chunks a and b change places with the other lane's
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t t = __shfl_xor_sync(0xffffffffu, hi ? v[4 * a + w] : v[4 * b + w], step);
+                if (hi) v[4 * a + w] = t;
+                else v[4 * b + w] = t;
+            }
+        }
+    }
+    const int col = at + (lane & 3) * 16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t row = __shfl_sync(0xffffffffu, dst, (lane & ~3) | k);
+        if (row != 0 && col < bytes)
+            *reinterpret_cast<uint4 *>(row + col) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+}
 
 struct AttnMaps {
     CUtensorMap q, q1, k, v;   // q: tq tokens of a group's heads; q1: one token's
@@ -105,7 +139,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool ok = mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
         return __all_sync(0xffffffffu, ok) != 0;
     };
-    auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -150,9 +183,53 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 8) {
         // ===================== loader =========================================
+        setmaxnreg_dec<kOtherRegs>();
         uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0;
-        // one (block, head) piece: hand it to the other roles, then load it
-        auto emit = [&](const AttnBlock &b, int kvh, int t0, int t1, int parts, int slot, int unit0) {
+        const bool cut = hdr.cut != 0;
+        int64_t unit = blockIdx.x;
+        // cut: my unit's tiles [pos, end) of the list; lo: the block that pos is in
+        int64_t pos = unit * hdr.unit_tiles;
+        const int64_t end = min(pos + hdr.unit_tiles, hdr.tiles);
+        int lo = 0, kvh = 0;
+        AttnBlock b;
+        bool ok = true;
+        if (cut && unit < hdr.units) {
+            // the last block whose tiles start at or before pos
+            int hi = hdr.nblocks;
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32;
+                const int at = lo + step * lane;
+                const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
+                const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lanes 0..k, lane 0 always
+                lo += step * k;
+                hi = min(hi, lo + step);
+            }
+            b = p.blocks[lo];
+            kvh = static_cast<int>((pos - b.pre * p.kv_heads) / b.tiles);
+        }
+        while (ok && unit < hdr.units) {
+            // the next piece: key tiles [t0, t1) of (block b, head kvh)
+            int t0 = 0, t1, parts = 1, slot = 0, unit0 = 0;
+            if (!cut) {
+                // whole groups, longest first; the heads of a section together
+                const int64_t per = static_cast<int64_t>(hdr.nblocks) * hdr.sec_heads;
+                const int sec = static_cast<int>(unit / per);
+                const int64_t rem = unit - sec * per;
+                const int hs = min(hdr.sec_heads, p.kv_heads - sec * hdr.sec_heads);
+                b = p.blocks[p.order[rem / hs]];
+                kvh = sec * hdr.sec_heads + static_cast<int>(rem % hs);
+                t1 = b.tiles;
+            } else {
+                if (pos >= end) break;
+                const int64_t g0 = b.pre * p.kv_heads + static_cast<int64_t>(kvh) * b.tiles;
+                t0 = static_cast<int>(pos - g0);
+                t1 = static_cast<int>(min(static_cast<int64_t>(b.tiles), t0 + (end - pos)));
+                const int64_t u0 = g0 / hdr.unit_tiles, u1 = (g0 + b.tiles - 1) / hdr.unit_tiles;
+                parts = static_cast<int>(u1 - u0 + 1);
+                slot = static_cast<int>(unit == u0 ? 2 * unit + 1 : 2 * unit);
+                unit0 = static_cast<int>(u0);
+            }
+            // hand it to the other roles, then load it
             AttnItem w;
             w.valid = 1;
             w.pair = b.ntok > p.tq;
@@ -169,7 +246,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             w.slot = slot;
             w.unit0 = unit0;
             const int is = nitem % kItems;
-            if (nitem >= kItems) wait(&item_empty[is], (nitem / kItems - 1) & 1);
+            if (nitem >= kItems) ok &= wait(&item_empty[is], (nitem / kItems - 1) & 1);
             if (lane == 0) {
                 items[is] = w;
                 mbar_arrive(&item_full[is]);
@@ -216,7 +293,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int valid = max(0, min(kAttnTileK, seen - tile * kAttnTileK));
                 const int boxes = (valid + box - 1) / box;
                 const int s = it % kStages;
-                if (it >= kStages) wait(&empty[s], (it / kStages - 1) & 1);
+                if (it >= kStages) ok &= wait(&empty[s], (it / kStages - 1) & 1);
+                if (!ok) return;
                 ++it;
                 if (lane == 0) mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
                 __syncwarp();
@@ -232,8 +310,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             // a few tiles go ahead of the queries, whose buffers the previous piece may still hold
             const int ahead = min(3, 2 * n);
-            for (int i = 0; i < ahead; ++i) load(i);
-            if (nitem > 1) wait(q_empty, (nitem - 2) & 1);
+            for (int i = 0; i < ahead && ok; ++i) load(i);
+            if (nitem > 1) ok &= wait(q_empty, (nitem - 2) & 1);
+            if (!ok) break;
             const int g = p.group, few = 4;
             for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
                 const int first = s * p.tq, ntok = min(p.tq, b.ntok - first);
@@ -255,53 +334,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (s) ++nq1;
                 else ++nq0;
             }
-            for (int i = ahead; i < 2 * n && !aborted(); ++i) load(i);
-        };
-        int64_t unit = blockIdx.x;
-        while (unit < hdr.units && !aborted()) {
-            if (!hdr.cut) {
-                // whole groups, longest first; the heads of a section together
-                const int64_t per = static_cast<int64_t>(hdr.nblocks) * hdr.sec_heads;
-                const int sec = static_cast<int>(unit / per);
-                const int64_t rem = unit - sec * per;
-                const int hs = min(hdr.sec_heads, p.kv_heads - sec * hdr.sec_heads);
-                const AttnBlock b = p.blocks[p.order[rem / hs]];
-                emit(b, sec * hdr.sec_heads + static_cast<int>(rem % hs), 0, b.tiles, 1, 0, 0);
+            for (int i = ahead; i < 2 * n && ok; ++i) load(i);
+            if (!cut) {
                 int next = 0;
                 if (lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
                 unit = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
             } else {
-                const int64_t c = hdr.unit_tiles;
-                int64_t pos = unit * c;
-                const int64_t end = min(pos + c, hdr.tiles);
-                // the block that tile `pos` is in: the last one whose tiles start at or before it
-                int lo = 0, hi = hdr.nblocks;
-                while (hi - lo > 1) {
-                    const int step = (hi - lo + 31) / 32;
-                    const int at = lo + step * lane;
-                    const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
-                    const unsigned m = __ballot_sync(0xffffffffu, le);   // lanes 0..k: lane 0 always
-                    const int k = 31 - __clz(m);
-                    const int nlo = lo + step * k;
-                    hi = min(hi, nlo + step);
-                    lo = nlo;
+                pos += t1 - t0;
+                if (++kvh == p.kv_heads) {
+                    kvh = 0;
+                    if (++lo < hdr.nblocks) b = p.blocks[lo];
                 }
-                AttnBlock b = p.blocks[lo];
-                int kvh = static_cast<int>((pos - b.pre * p.kv_heads) / b.tiles);
-                while (pos < end && !aborted()) {
-                    const int64_t g0 = b.pre * p.kv_heads + static_cast<int64_t>(kvh) * b.tiles;
-                    const int t0 = static_cast<int>(pos - g0);
-                    const int t1 = static_cast<int>(min(static_cast<int64_t>(b.tiles), t0 + (end - pos)));
-                    const int64_t u0 = g0 / c, u1 = (g0 + b.tiles - 1) / c;
-                    emit(b, kvh, t0, t1, static_cast<int>(u1 - u0 + 1),
-                         static_cast<int>(unit == u0 ? 2 * unit + 1 : 2 * unit), static_cast<int>(u0));
-                    pos += t1 - t0;
-                    if (++kvh == p.kv_heads) {
-                        kvh = 0;
-                        if (++lo < hdr.nblocks) b = p.blocks[lo];
-                    }
-                }
-                break;   // one unit a CTA
             }
         }
         const int is = nitem % kItems;
@@ -314,144 +357,144 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             drain[2] = static_cast<int>(nq1);
         }
     } else if (warp == 9) {
+        setmaxnreg_dec<kOtherRegs>();
         // ===================== MMA issuer =====================================
-        uint32_t it = 0, nitem = 0;
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-        const uint64_t qdesc = umma_sdesc(smem_u32(qbuf), 1024, kSwizzle128);
-        const uint64_t kdesc = umma_sdesc(smem_u32(ring), 1024, kSwizzle128);
-        const uint64_t vdesc = umma_sdesc_nmajor(smem_u32(ring), kAttnTileK * 128, 1024);
+        // All lanes run the same code and lane 0's instructions take effect;
+        // what the descriptors are made of is kept uniform across the warp, and
+        // the steps are unrolled: issuing 8 products must take less than
+        // executing them (64 cycles each).
+        uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+        const uint32_t lead = lane == 0;
+        const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
+        const uint32_t klo = umma_lo(smem_u32(ring), 16), vlo = umma_lo(smem_u32(ring), kAttnTileK * 128);
         const int dsteps = (p.head_dim + 15) / 16;
         const uint32_t idesc_pv = umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
+        bool ok = true;
         while (true) {
             const int is = nitem % kItems;
             if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
-            const AttnItem w = items[is];
+            const AttnItem &wi = items[is];
+            const int valid = uniform(wi.valid), pair = uniform(wi.pair), t0 = uniform(wi.t0);
+            const int n = uniform(wi.t1) - t0;
+            const int seen = uniform(min(wi.kv_len, wi.qpos0 + wi.ntok)) - t0 * kAttnTileK;   // keys that any row sees
+            const int n0 = max(0, min(n, uniform(wi.end0) - t0));   // pair: stream 0's tiles
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
             ++nitem;
-            if (!w.valid) break;
-            const int n = w.t1 - w.t0;
-            const int seen = min(w.kv_len, w.qpos0 + w.ntok);
-            const int n0 = max(0, min(w.t1, w.end0) - w.t0);   // pair: stream 0's tiles
-            auto valid_of = [&](int t) { return max(0, min(kAttnTileK, seen - (w.t0 + t) * kAttnTileK)); };
-            auto stage_of = [&](uint32_t i) { return static_cast<int>((it + i) % kStages); };
+            if (!valid) break;
+            // one more product step of a stream: the load i holds its tile, t counts from the piece's first
+            auto stage_of = [&](uint32_t i) { return (it + i) % kStages; };
             auto wait_stage = [&](uint32_t i) {
-                wait(&full[stage_of(i)], ((it + i) / kStages) & 1);
+                ok &= wait(&full[stage_of(i)], ((it + i) / kStages) & 1);
                 tc_fence_after();
             };
+            auto release = [&](uint32_t i) { umma_commit_if(lead, &empty[stage_of(i)]); };
             auto qk = [&](int s, int slot, uint32_t i, int t) {
-                const int nk = max(16, (valid_of(t) + 15) & ~15);
-                if (lane == 0) {
-                    const uint64_t qd = qdesc + static_cast<uint64_t>((slot * kTile) >> 4);
-                    const uint64_t kd = kdesc + static_cast<uint64_t>((stage_of(i) * kTile) >> 4);
-                    const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, nk);
-                    for (int kk = 0; kk < dsteps; ++kk) {
+                const int keys = min(kAttnTileK, seen - t * kAttnTileK);
+                const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
+                const uint32_t qd = qlo + ((slot * kTile) >> 4), kd = klo + stage_of(i) * (kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk)
+                    if (kk < dsteps) {
                         const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
-                        umma_bf16(tmem + s * kColS, qd + o, kd + o, idesc, kk > 0);
+                        umma_ss_if(lead, tmem + s * kColS, qd + o, kd + o, idesc, kk > 0);
                     }
-                    umma_commit(&s_full[s]);
-                }
-                __syncwarp();
+                umma_commit_if(lead, &s_full[s]);
+            };
+            auto pv = [&](int s, uint32_t i, int t, uint32_t acc) {
+                const int keys = max(0, min(kAttnTileK, seen - t * kAttnTileK));
+                const uint32_t vd = vlo + stage_of(i) * (kTile >> 4), a = tmem + s * kColS, d = tmem + kColO + s * DP;
+                ok &= wait(&p_full[s], (s ? np1++ : np0++) & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kAttnTileK / 16; ++kk)
+                    if (kk * 16 < keys) umma_ts_if(lead, d, a + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : acc);
             };
             // keys past the last one that a row sees: their p is 0, but 0 times what the
             // tile holds there (another request's rows, stale pages) may be NaN
             auto clean = [&](uint32_t i, int t) {
-                const int valid = valid_of(t), up = (valid + 15) & ~15;
-                if (valid == up) return;
+                const int keys = seen - t * kAttnTileK, up = (keys + 15) & ~15;
+                if (keys >= kAttnTileK || keys <= 0 || keys == up) return;
                 uint8_t *v = ring + stage_of(i) * kTile;
-                for (int e = lane; e < (up - valid) * 8 * kHalves; e += 32) {
-                    const int r = valid + e / (8 * kHalves), c = e % (8 * kHalves);
+                for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
+                    const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
                     *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            auto pv = [&](int s, uint32_t i, int t, bool first) {
-                wait(&p_full[s], np[s]++ & 1);
-                tc_fence_after();
-                const int ksteps = (valid_of(t) + 15) / 16;
-                if (lane == 0) {
-                    const uint64_t vd = vdesc + static_cast<uint64_t>((stage_of(i) * kTile) >> 4);
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        umma_bf16_ts(tmem + kColO + s * DP, tmem + s * kColS + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
-                                     !first || kk > 0);
-                }
-                __syncwarp();
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (lane == 0) umma_commit(bar);
-                __syncwarp();
-            };
-            wait(&q_full[0], nq[0]++ & 1);
-            if (w.pair) {
-                wait(&q_full[1], nq[1]++ & 1);
+            ok &= wait(&q_full[0], nq0++ & 1);
+            if (pair) {
+                ok &= wait(&q_full[1], nq1++ & 1);
                 // loads: K0 V0 K1 V1 ...
                 wait_stage(0);
                 if (n0 > 0) qk(0, 0, 0, 0);
                 qk(1, 1, 0, 0);
-                commit(&empty[stage_of(0)]);
-                if (n == 1) commit(q_empty);
-                for (int t = 0; t < n && !aborted(); ++t) {
+                release(0);
+                if (n == 1) umma_commit_if(lead, q_empty);
+                for (int t = 0; t < n && ok; ++t) {
                     const uint32_t vi = 2 * t + 1, ki = 2 * t + 2;
                     wait_stage(vi);
                     clean(vi, t);
                     if (t < n0) {
-                        pv(0, vi, t, t == 0);
-                        if (t == n0 - 1) commit(&o_full[0]);
+                        pv(0, vi, t, t > 0);
+                        if (t == n0 - 1) umma_commit_if(lead, &o_full[0]);
                     }
                     if (t + 1 < n) {
                         wait_stage(ki);
                         if (t + 1 < n0) qk(0, 0, ki, t + 1);
                     }
-                    pv(1, vi, t, t == 0);
-                    commit(&empty[stage_of(vi)]);
-                    if (t == n - 1) commit(&o_full[1]);
+                    pv(1, vi, t, t > 0);
+                    release(vi);
+                    if (t == n - 1) umma_commit_if(lead, &o_full[1]);
                     if (t + 1 < n) {
                         qk(1, 1, ki, t + 1);
-                        commit(&empty[stage_of(ki)]);
-                        if (t + 2 == n) commit(q_empty);
+                        release(ki);
+                        if (t + 2 == n) umma_commit_if(lead, q_empty);
                     }
                 }
             } else {
-                // loads: K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1)
-                wait_stage(0);
-                qk(0, 0, 0, 0);
-                commit(&empty[stage_of(0)]);
-                if (n > 1) {
-                    wait_stage(1);
-                    qk(1, 0, 1, 1);
-                    commit(&empty[stage_of(1)]);
+                // loads: K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1); tile t is stream t & 1's
+                for (int t = 0; t < 2 && t < n; ++t) {
+                    wait_stage(t);
+                    if (t == 0) qk(0, 0, 0, 0);
+                    else qk(1, 0, 1, 1);
+                    release(t);
                 }
-                if (n <= 2) commit(q_empty);
-                for (int t = 0; t < n && !aborted(); ++t) {
-                    const int s = t & 1;
+                if (n <= 2) umma_commit_if(lead, q_empty);
+                for (int t = 0; t < n && ok; ++t) {
                     const uint32_t vi = min(2 * t + 2, n + t), ki = 2 * t + 3;
                     wait_stage(vi);
                     clean(vi, t);
-                    pv(s, vi, t, t < 2);
-                    commit(&empty[stage_of(vi)]);
-                    if (t + 2 >= n) commit(&o_full[s]);
+                    if (t & 1) pv(1, vi, t, t > 1);
+                    else pv(0, vi, t, t > 1);
+                    release(vi);
+                    if (t + 2 >= n) umma_commit_if(lead, &o_full[t & 1]);
                     if (t + 2 < n) {
                         wait_stage(ki);
-                        qk(s, 0, ki, t + 2);
-                        commit(&empty[stage_of(ki)]);
-                        if (t + 3 == n) commit(q_empty);
+                        if (t & 1) qk(1, 0, ki, t + 2);
+                        else qk(0, 0, ki, t + 2);
+                        release(ki);
+                        if (t + 3 == n) umma_commit_if(lead, q_empty);
                     }
                 }
             }
             it += 2 * n;
-            if (aborted()) break;
+            if (!ok) break;
         }
+    } else if (warp > 9) {
+        setmaxnreg_dec<kOtherRegs>();
     } else {
         // ===================== softmax and results ============================
+        setmaxnreg_inc<kSoftmaxRegs>();
         const int s = warp >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;   // my row of the query tile
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lanes + s * kColS, t_o = tmem + lanes + kColO + s * DP;
         const int G = p.group, D = p.head_dim;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t nitem = 0, ns = 0, no[2] = {0, 0}, nx = 0;
+        uint32_t nitem = 0, ns = 0, no0 = 0, no1 = 0, nx = 0;
         auto meet = [&] {   // all 256 threads
             __syncwarp();
             if (lane == 0) mbar_arrive(xbar);
@@ -466,23 +509,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ++nitem;
             if (!w.valid) break;
             const int n = w.t1 - w.t0;
-            int cnt[2];
-            if (w.pair) {
-                cnt[0] = max(0, min(w.t1, w.end0) - w.t0);
-                cnt[1] = n;
-            } else {
-                cnt[0] = (n + 1) / 2;
-                cnt[1] = n / 2;
-            }
+            // key tiles of the two streams
+            const int cnt0 = w.pair ? max(0, min(w.t1, w.end0) - w.t0) : (n + 1) / 2, cnt1 = w.pair ? n : n / 2;
+            const int mine_n = s ? cnt1 : cnt0;
             const int i = r / G, tok = (w.pair && s ? p.tq : 0) + i;   // my token of the block
             const bool row_ok = i < p.tq && tok < w.ntok;
             const int limit = row_ok ? max(0, min(w.kv_len, w.qpos0 + tok + 1)) : 0;
             const bool live = __any_sync(0xffffffffu, limit > 0);
             float m = -INFINITY, l = 0.f;
-            for (int k = 0; k < cnt[s] && !aborted(); ++k) {
+            for (int k = 0; k < mine_n; ++k) {
                 const int tile = w.pair ? w.t0 + k : w.t0 + s + 2 * k;
                 const int rem = limit - tile * kAttnTileK;   // my visible columns of this tile
-                wait(&s_full[s], ns++ & 1);
+                if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
                 if (live) {
                     if (!__any_sync(0xffffffffu, rem > 0)) {   // no row of this warp sees the tile
@@ -564,12 +602,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float f0 = 1.f, f1 = 0.f;   // single: factors of the two streams' sums
             bool use0 = true, use1 = false;
             if (w.pair) {
-                if (cnt[s] > 0) wait(&o_full[s], no[s] & 1);
+                if (mine_n > 0) wait(&o_full[s], (s ? no1 : no0) & 1);
             } else {
                 // both streams worked on the same rows: stream 0's threads join them
                 if (s == 1) stats[r] = make_float2(m, l);
-                wait(&o_full[0], no[0] & 1);
-                if (cnt[1] > 0) wait(&o_full[1], no[1] & 1);
+                wait(&o_full[0], no0 & 1);
+                if (cnt1 > 0) wait(&o_full[1], no1 & 1);
                 meet();
                 if (s == 0) {
                     const float2 st = stats[r];
@@ -584,8 +622,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             tc_fence_after();
-            if (cnt[0] > 0) ++no[0];
-            if (cnt[1] > 0) ++no[1];
+            no0 += cnt0 > 0;
+            no1 += cnt1 > 0;
             const bool mine = w.pair || s == 0;
             const int rho = tok * G + g;   // my row of the block
             if (mine && __any_sync(0xffffffffu, row_ok)) {
@@ -593,11 +631,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const float inv = whole && l != 0.f ? 1.f / l : 1.f;
                 const int64_t row = static_cast<int64_t>(w.tok0) + tok;
                 const int head = w.kvh * G + g;
-                uint16_t *out = p.o + row * p.o_tok + head * p.o_head;
-                float *part = p.part + (static_cast<int64_t>(w.slot) * p.part_rows + rho) * D;
-#pragma unroll
-                for (int q = 0; q < DP / 32; ++q) {
-                    if (32 * q >= D) break;
+                uint8_t *out = whole ? reinterpret_cast<uint8_t *>(p.o + row * p.o_tok + head * p.o_head)
+                                     : reinterpret_cast<uint8_t *>(p.part + (static_cast<int64_t>(w.slot) * p.part_rows + rho) * D);
+                const uint64_t dst = row_ok ? reinterpret_cast<uint64_t>(out) : 0;
+                // 16 columns of fp32 or 32 of bf16 at a time: 64 bytes a row
+#pragma unroll 1
+                for (int q = 0; 32 * q < D; ++q) {
                     float o[32];
                     tmem_ld32(t_o + 32 * q, o);
                     tmem_ld_wait();
@@ -612,20 +651,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-                    if (!row_ok) continue;
+                    uint32_t v[16];
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (32 * q + e < D)
-                                *reinterpret_cast<uint4 *>(out + 32 * q + e) =
-                                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                               pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+                        store_rows(v, dst, 64 * q, D * 2, lane);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            if (32 * q + e < D)
-                                *reinterpret_cast<float4 *>(part + 32 * q + e) =
-                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[16 * h + e]);
+                            store_rows(v, dst, 128 * q + 64 * h, D * 4, lane);
+                        }
                     }
                 }
                 if (row_ok) {
@@ -677,7 +714,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 meet();   // O of stream 1 and its stats have been read
             }
             tc_fence_before();
-            if (aborted()) break;
         }
     }
 

@@ -7,31 +7,80 @@
 
 namespace lora {
 
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate: A's rows are
-// the tensor memory lanes, two bf16 columns to a 32-bit cell.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate)
+// The matrix products and commits below are run by a whole warp and take
+// effect for the lanes with `on` set (one), without a branch around them.
+//
+// Shared-memory descriptors in the 128-byte swizzle, as two words: umma_lo
+// (start address, leading byte offset) varies, kUmmaHi (1024 bytes from 8 rows
+// to the next 8, descriptor version 1, swizzle) does not.  K-major operands:
+// the leading offset is not used.  N-major ones (the N elements contiguous):
+// 64 N elements x 8 K rows make a 1024-byte atom, `lead` bytes go from one
+// group of 64 N elements to the next.
+constexpr uint32_t kUmmaHi = (1024 >> 4) | (1u << 14) | (static_cast<uint32_t>(kSwizzle128) << 29);
+__device__ __forceinline__ uint32_t umma_lo(uint32_t saddr, uint32_t lead)
+{
+    return ((saddr >> 4) & 0x3FFF) | ((lead >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_ss_if(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                           uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 e, %6, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kUmmaHi), "r"(on)
         : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are the tensor memory lanes, two
+// bf16 columns to a 32-bit cell.
+__device__ __forceinline__ void umma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %6, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kUmmaHi), "r"(on)
+        : "memory");
+}
+
+// Arrive once on `bar` when all tcgen05 operations issued so far complete.
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+
+// A value that is the same in all lanes, told to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Registers of the calling warpgroup (all four of its warps call).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Instruction descriptor as umma_idesc_bf16, with B stored N-major (its N
 // elements contiguous).
 __device__ __forceinline__ uint32_t umma_idesc_bf16_bn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
-
-// Shared-memory descriptor of an N-major operand in the 128-byte swizzle:
-// 64 N elements x 8 K rows to a 1024-byte atom; lbo: bytes from one group of
-// 64 N elements to the next, sbo: from 8 K rows to the next 8.
-__device__ __forceinline__ uint64_t umma_sdesc_nmajor(uint32_t saddr, uint32_t lbo, uint32_t sbo)
-{
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (static_cast<uint64_t>(1) << 46) | (kSwizzle128 << 61);
-}
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z)
 {
