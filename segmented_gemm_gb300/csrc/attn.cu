@@ -21,8 +21,10 @@
 // any m_i as good as the true maximum.
 //
 // Roles (384 threads): warps 0..3 and 4..7 the softmax and the results of
-// stream 0 and 1, warp 8 loads (TMA), warp 9 issues the matrix products (10 and
-// 11 fill the warpgroup up: registers move between warpgroups).
+// stream 0 and 1, warp 8 takes the work and loads keys (TMA), 9 issues the
+// matrix products, 10 loads values, 11 queries.  Three loaders, because a tile
+// of small pages is many TMA boxes, and because a new piece's queries must not
+// wait behind its tiles.
 // Shared memory: two query tiles and a ring of key and value tiles.
 // Persistent, one CTA per SM; work comes from the schedule (attn_schedule.cu).
 // A group (block, kv head) cut into pieces leaves partial (O, m, l) in the
@@ -50,6 +52,7 @@ constexpr uint32_t kColS = 128, kColO = 256;
 // a piece of one (block, kv head): key tiles [t0, t1)
 struct AttnItem {
     int32_t valid, pair, req, tok0, ntok, qpos0, kv_len, kvh;
+    int32_t seen;     // keys that any of its rows sees
     int32_t t0, t1;
     int32_t end0;     // pair: tiles that stream 0's rows reach
     int32_t parts;    // pieces of the group
@@ -66,7 +69,7 @@ struct AttnSmem {
     static constexpr int kItem = kStats + 128 * 8;
     static constexpr int kBars = kItem + kItems * static_cast<int>(sizeof(AttnItem));
     static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2;
-    static constexpr int kEnd = kBars + kNumBars * 8 + 32;
+    static constexpr int kEnd = kBars + kNumBars * 8 + 4 * (3 + kStages + 2);
     static constexpr int kBytes = kEnd + 1024;                 // room to align the base
     static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
 };
@@ -101,6 +104,12 @@ __device__ __forceinline__ void store_rows(uint32_t (&v)[16], uint64_t dst, int 
     }
 }
 
+// A piece's 2 n loads, in the order in which the products need them:
+//   pair    K0 V0 K1 V1 ...
+//   single  K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1)   (n = 1: K0 V0)
+__device__ __forceinline__ uint32_t load_of_key(int pair, int t) { return pair ? 2 * t : t < 2 ? t : 2 * t - 1; }
+__device__ __forceinline__ uint32_t load_of_value(int pair, int t, int n) { return pair ? 2 * t + 1 : min(2 * t + 2, n + t); }
+
 struct AttnMaps {
     CUtensorMap q, q1, k, v;   // q: tq tokens of a group's heads; q1: one token's
 };
@@ -127,8 +136,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t *end_bar = xbar + 1;             // after a wait gave up: the matrix products issued so far
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(end_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *drain = reinterpret_cast<int *>(tmem_slot + 2);   // [0] ring loads issued, [1], [2] query loads issued
-    int *join_flag = drain + 3;
+    int *join_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    int *drain = join_flag + 1;               // loads issued into each ring stage and query buffer
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *status = p.counters + CNT_STATUS;
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 9);   // 8 softmax warps, the MMA warp
+            mbar_init(&item_empty[i], 11);   // 8 softmax warps, the MMA warp, the value and query loaders
         }
         mbar_init(&q_full[0], 1);
         mbar_init(&q_full[1], 1);
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(xbar, 8);
         mbar_init(end_bar, 1);
         *abort_flag = 0;
-        drain[0] = drain[1] = drain[2] = 0;
+        for (int s = 0; s < kStages + 2; ++s) drain[s] = 0;
         fence_mbarrier_init();
     }
     if (warp == 8 && lane == 0) {
@@ -181,10 +190,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     pdl_wait();
     const AttnHdr hdr = *p.hdr;
 
+    // A tile of 128 keys in boxes of box_rows keys (a page, or 128 keys of a
+    // larger one; 32 packed rows), each 64 columns wide: one lane per box.
+    const int box = p.box_rows, box_shift = __ffs(box) - 1, per_tile = kAttnTileK >> box_shift;
+    const int mybox = lane / kHalves, myhalf = lane % kHalves;
+    // paged: lane l holds the page of box l % per_tile of tile l / per_tile of a
+    // window of 32 / per_tile tiles; the next window's pages are on their way
+    // while a window is used
+    const int win_shift = box_shift - 2;   // log2 of the window's tiles: 32 * box / 128
+    auto pages_of = [&](int req, int tile0, int win, int seen) {
+        const int64_t key = (static_cast<int64_t>(tile0 + (win << win_shift)) << 7) + (static_cast<int64_t>(lane) << box_shift);
+        const int64_t col = key >> p.page_shift;
+        return kPaged && key < seen && col < p.table_width ? p.block_table[req * p.table_stride + col] : -1;
+    };
+    // load i of the CTA's ring <- tile t of the piece; false after a wait gave up
+    auto load_tile = [&](const CUtensorMap *map, uint32_t i, int tile, int page, int seen, int kvh, int row0) {
+        const int boxes = (max(0, min(kAttnTileK, seen - tile * kAttnTileK)) + box - 1) >> box_shift;
+        const uint32_t s = i % kStages;
+        if (i >= kStages && !wait(&empty[s], (i / kStages - 1) & 1)) return false;
+        if (lane == 0) {
+            drain[s] = static_cast<int>(i / kStages) + 1;
+            mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
+        }
+        __syncwarp();
+        if (mybox < boxes) {
+            uint8_t *dst = ring + s * kTile + myhalf * (kAttnTileK * 128) + mybox * box * 128;
+            const int key = tile * kAttnTileK + mybox * box;
+            if (kPaged) {
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(status, LORA_DEV_BAD_PAGE);
+                    page = p.num_pages;   // outside the map: reads as zeros
+                }
+                tma_load_4d(dst, map, &full[s], myhalf * 64, key & ((1 << p.page_shift) - 1), kvh, page);
+            } else {
+                tma_load_3d(dst, map, &full[s], myhalf * 64, kvh, row0 + key);
+            }
+        }
+        return true;
+    };
+
     if (warp == 8) {
-        // ===================== loader =========================================
+        // ===================== work and keys ==================================
         setmaxnreg_dec<kOtherRegs>();
-        uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0;
+        uint32_t it = 0, nitem = 0;
         const bool cut = hdr.cut != 0;
         int64_t unit = blockIdx.x;
         // cut: my unit's tiles [pos, end) of the list; lo: the block that pos is in
@@ -229,118 +277,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 slot = static_cast<int>(unit == u0 ? 2 * unit + 1 : 2 * unit);
                 unit0 = static_cast<int>(u0);
             }
-            // hand it to the other roles, then load it
-            AttnItem w;
-            w.valid = 1;
-            w.pair = b.ntok > p.tq;
-            w.req = b.req;
-            w.tok0 = b.tok0;
-            w.ntok = b.ntok;
-            w.qpos0 = b.qpos0;
-            w.kv_len = b.kv_len;
-            w.kvh = kvh;
-            w.t0 = t0;
-            w.t1 = t1;
-            w.end0 = max(1, (min(b.kv_len, b.qpos0 + min(b.ntok, p.tq)) + kAttnTileK - 1) / kAttnTileK);
-            w.parts = parts;
-            w.slot = slot;
-            w.unit0 = unit0;
+            const int seen = min(b.kv_len, b.qpos0 + b.ntok);   // keys past this no row sees
+            // hand it to the other roles, then load its keys
             const int is = nitem % kItems;
-            if (nitem >= kItems) ok &= wait(&item_empty[is], (nitem / kItems - 1) & 1);
+            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) break;
             if (lane == 0) {
-                items[is] = w;
+                AttnItem &w = items[is];
+                w.valid = 1;
+                w.pair = b.ntok > p.tq;
+                w.req = b.req;
+                w.tok0 = b.tok0;
+                w.ntok = b.ntok;
+                w.qpos0 = b.qpos0;
+                w.kv_len = b.kv_len;
+                w.seen = seen;
+                w.kvh = kvh;
+                w.t0 = t0;
+                w.t1 = t1;
+                w.end0 = max(1, (min(b.kv_len, b.qpos0 + min(b.ntok, p.tq)) + kAttnTileK - 1) / kAttnTileK);
+                w.parts = parts;
+                w.slot = slot;
+                w.unit0 = unit0;
                 mbar_arrive(&item_full[is]);
             }
             ++nitem;
-            const int n = t1 - t0;
-            const int seen = min(b.kv_len, b.qpos0 + b.ntok);   // keys past this no row sees
-            const int box = p.box_rows;
-            const int mybox = lane / kHalves, myhalf = lane % kHalves;
-            // load i of the piece: its key and value tiles in the order in which the MMA warp needs them
-            auto what = [&](int i, bool &is_v) {
-                if (w.pair) {
-                    is_v = i & 1;
-                    return i >> 1;
+            const int n = t1 - t0, pair = b.ntok > p.tq;
+            int cur = pages_of(b.req, t0, 0, seen), nxt = pages_of(b.req, t0, 1, seen);
+            int next = 0;
+            for (int t = 0; t < n && ok; ++t) {
+                if (kPaged && t > 0 && (t & ((1 << win_shift) - 1)) == 0) {
+                    cur = nxt;
+                    nxt = pages_of(b.req, t0, (t >> win_shift) + 1, seen);
                 }
-                if (n == 1 || i < 2) {
-                    is_v = n == 1 && i == 1;
-                    return n == 1 ? 0 : i;
-                }
-                is_v = (i & 1) == 0 || i == 2 * n - 1;
-                return i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) >> 1 : (i - 2) >> 1;
-            };
-            // my box's page (paged), fetched one load ahead
-            auto page_of = [&](int i) {
-                bool v;
-                const int64_t key = static_cast<int64_t>(t0 + what(i, v)) * kAttnTileK + mybox * box;
-                const int64_t col = key >> p.page_shift;
-                int32_t page = -1;
-                if (key < seen && mybox * box < kAttnTileK) {
-                    if (col < p.table_width) page = p.block_table[b.req * p.table_stride + col];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(status, LORA_DEV_BAD_PAGE);
-                        page = p.num_pages;   // outside the map: reads as zeros
-                    }
-                }
-                return page;
-            };
-            int32_t next_page = kPaged ? page_of(0) : 0;
-            auto load = [&](int i) {
-                bool is_v;
-                const int tile = t0 + what(i, is_v);
-                const int32_t page = next_page;
-                if (kPaged && i + 1 < 2 * n) next_page = page_of(i + 1);
-                const int valid = max(0, min(kAttnTileK, seen - tile * kAttnTileK));
-                const int boxes = (valid + box - 1) / box;
-                const int s = it % kStages;
-                if (it >= kStages) ok &= wait(&empty[s], (it / kStages - 1) & 1);
-                if (!ok) return;
-                ++it;
-                if (lane == 0) mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
-                __syncwarp();
-                if (mybox < boxes) {
-                    uint8_t *dst = ring + s * kTile + myhalf * (kAttnTileK * 128) + mybox * box * 128;
-                    const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                    if (kPaged)
-                        tma_load_4d(dst, m, &full[s], myhalf * 64,
-                                    (tile * kAttnTileK + mybox * box) & ((1 << p.page_shift) - 1), kvh, page);
-                    else
-                        tma_load_3d(dst, m, &full[s], myhalf * 64, kvh, b.tok0 - b.qpos0 + tile * kAttnTileK + mybox * box);
-                }
-            };
-            // a few tiles go ahead of the queries, whose buffers the previous piece may still hold
-            const int ahead = min(3, 2 * n);
-            for (int i = 0; i < ahead && ok; ++i) load(i);
-            if (nitem > 1) ok &= wait(q_empty, (nitem - 2) & 1);
-            if (!ok) break;
-            const int g = p.group, few = 4;
-            for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
-                const int first = s * p.tq, ntok = min(p.tq, b.ntok - first);
-                uint8_t *dst = qbuf + s * kTile;
-                if (ntok <= few) {   // single tokens: their rows only, not the whole tile's
-                    if (lane == 0) mbar_expect_tx(&q_full[s], ntok * g * 128 * kHalves);
-                    __syncwarp();
-                    const int i = lane / kHalves;
-                    if (i < ntok)
-                        tma_load_3d(dst + myhalf * (kAttnTileQ * 128) + i * g * 128, &maps.q1, &q_full[s], myhalf * 64,
-                                    kvh * g, b.tok0 + first + i);
-                } else {
-                    if (lane == 0) mbar_expect_tx(&q_full[s], p.tq * g * 128 * kHalves);
-                    __syncwarp();
-                    if (lane < kHalves)
-                        tma_load_3d(dst + lane * (kAttnTileQ * 128), &maps.q, &q_full[s], lane * 64, kvh * g,
-                                    b.tok0 + first);
-                }
-                if (s) ++nq1;
-                else ++nq0;
+                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & ((1 << win_shift) - 1)) * per_tile + mybox) : 0;
+                // the next unit is claimed under the wait for the last tile's stage
+                if (!cut && t == n - 1 && lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
+                ok = load_tile(&maps.k, it + load_of_key(pair, t), t0 + t, page, seen, kvh, b.tok0 - b.qpos0);
             }
-            for (int i = ahead; i < 2 * n && ok; ++i) load(i);
+            it += 2 * n;
             if (!cut) {
-                int next = 0;
-                if (lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
                 unit = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
             } else {
-                pos += t1 - t0;
+                pos += n;
                 if (++kvh == p.kv_heads) {
                     kvh = 0;
                     if (++lo < hdr.nblocks) b = p.blocks[lo];
@@ -352,19 +330,61 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) {
             items[is].valid = 0;
             mbar_arrive(&item_full[is]);
-            drain[0] = static_cast<int>(it);
-            drain[1] = static_cast<int>(nq0);
-            drain[2] = static_cast<int>(nq1);
+        }
+    } else if (warp >= 10) {
+        // ===================== values (10), queries (11) ======================
+        setmaxnreg_dec<kOtherRegs>();
+        uint32_t it = 0, nitem = 0;
+        bool ok = true;
+        while (ok) {
+            const int is = nitem % kItems;
+            if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
+            const AttnItem w = items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[is]);
+            ++nitem;
+            if (!w.valid) break;
+            if (warp == 10) {
+                const int n = w.t1 - w.t0;
+                int cur = pages_of(w.req, w.t0, 0, w.seen), nxt = pages_of(w.req, w.t0, 1, w.seen);
+                for (int t = 0; t < n && ok; ++t) {
+                    if (kPaged && t > 0 && (t & ((1 << win_shift) - 1)) == 0) {
+                        cur = nxt;
+                        nxt = pages_of(w.req, w.t0, (t >> win_shift) + 1, w.seen);
+                    }
+                    const int page =
+                        kPaged ? __shfl_sync(0xffffffffu, cur, (t & ((1 << win_shift) - 1)) * per_tile + mybox) : 0;
+                    ok = load_tile(&maps.v, it + load_of_value(w.pair, t, n), w.t0 + t, page, w.seen, w.kvh,
+                                   w.tok0 - w.qpos0);
+                }
+                it += 2 * n;
+            } else {
+                // the previous piece's products have read its queries
+                if (nitem > 1 && !wait(q_empty, (nitem - 2) & 1)) break;
+                const int g = p.group;
+                constexpr int kFew = 4;
+                for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
+                    const int first = s * p.tq, ntok = min(p.tq, w.ntok - first);
+                    uint8_t *dst = qbuf + s * kTile;
+                    const bool few = ntok <= kFew;   // single tokens: their rows only, not the whole tile's
+                    if (lane == 0) {
+                        ++drain[kStages + s];
+                        mbar_expect_tx(&q_full[s], (few ? ntok : p.tq) * g * 128 * kHalves);
+                    }
+                    __syncwarp();
+                    if (mybox < (few ? ntok : 1))
+                        tma_load_3d(dst + myhalf * (kAttnTileQ * 128) + mybox * g * 128, few ? &maps.q1 : &maps.q,
+                                    &q_full[s], myhalf * 64, w.kvh * g, w.tok0 + first + mybox);
+                }
+            }
         }
     } else if (warp == 9) {
         setmaxnreg_dec<kOtherRegs>();
         // ===================== MMA issuer =====================================
-        // All lanes run the same code and lane 0's instructions take effect;
-        // what the descriptors are made of is kept uniform across the warp, and
-        // the steps are unrolled: issuing 8 products must take less than
-        // executing them (64 cycles each).
+        // All lanes run the same code and the elected one's instructions take
+        // effect, and whole tiles' steps are unrolled: a product executes in 64
+        // cycles, and issuing one this way takes 35 (66 with a branch around it).
         uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
-        const uint32_t lead = lane == 0;
         const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
         const uint32_t klo = umma_lo(smem_u32(ring), 16), vlo = umma_lo(smem_u32(ring), kAttnTileK * 128);
         const int dsteps = (p.head_dim + 15) / 16;
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const AttnItem &wi = items[is];
             const int valid = uniform(wi.valid), pair = uniform(wi.pair), t0 = uniform(wi.t0);
             const int n = uniform(wi.t1) - t0;
-            const int seen = uniform(min(wi.kv_len, wi.qpos0 + wi.ntok)) - t0 * kAttnTileK;   // keys that any row sees
+            const int seen = uniform(wi.seen) - t0 * kAttnTileK;   // keys that any row sees
             const int n0 = max(0, min(n, uniform(wi.end0) - t0));   // pair: stream 0's tiles
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
@@ -388,27 +408,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 ok &= wait(&full[stage_of(i)], ((it + i) / kStages) & 1);
                 tc_fence_after();
             };
-            auto release = [&](uint32_t i) { umma_commit_if(lead, &empty[stage_of(i)]); };
+            auto commit = [&](uint64_t *bar) { umma_commit_if(elect_one(), bar); };
+            auto release = [&](uint32_t i) { commit(&empty[stage_of(i)]); };
             auto qk = [&](int s, int slot, uint32_t i, int t) {
                 const int keys = min(kAttnTileK, seen - t * kAttnTileK);
                 const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
                 const uint32_t qd = qlo + ((slot * kTile) >> 4), kd = klo + stage_of(i) * (kTile >> 4);
+                const uint32_t lead = elect_one(), d = tmem + s * kColS;
+                auto step = [&](int kk) {
+                    const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
+                    umma_ss_if(lead, d, qd + o, kd + o, idesc, kk > 0);
+                };
+                if (dsteps == DP / 16) {
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk)
-                    if (kk < dsteps) {
-                        const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
-                        umma_ss_if(lead, tmem + s * kColS, qd + o, kd + o, idesc, kk > 0);
-                    }
-                umma_commit_if(lead, &s_full[s]);
+                    for (int kk = 0; kk < DP / 16; ++kk) step(kk);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < dsteps; ++kk) step(kk);
+                }
+                commit(&s_full[s]);
             };
             auto pv = [&](int s, uint32_t i, int t, uint32_t acc) {
                 const int keys = max(0, min(kAttnTileK, seen - t * kAttnTileK));
                 const uint32_t vd = vlo + stage_of(i) * (kTile >> 4), a = tmem + s * kColS, d = tmem + kColO + s * DP;
                 ok &= wait(&p_full[s], (s ? np1++ : np0++) & 1);
                 tc_fence_after();
+                const uint32_t lead = elect_one();
+                auto step = [&](int kk) {
+                    umma_ts_if(lead, d, a + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : acc);
+                };
+                if (keys == kAttnTileK) {
 #pragma unroll
-                for (int kk = 0; kk < kAttnTileK / 16; ++kk)
-                    if (kk * 16 < keys) umma_ts_if(lead, d, a + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : acc);
+                    for (int kk = 0; kk < kAttnTileK / 16; ++kk) step(kk);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk * 16 < keys; ++kk) step(kk);
+                }
             };
             // keys past the last one that a row sees: their p is 0, but 0 times what the
             // tile holds there (another request's rows, stale pages) may be NaN
@@ -432,14 +467,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (n0 > 0) qk(0, 0, 0, 0);
                 qk(1, 1, 0, 0);
                 release(0);
-                if (n == 1) umma_commit_if(lead, q_empty);
+                if (n == 1) commit(q_empty);
                 for (int t = 0; t < n && ok; ++t) {
                     const uint32_t vi = 2 * t + 1, ki = 2 * t + 2;
                     wait_stage(vi);
                     clean(vi, t);
                     if (t < n0) {
                         pv(0, vi, t, t > 0);
-                        if (t == n0 - 1) umma_commit_if(lead, &o_full[0]);
+                        if (t == n0 - 1) commit(&o_full[0]);
                     }
                     if (t + 1 < n) {
                         wait_stage(ki);
@@ -447,11 +482,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     pv(1, vi, t, t > 0);
                     release(vi);
-                    if (t == n - 1) umma_commit_if(lead, &o_full[1]);
+                    if (t == n - 1) commit(&o_full[1]);
                     if (t + 1 < n) {
                         qk(1, 1, ki, t + 1);
                         release(ki);
-                        if (t + 2 == n) umma_commit_if(lead, q_empty);
+                        if (t + 2 == n) commit(q_empty);
                     }
                 }
             } else {
@@ -462,7 +497,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     else qk(1, 0, 1, 1);
                     release(t);
                 }
-                if (n <= 2) umma_commit_if(lead, q_empty);
+                if (n <= 2) commit(q_empty);
                 for (int t = 0; t < n && ok; ++t) {
                     const uint32_t vi = min(2 * t + 2, n + t), ki = 2 * t + 3;
                     wait_stage(vi);
@@ -470,21 +505,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (t & 1) pv(1, vi, t, t > 1);
                     else pv(0, vi, t, t > 1);
                     release(vi);
-                    if (t + 2 >= n) umma_commit_if(lead, &o_full[t & 1]);
+                    if (t + 2 >= n) commit(&o_full[t & 1]);
                     if (t + 2 < n) {
                         wait_stage(ki);
                         if (t & 1) qk(1, 0, ki, t + 2);
                         else qk(0, 0, ki, t + 2);
                         release(ki);
-                        if (t + 3 == n) umma_commit_if(lead, q_empty);
+                        if (t + 3 == n) commit(q_empty);
                     }
                 }
             }
             it += 2 * n;
             if (!ok) break;
         }
-    } else if (warp > 9) {
-        setmaxnreg_dec<kOtherRegs>();
     } else {
         // ===================== softmax and results ============================
         setmaxnreg_inc<kSoftmaxRegs>();
@@ -727,14 +760,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         auto settle = [&](uint64_t *bar, uint32_t parity) {
             mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
         };
-        if (warp == 8 && lane == 0) {
-            const uint32_t n = static_cast<uint32_t>(drain[0]);
-            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) settle(&full[i % kStages], (i / kStages) & 1);
+        if (warp == 8 && lane == 0)
+            for (int s = 0; s < kStages; ++s)
+                if (drain[s] > 0) settle(&full[s], (drain[s] - 1) & 1);
+        if (warp == 11 && lane == 0)
             for (int s = 0; s < 2; ++s)
-                if (drain[1 + s] > 0) settle(&q_full[s], (drain[1 + s] - 1) & 1);
-        }
-        if (warp == 9 && lane == 0) {
-            umma_commit(end_bar);
+                if (drain[kStages + s] > 0) settle(&q_full[s], (drain[kStages + s] - 1) & 1);
+        if (warp == 9) {
+            umma_commit_if(elect_one(), end_bar);
             settle(end_bar, 0);
         }
         tc_fence_before();

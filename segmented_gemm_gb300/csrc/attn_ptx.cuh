@@ -7,6 +7,14 @@
 
 namespace lora {
 
+// 1 in one lane of the (converged) warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on;
+}
+
 // The matrix products and commits below are run by a whole warp and take
 // effect for the lanes with `on` set (one), without a branch around them.
 //
