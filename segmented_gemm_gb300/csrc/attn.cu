@@ -21,10 +21,8 @@
 // any m_i as good as the true maximum.
 //
 // Roles (384 threads): warps 0..3 and 4..7 the softmax and the results of
-// stream 0 and 1, warp 8 takes the work and loads keys (TMA), 9 issues the
-// matrix products, 10 loads values, 11 queries.  Three loaders, because a tile
-// of small pages is many TMA boxes, and because a new piece's queries must not
-// wait behind its tiles.
+// stream 0 and 1; warp 8 takes the work and loads keys, 11 loads queries and
+// values (TMA); 9 and 10 issue the matrix products of stream 0 and 1.
 // Shared memory: two query tiles and a ring of key and value tiles.
 // Persistent, one CTA per SM; work comes from the schedule (attn_schedule.cu).
 // A group (block, kv head) cut into pieces leaves partial (O, m, l) in the
@@ -68,7 +66,7 @@ struct AttnSmem {
     static constexpr int kStats = 2 * kTile + kStages * kTile; // offsets
     static constexpr int kItem = kStats + 128 * 8;
     static constexpr int kBars = kItem + kItems * static_cast<int>(sizeof(AttnItem));
-    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2;
+    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2 + 2;
     static constexpr int kEnd = kBars + kNumBars * 8 + 4 * (3 + kStages + 2);
     static constexpr int kBytes = kEnd + 1024;                 // room to align the base
     static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
@@ -114,6 +112,37 @@ struct AttnMaps {
     CUtensorMap q, q1, k, v;   // q: tq tokens of a group's heads; q1: one token's
 };
 
+// mbar_wait with a 32-bit clock and without the status bit (set once, at the
+// end): it stands in the kernel many times.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t limit)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+    while (!mbar_try_wait(bar, parity)) {
+        const uint32_t most = *abort_flag ? min(limit, static_cast<uint32_t>(kWaitShort)) : limit;
+        if (static_cast<uint32_t>(clock()) - t0 > most) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// Bounded wait until *count > n (shared memory, written with release).
+__device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatile int *abort_flag, uint32_t limit)
+{
+    if (ld_acquire_shared(count) > n) return true;
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+    while (ld_acquire_shared(count) <= n) {
+        const uint32_t most = *abort_flag ? min(limit, static_cast<uint32_t>(kWaitShort)) : limit;
+        if (static_cast<uint32_t>(clock()) - t0 > most) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 template <int DP, bool kPaged>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
@@ -130,47 +159,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t *q_full = item_empty + kItems;   // [2]
     uint64_t *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 1;           // [2]
-    uint64_t *p_full = s_full + 2;            // [2]
+    uint64_t *p_half = s_full + 2;            // [2] P of the tile's first 64 keys is in place
+    uint64_t *p_full = p_half + 2;            // [2]
     uint64_t *o_full = p_full + 2;            // [2]
     uint64_t *xbar = o_full + 2;              // the 256 softmax threads meet here
-    uint64_t *end_bar = xbar + 1;             // after a wait gave up: the matrix products issued so far
+    uint64_t *end_bar = xbar + 1;             // all matrix products are done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(end_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *join_flag = reinterpret_cast<int *>(tmem_slot + 2);
-    int *drain = join_flag + 1;               // loads issued into each ring stage and query buffer
+    // Loads issued into each ring stage and query buffer.  No loader and (single)
+    // no stream sees every phase of a stage's barriers, and a parity tells only
+    // neighbouring phases apart: a barrier is waited on once this says that it is
+    // in that phase or the one before.
+    int *issued = join_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *status = p.counters + CNT_STATUS;
-    const long long budget = p.wait_cycles;
-    // called by whole warps; the answer is the same for all lanes, so a wait
-    // that gives up takes its warp out together
+    // Bounded wait, called by whole warps; the answer is the same for all lanes,
+    // so a wait that gives up takes its warp out together.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        const bool ok = mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
-        return __all_sync(0xffffffffu, ok) != 0;
+        return __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles)) != 0;
+    };
+    // load number f of stage s (from 0) has been issued
+    auto wait_issued = [&](uint32_t s, uint32_t f) {
+        return __all_sync(0xffffffffu, attn_wait_count(&issued[s], static_cast<int>(f), abort_flag, p.wait_cycles)) != 0;
     };
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);   // one arrival a stream (two from the only one that uses the stage)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 11);   // 8 softmax warps, the MMA warp, the value and query loaders
+            mbar_init(&item_empty[i], 11);   // 8 softmax warps, 2 MMA warps, the value loader
         }
         mbar_init(&q_full[0], 1);
         mbar_init(&q_full[1], 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
+            mbar_init(&p_half[s], 4);
             mbar_init(&p_full[s], 4);
             mbar_init(&o_full[s], 1);
         }
         mbar_init(xbar, 8);
-        mbar_init(end_bar, 1);
+        mbar_init(end_bar, 2);
         *abort_flag = 0;
-        for (int s = 0; s < kStages + 2; ++s) drain[s] = 0;
+        for (int s = 0; s < kStages + 2; ++s) issued[s] = 0;
         fence_mbarrier_init();
     }
     if (warp == 8 && lane == 0) {
@@ -188,42 +225,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
+    AttnBlock early = {};   // of a short list, the loader's lanes fetch a block each along with the header
+    if (warp == 8 && lane < p.max_blocks) early = p.blocks[lane];
     const AttnHdr hdr = *p.hdr;
 
     // A tile of 128 keys in boxes of box_rows keys (a page, or 128 keys of a
-    // larger one; 32 packed rows), each 64 columns wide: one lane per box.
+    // larger one; 32 or 128 packed rows), each 64 columns wide: one lane per box.
     const int box = p.box_rows, box_shift = __ffs(box) - 1, per_tile = kAttnTileK >> box_shift;
     const int mybox = lane / kHalves, myhalf = lane % kHalves;
     // paged: lane l holds the page of box l % per_tile of tile l / per_tile of a
     // window of 32 / per_tile tiles; the next window's pages are on their way
     // while a window is used
-    const int win_shift = box_shift - 2;   // log2 of the window's tiles: 32 * box / 128
-    auto pages_of = [&](int req, int tile0, int win, int seen) {
-        const int64_t key = (static_cast<int64_t>(tile0 + (win << win_shift)) << 7) + (static_cast<int64_t>(lane) << box_shift);
+    const int win_shift = box_shift - 2, in_win = (1 << win_shift) - 1;
+    auto pages_of = [&](const int32_t *table, int tile, int seen) {
+        const int64_t key = (static_cast<int64_t>(tile) << 7) + (static_cast<int64_t>(lane) << box_shift);
         const int64_t col = key >> p.page_shift;
-        return kPaged && key < seen && col < p.table_width ? p.block_table[req * p.table_stride + col] : -1;
+        return key < seen && col < p.table_width ? table[col] : -1;
     };
-    // load i of the CTA's ring <- tile t of the piece; false after a wait gave up
+    // load i of the CTA <- a key or value tile; false after a wait gave up
     auto load_tile = [&](const CUtensorMap *map, uint32_t i, int tile, int page, int seen, int kvh, int row0) {
+        const int key = tile * kAttnTileK + mybox * box;
         const int boxes = (max(0, min(kAttnTileK, seen - tile * kAttnTileK)) + box - 1) >> box_shift;
-        const uint32_t s = i % kStages;
-        if (i >= kStages && !wait(&empty[s], (i / kStages - 1) & 1)) return false;
+        const uint32_t s = i % kStages, f = i / kStages;
+        // the stage's previous load has been issued (perhaps by the other loader), and is used up
+        if (f > 0 && !(wait_issued(s, f - 1) && wait(&empty[s], (f - 1) & 1))) return false;
         if (lane == 0) {
-            drain[s] = static_cast<int>(i / kStages) + 1;
+            st_release_shared(&issued[s], static_cast<int>(f) + 1);
             mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
         }
         __syncwarp();
         if (mybox < boxes) {
-            uint8_t *dst = ring + s * kTile + myhalf * (kAttnTileK * 128) + mybox * box * 128;
-            const int key = tile * kAttnTileK + mybox * box;
+            const uint32_t dst = smem_u32(ring) + s * kTile + myhalf * (kAttnTileK * 128) + mybox * box * 128;
             if (kPaged) {
                 if (page < 0 || page >= p.num_pages) {
                     atomicOr(status, LORA_DEV_BAD_PAGE);
                     page = p.num_pages;   // outside the map: reads as zeros
                 }
-                tma_load_4d(dst, map, &full[s], myhalf * 64, key & ((1 << p.page_shift) - 1), kvh, page);
+                tma_load_4d_if(1, dst, map, smem_u32(&full[s]), myhalf * 64, key & ((1 << p.page_shift) - 1), kvh, page);
             } else {
-                tma_load_3d(dst, map, &full[s], myhalf * 64, kvh, row0 + key);
+                tma_load_3d_if(1, dst, map, smem_u32(&full[s]), myhalf * 64, kvh, row0 + key);
             }
         }
         return true;
@@ -234,63 +274,74 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         setmaxnreg_dec<kOtherRegs>();
         uint32_t it = 0, nitem = 0;
         const bool cut = hdr.cut != 0;
-        int64_t unit = blockIdx.x;
-        // cut: my unit's tiles [pos, end) of the list; lo: the block that pos is in
-        int64_t pos = unit * hdr.unit_tiles;
-        const int64_t end = min(pos + hdr.unit_tiles, hdr.tiles);
+        int unit = blockIdx.x;
+        // cut: my unit [pos, end) of the list; lo: the block that pos is in
+        int pos = cut ? unit * hdr.unit_cost : 0;
+        const int end = min(pos + hdr.unit_cost, hdr.cost);
         int lo = 0, kvh = 0;
-        AttnBlock b;
-        bool ok = true;
+        AttnBlock b = early;
         if (cut && unit < hdr.units) {
-            // the last block whose tiles start at or before pos
+            // the last block that starts at or before pos; of up to 32 blocks each lane has one already
             int hi = hdr.nblocks;
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32;
-                const int at = lo + step * lane;
-                const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
-                const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lanes 0..k, lane 0 always
-                lo += step * k;
-                hi = min(hi, lo + step);
-            }
-            b = p.blocks[lo];
-            kvh = static_cast<int>((pos - b.pre * p.kv_heads) / b.tiles);
-        }
-        while (ok && unit < hdr.units) {
-            // the next piece: key tiles [t0, t1) of (block b, head kvh)
-            int t0 = 0, t1, parts = 1, slot = 0, unit0 = 0;
-            if (!cut) {
-                // whole groups, longest first; the heads of a section together
-                const int64_t per = static_cast<int64_t>(hdr.nblocks) * hdr.sec_heads;
-                const int sec = static_cast<int>(unit / per);
-                const int64_t rem = unit - sec * per;
-                const int hs = min(hdr.sec_heads, p.kv_heads - sec * hdr.sec_heads);
-                b = p.blocks[p.order[rem / hs]];
-                kvh = sec * hdr.sec_heads + static_cast<int>(rem % hs);
-                t1 = b.tiles;
+            if (hi <= 32) {
+                lo = 31 - __clz(__ballot_sync(0xffffffffu, lane < hi && early.pre * p.kv_heads <= pos));
+                b.pre = __shfl_sync(0xffffffffu, early.pre, lo);
+                b.req = __shfl_sync(0xffffffffu, early.req, lo);
+                b.tok0 = __shfl_sync(0xffffffffu, early.tok0, lo);
+                b.ntok = __shfl_sync(0xffffffffu, early.ntok, lo);
+                b.qpos0 = __shfl_sync(0xffffffffu, early.qpos0, lo);
+                b.kv_len = __shfl_sync(0xffffffffu, early.kv_len, lo);
+                b.tiles = __shfl_sync(0xffffffffu, early.tiles, lo);
             } else {
-                if (pos >= end) break;
-                const int64_t g0 = b.pre * p.kv_heads + static_cast<int64_t>(kvh) * b.tiles;
-                t0 = static_cast<int>(pos - g0);
-                t1 = static_cast<int>(min(static_cast<int64_t>(b.tiles), t0 + (end - pos)));
-                const int64_t u0 = g0 / hdr.unit_tiles, u1 = (g0 + b.tiles - 1) / hdr.unit_tiles;
-                parts = static_cast<int>(u1 - u0 + 1);
-                slot = static_cast<int>(unit == u0 ? 2 * unit + 1 : 2 * unit);
-                unit0 = static_cast<int>(u0);
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 31) / 32;
+                    const int at = lo + step * lane;
+                    const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
+                    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lanes 0..k, lane 0 always
+                    lo += step * k;
+                    hi = min(hi, lo + step);
+                }
+                b = p.blocks[lo];
             }
-            const int seen = min(b.kv_len, b.qpos0 + b.ntok);   // keys past this no row sees
-            // hand it to the other roles, then load its keys
+            kvh = static_cast<int>(static_cast<uint32_t>(pos - b.pre * p.kv_heads) / static_cast<uint32_t>(b.tiles + kAttnItemCost));
+        }
+        while (true) {
+            // the next piece: key tiles [t0, t1) of (block b, head kvh)
+            bool more = unit < hdr.units;
+            int t0 = 0, t1 = 0, parts = 1, slot = 0, unit0 = 0;
+            if (more && !cut) {
+                // whole groups, longest first; the heads of a section together
+                const uint32_t per = hdr.nblocks * hdr.sec_heads, sec = unit / per, rem = unit - sec * per;
+                const uint32_t hs = min(hdr.sec_heads, p.kv_heads - static_cast<int>(sec) * hdr.sec_heads), at = rem / hs;
+                b = p.blocks[at];
+                kvh = static_cast<int>(sec * hdr.sec_heads + rem - at * hs);
+                t1 = b.tiles;
+            } else if (more) {
+                // the group's tiles start kAttnItemCost into its share of the list
+                const int g0 = b.pre * p.kv_heads + kvh * (b.tiles + kAttnItemCost) + kAttnItemCost;
+                more = pos < end && g0 < end;
+                t0 = max(0, pos - g0);
+                t1 = min(b.tiles, end - g0);
+                const uint32_t c = hdr.unit_cost, u0 = static_cast<uint32_t>(g0) / c, u1 = static_cast<uint32_t>(g0 + b.tiles - 1) / c;
+                parts = static_cast<int>(u1 - u0 + 1);
+                slot = 2 * unit + (static_cast<uint32_t>(unit) == u0);
+                unit0 = static_cast<int>(u0);
+                pos = g0 + t1;   // the end of the group or of the unit
+            }
+            // hand it to the other roles
             const int is = nitem % kItems;
-            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) break;
+            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) more = false;
+            const int pair = b.ntok > p.tq;
             if (lane == 0) {
                 AttnItem &w = items[is];
-                w.valid = 1;
-                w.pair = b.ntok > p.tq;
+                w.valid = more;
+                w.pair = pair;
                 w.req = b.req;
                 w.tok0 = b.tok0;
                 w.ntok = b.ntok;
                 w.qpos0 = b.qpos0;
                 w.kv_len = b.kv_len;
-                w.seen = seen;
+                w.seen = min(b.kv_len, b.qpos0 + b.ntok);
                 w.kvh = kvh;
                 w.t0 = t0;
                 w.t1 = t1;
@@ -300,224 +351,205 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 w.unit0 = unit0;
                 mbar_arrive(&item_full[is]);
             }
+            if (!more) break;
             ++nitem;
-            const int n = t1 - t0, pair = b.ntok > p.tq;
-            int cur = pages_of(b.req, t0, 0, seen), nxt = pages_of(b.req, t0, 1, seen);
-            int next = 0;
-            for (int t = 0; t < n && ok; ++t) {
-                if (kPaged && t > 0 && (t & ((1 << win_shift) - 1)) == 0) {
-                    cur = nxt;
-                    nxt = pages_of(b.req, t0, (t >> win_shift) + 1, seen);
+            bool ok = true;
+            const int n = t1 - t0, seen = min(b.kv_len, b.qpos0 + b.ntok), row0 = b.tok0 - b.qpos0;
+            const int32_t *table = p.block_table + b.req * p.table_stride;
+            int next = 0, cur = -1, nxt = -1;
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                if (kPaged && (t & in_win) == 0) {
+                    cur = t == 0 ? pages_of(table, t0, seen) : nxt;
+                    nxt = pages_of(table, t0 + t + in_win + 1, seen);
                 }
-                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & ((1 << win_shift) - 1)) * per_tile + mybox) : 0;
-                // the next unit is claimed under the wait for the last tile's stage
+                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & in_win) * per_tile + mybox) : 0;
+                // whole: the next unit is claimed late, so that the last ones go to the CTAs
+                // that come free first, and under the wait for the last tile's stage
                 if (!cut && t == n - 1 && lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
-                ok = load_tile(&maps.k, it + load_of_key(pair, t), t0 + t, page, seen, kvh, b.tok0 - b.qpos0);
+                ok = load_tile(&maps.k, it + load_of_key(pair, t), t0 + t, page, seen, kvh, row0);
+                if (!ok) break;
             }
             it += 2 * n;
             if (!cut) {
-                unit = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
-            } else {
-                pos += n;
-                if (++kvh == p.kv_heads) {
-                    kvh = 0;
-                    if (++lo < hdr.nblocks) b = p.blocks[lo];
-                }
+                unit = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
+            } else if (++kvh == p.kv_heads) {
+                kvh = 0;
+                if (++lo < hdr.nblocks) b = p.blocks[lo];
+                else pos = end;
             }
+            if (!ok) unit = hdr.units;   // hand out the end, then stop
         }
-        const int is = nitem % kItems;
-        if (nitem >= kItems) wait(&item_empty[is], (nitem / kItems - 1) & 1);
-        if (lane == 0) {
-            items[is].valid = 0;
-            mbar_arrive(&item_full[is]);
-        }
-    } else if (warp >= 10) {
-        // ===================== values (10), queries (11) ======================
+    } else if (warp == 11) {
+        // ===================== queries and values =============================
         setmaxnreg_dec<kOtherRegs>();
         uint32_t it = 0, nitem = 0;
         bool ok = true;
         while (ok) {
             const int is = nitem % kItems;
             if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
-            const AttnItem w = items[is];
+            const AttnItem &wi = items[is];
+            const int valid = wi.valid, pair = wi.pair, t0 = wi.t0, n = wi.t1 - t0, seen = wi.seen, kvh = wi.kvh;
+            const int tok0 = wi.tok0, all_tok = wi.ntok, row0 = tok0 - wi.qpos0;
+            const int32_t *table = p.block_table + wi.req * p.table_stride;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
             ++nitem;
-            if (!w.valid) break;
-            if (warp == 10) {
-                const int n = w.t1 - w.t0;
-                int cur = pages_of(w.req, w.t0, 0, w.seen), nxt = pages_of(w.req, w.t0, 1, w.seen);
-                for (int t = 0; t < n && ok; ++t) {
-                    if (kPaged && t > 0 && (t & ((1 << win_shift) - 1)) == 0) {
-                        cur = nxt;
-                        nxt = pages_of(w.req, w.t0, (t >> win_shift) + 1, w.seen);
-                    }
-                    const int page =
-                        kPaged ? __shfl_sync(0xffffffffu, cur, (t & ((1 << win_shift) - 1)) * per_tile + mybox) : 0;
-                    ok = load_tile(&maps.v, it + load_of_value(w.pair, t, n), w.t0 + t, page, w.seen, w.kvh,
-                                   w.tok0 - w.qpos0);
+            if (!valid) break;
+            int cur = -1, nxt = kPaged ? pages_of(table, t0, seen) : -1;
+            // the queries, once the previous piece's products have read theirs
+            if (nitem > 1 && !wait(q_empty, (nitem - 2) & 1)) break;
+            constexpr int kFew = 4;
+#pragma unroll 1
+            for (int s = 0; s <= pair; ++s) {
+                const int first = s * p.tq, ntok = min(p.tq, all_tok - first);
+                const bool few = ntok <= kFew;   // single tokens: their rows only, not the whole tile's
+                if (lane == 0) {
+                    ++issued[kStages + s];
+                    mbar_expect_tx(&q_full[s], (few ? ntok : p.tq) * p.group * 128 * kHalves);
                 }
-                it += 2 * n;
-            } else {
-                // the previous piece's products have read its queries
-                if (nitem > 1 && !wait(q_empty, (nitem - 2) & 1)) break;
-                const int g = p.group;
-                constexpr int kFew = 4;
-                for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
-                    const int first = s * p.tq, ntok = min(p.tq, w.ntok - first);
-                    uint8_t *dst = qbuf + s * kTile;
-                    const bool few = ntok <= kFew;   // single tokens: their rows only, not the whole tile's
-                    if (lane == 0) {
-                        ++drain[kStages + s];
-                        mbar_expect_tx(&q_full[s], (few ? ntok : p.tq) * g * 128 * kHalves);
-                    }
-                    __syncwarp();
-                    if (mybox < (few ? ntok : 1))
-                        tma_load_3d(dst + myhalf * (kAttnTileQ * 128) + mybox * g * 128, few ? &maps.q1 : &maps.q,
-                                    &q_full[s], myhalf * 64, w.kvh * g, w.tok0 + first + mybox);
-                }
+                __syncwarp();
+                if (mybox < (few ? ntok : 1))
+                    tma_load_3d_if(1, smem_u32(qbuf) + s * kTile + myhalf * (kAttnTileQ * 128) + mybox * p.group * 128,
+                                   few ? &maps.q1 : &maps.q, smem_u32(&q_full[s]), myhalf * 64, kvh * p.group,
+                                   tok0 + first + mybox);
             }
+#pragma unroll 1
+            for (int t = 0; t < n && ok; ++t) {
+                if (kPaged && (t & in_win) == 0) {
+                    cur = nxt;
+                    nxt = pages_of(table, t0 + t + in_win + 1, seen);
+                }
+                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & in_win) * per_tile + mybox) : 0;
+                ok = load_tile(&maps.v, it + load_of_value(pair, t, n), t0 + t, page, seen, kvh, row0);
+            }
+            it += 2 * n;
         }
-    } else if (warp == 9) {
+    } else if (warp >= 9) {
+        // ===================== MMA issuers ====================================
+        // Warp 9 + s issues stream s's products: a product executes in 64 cycles
+        // and issuing one takes 35 (66 with a branch around it), so one warp for
+        // both streams would be as busy as the tensor cores.  All lanes run the
+        // same code and the elected one's instructions take effect.
         setmaxnreg_dec<kOtherRegs>();
-        // ===================== MMA issuer =====================================
-        // All lanes run the same code and the elected one's instructions take
-        // effect, and whole tiles' steps are unrolled: a product executes in 64
-        // cycles, and issuing one this way takes 35 (66 with a branch around it).
-        uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+        const int s = warp - 9;
+        uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np = 0;
         const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
         const uint32_t klo = umma_lo(smem_u32(ring), 16), vlo = umma_lo(smem_u32(ring), kAttnTileK * 128);
         const int dsteps = (p.head_dim + 15) / 16;
         const uint32_t idesc_pv = umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
+        const uint32_t s_cells = tmem + s * kColS, o_cells = tmem + kColO + s * DP;
+        auto commit = [&](uint64_t *bar) { umma_commit_if(elect_one(), bar); };
         bool ok = true;
-        while (true) {
+        while (ok) {
             const int is = nitem % kItems;
             if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
             const int valid = uniform(wi.valid), pair = uniform(wi.pair), t0 = uniform(wi.t0);
             const int n = uniform(wi.t1) - t0;
-            const int seen = uniform(wi.seen) - t0 * kAttnTileK;   // keys that any row sees
-            const int n0 = max(0, min(n, uniform(wi.end0) - t0));   // pair: stream 0's tiles
+            const int seen = uniform(wi.seen) - t0 * kAttnTileK;   // keys that any row sees, from t0
+            // pair: both streams go through all tiles, stream 0 uses its first `mine`;
+            // single: stream s uses tiles s, s + 2, ...
+            const int mine = pair ? (s ? n : max(0, min(n, uniform(wi.end0) - t0))) : (n - s + 1) >> 1;
+            const int all = pair ? n : mine;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
             ++nitem;
             if (!valid) break;
-            // one more product step of a stream: the load i holds its tile, t counts from the piece's first
-            auto stage_of = [&](uint32_t i) { return (it + i) % kStages; };
-            auto wait_stage = [&](uint32_t i) {
-                ok &= wait(&full[stage_of(i)], ((it + i) / kStages) & 1);
-                tc_fence_after();
+            // load i of the CTA has landed
+            auto wait_load = [&](uint32_t i) {
+                const uint32_t st = i % kStages, f = i / kStages;
+                return wait_issued(st, f) && wait(&full[st], f & 1);
             };
-            auto commit = [&](uint64_t *bar) { umma_commit_if(elect_one(), bar); };
-            auto release = [&](uint32_t i) { commit(&empty[stage_of(i)]); };
-            auto qk = [&](int s, int slot, uint32_t i, int t) {
-                const int keys = min(kAttnTileK, seen - t * kAttnTileK);
-                const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
-                const uint32_t qd = qlo + ((slot * kTile) >> 4), kd = klo + stage_of(i) * (kTile >> 4);
-                const uint32_t lead = elect_one(), d = tmem + s * kColS;
-                auto step = [&](int kk) {
-                    const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
-                    umma_ss_if(lead, d, qd + o, kd + o, idesc, kk > 0);
-                };
-                if (dsteps == DP / 16) {
-#pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) step(kk);
-                } else {
-#pragma unroll 1
-                    for (int kk = 0; kk < dsteps; ++kk) step(kk);
-                }
-                commit(&s_full[s]);
-            };
-            auto pv = [&](int s, uint32_t i, int t, uint32_t acc) {
-                const int keys = max(0, min(kAttnTileK, seen - t * kAttnTileK));
-                const uint32_t vd = vlo + stage_of(i) * (kTile >> 4), a = tmem + s * kColS, d = tmem + kColO + s * DP;
-                ok &= wait(&p_full[s], (s ? np1++ : np0++) & 1);
-                tc_fence_after();
+            auto release = [&](uint32_t st) {
                 const uint32_t lead = elect_one();
-                auto step = [&](int kk) {
-                    umma_ts_if(lead, d, a + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : acc);
-                };
-                if (keys == kAttnTileK) {
-#pragma unroll
-                    for (int kk = 0; kk < kAttnTileK / 16; ++kk) step(kk);
-                } else {
-#pragma unroll 1
-                    for (int kk = 0; kk * 16 < keys; ++kk) step(kk);
-                }
-            };
-            // keys past the last one that a row sees: their p is 0, but 0 times what the
-            // tile holds there (another request's rows, stale pages) may be NaN
-            auto clean = [&](uint32_t i, int t) {
-                const int keys = seen - t * kAttnTileK, up = (keys + 15) & ~15;
-                if (keys >= kAttnTileK || keys <= 0 || keys == up) return;
-                uint8_t *v = ring + stage_of(i) * kTile;
-                for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
-                    const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
-                    *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+                umma_commit_if(lead, &empty[st]);
+                if (!pair) umma_commit_if(lead, &empty[st]);
             };
             ok &= wait(&q_full[0], nq0++ & 1);
-            if (pair) {
-                ok &= wait(&q_full[1], nq1++ & 1);
-                // loads: K0 V0 K1 V1 ...
-                wait_stage(0);
-                if (n0 > 0) qk(0, 0, 0, 0);
-                qk(1, 1, 0, 0);
-                release(0);
-                if (n == 1) commit(q_empty);
-                for (int t = 0; t < n && ok; ++t) {
-                    const uint32_t vi = 2 * t + 1, ki = 2 * t + 2;
-                    wait_stage(vi);
-                    clean(vi, t);
-                    if (t < n0) {
-                        pv(0, vi, t, t > 0);
-                        if (t == n0 - 1) commit(&o_full[0]);
+            if (pair) ok &= wait(&q_full[1], nq1++ & 1);
+            if (all == 0) commit(q_empty);
+            // tile k's values, then the keys of tile k + 1, whose scores go over the P
+            // just read; the first time only keys
+#pragma unroll 1
+            for (int k = -1; k < all && ok; ++k) {
+                if (k >= 0) {
+                    const int t = pair ? k : s + 2 * k;
+                    const uint32_t i = it + load_of_value(pair, t, n), st = i % kStages;
+                    const int keys = seen - t * kAttnTileK;   // of this tile, if below 128
+                    ok &= wait_load(i);
+                    if (k < mine) {
+                        // keys past the last one that a row sees: their p is 0, but 0 times
+                        // what the tile holds there (another request's rows, stale pages)
+                        // may be NaN
+                        const int up = (keys + 15) & ~15;
+                        if (keys > 0 && keys < kAttnTileK && keys != up) {
+                            uint8_t *v = ring + st * kTile;
+                            for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
+                                const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
+                                *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        const uint32_t vd = vlo + st * (kTile >> 4);
+                        const uint32_t par = np++ & 1;
+                        ok &= wait(&p_half[s], par);
+                        tc_fence_after();
+                        const uint32_t lead = elect_one();
+                        auto step = [&](int kk) {
+                            umma_ts_if(lead, o_cells, s_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
+                        };
+                        if (keys >= kAttnTileK) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) step(kk);
+                        }
+                        ok &= wait(&p_full[s], par);
+                        tc_fence_after();
+                        if (keys >= kAttnTileK) {
+#pragma unroll
+                            for (int kk = 4; kk < 8; ++kk) step(kk);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk * 16 < keys; ++kk) step(kk);
+                        }
+                        if (k == mine - 1) commit(&o_full[s]);
                     }
-                    if (t + 1 < n) {
-                        wait_stage(ki);
-                        if (t + 1 < n0) qk(0, 0, ki, t + 1);
-                    }
-                    pv(1, vi, t, t > 0);
-                    release(vi);
-                    if (t == n - 1) commit(&o_full[1]);
-                    if (t + 1 < n) {
-                        qk(1, 1, ki, t + 1);
-                        release(ki);
-                        if (t + 2 == n) commit(q_empty);
-                    }
+                    release(st);
                 }
-            } else {
-                // loads: K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1); tile t is stream t & 1's
-                for (int t = 0; t < 2 && t < n; ++t) {
-                    wait_stage(t);
-                    if (t == 0) qk(0, 0, 0, 0);
-                    else qk(1, 0, 1, 1);
-                    release(t);
-                }
-                if (n <= 2) commit(q_empty);
-                for (int t = 0; t < n && ok; ++t) {
-                    const uint32_t vi = min(2 * t + 2, n + t), ki = 2 * t + 3;
-                    wait_stage(vi);
-                    clean(vi, t);
-                    if (t & 1) pv(1, vi, t, t > 1);
-                    else pv(0, vi, t, t > 1);
-                    release(vi);
-                    if (t + 2 >= n) commit(&o_full[t & 1]);
-                    if (t + 2 < n) {
-                        wait_stage(ki);
-                        if (t & 1) qk(1, 0, ki, t + 2);
-                        else qk(0, 0, ki, t + 2);
-                        release(ki);
-                        if (t + 3 == n) commit(q_empty);
+                if (k + 1 < all) {
+                    const int t = pair ? k + 1 : s + 2 * (k + 1);
+                    const uint32_t i = it + load_of_key(pair, t), st = i % kStages;
+                    ok &= wait_load(i);
+                    if (k + 1 < mine) {
+                        tc_fence_after();
+                        const int keys = min(kAttnTileK, seen - t * kAttnTileK);
+                        const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
+                        const uint32_t qd = qlo + (pair && s ? kTile >> 4 : 0), kd = klo + st * (kTile >> 4);
+                        const uint32_t lead = elect_one();
+                        auto step = [&](int kk) {
+                            const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
+                            umma_ss_if(lead, s_cells, qd + o, kd + o, idesc, kk > 0);
+                        };
+                        if (dsteps == DP / 16) {
+#pragma unroll
+                            for (int kk = 0; kk < DP / 16; ++kk) step(kk);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < dsteps; ++kk) step(kk);
+                        }
+                        commit(&s_full[s]);
                     }
+                    release(st);
+                    if (k + 2 == all) commit(q_empty);
                 }
             }
             it += 2 * n;
-            if (!ok) break;
         }
+        // nothing issued here is in flight when the block ends
+        commit(end_bar);
+        wait(end_bar, 0);
     } else {
         // ===================== softmax and results ============================
         setmaxnreg_inc<kSoftmaxRegs>();
@@ -527,7 +559,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t t_s = tmem + lanes + s * kColS, t_o = tmem + lanes + kColO + s * DP;
         const int G = p.group, D = p.head_dim;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t nitem = 0, ns = 0, no0 = 0, no1 = 0, nx = 0;
+        uint32_t nitem = 0, ns = 0, no = 0, nx = 0;
         auto meet = [&] {   // all 256 threads
             __syncwarp();
             if (lane == 0) mbar_arrive(xbar);
@@ -556,74 +588,87 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
                 if (live) {
-                    if (!__any_sync(0xffffffffu, rem > 0)) {   // no row of this warp sees the tile
-                        uint32_t z[16];
+                    float x[128];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) z[e] = 0;
+                    for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, x + 32 * q);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_st16(t_s + 16 * q, z);
-                    } else {
-                        float x[128];
+                    for (int q = 0; q < 4; ++q) tmem_use32(x + 32 * q);
+                    if (__any_sync(0xffffffffu, rem < kAttnTileK)) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, x + 32 * q);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_use32(x + 32 * q);
-                        if (__any_sync(0xffffffffu, rem < kAttnTileK)) {
-#pragma unroll
-                            for (int e = 0; e < 128; ++e) x[e] = e < rem ? x[e] : -INFINITY;
-                        }
+                        for (int e = 0; e < 128; ++e) x[e] = e < rem ? x[e] : -INFINITY;
+                    }
+                    const uint64_t c2 = pack_f2(c, c);
+                    uint64_t sum[2];
+                    uint32_t pk[32];
+                    // The first half's p from the maximum so far, and the tile's maximum in the
+                    // shadow of its exponentials (MUFU is the busiest unit here); once more in
+                    // the rare case that the maximum has grown too far, and for a first tile.
+                    while (true) {
+                        const float off = m == -INFINITY ? 0.f : -m * c;
+                        const uint64_t off2 = pack_f2(off, off);
                         float mx[4] = {x[0], x[1], x[2], x[3]};
+                        sum[0] = sum[1] = 0;
 #pragma unroll
-                        for (int e = 4; e < 128; e += 8) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                mx[q] = e + 4 + q < 128 ? fmaxf(fmaxf(mx[q], x[e + q]), x[e + 4 + q])
-                                                        : fmaxf(mx[q], x[e + q]);
+                        for (int e = 0; e < 32; ++e) {
+                            float a, b;
+                            unpack_f2(fma_f2(pack_f2(x[2 * e], x[2 * e + 1]), c2, off2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
+                            pk[e] = pack_bf16x2(a, b);
+                            mx[e & 3] = fmaxf(fmaxf(mx[e & 3], x[4 * e]), x[4 * e + 1]);
+                            mx[(e + 2) & 3] = fmaxf(fmaxf(mx[(e + 2) & 3], x[4 * e + 2]), x[4 * e + 3]);
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        // the running maximum follows when it lags too far (always from -infinity)
-                        const bool grow = (top - m) * c > kRescaleBits;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float mn = grow ? top : m;
-                            const float f = grow ? ex2((m - mn) * c) : 1.f;   // 0 from -infinity
-                            m = mn;
-                            l *= f;
-                            if (k > 0) {   // O holds the earlier tiles' sums: S of this tile came after them
-                                float o[32];
+                        const bool grow = (top - m) * c > kRescaleBits;   // always from -infinity
+                        if (!__any_sync(0xffffffffu, grow)) break;
+                        const float mn = grow ? top : m;
+                        const float f = grow ? ex2((m - mn) * c) : 1.f;   // 0 from -infinity
+                        m = mn;
+                        l *= f;
+                        if (k > 0) {   // O holds the earlier tiles' sums: this tile's S came after them
+                            float o[32];
+#pragma unroll 1
+                            for (int q = 0; q < DP / 32; ++q) {
+                                tmem_ld32(t_o + 32 * q, o);
+                                tmem_ld_wait();
+                                tmem_use32(o);
 #pragma unroll
-                                for (int q = 0; q < DP / 32; ++q) {
-                                    tmem_ld32(t_o + 32 * q, o);
-                                    tmem_ld_wait();
-                                    tmem_use32(o);
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] *= f;
-                                    tmem_st32(t_o + 32 * q, o);
-                                }
+                                for (int e = 0; e < 32; ++e) o[e] *= f;
+                                tmem_st32(t_o + 32 * q, o);
                             }
                         }
-                        const float off = m == -INFINITY ? 0.f : -m * c;
-                        const uint64_t c2 = pack_f2(c, c), off2 = pack_f2(off, off);
-                        uint64_t sum[2] = {0, 0};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float a, b;
-                                unpack_f2(fma_f2(pack_f2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), c2, off2), a, b);
-                                a = ex2(a);
-                                b = ex2(b);
-                                sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
-                                pk[e] = pack_bf16x2(a, b);
-                            }
-                            tmem_st16(t_s + 16 * q, pk);
-                        }
-                        float a0, a1;
-                        unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
-                        l += a0 + a1;
                     }
+                    tmem_st16(t_s, pk);
+                    tmem_st16(t_s + 16, pk + 16);
+                    const float off = m == -INFINITY ? 0.f : -m * c;
+                    const uint64_t off2 = pack_f2(off, off);
+                    uint32_t pl[32];
+                    auto second = [&](int e) {
+                        float a, b;
+                        unpack_f2(fma_f2(pack_f2(x[64 + 2 * e], x[65 + 2 * e]), c2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
+                        pl[e] = pack_bf16x2(a, b);
+                    };
+#pragma unroll
+                    for (int e = 0; e < 12; ++e) second(e);   // while the first half's P goes out
                     tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_half[s]);
+#pragma unroll
+                    for (int e = 12; e < 32; ++e) second(e);
+                    tmem_st16(t_s + 32, pl);
+                    tmem_st16(t_s + 48, pl + 16);
+                    float a0, a1;
+                    unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
+                    l += a0 + a1;
+                    tmem_st_wait();
+                } else if (lane == 0) {
+                    mbar_arrive(&p_half[s]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -632,21 +677,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
             // ---- results ----------------------------------------------------
             const int g = r - i * G;
-            float f0 = 1.f, f1 = 0.f;   // single: factors of the two streams' sums
-            bool use0 = true, use1 = false;
-            if (w.pair) {
-                if (mine_n > 0) wait(&o_full[s], (s ? no1 : no0) & 1);
-            } else {
+            // factors of the two streams' sums (single); a stream without keys for the
+            // row has nothing defined in O
+            float f0 = 1.f, f1 = 0.f;
+            bool use0 = l != 0.f, use1 = false;
+            if (mine_n > 0) wait(&o_full[s], no++ & 1);
+            if (!w.pair) {
                 // both streams worked on the same rows: stream 0's threads join them
                 if (s == 1) stats[r] = make_float2(m, l);
-                wait(&o_full[0], no0 & 1);
-                if (cnt1 > 0) wait(&o_full[1], no1 & 1);
                 meet();
                 if (s == 0) {
                     const float2 st = stats[r];
                     const float mm = fmaxf(m, st.x);
-                    // a stream without keys for the row has nothing defined in O
-                    use0 = l != 0.f;
                     use1 = st.y != 0.f;
                     f0 = use0 ? ex2((m - mm) * c) : 0.f;
                     f1 = use1 ? ex2((st.x - mm) * c) : 0.f;
@@ -655,47 +697,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             tc_fence_after();
-            no0 += cnt0 > 0;
-            no1 += cnt1 > 0;
             const bool mine = w.pair || s == 0;
             const int rho = tok * G + g;   // my row of the block
             if (mine && __any_sync(0xffffffffu, row_ok)) {
                 const bool whole = w.parts == 1;
                 const float inv = whole && l != 0.f ? 1.f / l : 1.f;
+                f0 *= inv;
+                f1 *= inv;
                 const int64_t row = static_cast<int64_t>(w.tok0) + tok;
                 const int head = w.kvh * G + g;
                 uint8_t *out = whole ? reinterpret_cast<uint8_t *>(p.o + row * p.o_tok + head * p.o_head)
                                      : reinterpret_cast<uint8_t *>(p.part + (static_cast<int64_t>(w.slot) * p.part_rows + rho) * D);
                 const uint64_t dst = row_ok ? reinterpret_cast<uint64_t>(out) : 0;
-                // 16 columns of fp32 or 32 of bf16 at a time: 64 bytes a row
 #pragma unroll 1
                 for (int q = 0; 32 * q < D; ++q) {
                     float o[32];
                     tmem_ld32(t_o + 32 * q, o);
                     tmem_ld_wait();
                     tmem_use32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = use0 ? o[e] * f0 : 0.f;
                     if (!w.pair) {
                         float o1[32];
                         tmem_ld32(t_o + DP + 32 * q, o1);
                         tmem_ld_wait();
                         tmem_use32(o1);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = (use0 ? o[e] * f0 : 0.f) + (use1 ? o1[e] * f1 : 0.f);
+                        for (int e = 0; e < 32; ++e) o[e] += use1 ? o1[e] * f1 : 0.f;
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-                    uint32_t v[16];
                     if (whole) {
+                        uint32_t v[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
                         store_rows(v, dst, 64 * q, D * 2, lane);
                     } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[16 * h + e]);
-                            store_rows(v, dst, 128 * q + 64 * h, D * 4, lane);
-                        }
+                        for (int e = 0; e < 32; e += 4)
+                            if (row_ok && 32 * q + e < D)
+                                *reinterpret_cast<float4 *>(out + (32 * q + e) * 4) =
+                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
                 if (row_ok) {
@@ -719,18 +759,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     };
                     for (int u = threadIdx.x; u < rows * d4; u += 256) {
                         const int rr = u / d4, col = (u - rr * d4) * 4;
-                        float mm = -INFINITY;
-                        for (int k = 0; k < w.parts; ++k) mm = fmaxf(mm, __ldcg(&p.part_ml[slot_of(k) + rr].x));
-                        float ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+                        float mm = -INFINITY, ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
                         for (int k = 0; k < w.parts; ++k) {
                             const float2 ml = __ldcg(p.part_ml + slot_of(k) + rr);
                             const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(k) + rr) * D + col));
-                            const float f = ml.y == 0.f ? 0.f : ex2((ml.x - mm) * c);
-                            ll += f * ml.y;
-                            a[0] += f * v.x;
-                            a[1] += f * v.y;
-                            a[2] += f * v.z;
-                            a[3] += f * v.w;
+                            const float mn = fmaxf(mm, ml.x);
+                            const float f = ml.y == 0.f ? 0.f : ex2((ml.x - mn) * c), g = ll == 0.f ? 0.f : ex2((mm - mn) * c);
+                            mm = mn;
+                            ll = ll * g + f * ml.y;
+                            a[0] = a[0] * g + f * v.x;
+                            a[1] = a[1] * g + f * v.y;
+                            a[2] = a[2] * g + f * v.z;
+                            a[3] = a[3] * g + f * v.w;
                         }
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
                         const int tk = rr / G, hd = w.kvh * G + (rr - tk * G);
@@ -755,21 +796,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (*abort_flag) {
-        // loads in flight are waited for (bounded) before the shared memory goes,
-        // matrix products before the tensor memory does
+        // loads in flight are waited for (bounded) before the shared memory goes
         auto settle = [&](uint64_t *bar, uint32_t parity) {
-            mbar_wait(bar, parity, abort_flag, status, LORA_DEV_TIMEOUT, budget);
+            attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles);
         };
+        if (threadIdx.x == 0) atomicOr(status, LORA_DEV_TIMEOUT);
         if (warp == 8 && lane == 0)
             for (int s = 0; s < kStages; ++s)
-                if (drain[s] > 0) settle(&full[s], (drain[s] - 1) & 1);
+                if (issued[s] > 0) settle(&full[s], (issued[s] - 1) & 1);
         if (warp == 11 && lane == 0)
             for (int s = 0; s < 2; ++s)
-                if (drain[kStages + s] > 0) settle(&q_full[s], (drain[kStages + s] - 1) & 1);
-        if (warp == 9) {
-            umma_commit_if(elect_one(), end_bar);
-            settle(end_bar, 0);
-        }
+                if (issued[kStages + s] > 0) settle(&q_full[s], (issued[kStages + s] - 1) & 1);
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -836,7 +873,8 @@ cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
             !encode_map(&m.v, p.v, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     } else {
-        p.box_rows = 32;   // a short prompt's tile reads at most 31 rows too many
+        // long prompts: whole tiles; short ones: a tile reads at most 31 rows too many
+        p.box_rows = p.T >= 256 * static_cast<int64_t>(p.requests) ? kAttnTileK : 32;
         const uint64_t dims[3] = {D, static_cast<uint64_t>(p.kv_heads), static_cast<uint64_t>(p.T)};
         const uint64_t ks[2] = {bytes(p.k_head, p.kv_heads), bytes(p.k_tok, p.T)};
         const uint64_t vs[2] = {bytes(p.v_head, p.kv_heads), bytes(p.v_tok, p.T)};

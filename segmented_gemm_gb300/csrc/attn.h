@@ -4,8 +4,8 @@
 //   counters   status word, work-list counters, arrival counters of split
 //              groups                                   (zero at rest but the status)
 //   hdr        schedule header (AttnHdr)
-//   blocks     query blocks of the step (AttnBlock), in request order
-//   order      the blocks, longest first
+//   blocks     query blocks of the step (AttnBlock), longest first or (cut) in
+//              request order
 //   part       partial results of split groups: fp32 O rows, then (m, l) pairs
 #pragma once
 #include <cuda.h>
@@ -30,31 +30,37 @@ enum AttnCounters {
     ACNT_WORDS = ACNT_GROUP + kAttnMaxCtas
 };
 
+// What starting and ending a piece costs, in key tiles: the cut schedule leaves
+// that much room ahead of each group.
+constexpr int kAttnItemCost = 2;
+
 // A query block: up to two query tiles of one request, for every kv head.
-struct AttnBlock {
-    int64_t pre;      // key tiles of the blocks before it (one head)
+struct __align__(16) AttnBlock {
+    int32_t pre;      // cut: cost of the blocks before it (one head)
     int32_t req;
     int32_t tok0;     // first packed row
     int32_t ntok;
     int32_t qpos0;    // row tok0 sees keys [0, qpos0 + 1) (none when that is <= 0)
     int32_t kv_len;
     int32_t tiles;    // key tiles its last row reaches, at least 1
+    int32_t unused;
 };
 
-struct AttnHdr {
+struct __align__(16) AttnHdr {
     int32_t nblocks;
     int32_t units;      // pieces of work
-    int32_t cut;        // 0: a unit is one (block, head); 1: a unit is unit_tiles consecutive key tiles
+    int32_t cut;        // 0: a unit is one (block, head), blocks longest first; 1: unit_cost of the list's cost
     int32_t sec_heads;  // heads whose blocks run together (cut 0)
-    int64_t unit_tiles;
-    int64_t tiles;      // key tiles of all blocks and heads
+    int32_t unit_cost;  // cut 1
+    int32_t cost;       // of all blocks and heads (cut 1)
+    int32_t unused[2];
 };
 
 struct AttnLayout {
     int32_t tq;          // tokens of one query tile
     int64_t max_blocks;
     int32_t part_rows;   // rows of a partial slot
-    size_t counters, hdr, blocks, order, part, part_ml, total;
+    size_t counters, hdr, blocks, part, part_ml, total;
 };
 
 struct AttnSchedParams {
@@ -63,7 +69,6 @@ struct AttnSchedParams {
     int64_t T, max_kv, max_blocks;
     AttnHdr *hdr;
     AttnBlock *blocks;
-    int32_t *order;
     int32_t *counters;
 };
 
@@ -76,7 +81,7 @@ struct AttnParams {
     float scale;
     const AttnHdr *hdr;
     const AttnBlock *blocks;
-    const int32_t *order;
+    int64_t max_blocks;
     int32_t *counters;
     // keys and values: paged or packed rows
     const uint16_t *k, *v;
@@ -88,11 +93,12 @@ struct AttnParams {
     int32_t paged;
     int32_t box_rows;        // keys of one TMA box
     int64_t T;
+    int32_t requests;
     int32_t ctas;
     float *part;             // [2 * kAttnMaxCtas][part_rows][head_dim] partial O
     float2 *part_ml;         // [2 * kAttnMaxCtas][part_rows] partial (m, l)
     int32_t part_rows;
-    int64_t wait_cycles;     // long budget of the bounded waits, in SM clock cycles
+    uint32_t wait_cycles;    // long budget of the bounded waits, in SM clock cycles
 };
 
 struct KvPlanParams {

@@ -48,7 +48,6 @@ static AttnLayout make_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_he
         L.part_rows = static_cast<int32_t>(std::min<int64_t>(2 * L.tq, std::max<int64_t>(T, 1)) * group);
         L.hdr = take(sizeof(AttnHdr));
         L.blocks = take(static_cast<size_t>(L.max_blocks) * sizeof(AttnBlock));
-        L.order = take(static_cast<size_t>(L.max_blocks) * 4);
         L.part = take(static_cast<size_t>(2 * kAttnMaxCtas) * L.part_rows * head_dim * 4);
         L.part_ml = take(static_cast<size_t>(2 * kAttnMaxCtas) * L.part_rows * 8);
     }
@@ -122,7 +121,6 @@ static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R,
     p.max_blocks = L.max_blocks;
     p.hdr = at<AttnHdr>(ws, L.hdr);
     p.blocks = at<AttnBlock>(ws, L.blocks);
-    p.order = at<int32_t>(ws, L.order);
     p.counters = at<int32_t>(ws, L.counters);
     return launch_attn_schedule(p, stream) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
@@ -160,14 +158,15 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->scale = a->scale;
     p->hdr = at<AttnHdr>(ws, L.hdr);
     p->blocks = at<AttnBlock>(ws, L.blocks);
-    p->order = at<int32_t>(ws, L.order);
+    p->max_blocks = L.max_blocks;
     p->counters = at<int32_t>(ws, L.counters);
     p->T = a->num_tokens;
+    p->requests = a->num_requests;
     p->ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
     p->part = at<float>(ws, L.part);
     p->part_ml = at<float2>(ws, L.part_ml);
     p->part_rows = L.part_rows;
-    p->wait_cycles = tc_wait_cycles();
+    p->wait_cycles = static_cast<uint32_t>(std::min<int64_t>(tc_wait_cycles(), 2000000000));
     return LORA_OK;
 }
 

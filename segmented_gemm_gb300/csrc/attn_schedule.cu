@@ -1,19 +1,18 @@
 // The attention's work list, from the requests' lengths (lora_attn_schedule).
 //
 // A request's n query rows are cut into blocks of 2 tq tokens (two query tiles
-// of 128 rows: tq tokens times the group's heads each).  A block's cost is the
-// key tiles of 128 that its last token reaches, max(1, ceil(keys / 128)), once
-// for every kv head.
+// of 128 rows: tq tokens times the group's heads each).  A group is a block and
+// a kv head; it costs the key tiles of 128 that the block's last token reaches,
+// and kAttnItemCost more for starting and ending it.
 //
 // The persistent attention kernel takes units from the list in one of two ways,
 // chosen here by which ends sooner:
-//   whole   a unit is one (block, head), longest blocks first, taken as CTAs
-//           come free: nothing is split, the end is ragged by about half of the
-//           longest unit
-//   cut     the tiles of all (block, head) pairs laid end to end, cut into one
-//           equal piece a CTA: ends together, but a pair that spans pieces is
-//           written as partial results and joined
-// One CTA, one pass over the requests and two over the blocks; once a step.
+//   whole   a unit is one group, longest first, taken as CTAs come free: nothing
+//           is split, the end is ragged by about half of the units that run last
+//   cut     all groups laid end to end and cut into one equal piece a CTA: they
+//           end together, but a group that spans pieces is written as partial
+//           results and joined
+// One CTA, once a step.
 #include <cuda_runtime.h>
 
 #include "attn.h"
@@ -26,7 +25,7 @@ namespace lora {
 constexpr int kSchedThreads = 1024;
 constexpr int kSchedBuckets = 1024;          // block costs told apart by the sort
 constexpr int kMinPiece = 2;                 // key tiles of a piece, at least
-constexpr int kJoinSingle = 2, kJoinPair = 6; // what joining partial results costs, in key tiles
+constexpr int kJoinSingle = 2, kJoinPair = 8; // what joining partial results costs, in key tiles
 constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads that run together (L2 holds 126 MB)
 
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const AttnSchedParams p)
@@ -35,11 +34,12 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     extern __shared__ int32_t blk_start[];   // [R + 1] first block of each request
     __shared__ int64_t wsum[32];
     __shared__ int32_t hist[kSchedBuckets];
-    __shared__ int32_t s_max, s_pair;
+    __shared__ int32_t s_max, s_pair, s_tail;
     const int tid = threadIdx.x;
     const int R = p.R, tb = 2 * p.tq;
     if (tid == 0) {
         s_max = 0;
+        s_tail = 1;
         s_pair = 0;
     }
     hist[tid] = 0;
@@ -87,65 +87,80 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     int64_t all_keys;
     block_scan_i64(keys, wsum, &all_keys);   // also makes blk_start visible
 
-    carry = 0;
-    int my_max = 0, my_pair = 0;
-    for (int b0 = 0; b0 < nb; b0 += kSchedThreads) {
-        const int b = b0 + tid;
+    // block b: two query tiles at most, and what its last row reaches
+    auto block_of = [&](int b) {
         AttnBlock k = {};
-        if (b < nb) {
-            const int r = last_le(blk_start, R, b);
-            int32_t start;
-            const int32_t n = rows_of(r, &start), len = keys_of(r, n);
-            const int32_t local = (b - blk_start[r]) * tb;
-            k.req = r;
-            k.tok0 = start + local;
-            k.ntok = min(tb, n - local);
-            k.qpos0 = len - n + local;
-            k.kv_len = len;
-            const int32_t seen = max(0, k.qpos0 + k.ntok);   // <= len
-            k.tiles = max(1, (seen + kAttnTileK - 1) / kAttnTileK);
-            my_max = max(my_max, k.tiles);
-            my_pair |= k.ntok > p.tq;
-            atomicAdd(&hist[kSchedBuckets - min(k.tiles, kSchedBuckets)], 1);
-        }
-        int64_t total;
-        k.pre = carry + block_scan_i64(k.tiles, wsum, &total);
-        if (b < nb) p.blocks[b] = k;
-        carry += total;
+        const int r = last_le(blk_start, R, b);
+        int32_t start;
+        const int32_t n = rows_of(r, &start), len = keys_of(r, n);
+        const int32_t local = (b - blk_start[r]) * tb;
+        k.req = r;
+        k.tok0 = start + local;
+        k.ntok = min(tb, n - local);
+        k.qpos0 = len - n + local;
+        k.kv_len = len;
+        const int32_t seen = max(0, k.qpos0 + k.ntok);   // <= len
+        k.tiles = max(1, (seen + kAttnTileK - 1) / kAttnTileK);
+        return k;
+    };
+    auto bucket = [](int tiles) { return kSchedBuckets - min(tiles, kSchedBuckets); };
+    int64_t tiles = 0;
+    int my_max = 0, my_pair = 0;
+    for (int b = tid; b < nb; b += kSchedThreads) {
+        const AttnBlock k = block_of(b);
+        tiles += k.tiles;
+        my_max = max(my_max, k.tiles);
+        my_pair |= k.ntok > p.tq;
+        atomicAdd(&hist[bucket(k.tiles)], 1);
     }
     if (my_max) atomicMax(&s_max, my_max);
     if (my_pair) atomicOr(&s_pair, 1);
     if (bad) atomicOr(p.counters + CNT_STATUS, LORA_DEV_BAD_LENGTH);
+    int64_t all_tiles, total;
+    block_scan_i64(tiles, wsum, &all_tiles);   // also makes hist, s_max and s_pair visible
+    const int32_t here = hist[tid];
+    const int32_t before = static_cast<int32_t>(block_scan_i64(here, wsum, &total));
+    hist[tid] = before;   // first place of each cost in the longest-first order
+    // the cost of the units that run last when whole: those that start when about
+    // every CTA has one left
+    const int last = max(0, nb - (p.ctas + p.kv_heads - 1) / p.kv_heads);
+    if (here > 0 && before <= last && last < before + here) s_tail = kSchedBuckets - tid;
     __syncthreads();
 
-    // longest blocks first (ties in any order: they are whole either way)
-    {
-        int64_t total;
-        const int32_t h = hist[tid];
-        const int64_t ex = block_scan_i64(h, wsum, &total);
-        hist[tid] = static_cast<int32_t>(ex);
-        __syncthreads();
-        for (int b = tid; b < nb; b += kSchedThreads) {
-            const int at = atomicAdd(&hist[kSchedBuckets - min(p.blocks[b].tiles, kSchedBuckets)], 1);
-            p.order[at] = b;
-        }
-    }
+    const int64_t groups = static_cast<int64_t>(nb) * p.kv_heads;
+    const int64_t cost = all_tiles * p.kv_heads + groups * kAttnItemCost;
+    const int64_t each = max((cost + p.ctas - 1) / p.ctas, static_cast<int64_t>(kMinPiece));
+    const int64_t whole = max(groups >= p.ctas ? each + s_tail / 2 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
+    // (a list too long for 32-bit positions is never short of units)
+    const bool cut = each + (s_pair ? kJoinPair : kJoinSingle) < whole && cost + each < INT32_MAX;
     if (tid == 0) {
-        const int64_t W = carry * p.kv_heads;
-        AttnHdr h;
+        AttnHdr h = {};
         h.nblocks = nb;
-        h.tiles = W;
-        // key tiles a CTA runs, on average, and what each way adds to that
-        const int64_t each = (W + p.ctas - 1) / p.ctas;
-        const int64_t whole = max(each + (s_max + 1) / 2, static_cast<int64_t>(s_max));
-        const int64_t piece = max(each, static_cast<int64_t>(kMinPiece)) + (s_pair ? kJoinPair : kJoinSingle);
-        h.cut = piece < whole;
-        h.unit_tiles = max(each, static_cast<int64_t>(kMinPiece));
-        h.units = static_cast<int32_t>(h.cut ? (W + h.unit_tiles - 1) / h.unit_tiles
-                                             : min(static_cast<int64_t>(nb) * p.kv_heads, static_cast<int64_t>(INT32_MAX)));
+        h.cut = cut;
+        h.cost = cut ? static_cast<int32_t>(cost) : 0;
+        h.unit_cost = cut ? static_cast<int32_t>(each) : 0;
+        h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups, static_cast<int64_t>(INT32_MAX)));
         const int64_t head_bytes = max(static_cast<int64_t>(1), all_keys * p.head_dim * 4);
-        h.sec_heads = static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
+        h.sec_heads = static_cast<int32_t>(
+            max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
         *p.hdr = h;
+    }
+    if (!cut) {
+        // ties in any order: the results do not depend on it
+        for (int b = tid; b < nb; b += kSchedThreads) {
+            const AttnBlock k = block_of(b);
+            p.blocks[atomicAdd(&hist[bucket(k.tiles)], 1)] = k;
+        }
+    } else {
+        carry = 0;
+        for (int b0 = 0; b0 < nb; b0 += kSchedThreads) {
+            const int b = b0 + tid;
+            AttnBlock k = {};
+            if (b < nb) k = block_of(b);
+            k.pre = static_cast<int32_t>(carry + block_scan_i64(b < nb ? k.tiles + kAttnItemCost : 0, wsum, &total));
+            if (b < nb) p.blocks[b] = k;
+            carry += total;
+        }
     }
 }
 
