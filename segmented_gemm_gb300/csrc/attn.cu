@@ -1,6 +1,6 @@
 // Attention over packed rows or a paged cache (include/lora_attn.h):
 //   o_i = sum_j p_ij v_j / l_i,   p_ij = 2^(c q_i.k_j - c m_i),   l_i = sum_j p_ij,   c = scale log2(e)
-// over the keys j that row i sees, m_i a running maximum of the scores.
+// over the keys j that row i sees, m_i a reference score of the row.
 //
 // A query tile is 128 rows: tq tokens times the group's query heads, which
 // share the key/value head, so a key tile is loaded once for the group.  A
@@ -15,10 +15,12 @@
 //               over S's cells (half of them)
 //   O += P V    P from tensor memory, V from shared memory as it was loaded
 //               (its head dimension contiguous: an N-major operand)
-// O stays in tensor memory.  m_i moves only when the maximum has grown by more
-// than 2^8 in p (so p <= 256, well inside fp32 and bf16): O is rescaled then,
-// by the softmax threads themselves, and the division by l_i at the end makes
-// any m_i as good as the true maximum.
+// O stays in tensor memory.  m_i is the maximum of the first tile that the row
+// sees, and moves on only when half a tile's p sum to more than 2^40: p, l and O
+// are floating point (bf16 has fp32's range), so a larger p costs no precision,
+// and the division by l_i makes any m_i as good as the maximum.  Otherwise a
+// tile's maximum is not computed at all.  When m_i does move, the softmax threads
+// rescale O themselves.
 //
 // Roles (384 threads): warps 0..3 and 4..7 the softmax and the results of
 // stream 0 and 1; warp 8 takes the work and loads keys, 11 loads queries and
@@ -41,7 +43,7 @@ constexpr int kAttnThreads = 384;
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the split draws on the launch's registers");
 constexpr int kItems = 4;             // work items in flight between the loader and the others
-constexpr float kRescaleBits = 8.f;   // m_i may lag the maximum by this many powers of two
+constexpr float kMostP = 0x1p40f;     // half a tile whose p sum to more than this moves m_i
 
 // tensor memory columns (512 in all): S of stream s at s * 128 (P over its
 // first 64), O of stream s at 256 + s * DP
@@ -66,7 +68,7 @@ struct AttnSmem {
     static constexpr int kStats = 2 * kTile + kStages * kTile; // offsets
     static constexpr int kItem = kStats + 128 * 8;
     static constexpr int kBars = kItem + kItems * static_cast<int>(sizeof(AttnItem));
-    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2 + 2;
+    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int kEnd = kBars + kNumBars * 8 + 4 * (3 + kStages + 2);
     static constexpr int kBytes = kEnd + 1024;                 // room to align the base
     static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
@@ -128,12 +130,13 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
-// Bounded wait until *count > n (shared memory, written with release).
+// Bounded wait until *count > n (shared memory; what it counts is ordered by the
+// barrier that is waited on next).
 __device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatile int *abort_flag, uint32_t limit)
 {
-    if (ld_acquire_shared(count) > n) return true;
+    if (ld_volatile_shared(count) > n) return true;
     const uint32_t t0 = static_cast<uint32_t>(clock());
-    while (ld_acquire_shared(count) <= n) {
+    while (ld_volatile_shared(count) <= n) {
         const uint32_t most = *abort_flag ? min(limit, static_cast<uint32_t>(kWaitShort)) : limit;
         if (static_cast<uint32_t>(clock()) - t0 > most) {
             *abort_flag = 1;
@@ -161,7 +164,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t *s_full = q_empty + 1;           // [2]
     uint64_t *p_half = s_full + 2;            // [2] P of the tile's first 64 keys is in place
     uint64_t *p_full = p_half + 2;            // [2]
-    uint64_t *o_full = p_full + 2;            // [2]
+    uint64_t *pv_half = p_full + 2;           // [2] the products of the first 64 keys are done
+    uint64_t *o_full = pv_half + 2;           // [2]
     uint64_t *xbar = o_full + 2;              // the 256 softmax threads meet here
     uint64_t *end_bar = xbar + 1;             // all matrix products are done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(end_bar + 1);
@@ -179,6 +183,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // so a wait that gives up takes its warp out together.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles)) != 0;
+    };
+    // The same without agreement: lanes go on together whatever it says, and
+    // agree at the end of their loop's round.
+    auto wait_each = [&](uint64_t *bar, uint32_t parity) {
+        return attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles);
     };
     // load number f of stage s (from 0) has been issued
     auto wait_issued = [&](uint32_t s, uint32_t f) {
@@ -202,6 +211,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&s_full[s], 1);
             mbar_init(&p_half[s], 4);
             mbar_init(&p_full[s], 4);
+            mbar_init(&pv_half[s], 1);
             mbar_init(&o_full[s], 1);
         }
         mbar_init(xbar, 8);
@@ -459,91 +469,96 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // load i of the CTA has landed
             auto wait_load = [&](uint32_t i) {
                 const uint32_t st = i % kStages, f = i / kStages;
-                return wait_issued(st, f) && wait(&full[st], f & 1);
+                ok &= attn_wait_count(&issued[st], static_cast<int>(f), abort_flag, p.wait_cycles);
+                ok &= wait_each(&full[st], f & 1);
             };
             auto release = [&](uint32_t st) {
                 const uint32_t lead = elect_one();
                 umma_commit_if(lead, &empty[st]);
                 if (!pair) umma_commit_if(lead, &empty[st]);
             };
-            ok &= wait(&q_full[0], nq0++ & 1);
-            if (pair) ok &= wait(&q_full[1], nq1++ & 1);
+            ok &= wait_each(&q_full[0], nq0++ & 1);
+            if (pair) ok &= wait_each(&q_full[1], nq1++ & 1);
             if (all == 0) commit(q_empty);
-            // tile k's values, then the keys of tile k + 1, whose scores go over the P
-            // just read; the first time only keys
+            // Round k: tile k's values, then the keys of tile k + 1, whose scores go over
+            // the P just read (round -1: only keys).  What can be waited for ahead of P
+            // is, and the stages go back last: from P to the next scores nothing is in
+            // the way of the tensor cores.
 #pragma unroll 1
-            for (int k = -1; k < all && ok; ++k) {
-                if (k >= 0) {
-                    const int t = pair ? k : s + 2 * k;
-                    const uint32_t i = it + load_of_value(pair, t, n), st = i % kStages;
-                    const int keys = seen - t * kAttnTileK;   // of this tile, if below 128
-                    ok &= wait_load(i);
-                    if (k < mine) {
-                        // keys past the last one that a row sees: their p is 0, but 0 times
-                        // what the tile holds there (another request's rows, stale pages)
-                        // may be NaN
-                        const int up = (keys + 15) & ~15;
-                        if (keys > 0 && keys < kAttnTileK && keys != up) {
-                            uint8_t *v = ring + st * kTile;
-                            for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
-                                const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
-                                *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
+            for (int k = -1; k < all; ++k) {
+                const int tv = pair ? k : s + 2 * k, tk = pair ? k + 1 : s + 2 * k + 2;
+                const uint32_t iv = it + load_of_value(pair, tv, n), ik = it + load_of_key(pair, tk);
+                const uint32_t stv = iv % kStages, stk = ik % kStages;
+                const bool more = k + 1 < all;
+                if (k >= 0) wait_load(iv);
+                if (more) wait_load(ik);
+                if (k >= 0 && k < mine) {
+                    const int keys = min(kAttnTileK, seen - tv * kAttnTileK);
+                    // keys past the last one that a row sees: their p is 0, but 0 times
+                    // what the tile holds there (another request's rows, stale pages)
+                    // may be NaN
+                    const int up = (keys + 15) & ~15;
+                    if (keys > 0 && keys != up) {
+                        uint8_t *v = ring + stv * kTile;
+                        for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
+                            const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
+                            *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
                         }
-                        const uint32_t vd = vlo + st * (kTile >> 4);
-                        const uint32_t par = np++ & 1;
-                        ok &= wait(&p_half[s], par);
-                        tc_fence_after();
-                        const uint32_t lead = elect_one();
-                        auto step = [&](int kk) {
-                            umma_ts_if(lead, o_cells, s_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
-                        };
-                        if (keys >= kAttnTileK) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) step(kk);
-                        }
-                        ok &= wait(&p_full[s], par);
-                        tc_fence_after();
-                        if (keys >= kAttnTileK) {
-#pragma unroll
-                            for (int kk = 4; kk < 8; ++kk) step(kk);
-                        } else {
-#pragma unroll 1
-                            for (int kk = 0; kk * 16 < keys; ++kk) step(kk);
-                        }
-                        if (k == mine - 1) commit(&o_full[s]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    release(st);
-                }
-                if (k + 1 < all) {
-                    const int t = pair ? k + 1 : s + 2 * (k + 1);
-                    const uint32_t i = it + load_of_key(pair, t), st = i % kStages;
-                    ok &= wait_load(i);
-                    if (k + 1 < mine) {
-                        tc_fence_after();
-                        const int keys = min(kAttnTileK, seen - t * kAttnTileK);
-                        const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
-                        const uint32_t qd = qlo + (pair && s ? kTile >> 4 : 0), kd = klo + st * (kTile >> 4);
-                        const uint32_t lead = elect_one();
-                        auto step = [&](int kk) {
-                            const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
-                            umma_ss_if(lead, s_cells, qd + o, kd + o, idesc, kk > 0);
-                        };
-                        if (dsteps == DP / 16) {
+                    const uint32_t vd = vlo + stv * (kTile >> 4);
+                    const uint32_t par = np++ & 1;
+                    auto step = [&](uint32_t lead, int kk) {
+                        umma_ts_if(lead, o_cells, s_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
+                    };
+                    ok &= wait_each(&p_half[s], par);
+                    tc_fence_after();
+                    const uint32_t lead = elect_one();
+                    if (keys == kAttnTileK) {
 #pragma unroll
-                            for (int kk = 0; kk < DP / 16; ++kk) step(kk);
-                        } else {
+                        for (int kk = 0; kk < 4; ++kk) step(lead, kk);
+                    } else {
 #pragma unroll 1
-                            for (int kk = 0; kk < dsteps; ++kk) step(kk);
-                        }
-                        commit(&s_full[s]);
+                        for (int kk = 0; kk < 4 && kk * 16 < keys; ++kk) step(lead, kk);
                     }
-                    release(st);
-                    if (k + 2 == all) commit(q_empty);
+                    umma_commit_if(lead, &pv_half[s]);
+                    ok &= wait_each(&p_full[s], par);
+                    tc_fence_after();
+                    if (keys == kAttnTileK) {
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk) step(lead, kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 4; kk * 16 < keys; ++kk) step(lead, kk);
+                    }
+                    if (k == mine - 1) umma_commit_if(lead, &o_full[s]);
                 }
+                if (k + 1 < mine) {
+                    tc_fence_after();
+                    const int keys = min(kAttnTileK, seen - tk * kAttnTileK);
+                    const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
+                    const uint32_t qd = qlo + (pair && s ? kTile >> 4 : 0), kd = klo + stk * (kTile >> 4);
+                    const uint32_t lead = elect_one();
+                    auto step = [&](int kk) {
+                        const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
+                        umma_ss_if(lead, s_cells, qd + o, kd + o, idesc, kk > 0);
+                    };
+                    if (dsteps == DP / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk) step(kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < dsteps; ++kk) step(kk);
+                    }
+                    umma_commit_if(lead, &s_full[s]);
+                }
+                if (k >= 0) release(stv);
+                if (more) release(stk);
+                if (k + 2 == all) commit(q_empty);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
             it += 2 * n;
         }
@@ -599,35 +614,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int e = 0; e < 128; ++e) x[e] = e < rem ? x[e] : -INFINITY;
                     }
                     const uint64_t c2 = pack_f2(c, c);
-                    uint64_t sum[2];
-                    uint32_t pk[32];
-                    // The first half's p from the maximum so far, and the tile's maximum in the
-                    // shadow of its exponentials (MUFU is the busiest unit here); once more in
-                    // the rare case that the maximum has grown too far, and for a first tile.
-                    while (true) {
-                        const float off = m == -INFINITY ? 0.f : -m * c;
-                        const uint64_t off2 = pack_f2(off, off);
+                    // m, and with it l and O (if it holds anything yet), up to this tile's maximum
+                    auto raise = [&](bool have_o) {
                         float mx[4] = {x[0], x[1], x[2], x[3]};
-                        sum[0] = sum[1] = 0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float a, b;
-                            unpack_f2(fma_f2(pack_f2(x[2 * e], x[2 * e + 1]), c2, off2), a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
-                            pk[e] = pack_bf16x2(a, b);
-                            mx[e & 3] = fmaxf(fmaxf(mx[e & 3], x[4 * e]), x[4 * e + 1]);
-                            mx[(e + 2) & 3] = fmaxf(fmaxf(mx[(e + 2) & 3], x[4 * e + 2]), x[4 * e + 3]);
-                        }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        const bool grow = (top - m) * c > kRescaleBits;   // always from -infinity
-                        if (!__any_sync(0xffffffffu, grow)) break;
-                        const float mn = grow ? top : m;
-                        const float f = grow ? ex2((m - mn) * c) : 1.f;   // 0 from -infinity
+                        for (int e = 4; e < 124; e += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(fmaxf(mx[q], x[e + q]), x[e + 4 + q]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[124 + q]);
+                        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                        const float f = mn == m ? 1.f : ex2((m - mn) * c);   // 0 from -infinity
                         m = mn;
                         l *= f;
-                        if (k > 0) {   // O holds the earlier tiles' sums: this tile's S came after them
+                        if (have_o) {
                             float o[32];
 #pragma unroll 1
                             for (int q = 0; q < DP / 32; ++q) {
@@ -639,33 +639,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 tmem_st32(t_o + 32 * q, o);
                             }
                         }
-                    }
-                    tmem_st16(t_s, pk);
-                    tmem_st16(t_s + 16, pk + 16);
-                    const float off = m == -INFINITY ? 0.f : -m * c;
-                    const uint64_t off2 = pack_f2(off, off);
-                    uint32_t pl[32];
-                    auto second = [&](int e) {
+                        return f;
+                    };
+                    uint64_t off2, sum[2];
+                    uint32_t pk[32];
+                    float part[2];
+                    auto reference = [&] {
+                        const float off = m == -INFINITY ? 0.f : -m * c;
+                        off2 = pack_f2(off, off);
+                        sum[0] = sum[1] = 0;
+                    };
+                    auto pair_of = [&](int h, int e) {   // p of keys 64 h + 2 e and the next
                         float a, b;
-                        unpack_f2(fma_f2(pack_f2(x[64 + 2 * e], x[65 + 2 * e]), c2, off2), a, b);
+                        unpack_f2(fma_f2(pack_f2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), c2, off2), a, b);
                         a = ex2(a);
                         b = ex2(b);
                         sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
-                        pl[e] = pack_bf16x2(a, b);
+                        pk[e] = pack_bf16x2(a, b);
                     };
+                    auto total = [&] {
+                        float a, b;
+                        unpack_f2(add_f2(sum[0], sum[1]), a, b);
+                        return a + b;
+                    };
+                    // the first 64 keys
+                    bool fresh = m == -INFINITY && rem > 0;
+                    while (true) {
+                        if (__any_sync(0xffffffffu, fresh)) raise(k > 0);   // S of this tile came after O's products
+                        reference();
 #pragma unroll
-                    for (int e = 0; e < 12; ++e) second(e);   // while the first half's P goes out
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_half[s]);
+                        for (int e = 0; e < 32; ++e) pair_of(0, e);
+                        part[0] = total();
+                        fresh = part[0] > kMostP;
+                        if (!__any_sync(0xffffffffu, fresh)) break;
+                    }
+                    tmem_st16(t_s, pk);
+                    tmem_st16(t_s + 16, pk + 16);
+                    // the other 64, the first ones' P going out meanwhile
+                    bool sent = false;
+                    while (true) {
+                        reference();
 #pragma unroll
-                    for (int e = 12; e < 32; ++e) second(e);
-                    tmem_st16(t_s + 32, pl);
-                    tmem_st16(t_s + 48, pl + 16);
-                    float a0, a1;
-                    unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
-                    l += a0 + a1;
+                        for (int e = 0; e < 32; ++e) {
+                            if (e == 8 && !sent) {
+                                tmem_st_wait();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&p_half[s]);
+                                sent = true;
+                            }
+                            pair_of(1, e);
+                        }
+                        part[1] = total();
+                        if (!__any_sync(0xffffffffu, part[1] > kMostP)) break;
+                        wait(&pv_half[s], (ns - 1) & 1);   // the first half is in O
+                        tc_fence_after();
+                        part[0] *= raise(true);
+                    }
+                    tmem_st16(t_s + 32, pk);
+                    tmem_st16(t_s + 48, pk + 16);
+                    l += part[0] + part[1];
                     tmem_st_wait();
                 } else if (lane == 0) {
                     mbar_arrive(&p_half[s]);

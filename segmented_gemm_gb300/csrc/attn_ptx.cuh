@@ -170,10 +170,10 @@ __device__ __forceinline__ void st_release_shared(int *p, int v)
 {
     asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
-__device__ __forceinline__ int ld_acquire_shared(const int *p)
+__device__ __forceinline__ int ld_volatile_shared(const int *p)
 {
     int v;
-    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    asm volatile("ld.volatile.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
     return v;
 }
 
