@@ -15,7 +15,7 @@
 //               over S's cells (half of them)
 //   O += P V    P from tensor memory, V from shared memory as it was loaded
 //               (its head dimension contiguous: an N-major operand)
-// O stays in tensor memory.  m_i is the maximum of the first tile that the row
+// O stays in tensor memory.  m_i is the maximum of the first half tile that the row
 // sees, and moves on only when half a tile's p sum to more than 2^40: p, l and O
 // are floating point (bf16 has fp32's range), so a larger p costs no precision,
 // and the division by l_i makes any m_i as good as the maximum.  Otherwise a
@@ -39,9 +39,6 @@
 namespace lora {
 
 constexpr int kAttnThreads = 384;
-// registers a thread: 168 at launch; a softmax thread holds a row's 128 scores
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the split draws on the launch's registers");
 constexpr int kItems = 4;             // work items in flight between the loader and the others
 constexpr float kMostP = 0x1p40f;     // half a tile whose p sum to more than this moves m_i
 
@@ -281,7 +278,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 8) {
         // ===================== work and keys ==================================
-        setmaxnreg_dec<kOtherRegs>();
         uint32_t it = 0, nitem = 0;
         const bool cut = hdr.cut != 0;
         int unit = blockIdx.x;
@@ -392,7 +388,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     } else if (warp == 11) {
         // ===================== queries and values =============================
-        setmaxnreg_dec<kOtherRegs>();
         uint32_t it = 0, nitem = 0;
         bool ok = true;
         while (ok) {
@@ -441,7 +436,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // and issuing one takes 35 (66 with a branch around it), so one warp for
         // both streams would be as busy as the tensor cores.  All lanes run the
         // same code and the elected one's instructions take effect.
-        setmaxnreg_dec<kOtherRegs>();
         const int s = warp - 9;
         uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np = 0;
         const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
@@ -567,7 +561,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         wait(end_bar, 0);
     } else {
         // ===================== softmax and results ============================
-        setmaxnreg_inc<kSoftmaxRegs>();
         const int s = warp >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;   // my row of the query tile
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -603,102 +596,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
                 if (live) {
-                    float x[128];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, x + 32 * q);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_use32(x + 32 * q);
-                    if (__any_sync(0xffffffffu, rem < kAttnTileK)) {
-#pragma unroll
-                        for (int e = 0; e < 128; ++e) x[e] = e < rem ? x[e] : -INFINITY;
-                    }
                     const uint64_t c2 = pack_f2(c, c);
-                    // m, and with it l and O (if it holds anything yet), up to this tile's maximum
-                    auto raise = [&](bool have_o) {
-                        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                        for (int e = 4; e < 124; e += 8)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(fmaxf(mx[q], x[e + q]), x[e + 4 + q]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[124 + q]);
-                        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                        const float f = mn == m ? 1.f : ex2((m - mn) * c);   // 0 from -infinity
-                        m = mn;
-                        l *= f;
-                        if (have_o) {
-                            float o[32];
+                    // two halves of 64 keys, so that the first one's products start early
 #pragma unroll 1
-                            for (int q = 0; q < DP / 32; ++q) {
-                                tmem_ld32(t_o + 32 * q, o);
-                                tmem_ld_wait();
-                                tmem_use32(o);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t cells = t_s + 64 * h;
+                        const int seen = rem - 64 * h;   // my visible columns of this half
+                        float x[64];
+                        tmem_ld32(cells, x);
+                        tmem_ld32(cells + 32, x + 32);
+                        if (h == 1) tmem_st_wait();      // the first half's P is in place
+                        tmem_ld_wait();
+                        tmem_use32(x);
+                        tmem_use32(x + 32);
+                        if (h == 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_half[s]);
+                        }
+                        if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= f;
-                                tmem_st32(t_o + 32 * q, o);
+                            for (int e = 0; e < 64; ++e) x[e] = e < seen ? x[e] : -INFINITY;
+                        }
+                        uint32_t pk[32];
+                        bool move = m == -INFINITY && seen > 0;
+                        while (true) {
+                            if (__any_sync(0xffffffffu, move)) {
+                                // m, and with it l and O, up to this half's maximum.  O holds the tiles
+                                // before this one, and the first half of this one once the second is here.
+                                if (h == 1) {
+                                    wait(&pv_half[s], (ns - 1) & 1);
+                                    tc_fence_after();
+                                }
+                                float mn = m, y[32];
+#pragma unroll 1
+                                for (int q = 0; q < 2; ++q) {
+                                    tmem_ld32(cells + 32 * q, y);
+                                    tmem_ld_wait();
+                                    tmem_use32(y);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) mn = fmaxf(mn, e < seen - 32 * q ? y[e] : -INFINITY);
+                                }
+                                const float f = mn == m ? 1.f : ex2((m - mn) * c);   // 0 from -infinity
+                                m = mn;
+                                l *= f;
+#pragma unroll 1
+                                for (int q = 0; q < (k + h > 0 ? DP / 32 : 0); ++q) {
+                                    tmem_ld32(t_o + 32 * q, y);
+                                    tmem_ld_wait();
+                                    tmem_use32(y);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) y[e] *= f;
+                                    tmem_st32(t_o + 32 * q, y);
+                                }
+                            }
+                            const float off = m == -INFINITY ? 0.f : -m * c;
+                            const uint64_t off2 = pack_f2(off, off);
+                            uint64_t sum[2] = {0, 0};
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float a, b;
+                                unpack_f2(fma_f2(pack_f2(x[2 * e], x[2 * e + 1]), c2, off2), a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
+                                pk[e] = pack_bf16x2(a, b);
+                            }
+                            float a, b;
+                            unpack_f2(add_f2(sum[0], sum[1]), a, b);
+                            move = a + b > kMostP;
+                            if (!__any_sync(0xffffffffu, move)) {
+                                l += a + b;
+                                break;
                             }
                         }
-                        return f;
-                    };
-                    uint64_t off2, sum[2];
-                    uint32_t pk[32];
-                    float part[2];
-                    auto reference = [&] {
-                        const float off = m == -INFINITY ? 0.f : -m * c;
-                        off2 = pack_f2(off, off);
-                        sum[0] = sum[1] = 0;
-                    };
-                    auto pair_of = [&](int h, int e) {   // p of keys 64 h + 2 e and the next
-                        float a, b;
-                        unpack_f2(fma_f2(pack_f2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), c2, off2), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
-                        pk[e] = pack_bf16x2(a, b);
-                    };
-                    auto total = [&] {
-                        float a, b;
-                        unpack_f2(add_f2(sum[0], sum[1]), a, b);
-                        return a + b;
-                    };
-                    // the first 64 keys
-                    bool fresh = m == -INFINITY && rem > 0;
-                    while (true) {
-                        if (__any_sync(0xffffffffu, fresh)) raise(k > 0);   // S of this tile came after O's products
-                        reference();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) pair_of(0, e);
-                        part[0] = total();
-                        fresh = part[0] > kMostP;
-                        if (!__any_sync(0xffffffffu, fresh)) break;
+                        tmem_st16(t_s + 32 * h, pk);
+                        tmem_st16(t_s + 32 * h + 16, pk + 16);
                     }
-                    tmem_st16(t_s, pk);
-                    tmem_st16(t_s + 16, pk + 16);
-                    // the other 64, the first ones' P going out meanwhile
-                    bool sent = false;
-                    while (true) {
-                        reference();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (e == 8 && !sent) {
-                                tmem_st_wait();
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&p_half[s]);
-                                sent = true;
-                            }
-                            pair_of(1, e);
-                        }
-                        part[1] = total();
-                        if (!__any_sync(0xffffffffu, part[1] > kMostP)) break;
-                        wait(&pv_half[s], (ns - 1) & 1);   // the first half is in O
-                        tc_fence_after();
-                        part[0] *= raise(true);
-                    }
-                    tmem_st16(t_s + 32, pk);
-                    tmem_st16(t_s + 48, pk + 16);
-                    l += part[0] + part[1];
                     tmem_st_wait();
                 } else if (lane == 0) {
                     mbar_arrive(&p_half[s]);

@@ -74,18 +74,6 @@ __device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t *bar)
 // A value that is the same in all lanes, told to the compiler.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Registers of the calling warpgroup (all four of its warps call).
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Instruction descriptor as umma_idesc_bf16, with B stored N-major (its N
 // elements contiguous).
 __device__ __forceinline__ uint32_t umma_idesc_bf16_bn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
