@@ -208,7 +208,8 @@ int lora_attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *cache, const
 /*
  * Causal attention over whole prompts packed one after another: request r's
  * queries, keys and values are rows [cu[r], cu[r+1]).  k, v: DEVICE bf16 like
- * q, with kv_heads heads.  sched: built with kv_len NULL, or NULL.
+ * q, with kv_heads heads.  sched: built with kv_len NULL, or NULL (the list of a
+ * few short prompts is then made by the attention kernel itself).
  */
 int lora_attn_prompt(const lora_attn_t *attn, const lora_bf16_t *k, int64_t k_token_stride, int64_t k_head_stride,
                      const lora_bf16_t *v, int64_t v_token_stride, int64_t v_head_stride,

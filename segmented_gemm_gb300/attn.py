@@ -15,10 +15,12 @@ permuted view of any order whose last dimension is contiguous fits).
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
 
+from . import lora as _lora
 from .lora import LORA_OK, LoraError, load_library
 
 LORA_DEV_BAD_LENGTH, LORA_DEV_NO_PAGE, LORA_DEV_BAD_PAGE = 1 << 8, 1 << 9, 1 << 10
@@ -53,28 +55,38 @@ class lora_attn_sched_t(ctypes.Structure):
                 ("kv_heads", _I32), ("head_dim", _I32), ("prompt", _I32)]
 
 
+# The same structures as packed bytes: a decode step makes a handful of these
+# calls a layer, and a ctypes structure costs twice as much to fill.
+_CACHE = struct.Struct("@QQqqqiiii")
+_PLAN = struct.Struct("@QQQi4xQi4xqQi4xQiiqQQQQQQ")
+_ATTN = struct.Struct("@QQQQqqqqqiiiif4x")
+assert (_CACHE.size, _PLAN.size, _ATTN.size) == tuple(
+    ctypes.sizeof(t) for t in (lora_kv_cache_t, lora_kv_plan_t, lora_attn_t))
+
+_BF16, _I32T, _F32 = torch.bfloat16, torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _bound = {}
 
 
 def _lib():
-    lib = load_library()
-    f = _bound.get(lib._name)
-    if f is None:
-        VP, CP = ctypes.c_void_p, ctypes.c_void_p   # structures go by address
+    lib = _bound.get(_lora._active)
+    if lib is None:
+        lib = load_library()
+        VP = ctypes.c_void_p   # structures go by address
         sig = {
             "lora_kv_plan": (ctypes.c_int, [VP, _P, _SZ, _P]),
-            "lora_kv_store": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64, CP, _P, _P, _SZ, _P]),
+            "lora_kv_store": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64, VP, _P, _P, _SZ, _P]),
             "lora_attn_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
             "lora_attn_schedule": (ctypes.c_int, [_P, _P, _I32, _I64, _I64, _I32, _I32, _I32, VP, _P, _SZ, _P]),
-            "lora_attn_paged": (ctypes.c_int, [VP, CP, _P, _I32, _I64, _P, VP, _P, _SZ, _P]),
+            "lora_attn_paged": (ctypes.c_int, [VP, VP, _P, _I32, _I64, _P, VP, _P, _SZ, _P]),
             "lora_attn_prompt": (ctypes.c_int, [VP, _P, _I64, _I64, _P, _I64, _I64, VP, _P, _SZ, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        f = _bound[lib._name] = lib
-    return f
+        _bound[_lora._active] = lib
+    return lib
 
 
 def _check(code: int, where: str):
@@ -82,24 +94,39 @@ def _check(code: int, where: str):
         raise LoraError(code, where)
 
 
-def _raw_stream(t: torch.Tensor, stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _need(t: torch.Tensor, dtype, ndim: int, name: str):
-    if t.dtype != dtype or t.dim() != ndim or not t.is_cuda:
-        raise ValueError(f"{name}: a {ndim}-dimensional {dtype} tensor on the device")
-
-
-def _ints(t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
-    """The address of a contiguous device int32 vector of at least n entries."""
+def _ints(t: Optional[torch.Tensor], n: int, name: str) -> int:
+    """The address of a contiguous device int32 vector of at least n entries (0 for None)."""
     if t is None:
-        return None
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        return 0
+    if t.dtype is not _I32T or not t.is_cuda or t.ndim != 1 or t.shape[0] < n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 vector of {n} entries on the device")
     return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Shape and (token, head) strides of [tokens, heads, head_dim] bf16 on the device."""
+    shape, s = t.shape, t.stride()
+    if len(s) != 3 or s[2] != 1 or t.dtype is not _BF16 or not t.is_cuda:
+        raise ValueError(f"{name}: [tokens, heads, head_dim] bfloat16 on the device, the last dimension contiguous")
+    return shape, s
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """The packed lora_kv_cache_t, and its shape."""
+    shape, s = k_cache.shape, k_cache.stride()
+    if (len(s) != 4 or s[3] != 1 or v_cache.shape != shape or v_cache.stride() != s or k_cache.dtype is not _BF16 or
+            v_cache.dtype is not _BF16 or not k_cache.is_cuda or not v_cache.is_cuda):
+        raise ValueError("k_cache, v_cache: bfloat16 [pages, kv_heads, page_size, head_dim] on the device, of equal "
+                         "strides, the last dimension contiguous")
+    n, h, p, d = shape
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), s[0], s[1], s[2], n, p, h, d), shape
+
+
+def _table(t: torch.Tensor, R: int):
+    shape, s = t.shape, t.stride()
+    if len(s) != 2 or shape[0] < R or (shape[1] > 1 and s[1] != 1) or t.dtype is not _I32T or not t.is_cuda:
+        raise ValueError("block_table: int32 on the device, a contiguous row a request")
+    return shape[1], s[0]
 
 
 def lora_attn_workspace_size(T: int, R: int, heads: int = 0, kv_heads: int = 0, head_dim: int = 0) -> int:
@@ -116,10 +143,11 @@ class AttnWorkspace:
         if self.nbytes == 0:
             raise ValueError("AttnWorkspace: token, request or head counts out of range")
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        self.addr = self.buf.data_ptr()
 
     @property
     def ptr(self):
-        return ctypes.c_void_p(self.buf.data_ptr())
+        return ctypes.c_void_p(self.addr)
 
 
 class KvPlan:
@@ -145,51 +173,33 @@ def lora_kv_plan(new_len: torch.Tensor, ctx_len: torch.Tensor, block_table: torc
         if max_tokens is None:
             raise ValueError("lora_kv_plan: out or max_tokens")
         out = KvPlan(max_tokens, R, new_len.device)
-    _need(block_table, torch.int32, 2, "block_table")
-    if block_table.shape[0] != R or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or out.num_requests != R:
-        raise ValueError("lora_kv_plan: one table row and one output a request, rows contiguous")
-    T = out.max_tokens
-    a = lora_kv_plan_t(
-        _ints(new_len, R, "new_len"), _ints(ctx_len, R, "ctx_len"), _ints(req_adapter, R, "req_adapter"), R,
-        block_table.data_ptr(), block_table.shape[1], block_table.stride(0),
-        _ints(free_pages, 0, "free_pages"), free_pages.shape[0], _ints(free_head, 1, "free_head"), page_size, num_pages,
-        T, out.cu_new.data_ptr(), out.kv_len.data_ptr(), out.slot_map.data_ptr(), out.position.data_ptr(),
-        out.lora_id_map.data_ptr() if req_adapter is not None else None, out.free_head.data_ptr())
-    _check(_lib().lora_kv_plan(ctypes.addressof(a), ws.buf.data_ptr(), ws.nbytes, _raw_stream(new_len, stream)),
+    width, row = _table(block_table, R)
+    if out.num_requests != R:
+        raise ValueError("lora_kv_plan: out was made for another number of requests")
+    a = _PLAN.pack(_ints(new_len, R, "new_len"), _ints(ctx_len, R, "ctx_len"), _ints(req_adapter, R, "req_adapter"), R,
+                   block_table.data_ptr(), width, row, _ints(free_pages, 0, "free_pages"), free_pages.shape[0],
+                   _ints(free_head, 1, "free_head"), page_size, num_pages, out.max_tokens, out.cu_new.data_ptr(),
+                   out.kv_len.data_ptr(), out.slot_map.data_ptr(), out.position.data_ptr(),
+                   0 if req_adapter is None else out.lora_id_map.data_ptr(), out.free_head.data_ptr())
+    _check(_lib().lora_kv_plan(a, ws.addr, ws.nbytes,
+                               _raw_stream(new_len.get_device()) if stream is None else stream.cuda_stream),
            "lora_kv_plan")
     return out
-
-
-def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> lora_kv_cache_t:
-    _need(k_cache, torch.bfloat16, 4, "k_cache")
-    _need(v_cache, torch.bfloat16, 4, "v_cache")
-    s = k_cache.stride()
-    if v_cache.shape != k_cache.shape or v_cache.stride() != s or s[3] != 1:
-        raise ValueError("k_cache, v_cache: [pages, kv_heads, page_size, head_dim] of equal strides, last contiguous")
-    n, h, p, d = k_cache.shape
-    return lora_kv_cache_t(k_cache.data_ptr(), v_cache.data_ptr(), s[0], s[1], s[2], n, p, h, d)
-
-
-def _rows(t: torch.Tensor, name: str):
-    """[tokens, heads, head_dim] bf16: token and head strides."""
-    _need(t, torch.bfloat16, 3, name)
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}: the head dimension must be contiguous")
-    return s[0], s[1]
 
 
 def lora_kv_store(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   slot_map: torch.Tensor, ws: AttnWorkspace, stream=None):
     """Write k, v [T, kv_heads, head_dim] into the cache's slots slot_map [T]
     (-1: skipped)."""
-    c = _cache(k_cache, v_cache)
-    ks, vs = _rows(k, "k"), _rows(v, "v")
-    if v.shape != k.shape or k.shape[1] != c.kv_heads or k.shape[2] != c.head_dim:
+    c, (_, heads, _, dim) = _cache(k_cache, v_cache)
+    shape, ks = _rows(k, "k")
+    v_shape, vs = _rows(v, "v")
+    if v_shape != shape or shape[1] != heads or shape[2] != dim:
         raise ValueError("lora_kv_store: k and v are [T, kv_heads, head_dim] of the cache")
-    _check(_lib().lora_kv_store(k.data_ptr(), v.data_ptr(), k.shape[0], ks[0], ks[1], vs[0], vs[1], ctypes.addressof(c),
-                                _ints(slot_map, k.shape[0], "slot_map"), ws.buf.data_ptr(), ws.nbytes,
-                                _raw_stream(k, stream)), "lora_kv_store")
+    T = shape[0]
+    _check(_lib().lora_kv_store(k.data_ptr(), v.data_ptr(), T, ks[0], ks[1], vs[0], vs[1], c,
+                                _ints(slot_map, T, "slot_map"), ws.addr, ws.nbytes,
+                                _raw_stream(k.get_device()) if stream is None else stream.cuda_stream), "lora_kv_store")
 
 
 def lora_attn_schedule(cu: torch.Tensor, kv_len: Optional[torch.Tensor], T: int, max_kv: int, heads: int, kv_heads: int,
@@ -198,27 +208,30 @@ def lora_attn_schedule(cu: torch.Tensor, kv_len: Optional[torch.Tensor], T: int,
     prompts, max_kv = T), built in ws; it serves every layer of the step."""
     R = cu.shape[0] - 1
     out = lora_attn_sched_t()
-    _check(_lib().lora_attn_schedule(_ints(cu, 1, "cu"), _ints(kv_len, R, "kv_len"), R, T, max_kv, heads, kv_heads,
-                                     head_dim, ctypes.addressof(out), ws.buf.data_ptr(), ws.nbytes,
-                                     _raw_stream(cu, stream)), "lora_attn_schedule")
+    _check(_lib().lora_attn_schedule(_ints(cu, 1, "cu"), _ints(kv_len, R, "kv_len") or None, R, T, max_kv, heads,
+                                     kv_heads, head_dim, ctypes.addressof(out), ws.addr, ws.nbytes,
+                                     _raw_stream(cu.get_device()) if stream is None else stream.cuda_stream),
+           "lora_attn_schedule")
+    out.addr = ctypes.addressof(out)
     return out
 
 
-def _attn(q, kv_heads, cu, scale, o, lse):
-    qs = _rows(q, "q")
-    T, H, D = q.shape
+def _attn(q, kv_heads, cu, R, scale, o, lse):
+    """The packed lora_attn_t, and o."""
+    shape, qs = _rows(q, "q")
     if o is None:
-        o = torch.empty(T, H, D, dtype=torch.bfloat16, device=q.device)
-    os_ = _rows(o, "o")
-    if o.shape != q.shape:
+        o = torch.empty(shape, dtype=_BF16, device=q.device)
+    o_shape, os_ = _rows(o, "o")
+    if o_shape != shape:
         raise ValueError("o: the shape of q")
-    lp = None
+    T, H, D = shape
+    lp = 0
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous() or not lse.is_cuda:
+        if lse.dtype is not _F32 or lse.shape != (T, H) or not lse.is_contiguous() or not lse.is_cuda:
             raise ValueError("lse: contiguous float32 [tokens, heads] on the device")
         lp = lse.data_ptr()
-    return lora_attn_t(q.data_ptr(), o.data_ptr(), lp, _ints(cu, 1, "cu"), qs[0], qs[1], os_[0], os_[1], T,
-                       cu.shape[0] - 1, H, kv_heads, D, scale), o
+    return _ATTN.pack(q.data_ptr(), o.data_ptr(), lp, _ints(cu, 1, "cu"), qs[0], qs[1], os_[0], os_[1], T, R, H, kv_heads,
+                      D, scale), o
 
 
 def lora_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -228,16 +241,16 @@ def lora_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of the step's new tokens q [T, heads, head_dim] over the
     paged cache: rows [cu[r], cu[r+1]) against request r's kv_len[r] keys,
     causal.  ``lse``: fp32 [T, heads], written when given."""
-    c = _cache(k_cache, v_cache)
-    a, o = _attn(q, c.kv_heads, cu, scale, o, lse)
-    _need(block_table, torch.int32, 2, "block_table")
-    if (block_table.shape[0] < a.num_requests or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or
-            a.head_dim != c.head_dim):
-        raise ValueError("lora_attn_paged: one contiguous table row a request, and the cache's head dimension")
-    _check(_lib().lora_attn_paged(ctypes.addressof(a), ctypes.addressof(c), block_table.data_ptr(),
-                                  block_table.shape[1], block_table.stride(0), _ints(kv_len, a.num_requests, "kv_len"),
-                                  None if sched is None else ctypes.addressof(sched), ws.buf.data_ptr(), ws.nbytes,
-                                  _raw_stream(q, stream)), "lora_attn_paged")
+    c, (_, kv_heads, _, dim) = _cache(k_cache, v_cache)
+    R = cu.shape[0] - 1
+    a, o = _attn(q, kv_heads, cu, R, scale, o, lse)
+    width, row = _table(block_table, R)
+    if q.shape[2] != dim:
+        raise ValueError("lora_attn_paged: q and the cache have the same head dimension")
+    _check(_lib().lora_attn_paged(a, c, block_table.data_ptr(), width, row, _ints(kv_len, R, "kv_len"),
+                                  None if sched is None else sched.addr, ws.addr, ws.nbytes,
+                                  _raw_stream(q.get_device()) if stream is None else stream.cuda_stream),
+           "lora_attn_paged")
     return o
 
 
@@ -246,11 +259,13 @@ def lora_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torc
                      lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention over packed prompts: q [T, heads, head_dim], k and v
     [T, kv_heads, head_dim], request r's rows [cu[r], cu[r+1])."""
-    ks, vs = _rows(k, "k"), _rows(v, "v")
-    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError("lora_attn_prompt: k and v are [T, kv_heads, head_dim]")
-    a, o = _attn(q, k.shape[1], cu, scale, o, lse)
-    _check(_lib().lora_attn_prompt(ctypes.addressof(a), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                                   None if sched is None else ctypes.addressof(sched), ws.buf.data_ptr(), ws.nbytes,
-                                   _raw_stream(q, stream)), "lora_attn_prompt")
+    shape, ks = _rows(k, "k")
+    v_shape, vs = _rows(v, "v")
+    if v_shape != shape or shape[0] != q.shape[0] or shape[2] != q.shape[2]:
+        raise ValueError("lora_attn_prompt: k and v are [T, kv_heads, head_dim] with q's tokens and head dimension")
+    a, o = _attn(q, shape[1], cu, cu.shape[0] - 1, scale, o, lse)
+    _check(_lib().lora_attn_prompt(a, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                   None if sched is None else sched.addr, ws.addr, ws.nbytes,
+                                   _raw_stream(q.get_device()) if stream is None else stream.cuda_stream),
+           "lora_attn_prompt")
     return o

@@ -94,6 +94,8 @@ struct AttnParams {
     int32_t box_rows;        // keys of one TMA box
     int64_t T;
     int32_t requests;
+    int32_t short_list;      // 1: the list is made from cu in the kernel (hdr and blocks are not read)
+    const int32_t *cu;
     int32_t ctas;
     float *part;             // [2 * kAttnMaxCtas][part_rows][head_dim] partial O
     float2 *part_ml;         // [2 * kAttnMaxCtas][part_rows] partial (m, l)

@@ -132,12 +132,14 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     const AttnLayout L = make_layout(a->num_tokens, a->num_requests, a->heads, a->kv_heads, a->head_dim);
     const int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
+    const int ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
+    const bool short_list = !sched && !kv_len && a->num_requests <= 32 && L.max_blocks * a->kv_heads <= 2 * ctas;
     if (sched) {
         if (sched->plan != ws || sched->num_tokens != a->num_tokens || sched->num_requests != a->num_requests ||
             sched->heads != a->heads || sched->kv_heads != a->kv_heads || sched->head_dim != a->head_dim ||
             sched->max_kv > max_kv || sched->prompt != (kv_len ? 0 : 1))
             return LORA_ERR_SEGMENTS;
-    } else {
+    } else if (!short_list) {
         const int e = enqueue_schedule(a->cu, kv_len, a->num_requests, a->num_tokens, max_kv, a->kv_heads, a->head_dim,
                                        L, ws, stream);
         if (e) return e;
@@ -162,7 +164,9 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->counters = at<int32_t>(ws, L.counters);
     p->T = a->num_tokens;
     p->requests = a->num_requests;
-    p->ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
+    p->short_list = short_list;
+    p->cu = a->cu;
+    p->ctas = ctas;
     p->part = at<float>(ws, L.part);
     p->part_ml = at<float2>(ws, L.part_ml);
     p->part_rows = L.part_rows;
