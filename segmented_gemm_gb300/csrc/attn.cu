@@ -15,6 +15,9 @@
 //               over S's cells (half of them)
 //   O += P V    P from tensor memory, V from shared memory as it was loaded
 //               (its head dimension contiguous: an N-major operand)
+// With up to 16 rows (a decoded token, or a few) a thread per row would leave all
+// but a few lanes idle over 128 keys each: there the four lanes of a quad share
+// a row (tensor memory loads of 16 lanes x 256 bits), 32 keys each.
 // O stays in tensor memory.  m_i is the maximum of the first half tile that the row
 // sees, and moves on only when half a tile's p sum to more than 2^40: p, l and O
 // are floating point (bf16 has fp32's range), so a larger p costs no precision,
@@ -202,7 +205,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qbuf = smem, *ring = smem + 2 * kTile;
-    float2 *stats = reinterpret_cast<float2 *>(smem + Sm::kStats);   // stream 1's (m, l), single items
+    // single items: stream 1's (m, l) by row; narrow ones: stream 0's too, from entry 64 on
+    float2 *stats = reinterpret_cast<float2 *>(smem + Sm::kStats);
     AttnItem *items = reinterpret_cast<AttnItem *>(smem + Sm::kItem);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Sm::kBars), *empty = full + kStages;
     uint64_t *item_full = empty + kStages, *item_empty = item_full + kItems;
@@ -650,13 +654,110 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool row_ok = i < p.tq && tok < w.ntok;
             const int limit = row_ok ? max(0, min(w.kv_len, w.qpos0 + tok + 1)) : 0;
             const bool live = __any_sync(0xffffffffu, limit > 0);
+            const bool narrow = !w.pair && w.ntok * G <= 16, two = w.ntok * G > 8;   // two: rows past the eighth
             float m = -INFINITY, l = 0.f;
+            // narrow: rows lane / 4 and 8 more, of which this lane has keys 8 j + 2 (lane % 4) and the next
+            float nm[2] = {-INFINITY, -INFINITY}, nl[2] = {0.f, 0.f};
+            int nlim[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = ((lane >> 2) + 8 * h) / G;
+                nlim[h] = t < w.ntok ? max(0, min(w.kv_len, w.qpos0 + t + 1)) : 0;
+            }
             for (int k = 0; k < mine_n; ++k) {
                 const int tile = w.pair ? w.t0 + k : w.t0 + s + 2 * k;
                 const int rem = limit - tile * kAttnTileK;   // my visible columns of this tile
                 if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
-                if (live) {
+                if (narrow && live) {
+                    const uint64_t c2 = pack_f2(c, c);
+                    const int first = 2 * (lane & 3);
+                    int see[2];   // visible columns, from my first on
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) see[h] = nlim[h] - tile * kAttnTileK - first;
+                    float x[64];   // x[4 j + 2 h + e]: row 8 h + lane / 4, key 8 j + first + e
+                    tmem_ld_16x256(t_s, x);
+                    tmem_ld_wait();
+                    tmem_use32(x);
+                    tmem_use32(x + 32);
+                    if (__any_sync(0xffffffffu, see[0] + first < kAttnTileK || (two && see[1] + first < kAttnTileK))) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 1 && !two) continue;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    x[4 * j + 2 * h + e] = 8 * j + e < see[h] ? x[4 * j + 2 * h + e] : -INFINITY;
+                        }
+                    }
+                    uint32_t pk[32];
+                    bool move = (nm[0] == -INFINITY && see[0] + first > 0) || (two && nm[1] == -INFINITY && see[1] + first > 0);
+                    for (int round = 0;; ++round) {
+                        if (__any_sync(0xffffffffu, move)) {
+                            float f[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                f[h] = 1.f;
+                                if (h == 1 && !two) continue;
+                                float mn = nm[h];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) mn = fmaxf(fmaxf(mn, x[4 * j + 2 * h]), x[4 * j + 2 * h + 1]);
+                                mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+                                mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+                                f[h] = mn == nm[h] ? 1.f : ex2((nm[h] - mn) * c);
+                                nm[h] = mn;
+                                nl[h] *= f[h];
+                            }
+#pragma unroll 1
+                            for (int q = 0; q < (k > 0 ? DP / 64 : 0); ++q) {
+                                float y[32];
+                                tmem_ld_16x256_half(t_o + 64 * q, y);
+                                tmem_ld_wait();
+                                tmem_use32(y);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) y[e] *= f[(e >> 1) & 1];
+                                tmem_st_16x256_half(t_o + 64 * q, y);
+                            }
+                        }
+                        float part[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            part[h] = 0.f;
+                            if (h == 1 && !two) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) pk[2 * j + 1] = 0;
+                                continue;
+                            }
+                            const float off = nm[h] == -INFINITY ? 0.f : -nm[h] * c;
+                            const uint64_t off2 = pack_f2(off, off);
+                            uint64_t sum[2] = {0, 0};
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float a, b;
+                                unpack_f2(fma_f2(pack_f2(x[4 * j + 2 * h], x[4 * j + 2 * h + 1]), c2, off2), a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                sum[j & 1] = add_f2(sum[j & 1], pack_f2(a, b));
+                                pk[2 * j + h] = pack_bf16x2(a, b);
+                            }
+                            float a, b;
+                            unpack_f2(add_f2(sum[0], sum[1]), a, b);
+                            part[h] = a + b;
+                        }
+                        move = part[0] > kMostP || part[1] > kMostP;
+                        if (round == 1 || !__any_sync(0xffffffffu, move)) {
+                            nl[0] += part[0];
+                            nl[1] += part[1];
+                            break;
+                        }
+                    }
+                    tmem_st_16x128(t_s, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_half[s]);
+                } else if (live) {
                     const uint64_t c2 = pack_f2(c, c);
                     // two halves of 64 keys, so that the first one's products start early
 #pragma unroll 1
@@ -681,7 +782,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         uint32_t pk[32];
                         bool move = m == -INFINITY && seen > 0;
-                        while (true) {
+                        for (int round = 0;; ++round) {   // again if the sum asks for it: after a move it cannot
                             if (__any_sync(0xffffffffu, move)) {
                                 // m, and with it l and O, up to this half's maximum.  O holds the tiles
                                 // before this one, and the first half of this one once the second is here.
@@ -726,7 +827,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
                             move = a + b > kMostP;
-                            if (!__any_sync(0xffffffffu, move)) {
+                            if (round == 1 || !__any_sync(0xffffffffu, move)) {
                                 l += a + b;
                                 break;
                             }
@@ -752,10 +853,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (mine_n > 0) wait(&o_full[s], no++ & 1);
             if (!w.pair) {
                 // both streams worked on the same rows: stream 0's threads join them
-                if (s == 1) stats[r] = make_float2(m, l);
+                if (narrow) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        nl[h] += __shfl_xor_sync(0xffffffffu, nl[h], 1);
+                        nl[h] += __shfl_xor_sync(0xffffffffu, nl[h], 2);
+                        if (quad == 0 && (lane & 3) == 0)
+                            stats[(s ? 0 : 64) + (lane >> 2) + 8 * h] = make_float2(nm[h], nl[h]);
+                    }
+                } else if (s == 1) {
+                    stats[r] = make_float2(m, l);
+                }
                 meet();
                 if (s == 0) {
-                    const float2 st = stats[r];
+                    if (narrow) {
+                        const float2 own = stats[64 + (r & 15)];
+                        m = own.x;
+                        l = own.y;
+                        use0 = l != 0.f;
+                    }
+                    const float2 st = stats[narrow ? r & 15 : r];
                     const float mm = fmaxf(m, st.x);
                     use1 = st.y != 0.f;
                     f0 = use0 ? ex2((m - mm) * c) : 0.f;

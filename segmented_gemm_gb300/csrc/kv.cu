@@ -19,13 +19,16 @@ namespace lora {
 // before_r is increasing, so the served requests that need pages are a prefix
 // and take free pages [head, head + before_r + need_r) without gaps.
 //
-// A few KB in all: launch latency bounds it.  So it is one launch without any
+// A few hundred KB at most: latency bounds it.  So it is one launch without any
 // exchange between CTAs: every CTA scans all lengths (at most 4096, in shared
-// memory) for itself, then takes its share of the tokens and of the new table
-// entries.  A token whose page is new in this call computes the page from the
-// scan instead of reading the table that another CTA may be writing.
+// memory, a run of consecutive requests a thread) for itself, then takes its
+// share of the tokens and of the new table entries.  A token whose page is new
+// in this call computes the page from the scan instead of reading the table that
+// another CTA may be writing.  One or two tokens a thread: a token costs a
+// search of its request (ten dependent shared loads for 777 requests), and with
+// eight a thread those searches were most of the time (13.7 us for 38 K tokens).
 constexpr int kPlanThreads = 256;
-constexpr int kPlanTokens = 2048;   // tokens a CTA takes at least, so that small steps stay in few CTAs
+constexpr int kPlanTokens = 512;   // tokens of a CTA, more only when all SMs have some
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParams prm)
 {
@@ -33,97 +36,65 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     const lora_kv_plan_t &a = prm.a;
     extern __shared__ int32_t sm[];
     const int R = a.num_requests;
-    int32_t *cu = sm;              // [R + 1]
+    int32_t *cu = sm;              // [R + 1] new tokens of a request, then the offsets
     int32_t *before = cu + R + 1;  // [R + 1] pages needed by the requests before r
     int32_t *ctx = before + R + 1; // [R]
     __shared__ int64_t wsum[32];
     const int tid = threadIdx.x;
     const int P = a.page_size, shift = __ffs(P) - 1;
     const int64_t cap = static_cast<int64_t>(a.table_width) << shift;
+    const int run = (R + kPlanThreads - 1) / kPlanThreads, r0 = min(R, tid * run), r1 = min(R, r0 + run);
     pdl_wait();
 
+    const int32_t head0 = *a.free_head;
     int bad = 0, missing = 0;
+#pragma unroll 4
+    for (int r = tid; r < R; r += kPlanThreads) {
+        const int n0 = a.new_len[r], c0 = a.ctx_len[r];
+        const int64_t c = c0 < 0 ? 0 : c0 > cap ? cap : c0;
+        const int64_t n = n0 < 0 ? 0 : n0 > cap - c ? cap - c : n0;
+        bad |= (c != c0) | (n != n0);
+        ctx[r] = static_cast<int32_t>(c);
+        cu[r] = static_cast<int32_t>(n);
+    }
+    __syncthreads();
     // packed offsets: at most max_tokens in all
-    int64_t carry = 0;
-    for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
-        const int r = r0 + tid;
-        int64_t n = 0;
-        if (r < R) {
-            const int n0 = a.new_len[r], c0 = a.ctx_len[r];
-            const int64_t c = c0 < 0 ? 0 : c0 > cap ? cap : c0;
-            n = n0 < 0 ? 0 : n0 > cap - c ? cap - c : n0;
-            bad |= (c != c0) | (n != n0);
-            ctx[r] = static_cast<int32_t>(c);
-        }
-        int64_t total;
-        const int64_t ex = carry + block_scan_i64(n, wsum, &total);
-        if (r < R) cu[r] = static_cast<int32_t>(ex < a.max_tokens ? ex : a.max_tokens);
-        carry += total;
+    int64_t sum = 0, total;
+    for (int r = r0; r < r1; ++r) sum += cu[r];
+    int64_t at = block_scan_i64(sum, wsum, &total);
+    for (int r = r0; r < r1; ++r) {
+        const int32_t n = cu[r];
+        cu[r] = static_cast<int32_t>(at < a.max_tokens ? at : a.max_tokens);
+        at += n;
     }
-    if (tid == 0) cu[R] = static_cast<int32_t>(carry < a.max_tokens ? carry : a.max_tokens);
-    bad |= carry > a.max_tokens;
+    if (tid == 0) cu[R] = static_cast<int32_t>(total < a.max_tokens ? total : a.max_tokens);
+    bad |= total > a.max_tokens;
     __syncthreads();
-    // pages needed: below 2^31 in all unless the free list is short of them anyway
-    const int32_t head = max(0, min(*a.free_head, a.num_free));
-    bad |= head != *a.free_head;
+    // pages needed, saturated one above what the list can serve: such a request is not served
+    const int32_t head = max(0, min(head0, a.num_free));
+    bad |= head != head0;
     const int32_t left = a.num_free - head;
-    carry = 0;
-    for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
-        const int r = r0 + tid;
-        int64_t need = 0;
-        if (r < R) {
-            const int64_t c = ctx[r], n = cu[r + 1] - cu[r];
-            need = ((c + n + P - 1) >> shift) - ((c + P - 1) >> shift);
-        }
-        int64_t total;
-        const int64_t ex = carry + block_scan_i64(need, wsum, &total);
-        // saturated one above what the list can serve: such a request is not served
-        const int64_t lim = static_cast<int64_t>(left) + 1;
-        if (r < R) {
-            before[r] = static_cast<int32_t>(ex < lim ? ex : lim);
-            missing |= need > 0 && ex + need > left;
-        }
-        carry += total;
-    }
-    if (tid == 0) before[R] = static_cast<int32_t>(carry < left + int64_t(1) ? carry : left + int64_t(1));
-    __syncthreads();
-
+    const int64_t lim = static_cast<int64_t>(left) + 1;
     auto need_of = [&](int r) {
         const int64_t c = ctx[r], n = cu[r + 1] - cu[r];
         return static_cast<int32_t>(((c + n + P - 1) >> shift) - ((c + P - 1) >> shift));
     };
+    sum = 0;
+    for (int r = r0; r < r1; ++r) sum += need_of(r);
+    at = block_scan_i64(sum, wsum, &total);
+    for (int r = r0; r < r1; ++r) {
+        const int32_t need = need_of(r);
+        before[r] = static_cast<int32_t>(at < lim ? at : lim);
+        missing |= need > 0 && at + need > left;
+        at += need;
+    }
+    if (tid == 0) before[R] = static_cast<int32_t>(total < lim ? total : lim);
+    __syncthreads();
+
     auto served = [&](int r, int32_t need) { return need == 0 || static_cast<int64_t>(before[r]) + need <= left; };
 
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-    // per request
-    int32_t taken = 0;
-    for (int r = tid; r < R; r += kPlanThreads) {
-        const int32_t need = need_of(r);
-        const bool ok = served(r, need);
-        if (ok) taken += need;
-        if (r % gridDim.x == blockIdx.x) {
-            a.cu_new[r] = cu[r];
-            a.kv_len[r] = ok ? ctx[r] + cu[r + 1] - cu[r] : 0;
-        }
-    }
-    if (blockIdx.x == 0) {
-        int64_t total;
-        block_scan_i64(taken, wsum, &total);
-        if (tid == 0) {
-            a.cu_new[R] = cu[R];
-            *a.free_head_out = head + static_cast<int32_t>(total);
-        }
-    }
-    // new table entries: entry e is one of the pages the served requests take
-    const int64_t entries = before[R] < left ? before[R] : left;
-    for (int64_t e = gid; e < entries; e += stride) {
-        const int r = last_le(before, R, static_cast<int32_t>(e));
-        const int32_t need = need_of(r);
-        if (!served(r, need)) continue;
-        const int64_t col = ((static_cast<int64_t>(ctx[r]) + P - 1) >> shift) + (e - before[r]);
-        a.block_table[r * a.table_stride + col] = a.free_pages[head + e];
-    }
     // tokens
     const int32_t tokens = cu[R];
     int bad_page = 0;
@@ -145,6 +116,32 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
         a.slot_map[t] = slot;
         a.position[t] = pos;
         if (a.lora_id_map) a.lora_id_map[t] = id;
+    }
+    // per request
+    for (int64_t r = gid; r < R; r += stride) {
+        const int i = static_cast<int>(r);
+        a.cu_new[i] = cu[i];
+        a.kv_len[i] = served(i, need_of(i)) ? ctx[i] + cu[i + 1] - cu[i] : 0;
+    }
+    // new table entries: entry e is one of the pages the served requests take
+    const int64_t entries = before[R] < left ? before[R] : left;
+    for (int64_t e = gid; e < entries; e += stride) {
+        const int r = last_le(before, R, static_cast<int32_t>(e));
+        if (!served(r, need_of(r))) continue;
+        const int64_t col = ((static_cast<int64_t>(ctx[r]) + P - 1) >> shift) + (e - before[r]);
+        a.block_table[r * a.table_stride + col] = a.free_pages[head + e];
+    }
+    if (blockIdx.x == 0) {
+        int64_t taken = 0;
+        for (int r = r0; r < r1; ++r) {
+            const int32_t need = need_of(r);
+            if (served(r, need)) taken += need;
+        }
+        block_scan_i64(taken, wsum, &total);
+        if (tid == 0) {
+            a.cu_new[R] = cu[R];
+            *a.free_head_out = head + static_cast<int32_t>(total);
+        }
     }
     const int flags = (bad ? LORA_DEV_BAD_LENGTH : 0) | (missing ? LORA_DEV_NO_PAGE : 0) |
                       (bad_page ? LORA_DEV_BAD_PAGE : 0);
@@ -175,33 +172,49 @@ cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream)
 // ---------------------------------------------------------------------------
 // lora_kv_store
 // ---------------------------------------------------------------------------
-// A copy: 16-byte units of K and V, each thread one unit of both at a time, so
-// two loads are in flight; consecutive threads take consecutive units of a
-// head, then of a token.  HBM (or L2, for rows just written) bounds it.
+// A copy: 16-byte units of K and V, consecutive threads taking consecutive units
+// of a head, then of a token.  HBM (or L2, for rows just written) bounds it, so a
+// thread has the four loads of two units in flight, and its slots with them,
+// before it stores anything.
 constexpr int kStoreThreads = 256;
+constexpr int kStoreUnits = 2;
 
 __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const KvStoreParams p)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int per = p.kv_heads * p.vecs;
+    const uint32_t per = static_cast<uint32_t>(p.kv_heads * p.vecs);
     const int64_t total = p.T * per;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kStoreThreads;
     int bad = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i < total; i += stride) {
-        const int64_t t = i / per;
-        const int u = static_cast<int>(i - t * per), h = u / p.vecs, c = u - h * p.vecs;
-        const int32_t slot = p.slot_map[t];
-        if (slot < 0 || slot >= p.slots) {
-            bad |= slot != -1;
-            continue;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i0 < total;
+         i0 += kStoreUnits * stride) {
+        uint4 kv[kStoreUnits], vv[kStoreUnits];
+        int32_t slot[kStoreUnits];
+        int64_t to[kStoreUnits];
+#pragma unroll
+        for (int q = 0; q < kStoreUnits; ++q) {
+            const int64_t i = i0 + q * stride;
+            slot[q] = -1;
+            if (i >= total) continue;
+            const int64_t t = total < (int64_t(1) << 32) ? static_cast<uint32_t>(i) / per : i / per;
+            const int u = static_cast<int>(i - t * per), h = u / p.vecs, c = u - h * p.vecs;
+            slot[q] = p.slot_map[t];
+            kv[q] = *reinterpret_cast<const uint4 *>(p.k + t * p.k_tok + h * p.k_head + c * 8);
+            vv[q] = *reinterpret_cast<const uint4 *>(p.v + t * p.v_tok + h * p.v_head + c * 8);
+            to[q] = h * p.head_stride + c * 8;
         }
-        const int64_t page = slot >> p.page_shift, line = slot & ((1 << p.page_shift) - 1);
-        const int64_t dst = page * p.page_stride + h * p.head_stride + line * p.slot_stride + c * 8;
-        const uint4 kv = *reinterpret_cast<const uint4 *>(p.k + t * p.k_tok + h * p.k_head + c * 8);
-        const uint4 vv = *reinterpret_cast<const uint4 *>(p.v + t * p.v_tok + h * p.v_head + c * 8);
-        *reinterpret_cast<uint4 *>(p.kc + dst) = kv;
-        *reinterpret_cast<uint4 *>(p.vc + dst) = vv;
+#pragma unroll
+        for (int q = 0; q < kStoreUnits; ++q) {
+            if (slot[q] < 0 || slot[q] >= p.slots) {
+                bad |= slot[q] != -1;
+                continue;
+            }
+            const int64_t page = slot[q] >> p.page_shift, line = slot[q] & ((1 << p.page_shift) - 1);
+            const int64_t dst = page * p.page_stride + line * p.slot_stride + to[q];
+            *reinterpret_cast<uint4 *>(p.kc + dst) = kv[q];
+            *reinterpret_cast<uint4 *>(p.vc + dst) = vv[q];
+        }
     }
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
 }
