@@ -36,6 +36,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_piece.cuh"
 #include "attn_ptx.cuh"
 #include "internal.h"
 
@@ -45,20 +46,12 @@ constexpr int kAttnThreads = 384;
 constexpr int kItems = 4;             // work items in flight between the loader and the others
 constexpr float kMostP = 0x1p40f;     // half a tile whose p sum to more than this moves m_i
 
-// tensor memory columns (512 in all): S of stream s at s * 128 (P over its
-// first 64), O of stream s at 256 + s * DP
-constexpr uint32_t kColS = 128, kColO = 256;
-
-// a piece of one (block, kv head): key tiles [t0, t1)
-struct AttnItem {
-    int32_t valid, pair, req, tok0, ntok, qpos0, kv_len, kvh;
-    int32_t seen;     // keys that any of its rows sees
-    int32_t t0, t1;
-    int32_t end0;     // pair: tiles that stream 0's rows reach
-    int32_t parts;    // pieces of the group
-    int32_t slot;     // this piece's partial results (parts > 1)
-    int32_t unit0;    // the unit that the group starts in (its counter; parts > 1)
-};
+// tensor memory columns (512 in all): S of stream s at s * 128, O at 256 + s * DP.
+// With a head dimension of 128 that is all of them, and P lies over S's first 64:
+// the next scores wait for its product.  With 64 there is room for P of its own,
+// and they only wait until S has been read: softmax and products overlap within a
+// stream.
+constexpr uint32_t kColS = 128, kColO = 256, kColP = 384;
 
 template <int DP>
 struct AttnSmem {
@@ -68,7 +61,8 @@ struct AttnSmem {
     static constexpr int kStats = 2 * kTile + kStages * kTile; // offsets
     static constexpr int kItem = kStats + 128 * 8;
     static constexpr int kBars = kItem + kItems * static_cast<int>(sizeof(AttnItem));
-    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2;
+    static constexpr bool kOwnP = DP == 64;                    // P does not share S's cells
+    static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int kEnd = kBars + kNumBars * 8 + 4 * (3 + kStages + 2);
     static constexpr int kBytes = kEnd + 1024;                 // room to align the base
     static_assert(kBytes <= 232448, "fits the opt-in shared memory of a CTA");
@@ -116,11 +110,18 @@ __device__ __forceinline__ uint32_t load_of_value(int pair, int t, int n) { retu
 // list (3.5 of 13 us for a prompt of 77 tokens).
 struct ShortList {
     int start, rows, first, nb;   // the lane's request: its rows, its first block; all blocks
-    __device__ __forceinline__ AttnHdr header(const AttnParams &p, int32_t *status, int lane)
+    __device__ __forceinline__ void load(const AttnParams &p, int lane)
     {
         start = rows = 0;
         if (lane < p.requests) {
-            const int32_t c0 = p.cu[lane], c1 = p.cu[lane + 1], T = static_cast<int32_t>(p.T);
+            start = p.cu[lane];
+            rows = p.cu[lane + 1];   // the end, until header() has seen it
+        }
+    }
+    __device__ __forceinline__ AttnHdr header(const AttnParams &p, int32_t *status, int lane)
+    {
+        if (lane < p.requests) {
+            const int32_t c0 = start, c1 = rows, T = static_cast<int32_t>(p.T);
             start = max(0, min(c0, T));
             const int e = max(start, min(c1, T));
             rows = e - start;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 {
     using Sm = AttnSmem<DP>;
     constexpr int kStages = Sm::kStages, kTile = Sm::kTile, kHalves = Sm::kHalves;
+    constexpr bool kOwnP = Sm::kOwnP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qbuf = smem, *ring = smem + 2 * kTile;
@@ -216,7 +218,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t *p_half = s_full + 2;            // [2] P of the tile's first 64 keys is in place
     uint64_t *p_full = p_half + 2;            // [2]
     uint64_t *pv_half = p_full + 2;           // [2] the products of the first 64 keys are done
-    uint64_t *o_full = pv_half + 2;           // [2]
+    uint64_t *pv_done = pv_half + 2;          // [2] all of a tile's are (P of its own)
+    uint64_t *o_full = pv_done + 2;           // [2]
     uint64_t *xbar = o_full + 2;              // the 256 softmax threads meet here
     uint64_t *end_bar = xbar + 1;             // all matrix products are done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(end_bar + 1);
@@ -246,32 +249,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     pdl_launch_dependents();
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);   // one arrival a stream (two from the only one that uses the stage)
+    // The work list is on its way while the rest is set up.  (The wait is for the
+    // kernels ahead, once for all threads: nobody touches memory before the barrier.)
+    AttnHdr hdr = {};
+    ShortList list;
+    int word = 0;
+    if (warp == 8) {
+        pdl_wait();
+        if (p.short_list) {
+            list.load(p, lane);
+        } else {
+            hdr = *p.hdr;
+            if (lane < 16) word = reinterpret_cast<const int32_t *>(p.first + blockIdx.x)[lane];
         }
-        for (int i = 0; i < kItems; ++i) {
-            mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 11);   // 8 softmax warps, 2 MMA warps, the value loader
-        }
-        mbar_init(&q_full[0], 1);
-        mbar_init(&q_full[1], 1);
-        mbar_init(q_empty, 2);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_half[s], 4);
-            mbar_init(&p_full[s], 4);
-            mbar_init(&pv_half[s], 1);
-            mbar_init(&o_full[s], 1);
-        }
-        mbar_init(xbar, 8);
-        mbar_init(end_bar, 2);
-        *abort_flag = 0;
-        for (int s = 0; s < kStages + 2; ++s) issued[s] = 0;
+    } else if (threadIdx.x < Sm::kNumBars) {
+        uint64_t *bar = full + threadIdx.x;
+        const int n = bar < empty ? 1
+                      : bar < item_full ? 2      // empty: one arrival a stream (two from the only one that uses the stage)
+                      : bar < item_empty ? 1
+                      : bar < q_full ? 11        // item_empty: 8 softmax warps, 2 MMA warps, the value loader
+                      : bar < q_empty ? 1
+                      : bar == q_empty ? 2
+                      : bar >= p_half && bar < pv_half ? 4   // p_half, p_full: a stream's warps
+                      : bar == xbar ? 8
+                      : bar == end_bar ? 2 : 1;
+        mbar_init(bar, n);
         fence_mbarrier_init();
+    } else if (threadIdx.x < Sm::kNumBars + kStages + 2) {
+        issued[threadIdx.x - Sm::kNumBars] = 0;
+    } else if (threadIdx.x == Sm::kNumBars + kStages + 2) {
+        *abort_flag = 0;
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 11 && lane == 0) {
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.q1);
         tma_prefetch_map(&maps.k);
@@ -285,7 +294,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
 
     // A tile of 128 keys in boxes of box_rows keys (a page, or 128 keys of a
     // larger one; 32 or 128 packed rows), each 64 columns wide: one lane per box.
@@ -329,99 +337,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 8) {
         // ===================== work and keys ==================================
-        AttnBlock early = {};   // of a short list, the lanes fetch a block each along with the header
-        AttnHdr hdr = {};
-        ShortList list;
-        if (p.short_list) {
-            hdr = list.header(p, status, lane);
-        } else {
-            if (lane < p.max_blocks) early = p.blocks[lane];
-            hdr = *p.hdr;
-        }
+        if (p.short_list) hdr = list.header(p, status, lane);
         uint32_t it = 0, nitem = 0;
         const bool cut = hdr.cut != 0;
         int unit = blockIdx.x;
-        // cut: my unit [pos, end) of the list; lo: the block that pos is in
-        int pos = cut ? unit * hdr.unit_cost : 0;
-        const int end = min(pos + hdr.unit_cost, hdr.cost);
-        int lo = 0, kvh = 0;
-        AttnBlock b = early;
-        if (cut && unit < hdr.units) {
-            // the last block that starts at or before pos; of up to 32 blocks each lane has one already
-            int hi = hdr.nblocks;
-            if (hi <= 32) {
-                lo = 31 - __clz(__ballot_sync(0xffffffffu, lane < hi && early.pre * p.kv_heads <= pos));
-                b.pre = __shfl_sync(0xffffffffu, early.pre, lo);
-                b.req = __shfl_sync(0xffffffffu, early.req, lo);
-                b.tok0 = __shfl_sync(0xffffffffu, early.tok0, lo);
-                b.ntok = __shfl_sync(0xffffffffu, early.ntok, lo);
-                b.qpos0 = __shfl_sync(0xffffffffu, early.qpos0, lo);
-                b.kv_len = __shfl_sync(0xffffffffu, early.kv_len, lo);
-                b.tiles = __shfl_sync(0xffffffffu, early.tiles, lo);
-            } else {
-                while (hi - lo > 1) {
-                    const int step = (hi - lo + 31) / 32;
-                    const int at = lo + step * lane;
-                    const bool le = at < hi && p.blocks[at].pre * p.kv_heads <= pos;
-                    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lanes 0..k, lane 0 always
-                    lo += step * k;
-                    hi = min(hi, lo + step);
-                }
-                b = p.blocks[lo];
-            }
-            kvh = static_cast<int>(static_cast<uint32_t>(pos - b.pre * p.kv_heads) / static_cast<uint32_t>(b.tiles + kAttnItemCost));
-        }
-        while (true) {
-            // the next piece: key tiles [t0, t1) of (block b, head kvh)
-            bool more = unit < hdr.units;
-            int t0 = 0, t1 = 0, parts = 1, slot = 0, unit0 = 0;
-            if (more && !cut) {
-                // whole groups, longest first; the heads of a section together
-                const uint32_t per = hdr.nblocks * hdr.sec_heads, sec = unit / per, rem = unit - sec * per;
-                const uint32_t hs = min(hdr.sec_heads, p.kv_heads - static_cast<int>(sec) * hdr.sec_heads), at = rem / hs;
-                b = p.short_list ? list.block(p, static_cast<int>(at)) : p.blocks[at];
-                kvh = static_cast<int>(sec * hdr.sec_heads + rem - at * hs);
-                t1 = b.tiles;
-            } else if (more) {
-                // the group's tiles start kAttnItemCost into its share of the list
-                const int g0 = b.pre * p.kv_heads + kvh * (b.tiles + kAttnItemCost) + kAttnItemCost;
-                more = pos < end && g0 < end;
-                t0 = max(0, pos - g0);
-                t1 = min(b.tiles, end - g0);
-                const uint32_t c = hdr.unit_cost, u0 = static_cast<uint32_t>(g0) / c, u1 = static_cast<uint32_t>(g0 + b.tiles - 1) / c;
-                parts = static_cast<int>(u1 - u0 + 1);
-                slot = 2 * unit + (static_cast<uint32_t>(unit) == u0);
-                unit0 = static_cast<int>(u0);
-                pos = g0 + t1;   // the end of the group or of the unit
-            }
-            // hand it to the other roles
+        // cut: my unit [pos, end) of the list
+        const int end = cut ? min((unit + 1) * hdr.unit_cost, hdr.cost) : 0;
+        int pos = 0;
+        AttnBlock b = {};
+        bool have_b = false, ok = true, more = true;
+        while (more) {
+            // the next piece, handed to the other roles
             const int is = nitem % kItems;
-            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) more = false;
-            const int pair = b.ntok > p.tq;
-            if (lane == 0) {
-                AttnItem &w = items[is];
-                w.valid = more;
-                w.pair = pair;
-                w.req = b.req;
-                w.tok0 = b.tok0;
-                w.ntok = b.ntok;
-                w.qpos0 = b.qpos0;
-                w.kv_len = b.kv_len;
-                w.seen = min(b.kv_len, b.qpos0 + b.ntok);
-                w.kvh = kvh;
-                w.t0 = t0;
-                w.t1 = t1;
-                w.end0 = max(1, (min(b.kv_len, b.qpos0 + min(b.ntok, p.tq)) + kAttnTileK - 1) / kAttnTileK);
-                w.parts = parts;
-                w.slot = slot;
-                w.unit0 = unit0;
-                mbar_arrive(&item_full[is]);
+            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) ok = false;
+            if (nitem == 0 && !p.short_list) {
+                if (lane < 16) reinterpret_cast<int32_t *>(&items[is])[lane] = word;   // laid out by the schedule
+                __syncwarp();
+            } else {
+                AttnItem w = {};
+                if (!cut && ok && unit < hdr.units) {
+                    int blk, kvh;
+                    whole_unit(hdr, p.kv_heads, unit, &blk, &kvh);
+                    w = item_of(p.short_list ? list.block(p, blk) : p.blocks[blk], blk, kvh, p.tq);
+                } else if (cut && ok) {
+                    const AttnItem &last = items[(nitem - 1) % kItems];
+                    int blk = last.blk, kvh = last.kvh + 1;
+                    if (kvh == p.kv_heads) {
+                        kvh = 0;
+                        if (++blk < hdr.nblocks) b = p.blocks[blk];
+                    }
+                    if (blk < hdr.nblocks) w = cut_piece(hdr, b, blk, kvh, p.kv_heads, p.tq, unit, end, &pos);
+                }
+                if (lane == 0) items[is] = w;
+                __syncwarp();
             }
-            if (!more) break;
+            const AttnItem &w = items[is];
+            const int pair = w.pair, t0 = w.t0, n = w.t1 - t0, seen = w.seen, kvh = w.kvh, row0 = w.tok0 - w.qpos0;
+            const int32_t *table = p.block_table + w.req * p.table_stride;
+            more = w.valid;
+            if (lane == 0) mbar_arrive(&item_full[is]);
             ++nitem;
-            bool ok = true;
-            const int n = t1 - t0, seen = min(b.kv_len, b.qpos0 + b.ntok), row0 = b.tok0 - b.qpos0;
-            const int32_t *table = p.block_table + b.req * p.table_stride;
+            if (!more) break;
+            if (cut && !have_b) {   // of the first piece's group, for what comes after it
+                b = p.blocks[w.blk];
+                pos = b.pre * p.kv_heads + kvh * (b.tiles + kAttnItemCost) + kAttnItemCost + w.t1;
+                have_b = true;
+            }
             int next = 0, cur = -1, nxt = -1;
 #pragma unroll 1
             for (int t = 0; t < n; ++t) {
@@ -437,14 +398,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!ok) break;
             }
             it += 2 * n;
-            if (!cut) {
-                unit = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
-            } else if (++kvh == p.kv_heads) {
-                kvh = 0;
-                if (++lo < hdr.nblocks) b = p.blocks[lo];
-                else pos = end;
-            }
-            if (!ok) unit = hdr.units;   // hand out the end, then stop
+            if (!cut) unit = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
         }
         // no CTA claims a unit any more once all have come here: the counters go back to zero
         if (lane == 0 && !cut && atom_acq_rel_gpu_add(p.counters + ACNT_DONE, 1) == static_cast<int>(gridDim.x) - 1) {
@@ -501,13 +455,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // and issuing one takes 35 (66 with a branch around it), so one warp for
         // both streams would be as busy as the tensor cores.  All lanes run the
         // same code and the elected one's instructions take effect.
-        const int s = warp - 9;
+        const int s = uniform(warp - 9);
+        const uint32_t tmem_u = uniform(static_cast<int>(tmem));
         uint32_t it = 0, nitem = 0, nq0 = 0, nq1 = 0, np = 0;
         const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
         const uint32_t klo = umma_lo(smem_u32(ring), 16), vlo = umma_lo(smem_u32(ring), kAttnTileK * 128);
         const int dsteps = (p.head_dim + 15) / 16;
         const uint32_t idesc_pv = umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
-        const uint32_t s_cells = tmem + s * kColS, o_cells = tmem + kColO + s * DP;
+        const uint32_t s_cells = tmem_u + s * kColS, o_cells = tmem_u + kColO + s * DP;
+        const uint32_t p_cells = kOwnP ? tmem_u + kColP + s * 64 : s_cells;
         auto commit = [&](uint64_t *bar) { umma_commit_if(elect_one(), bar); };
         bool ok = true;
         while (ok) {
@@ -551,50 +507,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const bool more = k + 1 < all;
                 if (k >= 0) wait_load(iv);
                 if (more) wait_load(ik);
-                if (k >= 0 && k < mine) {
-                    const int keys = min(kAttnTileK, seen - tv * kAttnTileK);
-                    // keys past the last one that a row sees: their p is 0, but 0 times
-                    // what the tile holds there (another request's rows, stale pages)
-                    // may be NaN
-                    const int up = (keys + 15) & ~15;
-                    if (keys > 0 && keys != up) {
-                        uint8_t *v = ring + stv * kTile;
-                        for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
-                            const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
-                            *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    const uint32_t vd = vlo + stv * (kTile >> 4);
-                    const uint32_t par = np++ & 1;
-                    auto step = [&](uint32_t lead, int kk) {
-                        umma_ts_if(lead, o_cells, s_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
-                    };
-                    ok &= wait_each(&p_half[s], par);
-                    tc_fence_after();
-                    const uint32_t lead = elect_one();
-                    if (keys == kAttnTileK) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) step(lead, kk);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 0; kk < 4 && kk * 16 < keys; ++kk) step(lead, kk);
-                    }
-                    umma_commit_if(lead, &pv_half[s]);
-                    ok &= wait_each(&p_full[s], par);
-                    tc_fence_after();
-                    if (keys == kAttnTileK) {
-#pragma unroll
-                        for (int kk = 4; kk < 8; ++kk) step(lead, kk);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 4; kk * 16 < keys; ++kk) step(lead, kk);
-                    }
-                    if (k == mine - 1) umma_commit_if(lead, &o_full[s]);
-                }
-                if (k + 1 < mine) {
+                auto scores = [&] {   // of tile k + 1
+                    if (k + 1 >= mine) return;
                     tc_fence_after();
                     const int keys = min(kAttnTileK, seen - tk * kAttnTileK);
                     const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
@@ -612,7 +526,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int kk = 0; kk < dsteps; ++kk) step(kk);
                     }
                     umma_commit_if(lead, &s_full[s]);
+                };
+                const bool values = k >= 0 && k < mine;
+                const int keys = values ? min(kAttnTileK, seen - tv * kAttnTileK) : 0;
+                const uint32_t vd = vlo + stv * (kTile >> 4), par = np & 1;
+                auto step = [&](uint32_t lead, int kk) {
+                    umma_ts_if(lead, o_cells, p_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
+                };
+                if (values) {
+                    // keys past the last one that a row sees: their p is 0, but 0 times
+                    // what the tile holds there (another request's rows, stale pages)
+                    // may be NaN
+                    const int up = (keys + 15) & ~15;
+                    if (keys > 0 && keys != up) {
+                        uint8_t *v = ring + stv * kTile;
+                        for (int e = lane; e < (up - keys) * 8 * kHalves; e += 32) {
+                            const int r = keys + e / (8 * kHalves), c = e % (8 * kHalves);
+                            *reinterpret_cast<uint4 *>(v + (c >> 3) * (kAttnTileK * 128) + r * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    ++np;
+                    ok &= wait_each(&p_half[s], par);   // the first half of P is in place, and S has been read
+                    tc_fence_after();
+                    const uint32_t lead = elect_one();
+                    if (keys == kAttnTileK) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) step(lead, kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < 4 && kk * 16 < keys; ++kk) step(lead, kk);
+                    }
+                    umma_commit_if(lead, &pv_half[s]);
                 }
+                if (kOwnP) scores();
+                if (values) {
+                    ok &= wait_each(&p_full[s], par);
+                    tc_fence_after();
+                    const uint32_t lead = elect_one();
+                    if (keys == kAttnTileK) {
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk) step(lead, kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 4; kk * 16 < keys; ++kk) step(lead, kk);
+                    }
+                    if (kOwnP) umma_commit_if(lead, &pv_done[s]);
+                    if (k == mine - 1) umma_commit_if(lead, &o_full[s]);
+                }
+                if (!kOwnP) scores();
                 if (k >= 0) release(stv);
                 if (more) release(stk);
                 if (k + 2 == all) commit(q_empty);
@@ -630,6 +594,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int r = quad * 32 + lane;   // my row of the query tile
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lanes + s * kColS, t_o = tmem + lanes + kColO + s * DP;
+        const uint32_t t_p = kOwnP ? tmem + lanes + kColP + s * 64 : t_s;
         const int G = p.group, D = p.head_dim;
         const float c = p.scale * 1.4426950408889634f;
         uint32_t nitem = 0, ns = 0, no = 0, nx = 0;
@@ -654,10 +619,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool row_ok = i < p.tq && tok < w.ntok;
             const int limit = row_ok ? max(0, min(w.kv_len, w.qpos0 + tok + 1)) : 0;
             const bool live = __any_sync(0xffffffffu, limit > 0);
-            const bool narrow = !w.pair && w.ntok * G <= 16, two = w.ntok * G > 8;   // two: rows past the eighth
+            const bool narrow = kPaged && !w.pair && w.ntok * G <= 16, two = w.ntok * G > 8;   // two: rows past the eighth
             float m = -INFINITY, l = 0.f;
             // narrow: rows lane / 4 and 8 more, of which this lane has keys 8 j + 2 (lane % 4) and the next
-            float nm[2] = {-INFINITY, -INFINITY}, nl[2] = {0.f, 0.f};
+            float nm[2] = {-INFINITY, -INFINITY}, nl[2] = {0.f, 0.f}, nf[2][2];
+            bool nu[2][2];
             int nlim[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -669,6 +635,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int rem = limit - tile * kAttnTileK;   // my visible columns of this tile
                 if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
+                // The previous tile's products are done: O holds them, P may be overwritten, and
+                // all warps of the stream have handed theirs over (none may be counted twice in
+                // one phase of p_full).  Sharing S's cells, these scores could not be here otherwise.
+                auto products_done = [&] {
+                    if (kOwnP && k > 0) {
+                        wait(&pv_done[s], (ns - 2) & 1);
+                        tc_fence_after();
+                    }
+                };
                 if (narrow && live) {
                     const uint64_t c2 = pack_f2(c, c);
                     const int first = 2 * (lane & 3);
@@ -695,6 +670,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     bool move = (nm[0] == -INFINITY && see[0] + first > 0) || (two && nm[1] == -INFINITY && see[1] + first > 0);
                     for (int round = 0;; ++round) {
                         if (__any_sync(0xffffffffu, move)) {
+                            products_done();
                             float f[2];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -752,7 +728,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             break;
                         }
                     }
-                    tmem_st_16x128(t_s, pk);
+                    products_done();
+                    tmem_st_16x128(t_p, pk);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -760,7 +737,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 } else if (live) {
                     const uint64_t c2 = pack_f2(c, c);
                     // two halves of 64 keys, so that the first one's products start early
-#pragma unroll 1
+#pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t cells = t_s + 64 * h;
                         const int seen = rem - 64 * h;   // my visible columns of this half
@@ -781,37 +758,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             for (int e = 0; e < 64; ++e) x[e] = e < seen ? x[e] : -INFINITY;
                         }
                         uint32_t pk[32];
-                        bool move = m == -INFINITY && seen > 0;
-                        for (int round = 0;; ++round) {   // again if the sum asks for it: after a move it cannot
-                            if (__any_sync(0xffffffffu, move)) {
-                                // m, and with it l and O, up to this half's maximum.  O holds the tiles
-                                // before this one, and the first half of this one once the second is here.
-                                if (h == 1) {
-                                    wait(&pv_half[s], (ns - 1) & 1);
-                                    tc_fence_after();
-                                }
-                                float mn = m, y[32];
-#pragma unroll 1
-                                for (int q = 0; q < 2; ++q) {
-                                    tmem_ld32(cells + 32 * q, y);
-                                    tmem_ld_wait();
-                                    tmem_use32(y);
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) mn = fmaxf(mn, e < seen - 32 * q ? y[e] : -INFINITY);
-                                }
-                                const float f = mn == m ? 1.f : ex2((m - mn) * c);   // 0 from -infinity
-                                m = mn;
-                                l *= f;
-#pragma unroll 1
-                                for (int q = 0; q < (k + h > 0 ? DP / 32 : 0); ++q) {
-                                    tmem_ld32(t_o + 32 * q, y);
-                                    tmem_ld_wait();
-                                    tmem_use32(y);
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) y[e] *= f;
-                                    tmem_st32(t_o + 32 * q, y);
-                                }
-                            }
+                        float total;
+                        auto exps = [&] {
                             const float off = m == -INFINITY ? 0.f : -m * c;
                             const uint64_t off2 = pack_f2(off, off);
                             uint64_t sum[2] = {0, 0};
@@ -826,18 +774,53 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             }
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
-                            move = a + b > kMostP;
-                            if (round == 1 || !__any_sync(0xffffffffu, move)) {
-                                l += a + b;
-                                break;
+                            total = a + b;
+                        };
+                        exps();
+                        if (__any_sync(0xffffffffu, total > kMostP || (m == -INFINITY && seen > 0))) {
+                            if (h == 0) {
+                                products_done();
+                            } else {
+                                wait(&pv_half[s], (ns - 1) & 1);
+                                tc_fence_after();
                             }
+                            float mn = m, y[32];
+                            if (kOwnP && h == 1) {   // S may be gone
+#pragma unroll
+                                for (int e = 0; e < 64; e += 2) mn = fmaxf(fmaxf(mn, x[e]), x[e + 1]);
+                            } else {
+#pragma unroll 1
+                                for (int q = 0; q < 2; ++q) {
+                                    tmem_ld32(cells + 32 * q, y);
+                                    tmem_ld_wait();
+                                    tmem_use32(y);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) mn = fmaxf(mn, e < seen - 32 * q ? y[e] : -INFINITY);
+                                }
+                            }
+                            const float f = mn == m ? 1.f : ex2((m - mn) * c);   // 0 from -infinity
+                            m = mn;
+                            l *= f;
+#pragma unroll 1
+                            for (int q = 0; q < (k + h > 0 ? DP / 32 : 0); ++q) {
+                                tmem_ld32(t_o + 32 * q, y);
+                                tmem_ld_wait();
+                                tmem_use32(y);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) y[e] *= f;
+                                tmem_st32(t_o + 32 * q, y);
+                            }
+                            exps();
                         }
-                        tmem_st16(t_s + 32 * h, pk);
-                        tmem_st16(t_s + 32 * h + 16, pk + 16);
+                        l += total;
+                        if (h == 0) products_done();
+                        tmem_st16(t_p + 32 * h, pk);
+                        tmem_st16(t_p + 32 * h + 16, pk + 16);
                     }
                     tmem_st_wait();
-                } else if (lane == 0) {
-                    mbar_arrive(&p_half[s]);
+                } else {
+                    products_done();   // not ahead of the stream's other warps
+                    if (lane == 0) mbar_arrive(&p_half[s]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -865,14 +848,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     stats[r] = make_float2(m, l);
                 }
                 meet();
-                if (s == 0) {
-                    if (narrow) {
-                        const float2 own = stats[64 + (r & 15)];
-                        m = own.x;
-                        l = own.y;
-                        use0 = l != 0.f;
-                    }
-                    const float2 st = stats[narrow ? r & 15 : r];
+                if (s == 0 && !narrow) {
+                    const float2 st = stats[r];
                     const float mm = fmaxf(m, st.x);
                     use1 = st.y != 0.f;
                     f0 = use0 ? ex2((m - mm) * c) : 0.f;
@@ -884,7 +861,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tc_fence_after();
             const bool mine = w.pair || s == 0;
             const int rho = tok * G + g;   // my row of the block
-            if (mine && __any_sync(0xffffffffu, row_ok)) {
+            if (narrow) {
+                // rows by quads, as in the softmax: stream s's first warp joins half of the
+                // columns, both streams' O of the row by one load each
+                if (quad == 0) {
+                    const bool whole = w.parts == 1;
+                    constexpr int kCols = DP / 2;   // columns of a stream's warp
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = (lane >> 2) + 8 * h;
+                        const float2 a = stats[64 + row], b = stats[row];
+                        const float mm = fmaxf(a.x, b.x);
+                        const bool u0 = a.y != 0.f, u1 = b.y != 0.f;
+                        const float e0 = u0 ? ex2((a.x - mm) * c) : 0.f, e1 = u1 ? ex2((b.x - mm) * c) : 0.f;
+                        nm[h] = mm;
+                        nl[h] = a.y * e0 + b.y * e1;
+                        const float inv = whole && nl[h] != 0.f ? 1.f / nl[h] : 1.f;
+                        nf[h][0] = e0 * inv;
+                        nf[h][1] = e1 * inv;
+                        nu[h][0] = u0;
+                        nu[h][1] = u1;
+                    }
+                    const uint32_t cells = tmem + kColO + s * kCols;
+                    float y[2][kCols / 2];   // [stream][4 j + 2 h + e]
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (DP == 128) tmem_ld_16x256_half(cells + q * DP, y[q]);
+                        else tmem_ld_16x256_quarter(cells + q * DP, y[q]);
+                    }
+                    tmem_ld_wait();
+                    tmem_use<kCols / 2>(y[0]);
+                    tmem_use<kCols / 2>(y[1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = (lane >> 2) + 8 * h, t = row / G, gg = row - t * G;
+                        if (t >= w.ntok) continue;
+                        const int head = w.kvh * G + gg, c0 = s * kCols + 2 * (lane & 3);
+                        const int64_t at = static_cast<int64_t>(w.tok0) + t;
+                        uint16_t *out = p.o + at * p.o_tok + head * p.o_head;
+                        float *part = p.part + (static_cast<int64_t>(w.slot) * p.part_rows + row) * D;
+#pragma unroll
+                        for (int j = 0; j < kCols / 8; ++j) {
+                            float v[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                v[e] = (nu[h][0] ? y[0][4 * j + 2 * h + e] * nf[h][0] : 0.f) +
+                                       (nu[h][1] ? y[1][4 * j + 2 * h + e] * nf[h][1] : 0.f);
+                            if (c0 + 8 * j >= D) continue;
+                            if (whole) *reinterpret_cast<uint32_t *>(out + c0 + 8 * j) = pack_bf16x2(v[0], v[1]);
+                            else *reinterpret_cast<float2 *>(part + c0 + 8 * j) = make_float2(v[0], v[1]);
+                        }
+                        if (s == 0 && (lane & 3) == 0) {
+                            if (!whole)
+                                p.part_ml[static_cast<int64_t>(w.slot) * p.part_rows + row] = make_float2(nm[h], nl[h]);
+                            else if (p.lse)
+                                p.lse[at * p.heads + head] =
+                                    nl[h] == 0.f ? -INFINITY : (nm[h] * c + log2f(nl[h])) * 0.6931471805599453f;
+                        }
+                    }
+                }
+            } else if (mine && __any_sync(0xffffffffu, row_ok)) {
                 const bool whole = w.parts == 1;
                 const float inv = whole && l != 0.f ? 1.f / l : 1.f;
                 f0 *= inv;
@@ -932,8 +968,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (w.parts > 1) {
                 // the piece that finishes last joins the group's pieces, in their order
-                __threadfence();
-                meet();
+                meet();   // with the release below, every thread's writes come before the count
                 if (threadIdx.x == 0)
                     *join_flag = atom_acq_rel_gpu_add(p.counters + ACNT_GROUP + w.unit0, 1) == w.parts - 1;
                 meet();
@@ -945,7 +980,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int u = threadIdx.x; u < rows * d4; u += 256) {
                         const int rr = u / d4, col = (u - rr * d4) * 4;
                         float mm = -INFINITY, ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 4
                         for (int k = 0; k < w.parts; ++k) {
                             const float2 ml = __ldcg(p.part_ml + slot_of(k) + rr);
                             const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(k) + rr) * D + col));

@@ -4,6 +4,7 @@
 //   counters   status word, work-list counters, arrival counters of split
 //              groups                                   (zero at rest but the status)
 //   hdr        schedule header (AttnHdr)
+//   first      each CTA's first piece of work (AttnItem)
 //   blocks     query blocks of the step (AttnBlock), longest first or (cut) in
 //              request order
 //   part       partial results of split groups: fp32 O rows, then (m, l) pairs
@@ -56,11 +57,25 @@ struct __align__(16) AttnHdr {
     int32_t unused[2];
 };
 
+// A piece of one (block, kv head) group: key tiles [t0, t1).
+struct __align__(16) AttnItem {
+    int32_t valid;    // 0: no more
+    int32_t pair;     // two query tiles (their streams share the key tiles), or one
+    int32_t req, tok0, ntok, qpos0, kv_len;
+    int32_t seen;     // keys that any of its rows sees
+    int32_t kvh, t0, t1;
+    int32_t end0;     // pair: tiles that stream 0's rows reach
+    int32_t parts;    // pieces of the group
+    int32_t slot;     // this piece's partial results (parts > 1)
+    int32_t unit0;    // the unit that the group starts in (its counter; parts > 1)
+    int32_t blk;      // its block
+};
+
 struct AttnLayout {
     int32_t tq;          // tokens of one query tile
     int64_t max_blocks;
     int32_t part_rows;   // rows of a partial slot
-    size_t counters, hdr, blocks, part, part_ml, total;
+    size_t counters, hdr, first, blocks, part, part_ml, total;
 };
 
 struct AttnSchedParams {
@@ -68,6 +83,7 @@ struct AttnSchedParams {
     int32_t R, tq, kv_heads, head_dim, ctas;
     int64_t T, max_kv, max_blocks;
     AttnHdr *hdr;
+    AttnItem *first;
     AttnBlock *blocks;
     int32_t *counters;
 };
@@ -80,6 +96,7 @@ struct AttnParams {
     int32_t heads, kv_heads, group, head_dim, tq;
     float scale;
     const AttnHdr *hdr;
+    const AttnItem *first;
     const AttnBlock *blocks;
     int64_t max_blocks;
     int32_t *counters;

@@ -47,6 +47,7 @@ static AttnLayout make_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_he
         L.max_blocks = T / (2 * L.tq) + R;
         L.part_rows = static_cast<int32_t>(std::min<int64_t>(2 * L.tq, std::max<int64_t>(T, 1)) * group);
         L.hdr = take(sizeof(AttnHdr));
+        L.first = take(static_cast<size_t>(kAttnMaxCtas) * sizeof(AttnItem));
         L.blocks = take(static_cast<size_t>(L.max_blocks) * sizeof(AttnBlock));
         L.part = take(static_cast<size_t>(2 * kAttnMaxCtas) * L.part_rows * head_dim * 4);
         L.part_ml = take(static_cast<size_t>(2 * kAttnMaxCtas) * L.part_rows * 8);
@@ -120,6 +121,7 @@ static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R,
     p.max_kv = max_kv;
     p.max_blocks = L.max_blocks;
     p.hdr = at<AttnHdr>(ws, L.hdr);
+    p.first = at<AttnItem>(ws, L.first);
     p.blocks = at<AttnBlock>(ws, L.blocks);
     p.counters = at<int32_t>(ws, L.counters);
     return launch_attn_schedule(p, stream) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
@@ -159,6 +161,7 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->tq = L.tq;
     p->scale = a->scale;
     p->hdr = at<AttnHdr>(ws, L.hdr);
+    p->first = at<AttnItem>(ws, L.first);
     p->blocks = at<AttnBlock>(ws, L.blocks);
     p->max_blocks = L.max_blocks;
     p->counters = at<int32_t>(ws, L.counters);

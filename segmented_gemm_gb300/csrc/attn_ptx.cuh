@@ -71,8 +71,9 @@ __device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t *bar)
         : "memory");
 }
 
-// A value that is the same in all lanes, told to the compiler.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// A value that is the same in all lanes, told to the compiler: a reduction's
+// result lives in a uniform register, and so does what is computed from it.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // Instruction descriptor as umma_idesc_bf16, with B stored N-major (its N
 // elements contiguous).
@@ -152,7 +153,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         : "memory");
 }
 
-// 16 lanes x 256 bit, 128 (_half: 64) columns: lane l of the warp gets, of columns
+template <int N>
+__device__ __forceinline__ void tmem_use(float *r)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]),
+                          "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]), "+f"(r[i + 10]), "+f"(r[i + 11]), "+f"(r[i + 12]),
+                          "+f"(r[i + 13]), "+f"(r[i + 14]), "+f"(r[i + 15]));
+}
+
+// 16 lanes x 256 bit, 128 (_half: 64, _quarter: 32) columns: lane l of the warp gets, of columns
 // 8 j + 2 (l % 4) and the next, rows l / 4 in r[4 j], r[4 j + 1] and l / 4 + 8 in
 // r[4 j + 2], r[4 j + 3].
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float *r)
@@ -185,6 +196,16 @@ __device__ __forceinline__ void tmem_ld_16x256_half(uint32_t taddr, float *r)
           "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]),
           "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]),
           "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256_quarter(uint32_t taddr, float *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
 }

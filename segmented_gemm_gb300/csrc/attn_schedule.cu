@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_piece.cuh"
 #include "block_scan.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -34,6 +35,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     extern __shared__ int32_t blk_start[];   // [R + 1] first block of each request
     __shared__ int64_t wsum[32];
     __shared__ int32_t hist[kSchedBuckets];
+    __shared__ int32_t unit_blk[kAttnMaxCtas];
     __shared__ int32_t s_max, s_pair, s_tail;
     const int tid = threadIdx.x;
     const int R = p.R, tb = 2 * p.tq;
@@ -133,18 +135,17 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     const int64_t whole = max(groups >= p.ctas ? each + s_tail / 2 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
     // (a list too long for 32-bit positions is never short of units)
     const bool cut = each + (s_pair ? kJoinPair : kJoinSingle) < whole && cost + each < INT32_MAX;
-    if (tid == 0) {
-        AttnHdr h = {};
-        h.nblocks = nb;
-        h.cut = cut;
-        h.cost = cut ? static_cast<int32_t>(cost) : 0;
-        h.unit_cost = cut ? static_cast<int32_t>(each) : 0;
-        h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups, static_cast<int64_t>(INT32_MAX)));
-        const int64_t head_bytes = max(static_cast<int64_t>(1), all_keys * p.head_dim * 4);
-        h.sec_heads = static_cast<int32_t>(
-            max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
-        *p.hdr = h;
-    }
+    AttnHdr h = {};
+    h.nblocks = nb;
+    h.cut = cut;
+    h.cost = cut ? static_cast<int32_t>(cost) : 0;
+    h.unit_cost = cut ? static_cast<int32_t>(each) : 0;
+    h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups, static_cast<int64_t>(INT32_MAX)));
+    const int64_t head_bytes = max(static_cast<int64_t>(1), all_keys * p.head_dim * 4);
+    h.sec_heads = static_cast<int32_t>(
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
+    if (tid == 0) *p.hdr = h;
+    // the blocks in their order, and (cut) the block that each unit starts in
     if (!cut) {
         // ties in any order: the results do not depend on it
         for (int b = tid; b < nb; b += kSchedThreads) {
@@ -157,10 +158,34 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
             const int b = b0 + tid;
             AttnBlock k = {};
             if (b < nb) k = block_of(b);
-            k.pre = static_cast<int32_t>(carry + block_scan_i64(b < nb ? k.tiles + kAttnItemCost : 0, wsum, &total));
-            if (b < nb) p.blocks[b] = k;
+            const int32_t own = b < nb ? k.tiles + kAttnItemCost : 0;
+            k.pre = static_cast<int32_t>(carry + block_scan_i64(own, wsum, &total));
+            if (b < nb) {
+                p.blocks[b] = k;
+                const int64_t from = static_cast<int64_t>(k.pre) * p.kv_heads, to = from + static_cast<int64_t>(own) * p.kv_heads;
+                for (int64_t u = (from + each - 1) / each; u * each < to && u < h.units; ++u) unit_blk[u] = b;
+            }
             carry += total;
         }
+    }
+    __syncthreads();
+    // each CTA's first piece, so that it need not look for it
+    if (tid < p.ctas) {
+        AttnItem w = {};
+        if (tid < h.units) {
+            int blk, kvh;
+            if (!cut) {
+                whole_unit(h, p.kv_heads, tid, &blk, &kvh);
+                w = item_of(p.blocks[blk], blk, kvh, p.tq);
+            } else {
+                blk = unit_blk[tid];
+                const AttnBlock b = p.blocks[blk];
+                int pos = tid * h.unit_cost;
+                kvh = (pos - b.pre * p.kv_heads) / (b.tiles + kAttnItemCost);
+                w = cut_piece(h, b, blk, kvh, p.kv_heads, p.tq, tid, min(pos + h.unit_cost, h.cost), &pos);
+            }
+        }
+        p.first[tid] = w;
     }
 }
 
