@@ -169,7 +169,10 @@ typedef struct {
  * (NULL: as many as it has query rows, for lora_attn_prompt).  Lengths are
  * clamped to [0, max_kv] and offsets to [0, num_tokens]
  * (LORA_DEV_BAD_LENGTH).
- * *out: HOST; passed to the attention calls with the same ws.
+ * *out: HOST; passed to the attention calls with the same ws.  It stands until
+ * another schedule is built in that ws (an attention call without one does so
+ * too); an attention call that finds one of other sizes there runs nothing and
+ * sets LORA_DEV_CHECK.  After LORA_DEV_TIMEOUT build it anew.
  */
 typedef struct {
     void *plan;

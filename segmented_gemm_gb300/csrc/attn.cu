@@ -339,7 +339,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 8) {
         // ===================== work and keys ==================================
-        if (p.short_list) hdr = list.header(p, status, lane);
+        if (p.short_list) {
+            hdr = list.header(p, status, lane);
+        } else if (hdr.stamp != p.stamp) {   // a list of other sizes, or none: nothing is run
+            if (lane == 0) atomicOr(status, LORA_DEV_CHECK);
+            hdr = {};
+            word = 0;
+        }
         uint32_t it = 0, nitem = 0;
         const bool cut = hdr.cut != 0;
         int unit = blockIdx.x;
@@ -589,7 +595,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         // nothing issued here is in flight when the block ends
         commit(end_bar);
-        wait(end_bar, 0);
+        attn_wait(smem_u32(end_bar), 0, abort_flag, max(p.wait_cycles, static_cast<uint32_t>(kWaitShort)));
     } else {
         // ===================== softmax and results ============================
         const int s = warp >> 2, quad = warp & 3;
@@ -1039,7 +1045,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (*abort_flag) {
         // loads in flight are waited for (bounded) before the shared memory goes
         auto settle = [&](uint64_t *bar, uint32_t parity) {
-            attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles);
+            attn_wait(smem_u32(bar), parity, abort_flag, static_cast<uint32_t>(kWaitShort));
         };
         if (threadIdx.x == 0) atomicOr(status, LORA_DEV_TIMEOUT);
         if (warp == 8 && lane == 0)

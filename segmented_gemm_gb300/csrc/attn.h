@@ -54,7 +54,7 @@ struct __align__(16) AttnHdr {
     int32_t sec_heads;  // heads whose blocks run together (cut 0)
     int32_t unit_cost;  // cut 1
     int32_t cost;       // of all blocks and heads (cut 1)
-    int32_t unused[2];
+    uint64_t stamp;     // of the sizes that it was made for (sched_stamp)
 };
 
 // A piece of one (block, kv head) group: key tiles [t0, t1).
@@ -82,6 +82,7 @@ struct AttnSchedParams {
     const int32_t *cu, *kv_len;
     int32_t R, tq, kv_heads, head_dim, ctas;
     int64_t T, max_kv, max_blocks;
+    uint64_t stamp;
     AttnHdr *hdr;
     AttnItem *first;
     AttnBlock *blocks;
@@ -99,6 +100,7 @@ struct AttnParams {
     const AttnItem *first;
     const AttnBlock *blocks;
     int64_t max_blocks;
+    uint64_t stamp;          // a list with another one is not run
     int32_t *counters;
     // keys and values: paged or packed rows
     const uint16_t *k, *v;

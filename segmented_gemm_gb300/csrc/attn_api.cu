@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "attn.h"
 #include "internal.h"
@@ -106,6 +107,19 @@ static int check_ws(const void *ws, size_t bytes, size_t need)
     return device_supported() ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 
+// What the places and the extents of a list in ws depend on, in 64 bits: a
+// workspace may have been given to a step of other sizes since.
+static uint64_t sched_stamp(const AttnLayout &L, int64_t T, int32_t R, int32_t kv_heads, int32_t head_dim, int32_t ctas)
+{
+    uint64_t h = 0x243f6a8885a308d3ull;
+    for (const uint64_t v : {uint64_t(T), uint64_t(R), uint64_t(kv_heads), uint64_t(head_dim), uint64_t(L.tq),
+                             uint64_t(L.part_rows), uint64_t(ctas)}) {
+        h = (h ^ v) * 0x9e3779b97f4a7c15ull;   // odd: one value is told from another exactly
+        h ^= h >> 29;
+    }
+    return h;
+}
+
 static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R, int64_t T, int64_t max_kv,
                             int32_t kv_heads, int32_t head_dim, const AttnLayout &L, void *ws, cudaStream_t stream)
 {
@@ -120,6 +134,7 @@ static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R,
     p.T = T;
     p.max_kv = max_kv;
     p.max_blocks = L.max_blocks;
+    p.stamp = sched_stamp(L, T, R, kv_heads, head_dim, p.ctas);
     p.hdr = at<AttnHdr>(ws, L.hdr);
     p.first = at<AttnItem>(ws, L.first);
     p.blocks = at<AttnBlock>(ws, L.blocks);
@@ -164,6 +179,7 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->first = at<AttnItem>(ws, L.first);
     p->blocks = at<AttnBlock>(ws, L.blocks);
     p->max_blocks = L.max_blocks;
+    p->stamp = sched_stamp(L, a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, ctas);
     p->counters = at<int32_t>(ws, L.counters);
     p->T = a->num_tokens;
     p->requests = a->num_requests;

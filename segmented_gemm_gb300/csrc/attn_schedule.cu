@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     // (a list too long for 32-bit positions is never short of units)
     const bool cut = each + (s_pair ? kJoinPair : kJoinSingle) < whole && cost + each < INT32_MAX;
     AttnHdr h = {};
+    h.stamp = p.stamp;
     h.nblocks = nb;
     h.cut = cut;
     h.cost = cut ? static_cast<int32_t>(cost) : 0;
