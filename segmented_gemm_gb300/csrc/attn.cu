@@ -197,6 +197,69 @@ __device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatil
     return true;
 }
 
+// The pieces of a group, joined by the 256 softmax threads in the pieces' order:
+//   m = max m_k,  l = sum l_k 2^(c (m_k - m)),  o = sum O_k 2^(c (m_k - m)) / l.
+// Latency bounds it (a piece's rows lie in L2), so a thread has four loads of each
+// piece in flight: with one, chunks of up to 700 tokens over 9000 cached took 147 us
+// instead of 139, three to five new tokens a request 61.5 instead of 59.5.
+// A function of its own: inlined it costs the softmax loop registers.
+__device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0, int kvh, int parts, int unit0, float c)
+{
+    const int G = p.group, D = p.head_dim, rows = ntok * G, d4 = D / 4;
+    auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * unit0 + 1 : 2 * (unit0 + k)) * p.part_rows; };
+    constexpr int kJoin = 4;   // elements of four columns at once
+    const int all = rows * d4;
+#pragma unroll 1
+    for (int u0 = threadIdx.x; u0 < all; u0 += 256 * kJoin) {
+        float mm[kJoin], ll[kJoin], a[kJoin][4];
+        int64_t at[kJoin];   // my elements' rows of a slot, and their columns
+        int col[kJoin];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            const int u = min(u0 + 256 * j, all - 1), rr = u / d4;
+            at[j] = rr;
+            col[j] = (u - rr * d4) * 4;
+            mm[j] = -INFINITY;
+            ll[j] = a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.f;
+        }
+#pragma unroll 1
+        for (int k = 0; k < parts; ++k) {
+            const int64_t slot = slot_of(k);
+            float2 ml[kJoin];
+            float4 v[kJoin];
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+                ml[j] = __ldcg(p.part_ml + slot + at[j]);
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot + at[j]) * D + col[j]));
+            }
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+                const float mn = fmaxf(mm[j], ml[j].x);
+                const float f = ml[j].y == 0.f ? 0.f : ex2((ml[j].x - mn) * c);
+                const float g = ll[j] == 0.f ? 0.f : ex2((mm[j] - mn) * c);
+                mm[j] = mn;
+                ll[j] = ll[j] * g + f * ml[j].y;
+                a[j][0] = a[j][0] * g + f * v[j].x;
+                a[j][1] = a[j][1] * g + f * v[j].y;
+                a[j][2] = a[j][2] * g + f * v[j].z;
+                a[j][3] = a[j][3] * g + f * v[j].w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            if (u0 + 256 * j >= all) continue;
+            const float inv = ll[j] == 0.f ? 0.f : 1.f / ll[j];
+            const int rr = static_cast<int>(at[j]), tk = rr / G, hd = kvh * G + (rr - tk * G);
+            const int64_t row = static_cast<int64_t>(tok0) + tk;
+            *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col[j]) =
+                make_uint2(pack_bf16x2(a[j][0] * inv, a[j][1] * inv), pack_bf16x2(a[j][2] * inv, a[j][3] * inv));
+            if (p.lse && col[j] == 0)
+                p.lse[row * p.heads + hd] =
+                    ll[j] == 0.f ? -INFINITY : (mm[j] * c + log2f(ll[j])) * 0.6931471805599453f;
+        }
+    }
+}
+
 template <int DP, bool kPaged>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
@@ -1000,34 +1063,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     *join_flag = atom_acq_rel_gpu_add(p.counters + ACNT_GROUP + w.unit0, 1) == w.parts - 1;
                 meet();
                 if (*join_flag) {
-                    const int rows = w.ntok * G, d4 = D / 4;
-                    auto slot_of = [&](int k) {
-                        return static_cast<int64_t>(k == 0 ? 2 * w.unit0 + 1 : 2 * (w.unit0 + k)) * p.part_rows;
-                    };
-                    for (int u = threadIdx.x; u < rows * d4; u += 256) {
-                        const int rr = u / d4, col = (u - rr * d4) * 4;
-                        float mm = -INFINITY, ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-                        for (int k = 0; k < w.parts; ++k) {
-                            const float2 ml = __ldcg(p.part_ml + slot_of(k) + rr);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(k) + rr) * D + col));
-                            const float mn = fmaxf(mm, ml.x);
-                            const float f = ml.y == 0.f ? 0.f : ex2((ml.x - mn) * c), g = ll == 0.f ? 0.f : ex2((mm - mn) * c);
-                            mm = mn;
-                            ll = ll * g + f * ml.y;
-                            a[0] = a[0] * g + f * v.x;
-                            a[1] = a[1] * g + f * v.y;
-                            a[2] = a[2] * g + f * v.z;
-                            a[3] = a[3] * g + f * v.w;
-                        }
-                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                        const int tk = rr / G, hd = w.kvh * G + (rr - tk * G);
-                        const int64_t row = static_cast<int64_t>(w.tok0) + tk;
-                        *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col) =
-                            make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
-                        if (p.lse && col == 0)
-                            p.lse[row * p.heads + hd] = ll == 0.f ? -INFINITY : (mm * c + log2f(ll)) * 0.6931471805599453f;
-                    }
+                    join_pieces(p, w.ntok, w.tok0, w.kvh, w.parts, w.unit0, c);
                     if (threadIdx.x == 0) p.counters[ACNT_GROUP + w.unit0] = 0;
                 }
             } else if (!w.pair) {
