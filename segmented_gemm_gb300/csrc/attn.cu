@@ -197,16 +197,24 @@ __device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatil
     return true;
 }
 
+// First row of the partial results of a group's piece k, of the group that starts in
+// unit unit0: the last piece of that unit, then the first of the units after it.
+__device__ __forceinline__ int64_t join_slot(const AttnParams &p, int unit0, int k)
+{
+    return static_cast<int64_t>(k == 0 ? 2 * unit0 + 1 : 2 * (unit0 + k)) * p.part_rows;
+}
+
 // The pieces of a group, joined by the 256 softmax threads in the pieces' order:
 //   m = max m_k,  l = sum l_k 2^(c (m_k - m)),  o = sum O_k 2^(c (m_k - m)) / l.
-// Latency bounds it (a piece's rows lie in L2), so a thread has four loads of each
-// piece in flight: with one, chunks of up to 700 tokens over 9000 cached took 147 us
-// instead of 139, three to five new tokens a request 61.5 instead of 59.5.
-// A function of its own: inlined it costs the softmax loop registers.
+// Latency bounds it (a piece's rows lie in L2), so a thread has four elements of a
+// piece in flight: with one, chunks of up to 700 tokens over 9000 cached took 148 us
+// instead of 141, up to five new tokens a request 61.4 instead of 59.3.  A function of
+// its own: inlined it costs the softmax loop registers.  A few rows (at most one
+// element a thread, often of many pieces) are joined where it is called instead, with
+// four pieces in flight: one decoded token takes 9.0 us so, 10.6 through this function.
 __device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0, int kvh, int parts, int unit0, float c)
 {
     const int G = p.group, D = p.head_dim, rows = ntok * G, d4 = D / 4;
-    auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * unit0 + 1 : 2 * (unit0 + k)) * p.part_rows; };
     constexpr int kJoin = 4;   // elements of four columns at once
     const int all = rows * d4;
 #pragma unroll 1
@@ -224,7 +232,7 @@ __device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0
         }
 #pragma unroll 1
         for (int k = 0; k < parts; ++k) {
-            const int64_t slot = slot_of(k);
+            const int64_t slot = join_slot(p, unit0, k);
             float2 ml[kJoin];
             float4 v[kJoin];
 #pragma unroll
@@ -1063,7 +1071,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     *join_flag = atom_acq_rel_gpu_add(p.counters + ACNT_GROUP + w.unit0, 1) == w.parts - 1;
                 meet();
                 if (*join_flag) {
-                    join_pieces(p, w.ntok, w.tok0, w.kvh, w.parts, w.unit0, c);
+                    const int d4 = D / 4, all = w.ntok * G * d4;
+                    if (all > 256) {
+                        join_pieces(p, w.ntok, w.tok0, w.kvh, w.parts, w.unit0, c);
+                    } else if (threadIdx.x < all) {   // a thread's element, four pieces in flight
+                        const int rr = threadIdx.x / d4, col = (threadIdx.x - rr * d4) * 4;
+                        float mm = -INFINITY, ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                        for (int k = 0; k < w.parts; ++k) {
+                            const float2 ml = __ldcg(p.part_ml + join_slot(p, w.unit0, k) + rr);
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (join_slot(p, w.unit0, k) + rr) * D + col));
+                            const float mn = fmaxf(mm, ml.x);
+                            const float f = ml.y == 0.f ? 0.f : ex2((ml.x - mn) * c), g = ll == 0.f ? 0.f : ex2((mm - mn) * c);
+                            mm = mn;
+                            ll = ll * g + f * ml.y;
+                            a[0] = a[0] * g + f * v.x;
+                            a[1] = a[1] * g + f * v.y;
+                            a[2] = a[2] * g + f * v.z;
+                            a[3] = a[3] * g + f * v.w;
+                        }
+                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                        const int tk = rr / G, hd = w.kvh * G + (rr - tk * G);
+                        const int64_t row = static_cast<int64_t>(w.tok0) + tk;
+                        *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col) =
+                            make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
+                        if (p.lse && col == 0)
+                            p.lse[row * p.heads + hd] = ll == 0.f ? -INFINITY : (mm * c + log2f(ll)) * 0.6931471805599453f;
+                    }
                     if (threadIdx.x == 0) p.counters[ACNT_GROUP + w.unit0] = 0;
                 }
             } else if (!w.pair) {
