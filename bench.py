@@ -128,6 +128,7 @@ KERNEL_SOURCES = {   # the sources each kernel is compiled from (besides interna
     "lora_splitk_kernel": ("fused_splitk.cu",),
     "seg_build_kernel": ("seg_build.cu", "seg_build_body.cuh"),
     "moe_pair_kernel": ("moe_pair.cu", "moe_pair.h"),
+    "attn_kernel": ("attn.cu", "attn.h", "attn_piece.cuh", "attn_ptx.cuh"),
 }
 
 

@@ -17,13 +17,16 @@
 //               (its head dimension contiguous: an N-major operand)
 // With up to 16 rows (a decoded token, or a few) a thread per row would leave all
 // but a few lanes idle over 128 keys each: there the four lanes of a quad share
-// a row (tensor memory loads of 16 lanes x 256 bits), 32 keys each.
-// O stays in tensor memory.  m_i is the maximum of the first half tile that the row
-// sees, and moves on only when half a tile's p sum to more than 2^40: p, l and O
-// are floating point (bf16 has fp32's range), so a larger p costs no precision,
-// and the division by l_i makes any m_i as good as the maximum.  Otherwise a
-// tile's maximum is not computed at all.  When m_i does move, the softmax threads
-// rescale O themselves.
+// a row (tensor memory loads of 16 lanes x 256 bits), 32 keys each: one token over
+// 1000 takes 8.9 us so and 11.3 by a thread per row, 32 requests of one token over up
+// to 8000 97 and 103.
+// O stays in tensor memory.  Any m_i near the scores is as good as their maximum: p, l
+// and O are floating point (bf16 has fp32's range), so a larger p costs no precision,
+// and the division by l_i takes m_i out again.  So m_i is the first score that the row
+// sees, and its own p = 1 keeps l_i from vanishing; it moves, to the maximum of the
+// half tile, only when half a tile's p sum to more than 2^40, and the softmax threads
+// rescale O then.  Otherwise no maximum is computed (with the first half tile's
+// maximum to start from, a prompt of 77 tokens took 8.9 us instead of 8.2).
 //
 // Roles (384 threads): warps 0..3 and 4..7 the softmax and the results of
 // stream 0 and 1; warp 8 takes the work and loads keys, 11 loads queries and
@@ -33,6 +36,19 @@
 // A group (block, kv head) cut into pieces leaves partial (O, m, l) in the
 // workspace; the piece that finishes last joins them in their order, so
 // results do not depend on timing.  Every wait is bounded.
+//
+// What bounds it, and what it measured (32 query and 8 kv heads of 128 unless said;
+// peaks: a 6690 GB/s copy, 1867 TFLOP/s bf16):
+//   decode        the cache's bytes.  128 requests of 1000 to 16000 tokens, 4.14 GB:
+//                 608 to 617 us, 6.7 to 6.8 TB/s; 32 requests of up to 8000, 579 MB:
+//                 97 us, 6.0 TB/s (the start, 4 us, and the last pieces' join show)
+//   long prompts  the exponentials' turns and the products alike: 16384 tokens,
+//                 2.2 TFLOP, 1280 us (1.72 PFLOP/s) cool, 1380 us under the power cap
+//   head dim 64   the softmax threads: the products take half as long for the same
+//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 141 us,
+//                 the special function units busy for 31 % of it and each warp
+//                 waiting mostly on its own chain of loads, exponentials and stores
+//   single calls  latency: one token over 1000 8.9 us, a prompt of 77 8.2 us
 #include <cuda_runtime.h>
 
 #include "attn.h"
@@ -162,7 +178,7 @@ struct ShortList {
 };
 
 struct AttnMaps {
-    CUtensorMap q, q1, k, v;   // q: tq tokens of a group's heads; q1: one token's
+    CUtensorMap q, k, v;
 };
 
 // mbar_wait with a 32-bit clock and without the status bit (set once, at the
@@ -355,7 +371,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (warp == 11 && lane == 0) {
         tma_prefetch_map(&maps.q);
-        tma_prefetch_map(&maps.q1);
         tma_prefetch_map(&maps.k);
         tma_prefetch_map(&maps.v);
     }
@@ -493,7 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
             const int valid = wi.valid, pair = wi.pair, t0 = wi.t0, n = wi.t1 - t0, seen = wi.seen, kvh = wi.kvh;
-            const int tok0 = wi.tok0, all_tok = wi.ntok, row0 = tok0 - wi.qpos0;
+            const int tok0 = wi.tok0, row0 = tok0 - wi.qpos0;
             const int32_t *table = p.block_table + wi.req * p.table_stride;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
@@ -502,20 +517,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int cur = -1, nxt = kPaged ? pages_of(table, t0, seen) : -1;
             // the queries, once the previous piece's products have read theirs
             if (nitem > 1 && !wait(q_empty, (nitem - 2) & 1)) break;
-            constexpr int kFew = 4;
 #pragma unroll 1
             for (int s = 0; s <= pair; ++s) {
-                const int first = s * p.tq, ntok = min(p.tq, all_tok - first);
-                const bool few = ntok <= kFew;   // single tokens: their rows only, not the whole tile's
                 if (lane == 0) {
                     ++issued[kStages + s];
-                    mbar_expect_tx(&q_full[s], (few ? ntok : p.tq) * p.group * 128 * kHalves);
+                    mbar_expect_tx(&q_full[s], p.tq * p.group * 128 * kHalves);
                 }
                 __syncwarp();
-                if (mybox < (few ? ntok : 1))
-                    tma_load_3d_if(1, smem_u32(qbuf) + s * kTile + myhalf * (kAttnTileQ * 128) + mybox * p.group * 128,
-                                   few ? &maps.q1 : &maps.q, smem_u32(&q_full[s]), myhalf * 64, kvh * p.group,
-                                   tok0 + first + mybox);
+                if (lane < kHalves)
+                    tma_load_3d_if(1, smem_u32(qbuf) + s * kTile + lane * (kAttnTileQ * 128), &maps.q, smem_u32(&q_full[s]),
+                                   lane * 64, kvh * p.group, tok0 + s * p.tq);
             }
 #pragma unroll 1
             for (int t = 0; t < n && ok; ++t) {
@@ -703,7 +714,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // two streams fall into step, both in their exponentials and then both waiting for
             // the tensor cores.  With two query tiles they take turns instead: stream 1's
             // exponentials of a tile follow stream 0's, which follow stream 1's of the tile
-            // before.  A 16384-token prompt takes 1310 us so, 1600 without; over one to three
+            // before.  A 16384-token prompt takes 1280 us so, 1600 without; over one to three
             // tiles waiting for the turn costs more than it gives (77 tokens: 8.5 us without,
             // 9.3 with).
             const bool in_turns = !kOwnP && w.pair && n >= 4;
@@ -849,6 +860,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 64; ++e) x[e] = e < seen ? x[e] : -INFINITY;
                         }
+                        if (h == 0) m = m == -INFINITY ? x[0] : m;   // the first score (-infinity if it is not seen)
                         uint32_t pk[32];
                         float total;
                         auto exps = [&] {
@@ -1166,10 +1178,8 @@ cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
     {
         const uint64_t dims[3] = {D, static_cast<uint64_t>(p.heads), static_cast<uint64_t>(p.T)};
         const uint64_t st[2] = {bytes(p.q_head, p.heads), bytes(p.q_tok, p.T)};
-        const uint32_t box[3] = {64, G, static_cast<uint32_t>(p.tq)}, box1[3] = {64, G, 1};
-        if (!encode_map(&m.q, p.q, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_map(&m.q1, p.q, 3, dims, st, box1, CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
+        const uint32_t box[3] = {64, G, static_cast<uint32_t>(p.tq)};
+        if (!encode_map(&m.q, p.q, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     }
     if (p.paged) {
         const int page = 1 << p.page_shift;
@@ -1183,8 +1193,7 @@ cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
             !encode_map(&m.v, p.v, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     } else {
-        // long prompts: whole tiles; short ones: a tile reads at most 31 rows too many
-        p.box_rows = p.T >= 256 * static_cast<int64_t>(p.requests) ? kAttnTileK : 32;
+        p.box_rows = kAttnTileK;   // (32 rows a box: no faster for prompts of 1 to 400 tokens, 1 % slower for long ones)
         const uint64_t dims[3] = {D, static_cast<uint64_t>(p.kv_heads), static_cast<uint64_t>(p.T)};
         const uint64_t ks[2] = {bytes(p.k_head, p.kv_heads), bytes(p.k_tok, p.T)};
         const uint64_t vs[2] = {bytes(p.v_head, p.kv_heads), bytes(p.v_tok, p.T)};

@@ -12,6 +12,10 @@
 //   cut     all groups laid end to end and cut into one equal piece a CTA: they
 //           end together, but a group that spans pieces is written as partial
 //           results and joined
+// One token over 1000 takes 8.9 us cut and 12.3 whole, 32 requests of one token over up
+// to 8000 98 and 121; a 16384-token prompt 1460 cut and 1360 whole.
+// Whole groups run by sections of heads whose keys and values L2 holds together (a
+// 65536-token prompt of 8 kv heads: 21.1 ms, 22.4 with all heads at once).
 // One CTA, once a step.
 #include <cuda_runtime.h>
 
@@ -25,7 +29,7 @@ namespace lora {
 
 constexpr int kSchedThreads = 1024;
 constexpr int kSchedBuckets = 1024;          // block costs told apart by the sort
-constexpr int kMinPiece = 2;                 // key tiles of a piece, at least
+constexpr int kMinPiece = 2;                 // key tiles of a piece, at least (one token over 1000: 8.9 us, 9.2 with 1, 10.8 with 4)
 constexpr int kJoinSingle = 2, kJoinPair = 8; // what joining partial results costs, in key tiles
 constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads that run together (L2 holds 126 MB)
 

@@ -26,7 +26,8 @@ namespace lora {
 // in this call computes the page from the scan instead of reading the table that
 // another CTA may be writing.  One or two tokens a thread: a token costs a
 // search of its request (ten dependent shared loads for 777 requests), and with
-// eight a thread those searches were most of the time (13.7 us for 38 K tokens).
+// eight a thread those searches were most of the time (13.7 us for 38 K tokens; 7.5 us
+// now).  256 requests of one token: 4.8 us, the launch and two dependent scans.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 512;   // tokens of a CTA, more only when all SMs have some
 
@@ -175,7 +176,8 @@ cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream)
 // A copy: 16-byte units of K and V, consecutive threads taking consecutive units
 // of a head, then of a token.  HBM (or L2, for rows just written) bounds it, so a
 // thread has the four loads of two units in flight, and its slots with them,
-// before it stores anything.
+// before it stores anything.  7300 tokens of 8 heads of 128 (59.5 MB moved): 11.3 us,
+// 5.3 TB/s (11.5 us with one unit a thread); 32 tokens: 1.7 us.
 constexpr int kStoreThreads = 256;
 constexpr int kStoreUnits = 2;
 

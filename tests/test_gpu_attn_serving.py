@@ -1,5 +1,6 @@
 """The attention operators in use: the serving example from one end to the
 other, waits that run out, and a work list that does not fit its call."""
+import math
 import os
 import sys
 
@@ -125,3 +126,25 @@ def test_random_prompts(seed):
                                D ** -0.5))
         t += n
     assert_attn(o, lse, *[torch.cat(x) for x in zip(*parts)], f"{lens}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first", [-300.0, 300.0, -math.inf])
+@pytest.mark.parametrize("n", [1, 40])
+def test_first_keys_far_from_the_others(D, first, n):
+    """Each row's first visible score (and the first of every tile, so of each
+    piece of a split context) far below, far above, or -infinity beside the others."""
+    s = Step([n, n], [3000, 500], 4, 1, D, 16, seed=3)
+    q = torch.randn(s.T, 4, D, generator=torch.Generator().manual_seed(4)).to(BF)
+    q[:, :, 0] = 1.0
+    s.q, s.q_cpu, s.scale = q.cuda(), q.double(), 0.25
+    kc = s.k_cache.cpu()
+    for r, length in enumerate(s.kv):
+        for pos in range(0, length, 128):   # scale * q . k = first there
+            page, slot = int(s.table[r, pos // 16]), pos % 16
+            kc[page, 0, slot] = 0
+            kc[page, 0, slot, 0] = first / s.scale
+            s.keys[r][pos, 0] = kc[page, 0, slot].double()
+    s.k_cache.copy_(kc)
+    s.check(f"{first}")
+    s.check("with a schedule", sched=s.schedule())
