@@ -42,10 +42,11 @@
 //   decode        the cache's bytes.  128 requests of 1000 to 16000 tokens, 4.14 GB:
 //                 608 to 617 us, 6.7 to 6.8 TB/s; 32 requests of up to 8000, 579 MB:
 //                 97 us, 6.0 TB/s (the start, 4 us, and the last pieces' join show)
-//   long prompts  the exponentials' turns and the products alike: 16384 tokens,
-//                 2.2 TFLOP, 1280 us (1.72 PFLOP/s) cool, 1380 us under the power cap
+//   long prompts  16384 tokens, 2.2 TFLOP: 1280 to 1340 us (1.64 to 1.72 PFLOP/s, the
+//                 tensor cores busy for 73 % of the cycles), 1380 to 1400 back to back,
+//                 where the power cap bounds it (a plain product then has 1710 TFLOP/s)
 //   head dim 64   the softmax threads: the products take half as long for the same
-//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 141 us,
+//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 139 us,
 //                 the special function units busy for 31 % of it and each warp
 //                 waiting mostly on its own chain of loads, exponentials and stores
 //   single calls  latency: one token over 1000 8.9 us, a prompt of 77 8.2 us
