@@ -111,6 +111,7 @@ struct AttnParams {
     int64_t page_stride, head_stride, slot_stride;
     int32_t paged;
     int32_t box_rows;        // keys of one TMA box
+    int32_t o_wide;          // every row of o starts on a 32-byte boundary
     int64_t T;
     int32_t requests;
     int32_t short_list;      // 1: the list is made from cu in the kernel (hdr and blocks are not read)

@@ -169,6 +169,8 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->q_head = a->q_head_stride;
     p->o_tok = a->o_token_stride;
     p->o_head = a->o_head_stride;
+    p->o_wide = aligned(a->o, 32) && (a->num_tokens == 1 || a->o_token_stride % 16 == 0) &&
+                (a->heads == 1 || a->o_head_stride % 16 == 0);
     p->heads = a->heads;
     p->kv_heads = a->kv_heads;
     p->group = a->heads / a->kv_heads;
