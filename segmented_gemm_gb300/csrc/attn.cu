@@ -176,11 +176,23 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
+// The same with its loop out of line, for the roles that only issue work.  What
+// they run per piece and the softmax do not fit the instruction cache together, so code
+// that only waits is kept out of it: 12 prompts of 500 to 700 tokens take 59.5 us
+// instead of 62.5, chunks of up to 700 over 9000 133 instead of 135.
+__device__ __noinline__ bool attn_wait_loop(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t limit)
+{
+    return attn_wait(bar, parity, abort_flag, limit);
+}
+__device__ __forceinline__ bool attn_wait_far(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t limit)
+{
+    return mbar_try_wait(bar, parity) || attn_wait_loop(bar, parity, abort_flag, limit);
+}
+
 // Bounded wait until *count > n (shared memory; what it counts is ordered by the
 // barrier that is waited on next).
-__device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatile int *abort_flag, uint32_t limit)
+__device__ __noinline__ bool attn_wait_count_loop(const int *count, int n, volatile int *abort_flag, uint32_t limit)
 {
-    if (ld_volatile_shared(count) > n) return true;
     const uint32_t t0 = static_cast<uint32_t>(clock());
     while (ld_volatile_shared(count) <= n) {
         const uint32_t most = *abort_flag ? min(limit, static_cast<uint32_t>(kWaitShort)) : limit;
@@ -190,6 +202,10 @@ __device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatil
         }
     }
     return true;
+}
+__device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatile int *abort_flag, uint32_t limit)
+{
+    return ld_volatile_shared(count) > n || attn_wait_count_loop(count, n, abort_flag, limit);
 }
 
 // First row of the partial results of a group's piece k, of the group that starts in
@@ -305,10 +321,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles)) != 0;
     };
+    auto wait_far = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, attn_wait_far(smem_u32(bar), parity, abort_flag, p.wait_cycles)) != 0;
+    };
     // The same without agreement: lanes go on together whatever it says, and
     // agree at the end of their loop's round.
     auto wait_each = [&](uint64_t *bar, uint32_t parity) {
-        return attn_wait(smem_u32(bar), parity, abort_flag, p.wait_cycles);
+        return attn_wait_far(smem_u32(bar), parity, abort_flag, p.wait_cycles);
     };
     // load number f of stage s (from 0) has been issued
     auto wait_issued = [&](uint32_t s, uint32_t f) {
@@ -381,7 +400,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int boxes = (max(0, min(kAttnTileK, seen - tile * kAttnTileK)) + box - 1) >> box_shift;
         const uint32_t s = i % kStages, f = i / kStages;
         // the stage's previous load has been issued (perhaps by the other loader), and is used up
-        if (f > 0 && !(wait_issued(s, f - 1) && wait(&empty[s], (f - 1) & 1))) return false;
+        if (f > 0 && !(wait_issued(s, f - 1) && wait_far(&empty[s], (f - 1) & 1))) return false;
         if (lane == 0) {
             st_release_shared(&issued[s], static_cast<int>(f) + 1);
             mbar_expect_tx(&full[s], boxes * box * 128 * kHalves);
@@ -422,7 +441,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         while (more) {
             // the next piece, handed to the other roles
             const int is = nitem % kItems;
-            if (nitem >= kItems && !wait(&item_empty[is], (nitem / kItems - 1) & 1)) ok = false;
+            if (nitem >= kItems && !wait_far(&item_empty[is], (nitem / kItems - 1) & 1)) ok = false;
             if (nitem == 0 && !p.short_list) {
                 if (lane < 16) reinterpret_cast<int32_t *>(&items[is])[lane] = word;   // laid out by the schedule
                 __syncwarp();
@@ -484,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool ok = true;
         while (ok) {
             const int is = nitem % kItems;
-            if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
+            if (!wait_far(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
             const int valid = wi.valid, pair = wi.pair, t0 = wi.t0, n = wi.t1 - t0, seen = wi.seen, kvh = wi.kvh;
             const int tok0 = wi.tok0, row0 = tok0 - wi.qpos0;
@@ -495,7 +514,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!valid) break;
             int cur = -1, nxt = kPaged ? pages_of(table, t0, seen) : -1;
             // the queries, once the previous piece's products have read theirs
-            if (nitem > 1 && !wait(q_empty, (nitem - 2) & 1)) break;
+            if (nitem > 1 && !wait_far(q_empty, (nitem - 2) & 1)) break;
 #pragma unroll 1
             for (int s = 0; s <= pair; ++s) {
                 if (lane == 0) {
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool ok = true;
         while (ok) {
             const int is = nitem % kItems;
-            if (!wait(&item_full[is], (nitem / kItems) & 1)) break;
+            if (!wait_far(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
             const int valid = uniform(wi.valid), pair = uniform(wi.pair), t0 = uniform(wi.t0);
             const int n = uniform(wi.t1) - t0;
