@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!more) break;
             if (cut && !have_b) {   // of the first piece's group, for what comes after it
                 b = p.blocks[w.blk];
-                pos = b.pre * p.kv_heads + kvh * (b.tiles + kAttnItemCost) + kAttnItemCost + w.t1;
+                pos = group_start(hdr, b, kvh, p.kv_heads, pair) + (w.t1 << (pair ? hdr.cut - 1 : 0));
                 have_b = true;
             }
             int next = 0, cur = -1, nxt = -1;

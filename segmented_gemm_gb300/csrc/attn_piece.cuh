@@ -34,22 +34,28 @@ __device__ __forceinline__ void whole_unit(const AttnHdr &h, int kv_heads, uint3
     *kvh = static_cast<int>(sec * h.sec_heads + rem - at * hs);
 }
 
+// cut: where the tiles of group (b, kvh) start in the list, a gap into its share
+__device__ __forceinline__ int group_start(const AttnHdr &h, const AttnBlock &b, int kvh, int kv_heads, bool pair)
+{
+    return b.pre * kv_heads + kvh * attn_share(b.tiles, pair, h.cut) + attn_gap(h.cut);
+}
+
 // cut: the part of group (b, kvh) that lies in [pos, end) of the list, where unit
-// `unit` ends; valid 0 if it starts past the end.  The group's tiles start
-// kAttnItemCost into its share of the list.  *pos moves to the end of what was taken.
+// `unit` ends; valid 0 if it starts past the end.  *pos moves to the end of what was taken.
 __device__ __forceinline__ AttnItem cut_piece(const AttnHdr &h, const AttnBlock &b, int blk, int kvh, int kv_heads, int tq,
                                               int unit, int end, int *pos)
 {
     AttnItem w = item_of(b, blk, kvh, tq);
-    const int g0 = b.pre * kv_heads + kvh * (b.tiles + kAttnItemCost) + kAttnItemCost;
+    const int g0 = group_start(h, b, kvh, kv_heads, w.pair), shift = w.pair ? h.cut - 1 : 0;   // a tile weighs 1 << shift
     w.valid = *pos < end && g0 < end;
-    w.t0 = max(0, *pos - g0);
-    w.t1 = min(b.tiles, end - g0);
-    const uint32_t c = h.unit_cost, u0 = static_cast<uint32_t>(g0) / c, u1 = static_cast<uint32_t>(g0 + b.tiles - 1) / c;
+    w.t0 = max(0, *pos - g0) >> shift;
+    w.t1 = min(b.tiles, (end - g0) >> shift);
+    const uint32_t c = h.unit_cost, u0 = static_cast<uint32_t>(g0) / c;
+    const uint32_t u1 = static_cast<uint32_t>(g0 + ((b.tiles - 1) << shift)) / c;
     w.parts = static_cast<int>(u1 - u0 + 1);
     w.slot = 2 * unit + (static_cast<uint32_t>(unit) == u0);
     w.unit0 = static_cast<int>(u0);
-    *pos = g0 + w.t1;
+    *pos = g0 + (w.t1 << shift);
     return w;
 }
 

@@ -30,7 +30,7 @@ namespace lora {
 constexpr int kSchedThreads = 1024;
 constexpr int kSchedBuckets = 1024;          // block costs told apart by the sort
 constexpr int kMinPiece = 2;                 // key tiles of a piece, at least (one token over 1000: 8.9 us, 9.2 with 1, 10.8 with 4)
-constexpr int kJoinSingle = 2, kJoinPair = 8; // what joining partial results costs, in key tiles
+constexpr int kJoinSingle = 2, kJoinPair = 16; // what joining partial results costs, in a cut list's units
 constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads that run together (L2 holds 126 MB)
 
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const AttnSchedParams p)
@@ -41,12 +41,14 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     __shared__ int32_t hist[kSchedBuckets];
     __shared__ int32_t unit_blk[kAttnMaxCtas];
     __shared__ int32_t s_max, s_pair, s_tail;
+    __shared__ unsigned long long s_shares;
     const int tid = threadIdx.x;
     const int R = p.R, tb = 2 * p.tq;
     if (tid == 0) {
         s_max = 0;
         s_tail = 1;
         s_pair = 0;
+        s_shares = 0;
     }
     hist[tid] = 0;
     pdl_wait();
@@ -110,11 +112,12 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
         return k;
     };
     auto bucket = [](int tiles) { return kSchedBuckets - min(tiles, kSchedBuckets); };
-    int64_t tiles = 0;
+    int64_t tiles = 0, shares = 0;   // shares: in a list with pairs
     int my_max = 0, my_pair = 0;
     for (int b = tid; b < nb; b += kSchedThreads) {
         const AttnBlock k = block_of(b);
         tiles += k.tiles;
+        shares += attn_share(k.tiles, k.ntok > p.tq, 2);
         my_max = max(my_max, k.tiles);
         my_pair |= k.ntok > p.tq;
         atomicAdd(&hist[bucket(k.tiles)], 1);
@@ -122,8 +125,11 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     if (my_max) atomicMax(&s_max, my_max);
     if (my_pair) atomicOr(&s_pair, 1);
     if (bad) atomicOr(p.counters + CNT_STATUS, LORA_DEV_BAD_LENGTH);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) shares += __shfl_xor_sync(0xffffffffu, shares, d);
+    if ((tid & 31) == 0 && shares) atomicAdd(&s_shares, static_cast<unsigned long long>(shares));
     int64_t all_tiles, total;
-    block_scan_i64(tiles, wsum, &all_tiles);   // also makes hist, s_max and s_pair visible
+    block_scan_i64(tiles, wsum, &all_tiles);   // also makes hist, s_max, s_pair and s_shares visible
     const int32_t here = hist[tid];
     const int32_t before = static_cast<int32_t>(block_scan_i64(here, wsum, &total));
     hist[tid] = before;   // first place of each cost in the longest-first order
@@ -134,15 +140,17 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     __syncthreads();
 
     const int64_t groups = static_cast<int64_t>(nb) * p.kv_heads;
-    const int64_t cost = all_tiles * p.kv_heads + groups * kAttnItemCost;
-    const int64_t each = max((cost + p.ctas - 1) / p.ctas, static_cast<int64_t>(kMinPiece));
-    const int64_t whole = max(groups >= p.ctas ? each + s_tail / 2 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
+    const int weight = s_pair ? 2 : 1;
+    const int64_t cost = (s_pair ? static_cast<int64_t>(s_shares) : all_tiles + static_cast<int64_t>(nb) * kAttnItemCost) * p.kv_heads;
+    const int64_t even = (cost + p.ctas - 1) / p.ctas;
+    const int64_t each = max((even + weight - 1) & -static_cast<int64_t>(weight), static_cast<int64_t>(kMinPiece));
+    const int64_t whole = weight * max(groups >= p.ctas ? each / weight + s_tail / 2 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
     // (a list too long for 32-bit positions is never short of units)
     const bool cut = each + (s_pair ? kJoinPair : kJoinSingle) < whole && cost + each < INT32_MAX;
     AttnHdr h = {};
     h.stamp = p.stamp;
     h.nblocks = nb;
-    h.cut = cut;
+    h.cut = cut ? weight : 0;
     h.cost = cut ? static_cast<int32_t>(cost) : 0;
     h.unit_cost = cut ? static_cast<int32_t>(each) : 0;
     h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups, static_cast<int64_t>(INT32_MAX)));
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
             const int b = b0 + tid;
             AttnBlock k = {};
             if (b < nb) k = block_of(b);
-            const int32_t own = b < nb ? k.tiles + kAttnItemCost : 0;
+            const int32_t own = b < nb ? attn_share(k.tiles, k.ntok > p.tq, weight) : 0;
             k.pre = static_cast<int32_t>(carry + block_scan_i64(own, wsum, &total));
             if (b < nb) {
                 p.blocks[b] = k;
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
                 blk = unit_blk[tid];
                 const AttnBlock b = p.blocks[blk];
                 int pos = tid * h.unit_cost;
-                kvh = (pos - b.pre * p.kv_heads) / (b.tiles + kAttnItemCost);
+                kvh = (pos - b.pre * p.kv_heads) / attn_share(b.tiles, b.ntok > p.tq, weight);
                 w = cut_piece(h, b, blk, kvh, p.kv_heads, p.tq, tid, min(pos + h.unit_cost, h.cost), &pos);
             }
         }
