@@ -42,12 +42,12 @@
 //   decode        the cache's bytes.  128 requests of 1000 to 16000 tokens, 4.14 GB:
 //                 608 to 617 us, 6.7 to 6.8 TB/s; 32 requests of up to 8000, 579 MB:
 //                 97 us, 6.0 TB/s (the start, 4 us, and the last pieces' join show)
-//   long prompts  16384 tokens, 2.2 TFLOP: 1280 to 1340 us (1.64 to 1.72 PFLOP/s, the
-//                 tensor cores busy for 73 % of the cycles), 1380 to 1400 back to back,
+//   long prompts  16384 tokens, 2.2 TFLOP: 1260 to 1310 us (1.68 to 1.74 PFLOP/s, the
+//                 tensor cores busy for 76 % of the cycles), 1335 to 1400 back to back,
 //                 where the power cap bounds it (a plain product then has 1710 TFLOP/s)
 //   head dim 64   the softmax threads: the products take half as long for the same
-//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 139 us,
-//                 the special function units busy for 31 % of it and each warp
+//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 133 us,
+//                 the special function units busy for 33 % of it and each warp
 //                 waiting mostly on its own chain of loads, exponentials and stores
 //   single calls  latency: one token over 1000 8.9 us, a prompt of 77 8.2 us
 #include <cuda_runtime.h>
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // two streams fall into step, both in their exponentials and then both waiting for
             // the tensor cores.  With two query tiles they take turns instead: stream 1's
             // exponentials of a tile follow stream 0's, which follow stream 1's of the tile
-            // before.  A 16384-token prompt takes 1280 us so, 1600 without; over one to three
+            // before.  A 16384-token prompt took 1280 us so, 1600 without; over one to three
             // tiles waiting for the turn costs more than it gives (77 tokens: 8.5 us without,
             // 9.3 with).
             const bool in_turns = !kOwnP && w.pair && n >= 4;

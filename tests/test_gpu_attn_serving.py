@@ -148,3 +148,16 @@ def test_first_keys_far_from_the_others(D, first, n):
     s.k_cache.copy_(kc)
     s.check(f"{first}")
     s.check("with a schedule", sched=s.schedule())
+
+
+@pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (8, 1, 64)])
+def test_chunks_beside_single_tokens_split_over_the_gpu(H, Hk, D):
+    """Pieces of pairs of query tiles and of single ones in one cut list, whose tiles weigh differently."""
+    tq = 128 * Hk // H
+    new = [1, 2 * tq + 1, 1, tq, 0, tq + 1, 1, 3]
+    s = Step(new, [2500, 2 * tq + 2001, 129, tq + 700, 40, tq + 1, 1, 1800], H, Hk, D, 16, seed=D)
+    s.check("mixed")
+    sched = s.schedule()
+    first = s.run(sched=sched)
+    again = s.run(sched=sched)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
