@@ -9,6 +9,8 @@
 //   pair     two query tiles against the same key tiles (long chunks, prompts)
 //   single   one query tile, the key tiles dealt to the streams in turn
 //            (decode and short chunks, where the cache's bytes bound the call)
+//   two      single tokens (or a few) of large batches: two kv heads of a request, a
+//            stream each, so that contexts of a tile or two keep both busy
 // Per stream and key tile of 128 keys, all on the tensor cores:
 //   S = Q K^T   both from shared memory, S [128 x 128] fp32 in tensor memory
 //   softmax     a thread per row: S to registers, p = 2^(..), P as bf16 back
@@ -279,7 +281,8 @@ __device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0
     }
 }
 
-template <int DP, bool kPaged>
+// kTwo: lists whose units are two heads of few rows are run too
+template <int DP, bool kPaged, bool kTwo>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
 {
@@ -451,6 +454,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int blk, kvh;
                     whole_unit(hdr, p.kv_heads, unit, &blk, &kvh);
                     w = item_of(p.short_list ? list.block(p, blk) : p.blocks[blk], blk, kvh, p.tq);
+                    if (kTwo) w.valid += hdr.unit_cost;
                 } else if (cut && ok) {
                     const AttnItem &last = items[(nitem - 1) % kItems];
                     int blk = last.blk, kvh = last.kvh + 1;
@@ -464,7 +468,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
             }
             const AttnItem &w = items[is];
-            const int pair = w.pair, t0 = w.t0, n = w.t1 - t0, seen = w.seen, kvh = w.kvh, row0 = w.tok0 - w.qpos0;
+            const int two = kTwo ? w.valid >> 1 : 0;   // two heads: their tiles take turns, 2 t + stream
+            const int pair = w.pair, t0 = w.t0, n = (w.t1 - t0) << two, seen = w.seen, kvh = w.kvh, row0 = w.tok0 - w.qpos0;
             const int32_t *table = p.block_table + w.req * p.table_stride;
             more = w.valid;
             if (lane == 0) mbar_arrive(&item_full[is]);
@@ -478,15 +483,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int next = 0, cur = -1, nxt = -1;
 #pragma unroll 1
             for (int t = 0; t < n; ++t) {
-                if (kPaged && (t & in_win) == 0) {
+                const int tile = t >> two, head = kvh + (t & two);
+                if (kPaged && (tile & in_win) == 0 && tile << two == t) {
                     cur = t == 0 ? pages_of(table, t0, seen) : nxt;
-                    nxt = pages_of(table, t0 + t + in_win + 1, seen);
+                    nxt = pages_of(table, t0 + tile + in_win + 1, seen);
                 }
-                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & in_win) * per_tile + mybox) : 0;
+                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (tile & in_win) * per_tile + mybox) : 0;
                 // whole: the next unit is claimed late, so that the last ones go to the CTAs
                 // that come free first, and under the wait for the last tile's stage
                 if (!cut && t == n - 1 && lane == 0) next = atomicAdd(p.counters + ACNT_NEXT, 1);
-                ok = load_tile(&maps.k, it + load_of_key(pair, t), t0 + t, page, seen, kvh, row0);
+                ok = load_tile(&maps.k, it + load_of_key(pair, t), t0 + tile, page, seen, head, row0);
                 if (!ok) break;
             }
             it += 2 * n;
@@ -505,7 +511,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int is = nitem % kItems;
             if (!wait_far(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
-            const int valid = wi.valid, pair = wi.pair, t0 = wi.t0, n = wi.t1 - t0, seen = wi.seen, kvh = wi.kvh;
+            const int valid = wi.valid, two = kTwo ? valid >> 1 : 0;
+            const int pair = wi.pair, t0 = wi.t0, n = (wi.t1 - t0) << two, seen = wi.seen, kvh = wi.kvh;
             const int tok0 = wi.tok0, row0 = tok0 - wi.qpos0;
             const int32_t *table = p.block_table + wi.req * p.table_stride;
             __syncwarp();
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // the queries, once the previous piece's products have read theirs
             if (nitem > 1 && !wait_far(q_empty, (nitem - 2) & 1)) break;
 #pragma unroll 1
-            for (int s = 0; s <= pair; ++s) {
+            for (int s = 0; s <= (pair | two); ++s) {
                 if (lane == 0) {
                     ++issued[kStages + s];
                     mbar_expect_tx(&q_full[s], p.tq * p.group * 128 * kHalves);
@@ -524,16 +531,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
                 if (lane < kHalves)
                     tma_load_3d_if(1, smem_u32(qbuf) + s * kTile + lane * (kAttnTileQ * 128), &maps.q, smem_u32(&q_full[s]),
-                                   lane * 64, kvh * p.group, tok0 + s * p.tq);
+                                   lane * 64, (kvh + (s & two)) * p.group, tok0 + (two ? 0 : s * p.tq));
             }
 #pragma unroll 1
             for (int t = 0; t < n && ok; ++t) {
-                if (kPaged && (t & in_win) == 0) {
+                const int tile = t >> two, head = kvh + (t & two);
+                if (kPaged && (tile & in_win) == 0 && tile << two == t) {
                     cur = nxt;
-                    nxt = pages_of(table, t0 + t + in_win + 1, seen);
+                    nxt = pages_of(table, t0 + tile + in_win + 1, seen);
                 }
-                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (t & in_win) * per_tile + mybox) : 0;
-                ok = load_tile(&maps.v, it + load_of_value(pair, t, n), t0 + t, page, seen, kvh, row0);
+                const int page = kPaged ? __shfl_sync(0xffffffffu, cur, (tile & in_win) * per_tile + mybox) : 0;
+                ok = load_tile(&maps.v, it + load_of_value(pair, t, n), t0 + tile, page, seen, head, row0);
             }
             it += 2 * n;
         }
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!wait_far(&item_full[is], (nitem / kItems) & 1)) break;
             const AttnItem &wi = items[is];
             const int valid = uniform(wi.valid), pair = uniform(wi.pair), t0 = uniform(wi.t0);
-            const int n = uniform(wi.t1) - t0;
+            const int two = kTwo ? valid >> 1 : 0, n = (uniform(wi.t1) - t0) << two;
             const int seen = uniform(wi.seen) - t0 * kAttnTileK;   // keys that any row sees, from t0
             // pair: both streams go through all tiles, stream 0 uses its first `mine`;
             // single: stream s uses tiles s, s + 2, ...
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!pair) umma_commit_if(lead, &empty[st]);
             };
             ok &= wait_each(&q_full[0], nq0++ & 1);
-            if (pair) ok &= wait_each(&q_full[1], nq1++ & 1);
+            if (pair | two) ok &= wait_each(&q_full[1], nq1++ & 1);
             if (all == 0) commit(q_empty);
             // Round k: tile k's values, then the keys of tile k + 1, whose scores go over
             // the P just read (round -1: only keys).  What can be waited for ahead of P
@@ -598,9 +606,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 auto scores = [&] {   // of tile k + 1
                     if (k + 1 >= mine) return;
                     tc_fence_after();
-                    const int keys = min(kAttnTileK, seen - tk * kAttnTileK);
+                    const int keys = min(kAttnTileK, seen - (tk >> two) * kAttnTileK);
                     const uint32_t idesc = umma_idesc_bf16(kAttnTileQ, max(16, (keys + 15) & ~15));
-                    const uint32_t qd = qlo + (pair && s ? kTile >> 4 : 0), kd = klo + stk * (kTile >> 4);
+                    const uint32_t qd = qlo + ((pair | two) && s ? kTile >> 4 : 0), kd = klo + stk * (kTile >> 4);
                     const uint32_t lead = elect_one();
                     auto step = [&](int kk) {
                         const uint32_t o = (kk >> 2) * ((kAttnTileK * 128) >> 4) + (kk & 3) * 2;
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     umma_commit_if(lead, &s_full[s]);
                 };
                 const bool values = k >= 0 && k < mine;
-                const int keys = values ? min(kAttnTileK, seen - tv * kAttnTileK) : 0;
+                const int keys = values ? min(kAttnTileK, seen - (tv >> two) * kAttnTileK) : 0;
                 const uint32_t vd = vlo + stv * (kTile >> 4), par = np & 1;
                 auto step = [&](uint32_t lead, int kk) {
                     umma_ts_if(lead, o_cells, p_cells + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : k > 0);
@@ -700,14 +708,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ++nitem;
             if (!w.valid) break;
             const int n = w.t1 - w.t0;
+            const bool own = kTwo && w.valid == 2;   // a head of its own for each stream
             // key tiles of the two streams
-            const int cnt0 = w.pair ? max(0, min(w.t1, w.end0) - w.t0) : (n + 1) / 2, cnt1 = w.pair ? n : n / 2;
+            const int cnt0 = w.pair ? max(0, min(w.t1, w.end0) - w.t0) : own ? n : (n + 1) / 2, cnt1 = w.pair || own ? n : n / 2;
             const int mine_n = s ? cnt1 : cnt0;
             const int i = r / G, tok = (w.pair && s ? p.tq : 0) + i;   // my token of the block
             const bool row_ok = i < p.tq && tok < w.ntok;
             const int limit = row_ok ? max(0, min(w.kv_len, w.qpos0 + tok + 1)) : 0;
             const bool live = __any_sync(0xffffffffu, limit > 0);
-            const bool narrow = kPaged && !w.pair && w.ntok * G <= 16, two = w.ntok * G > 8;   // two: rows past the eighth
+            const bool narrow = kPaged && !w.pair && w.ntok * G <= kAttnFewRows, two = w.ntok * G > 8;   // two: rows past the eighth
             // Where P shares S's cells a stream's softmax and products alternate; left alone the
             // two streams fall into step, both in their exponentials and then both waiting for
             // the tensor cores.  With two query tiles they take turns instead: stream 1's
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 nlim[h] = t < w.ntok ? max(0, min(w.kv_len, w.qpos0 + t + 1)) : 0;
             }
             for (int k = 0; k < mine_n; ++k) {
-                const int tile = w.pair ? w.t0 + k : w.t0 + s + 2 * k;
+                const int tile = w.pair || own ? w.t0 + k : w.t0 + s + 2 * k;
                 const int rem = limit - tile * kAttnTileK;   // my visible columns of this tile
                 if (!wait(&s_full[s], ns++ & 1)) break;
                 tc_fence_after();
@@ -949,13 +958,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         nl[h] += __shfl_xor_sync(0xffffffffu, nl[h], 1);
                         nl[h] += __shfl_xor_sync(0xffffffffu, nl[h], 2);
-                        if (quad == 0 && (lane & 3) == 0)
+                        if (!own && quad == 0 && (lane & 3) == 0)
                             stats[(s ? 0 : 64) + (lane >> 2) + 8 * h] = make_float2(nm[h], nl[h]);
                     }
                 } else if (s == 1) {
                     stats[r] = make_float2(m, l);
                 }
-                meet();
+                if (!own) meet();
                 if (s == 0 && !narrow) {
                     const float2 st = stats[r];
                     const float mm = fmaxf(m, st.x);
@@ -970,32 +979,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool mine = w.pair || s == 0;
             const int rho = tok * G + g;   // my row of the block
             if (narrow) {
-                // rows by quads, as in the softmax: stream s's first warp joins half of the
-                // columns, both streams' O of the row by one load each
+                // rows by quads, as in the softmax.  Stream s's first warp joins half of the
+                // columns, both streams' O of the row by one load each; or (own) it has all
+                // columns of its own rows, a half by each load
                 if (quad == 0) {
                     const bool whole = w.parts == 1;
                     constexpr int kCols = DP / 2;   // columns of a stream's warp
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int row = (lane >> 2) + 8 * h;
-                        const float2 a = stats[64 + row], b = stats[row];
+                        const float2 a = own ? make_float2(nm[h], nl[h]) : stats[64 + row], b = own ? a : stats[row];
                         const float mm = fmaxf(a.x, b.x);
                         const bool u0 = a.y != 0.f, u1 = b.y != 0.f;
                         const float e0 = u0 ? ex2((a.x - mm) * c) : 0.f, e1 = u1 ? ex2((b.x - mm) * c) : 0.f;
                         nm[h] = mm;
-                        nl[h] = a.y * e0 + b.y * e1;
+                        nl[h] = own ? a.y : a.y * e0 + b.y * e1;
                         const float inv = whole && nl[h] != 0.f ? 1.f / nl[h] : 1.f;
                         nf[h][0] = e0 * inv;
                         nf[h][1] = e1 * inv;
                         nu[h][0] = u0;
                         nu[h][1] = u1;
                     }
-                    const uint32_t cells = tmem + kColO + s * kCols;
-                    float y[2][kCols / 2];   // [stream][4 j + 2 h + e]
+                    const uint32_t cells = tmem + kColO + s * (own ? DP : kCols), next = own ? kCols : DP;
+                    float y[2][kCols / 2];   // [stream, or half][4 j + 2 h + e]
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        if (DP == 128) tmem_ld_16x256_half(cells + q * DP, y[q]);
-                        else tmem_ld_16x256_quarter(cells + q * DP, y[q]);
+                        if (DP == 128) tmem_ld_16x256_half(cells + q * next, y[q]);
+                        else tmem_ld_16x256_quarter(cells + q * next, y[q]);
                     }
                     tmem_ld_wait();
                     tmem_use<kCols / 2>(y[0]);
@@ -1004,12 +1014,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         const int row = (lane >> 2) + 8 * h, t = row / G, gg = row - t * G;
                         if (t >= w.ntok) continue;
-                        const int head = w.kvh * G + gg, c0 = s * kCols + 2 * (lane & 3);
+                        const int head = (w.kvh + (own ? s : 0)) * G + gg, c0 = (own ? 0 : s * kCols) + 2 * (lane & 3);
                         const int64_t at = static_cast<int64_t>(w.tok0) + t;
                         uint16_t *out = p.o + at * p.o_tok + head * p.o_head;
                         float *part = p.part + (static_cast<int64_t>(w.slot) * p.part_rows + row) * D;
 #pragma unroll
                         for (int j = 0; j < kCols / 8; ++j) {
+                            if (own) {
+#pragma unroll
+                                for (int q = 0; q < 2; ++q)
+                                    if (c0 + 8 * j + q * kCols < D)
+                                        *reinterpret_cast<uint32_t *>(out + c0 + 8 * j + q * kCols) =
+                                            nu[h][0] ? pack_bf16x2(y[q][4 * j + 2 * h] * nf[h][0], y[q][4 * j + 2 * h + 1] * nf[h][0])
+                                                     : 0;
+                                continue;
+                            }
                             float v[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
@@ -1019,7 +1038,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             if (whole) *reinterpret_cast<uint32_t *>(out + c0 + 8 * j) = pack_bf16x2(v[0], v[1]);
                             else *reinterpret_cast<float2 *>(part + c0 + 8 * j) = make_float2(v[0], v[1]);
                         }
-                        if (s == 0 && (lane & 3) == 0) {
+                        if ((own || s == 0) && (lane & 3) == 0) {
                             if (!whole)
                                 p.part_ml[static_cast<int64_t>(w.slot) * p.part_rows + row] = make_float2(nm[h], nl[h]);
                             else if (p.lse)
@@ -1121,7 +1140,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     if (threadIdx.x == 0) p.counters[ACNT_GROUP + w.unit0] = 0;
                 }
-            } else if (!w.pair) {
+            } else if (!w.pair && !own) {
                 tc_fence_before();
                 meet();   // O of stream 1 and its stats have been read
             }
@@ -1152,7 +1171,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int DP, bool kPaged>
+template <int DP, bool kPaged, bool kTwo>
 static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_t stream)
 {
     static int configured[64] = {0};
@@ -1161,7 +1180,7 @@ static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_
     constexpr int bytes = AttnSmem<DP>::kBytes;
     if (dev >= 64 || !configured[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(attn_kernel<DP, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaFuncSetAttribute(attn_kernel<DP, kPaged, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = 1;
     }
@@ -1172,7 +1191,7 @@ static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     pdl_attribute(cfg, at);
-    return cudaLaunchKernelEx(&cfg, attn_kernel<DP, kPaged>, maps, p);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<DP, kPaged, kTwo>, maps, p);
 }
 
 cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
@@ -1211,8 +1230,9 @@ cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
             !encode_map(&m.v, p.v, 3, dims, vs, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    if (p.head_dim <= 64) return p.paged ? launch<64, true>(m, p, stream) : launch<64, false>(m, p, stream);
-    return p.paged ? launch<128, true>(m, p, stream) : launch<128, false>(m, p, stream);
+    if (!p.paged) return p.head_dim <= 64 ? launch<64, false, false>(m, p, stream) : launch<128, false, false>(m, p, stream);
+    if (p.two) return p.head_dim <= 64 ? launch<64, true, true>(m, p, stream) : launch<128, true, true>(m, p, stream);
+    return p.head_dim <= 64 ? launch<64, true, false>(m, p, stream) : launch<128, true, false>(m, p, stream);
 }
 
 }  // namespace lora

@@ -21,6 +21,7 @@ namespace lora {
 
 constexpr int kAttnTileQ = 128;     // rows of one query tile (UMMA M): tokens x the group's heads
 constexpr int kAttnTileK = 128;     // keys of one key tile (UMMA N)
+constexpr int kAttnFewRows = 16;    // rows of a block that take the quads' path
 constexpr int kAttnMaxCtas = 160;   // upper bound on the persistent grid
 
 // counter block entries (int32); the status word is lora.h's CNT_STATUS (0)
@@ -64,14 +65,14 @@ struct __align__(16) AttnHdr {
     int32_t cut;        // 0: a unit is one (block, head), blocks longest first; 1, 2: unit_cost of the list's
                         // cost, with this weight of a pair's tiles
     int32_t sec_heads;  // heads whose blocks run together (cut 0)
-    int32_t unit_cost;  // cut
+    int32_t unit_cost;  // cut; whole: 1 if a unit is a block and two kv heads
     int32_t cost;       // of all blocks and heads (cut)
     uint64_t stamp;     // of the sizes that it was made for (sched_stamp)
 };
 
 // A piece of one (block, kv head) group: key tiles [t0, t1).
 struct __align__(16) AttnItem {
-    int32_t valid;    // 0: no more
+    int32_t valid;    // 0: no more; 2: two kv heads, kvh and the next, a stream each (few rows)
     int32_t pair;     // two query tiles (their streams share the key tiles), or one
     int32_t req, tok0, ntok, qpos0, kv_len;
     int32_t seen;     // keys that any of its rows sees
@@ -92,7 +93,7 @@ struct AttnLayout {
 
 struct AttnSchedParams {
     const int32_t *cu, *kv_len;
-    int32_t R, tq, kv_heads, head_dim, ctas;
+    int32_t R, tq, group, kv_heads, head_dim, ctas, two;
     int64_t T, max_kv, max_blocks;
     uint64_t stamp;
     AttnHdr *hdr;
@@ -126,6 +127,7 @@ struct AttnParams {
     int32_t o_wide;          // every row of o starts on a 32-byte boundary
     int64_t T;
     int32_t requests;
+    int32_t two;             // units of two heads may be in the list (two_heads)
     int32_t short_list;      // 1: the list is made from cu in the kernel (hdr and blocks are not read)
     const int32_t *cu;
     int32_t ctas;

@@ -109,32 +109,48 @@ static int check_ws(const void *ws, size_t bytes, size_t need)
 
 // What the places and the extents of a list in ws depend on, in 64 bits: a
 // workspace may have been given to a step of other sizes since.
-static uint64_t sched_stamp(const AttnLayout &L, int64_t T, int32_t R, int32_t kv_heads, int32_t head_dim, int32_t ctas)
+static uint64_t sched_stamp(const AttnLayout &L, int64_t T, int32_t R, int32_t kv_heads, int32_t head_dim, int32_t ctas,
+                            int32_t two)
 {
     uint64_t h = 0x243f6a8885a308d3ull;
     for (const uint64_t v : {uint64_t(T), uint64_t(R), uint64_t(kv_heads), uint64_t(head_dim), uint64_t(L.tq),
-                             uint64_t(L.part_rows), uint64_t(ctas)}) {
+                             uint64_t(L.part_rows), uint64_t(ctas), uint64_t(two)}) {
         h = (h ^ v) * 0x9e3779b97f4a7c15ull;   // odd: one value is told from another exactly
         h ^= h >> 29;
     }
     return h;
 }
 
-static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R, int64_t T, int64_t max_kv,
-                            int32_t kv_heads, int32_t head_dim, const AttnLayout &L, void *ws, cudaStream_t stream)
+// Whether a step's list may have units of two heads of few rows, a stream each: a
+// batch of single tokens (or a few) with more groups than the GPU holds several times
+// over.  512 requests of one token over 50 to 300 take 96 us so and 119 by one head a
+// unit, whose few tiles leave the second stream idle.  The kernel that can run both is
+// about 1 % slower elsewhere, so it is launched for such batches only.
+static bool two_heads(int64_t T, int32_t R, int32_t heads, int32_t kv_heads, bool paged, int32_t ctas)
 {
+    return paged && kv_heads % 2 == 0 && static_cast<int64_t>(R) * kv_heads >= 4 * ctas &&
+           T * (heads / kv_heads) <= static_cast<int64_t>(R) * kAttnFewRows;
+}
+
+static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R, int64_t T, int64_t max_kv,
+                            int32_t group, int32_t kv_heads, int32_t head_dim, const AttnLayout &L, void *ws,
+                            cudaStream_t stream)
+{
+    const int32_t ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
     AttnSchedParams p;
     p.cu = cu;
     p.kv_len = kv_len;
     p.R = R;
     p.tq = L.tq;
+    p.group = group;
+    p.two = two_heads(T, R, group * kv_heads, kv_heads, kv_len != nullptr, ctas);
     p.kv_heads = kv_heads;
     p.head_dim = head_dim;
-    p.ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
+    p.ctas = ctas;
     p.T = T;
     p.max_kv = max_kv;
     p.max_blocks = L.max_blocks;
-    p.stamp = sched_stamp(L, T, R, kv_heads, head_dim, p.ctas);
+    p.stamp = sched_stamp(L, T, R, kv_heads, head_dim, ctas, p.two);
     p.hdr = at<AttnHdr>(ws, L.hdr);
     p.first = at<AttnItem>(ws, L.first);
     p.blocks = at<AttnBlock>(ws, L.blocks);
@@ -157,8 +173,8 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
             sched->max_kv > max_kv || sched->prompt != (kv_len ? 0 : 1))
             return LORA_ERR_SEGMENTS;
     } else if (!short_list) {
-        const int e = enqueue_schedule(a->cu, kv_len, a->num_requests, a->num_tokens, max_kv, a->kv_heads, a->head_dim,
-                                       L, ws, stream);
+        const int e = enqueue_schedule(a->cu, kv_len, a->num_requests, a->num_tokens, max_kv,
+                                       a->heads / a->kv_heads, a->kv_heads, a->head_dim, L, ws, stream);
         if (e) return e;
     }
     std::memset(p, 0, sizeof *p);
@@ -181,10 +197,11 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->first = at<AttnItem>(ws, L.first);
     p->blocks = at<AttnBlock>(ws, L.blocks);
     p->max_blocks = L.max_blocks;
-    p->stamp = sched_stamp(L, a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, ctas);
     p->counters = at<int32_t>(ws, L.counters);
     p->T = a->num_tokens;
     p->requests = a->num_requests;
+    p->two = two_heads(a->num_tokens, a->num_requests, a->heads, a->kv_heads, kv_len != nullptr, ctas);
+    p->stamp = sched_stamp(L, a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, ctas, p->two);
     p->short_list = short_list;
     p->cu = a->cu;
     p->ctas = ctas;
@@ -292,7 +309,7 @@ extern "C" int lora_attn_schedule(const int32_t *cu, const int32_t *kv_len, int3
     out->head_dim = head_dim;
     out->prompt = kv_len ? 0 : 1;
     if (num_requests == 0 || num_tokens == 0) return LORA_OK;
-    return enqueue_schedule(cu, kv_len, num_requests, num_tokens, max_kv, kv_heads, head_dim, L, ws,
+    return enqueue_schedule(cu, kv_len, num_requests, num_tokens, max_kv, heads / kv_heads, kv_heads, head_dim, L, ws,
                             static_cast<cudaStream_t>(stream));
 }
 

@@ -25,13 +25,16 @@ __device__ __forceinline__ AttnItem item_of(const AttnBlock &b, int blk, int kvh
     return w;
 }
 
-// whole: unit u is a group; the heads of a section together, blocks longest first
+// whole: unit u is a group, or two of a block; the heads of a section together, blocks
+// longest first
 __device__ __forceinline__ void whole_unit(const AttnHdr &h, int kv_heads, uint32_t u, int *blk, int *kvh)
 {
+    const int two = h.unit_cost;
+    kv_heads >>= two;
     const uint32_t per = h.nblocks * h.sec_heads, sec = u / per, rem = u - sec * per;
     const uint32_t hs = min(h.sec_heads, kv_heads - static_cast<int>(sec) * h.sec_heads), at = rem / hs;
     *blk = static_cast<int>(at);
-    *kvh = static_cast<int>(sec * h.sec_heads + rem - at * hs);
+    *kvh = static_cast<int>(sec * h.sec_heads + rem - at * hs) << two;
 }
 
 // cut: where the tiles of group (b, kvh) start in the list, a gap into its share

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     __shared__ int64_t wsum[32];
     __shared__ int32_t hist[kSchedBuckets];
     __shared__ int32_t unit_blk[kAttnMaxCtas];
-    __shared__ int32_t s_max, s_pair, s_tail;
+    __shared__ int32_t s_max, s_pair, s_tail, s_ntok;
     __shared__ unsigned long long s_shares;
     const int tid = threadIdx.x;
     const int R = p.R, tb = 2 * p.tq;
@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
         s_max = 0;
         s_tail = 1;
         s_pair = 0;
+        s_ntok = 0;
         s_shares = 0;
     }
     hist[tid] = 0;
@@ -115,17 +116,19 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     };
     auto bucket = [](int tiles) { return kSchedBuckets - min(tiles, kSchedBuckets); };
     int64_t tiles = 0, shares = 0;   // shares: in a list with pairs
-    int my_max = 0, my_pair = 0;
+    int my_max = 0, my_pair = 0, my_ntok = 0;
     for (int b = tid; b < nb; b += kSchedThreads) {
         const AttnBlock k = block_of(b);
         tiles += k.tiles;
         shares += attn_share(k.tiles, k.ntok > p.tq, 2);
         my_max = max(my_max, k.tiles);
         my_pair |= k.ntok > p.tq;
+        my_ntok = max(my_ntok, k.ntok);
         atomicAdd(&hist[bucket(k.tiles)], 1);
     }
     if (my_max) atomicMax(&s_max, my_max);
     if (my_pair) atomicOr(&s_pair, 1);
+    if (my_ntok) atomicMax(&s_ntok, my_ntok);
     if (bad) atomicOr(p.counters + CNT_STATUS, LORA_DEV_BAD_LENGTH);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) shares += __shfl_xor_sync(0xffffffffu, shares, d);
@@ -154,11 +157,13 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     h.nblocks = nb;
     h.cut = cut ? weight : 0;
     h.cost = cut ? static_cast<int32_t>(cost) : 0;
-    h.unit_cost = cut ? static_cast<int32_t>(each) : 0;
-    h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups, static_cast<int64_t>(INT32_MAX)));
+    // whole groups of few rows: two heads at once, a stream each, while that leaves a few for every CTA
+    const int two = !cut && p.two && s_ntok * p.group <= kAttnFewRows && groups >= 4 * p.ctas;
+    h.unit_cost = cut ? static_cast<int32_t>(each) : two;
+    h.units = static_cast<int32_t>(cut ? (cost + each - 1) / each : min(groups >> two, static_cast<int64_t>(INT32_MAX)));
     const int64_t head_bytes = max(static_cast<int64_t>(1), all_keys * p.head_dim * 4);
     h.sec_heads = static_cast<int32_t>(
-        max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads), kSectionBytes / head_bytes)));
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.kv_heads >> two), kSectionBytes / (head_bytes << two))));
     if (tid == 0) *p.hdr = h;
     // the blocks in their order, and (cut) the block that each unit starts in
     if (!cut) {
@@ -192,6 +197,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
             if (!cut) {
                 whole_unit(h, p.kv_heads, tid, &blk, &kvh);
                 w = item_of(p.blocks[blk], blk, kvh, p.tq);
+                w.valid += two;
             } else {
                 blk = unit_blk[tid];
                 const AttnBlock b = p.blocks[blk];

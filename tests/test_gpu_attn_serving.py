@@ -161,3 +161,15 @@ def test_chunks_beside_single_tokens_split_over_the_gpu(H, Hk, D):
     first = s.run(sched=sched)
     again = s.run(sched=sched)
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("G,D,new", [(2, 128, 1), (4, 64, 2), (1, 72, 3), (16, 128, 1)])
+def test_many_short_contexts(G, D, new):
+    """More groups of few rows than the GPU holds several times over: two heads of a request at a time."""
+    R, Hk = 90, 8
+    n = [new if r % 7 else 0 for r in range(R)]
+    s = Step(n, [n[r] + (37 * r) % 290 if r % 11 else 0 for r in range(R)], G * Hk, Hk, D, 16, seed=G)
+    s.check("short contexts")
+    first = s.run(sched=s.schedule())
+    again = s.run(sched=s.schedule())
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
