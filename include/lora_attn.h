@@ -141,7 +141,9 @@ int lora_kv_store(const lora_bf16_t *k, const lora_bf16_t *v, int64_t num_tokens
  * second product (its sum is taken before that rounding), o once at the end.
  *
  * q, o: DEVICE bf16, head h of row t at t * token_stride + h * head_stride
- * elements (multiples of 8; 16-byte aligned bases).  lse: DEVICE fp32
+ * elements (multiples of 8; 16-byte aligned bases); o must not overlap q, the
+ * keys or the values.  Rows of o that start on 32 bytes are written faster.
+ * lse: DEVICE fp32
  * [num_tokens, heads] or NULL.  cu: DEVICE int32 [num_requests + 1].
  * heads a multiple of kv_heads, heads / kv_heads <= LORA_MAX_GROUP, head_dim
  * a multiple of 8 up to LORA_MAX_HEAD_DIM, scale positive and finite.
