@@ -35,12 +35,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
 {
     pdl_launch_dependents();
     const lora_kv_plan_t &a = prm.a;
-    extern __shared__ int32_t sm[];
+    extern __shared__ int64_t sm[];   // all of the kernel's shared memory (plan_shared)
     const int R = a.num_requests;
-    int32_t *cu = sm;              // [R + 1] new tokens of a request, then the offsets
+    int64_t *wsum = sm;            // [32] of the block scans
+    int32_t *cu = reinterpret_cast<int32_t *>(sm + 32);   // [R + 1] new tokens of a request, then the offsets
     int32_t *before = cu + R + 1;  // [R + 1] pages needed by the requests before r
     int32_t *ctx = before + R + 1; // [R]
-    __shared__ int64_t wsum[32];
     const int tid = threadIdx.x;
     const int P = a.page_size, shift = __ffs(P) - 1;
     const int64_t cap = static_cast<int64_t>(a.table_width) << shift;
@@ -149,12 +149,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     if (flags) atomicOr(prm.status, flags);
 }
 
+// Bytes of shared memory for R requests.  The kernel has no other: a launch's limit of 48 KB
+// without opting in is on static and dynamic memory together.
+static constexpr size_t plan_shared(int R) { return 32 * sizeof(int64_t) + (3 * static_cast<size_t>(R) + 2) * 4; }
+
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream)
 {
-    const size_t smem = (3 * static_cast<size_t>(p.a.num_requests) + 2) * 4;
+    const size_t smem = plan_shared(p.a.num_requests);
     if (smem > 49152) {   // only near LORA_MAX_REQUESTS
         const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (3 * LORA_MAX_REQUESTS + 2) * 4);
+                                                   static_cast<int>(plan_shared(LORA_MAX_REQUESTS)));
         if (e != cudaSuccess) return e;
     }
     int64_t ctas = (p.a.max_tokens + kPlanTokens - 1) / kPlanTokens;
