@@ -11,7 +11,8 @@
  * allocation, no synchronisation, LORA_ERR_* for what the host can see,
  * status bits in the workspace (lora_get_status) for what only the device
  * sees, all work in order on `stream`.  lora_set_wait_budget bounds the
- * attention kernel's waits too.
+ * attention kernel's waits too.  int32 and fp32 arrays start on 4 bytes, tensors
+ * on 16 and workspaces on 256 (LORA_ERR_ALIGN).
  *
  * The operators are an extension of this library: the page it follows leaves
  * attention to the serving engine.

@@ -17,6 +17,14 @@ static size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 static bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// int32 arrays: each is NULL or starts on 4 bytes (the kernels would fault on any other).
+static bool ints_aligned(std::initializer_list<const void *> arrays)
+{
+    for (const void *p : arrays)
+        if (!aligned(p, 4)) return false;
+    return true;
+}
+
 template <typename T>
 static T *at(void *ws, size_t off)
 {
@@ -244,6 +252,9 @@ extern "C" int lora_kv_plan(const lora_kv_plan_t *plan, void *ws, size_t ws_byte
     if (a.free_head == a.free_head_out || a.cu_new == a.new_len || a.cu_new == a.ctx_len || a.kv_len == a.ctx_len ||
         a.kv_len == a.new_len)
         return LORA_ERR_SHAPE;
+    if (!ints_aligned({a.new_len, a.ctx_len, a.req_adapter, a.block_table, a.free_pages, a.free_head, a.cu_new, a.kv_len,
+                       a.slot_map, a.position, a.lora_id_map, a.free_head_out}))
+        return LORA_ERR_ALIGN;
     const int rc = check_ws(ws, ws_bytes, make_layout(0, 0, 0, 0, 0).total);
     if (rc) return rc;
     KvPlanParams p;
@@ -297,6 +308,7 @@ extern "C" int lora_attn_schedule(const int32_t *cu, const int32_t *kv_len, int3
     if (!step_ok(num_tokens, num_requests) || !heads_ok(heads, kv_heads, head_dim) || max_kv < 0 || max_kv > kMaxTokens)
         return LORA_ERR_SHAPE;
     if (!out || (num_requests > 0 && num_tokens > 0 && !cu)) return LORA_ERR_NULL;
+    if (!ints_aligned({cu, kv_len})) return LORA_ERR_ALIGN;
     const AttnLayout L = make_layout(num_tokens, num_requests, heads, kv_heads, head_dim);
     const int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
@@ -326,6 +338,7 @@ extern "C" int lora_attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *c
     if (attn->num_requests > 1 && table_stride < table_width) return LORA_ERR_SHAPE;
     if (attn->num_tokens == 0 || attn->num_requests == 0) return LORA_OK;
     if (!kv_len || (table_width > 0 && !block_table)) return LORA_ERR_NULL;
+    if (!ints_aligned({kv_len, block_table})) return LORA_ERR_ALIGN;
     AttnParams p;
     rc = prepare_attn(attn, kv_len, static_cast<int64_t>(table_width) * cache->page_size, sched, ws, ws_bytes,
                       static_cast<cudaStream_t>(stream), &p);
