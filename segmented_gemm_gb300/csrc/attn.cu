@@ -148,8 +148,8 @@ struct ShortList {
         const int n = __shfl_sync(0xffffffffu, rows, r);
         const int local = (i - __shfl_sync(0xffffffffu, first, r)) * 2 * p.tq;
         AttnBlock b = {};
-        b.req = r;
-        b.tok0 = __shfl_sync(0xffffffffu, start, r) + local;
+        b.base = __shfl_sync(0xffffffffu, start, r);
+        b.tok0 = b.base + local;
         b.ntok = min(2 * p.tq, n - local);
         b.qpos0 = local;
         b.kv_len = n;
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             const AttnItem &w = items[is];
             const int two = kTwo ? w.valid >> 1 : 0;   // two heads: their tiles take turns, 2 t + stream
-            const int pair = w.pair, t0 = w.t0, n = (w.t1 - t0) << two, seen = w.seen, kvh = w.kvh, row0 = w.tok0 - w.qpos0;
-            const int32_t *table = p.block_table + w.req * p.table_stride;
+            const int pair = w.pair, t0 = w.t0, n = (w.t1 - t0) << two, seen = w.seen, kvh = w.kvh, row0 = w.base;
+            const int32_t *table = p.block_table + w.base * p.table_stride;
             more = w.valid;
             if (lane == 0) mbar_arrive(&item_full[is]);
             ++nitem;
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const AttnItem &wi = items[is];
             const int valid = wi.valid, two = kTwo ? valid >> 1 : 0;
             const int pair = wi.pair, t0 = wi.t0, n = (wi.t1 - t0) << two, seen = wi.seen, kvh = wi.kvh;
-            const int tok0 = wi.tok0, row0 = tok0 - wi.qpos0;
-            const int32_t *table = p.block_table + wi.req * p.table_stride;
+            const int tok0 = wi.tok0, row0 = wi.base;
+            const int32_t *table = p.block_table + wi.base * p.table_stride;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[is]);
             ++nitem;

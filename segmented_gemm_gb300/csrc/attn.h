@@ -50,7 +50,7 @@ inline __host__ __device__ int32_t attn_share(int32_t tiles, bool pair, int32_t 
 // A query block: up to two query tiles of one request, for every kv head.
 struct __align__(16) AttnBlock {
     int32_t pre;      // cut: cost of the blocks before it (one head)
-    int32_t req;
+    int32_t base;     // where key 0 is found: paged, the request (its row of the block table); packed, its first row
     int32_t tok0;     // first packed row
     int32_t ntok;
     int32_t qpos0;    // row tok0 sees keys [0, qpos0 + 1) (none when that is <= 0)
@@ -74,7 +74,7 @@ struct __align__(16) AttnHdr {
 struct __align__(16) AttnItem {
     int32_t valid;    // 0: no more; 2: two kv heads, kvh and the next, a stream each (few rows)
     int32_t pair;     // two query tiles (their streams share the key tiles), or one
-    int32_t req, tok0, ntok, qpos0, kv_len;
+    int32_t base, tok0, ntok, qpos0, kv_len;
     int32_t seen;     // keys that any of its rows sees
     int32_t kvh, t0, t1;
     int32_t end0;     // pair: tiles that stream 0's rows reach

@@ -11,7 +11,7 @@ __device__ __forceinline__ AttnItem item_of(const AttnBlock &b, int blk, int kvh
     AttnItem w = {};
     w.valid = 1;
     w.pair = b.ntok > tq;
-    w.req = b.req;
+    w.base = b.base;
     w.tok0 = b.tok0;
     w.ntok = b.ntok;
     w.qpos0 = b.qpos0;

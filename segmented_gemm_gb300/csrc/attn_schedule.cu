@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
         int32_t start;
         const int32_t n = rows_of(r, &start), len = keys_of(r, n);
         const int32_t local = (b - blk_start[r]) * tb;
-        k.req = r;
+        k.base = p.kv_len ? r : start;   // (not tok0 - qpos0: a clamped prompt's differs)
         k.tok0 = start + local;
         k.ntok = min(tb, n - local);
         k.qpos0 = len - n + local;

@@ -29,3 +29,33 @@ def test_plan_of_nearly_the_most_requests():
             "    check_plan(new, ctx, 16, 4, list(range(3 * R)), sum(new) + 3, 3 * R, seed=R)\n")
     run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_clamped_lengths_of_prompts(D):
+    """A prompt of n rows clamped to L keys: row i sees the first max(0, L - n + i + 1) keys of its prompt."""
+    p = Prompt([50, 300, 0, 131, 700], 4, 2, D, seed=D)
+    for most in (130, 299, 1):
+        sched = A.lora_attn_schedule(p.cu, None, p.T, most, 4, 2, D, p.ws)
+        o, lse = p.run(sched=sched)
+        assert L.lora_get_status(p.ws) == A.LORA_DEV_BAD_LENGTH
+        parts, t = [], 0
+        for n in p.lens:
+            q, k, v = (x[t:t + n] for x in p.cpu)
+            parts.append(reference(q, k, v, [max(0, min(n, most) - n + i + 1) for i in range(n)], p.scale))
+            t += n
+        assert_attn(o, lse, *[torch.cat(x) for x in zip(*parts)], f"at most {most}")
+
+
+def test_clamped_lengths_of_a_cache():
+    s = Step([2, 150, 1], [40, 400, 900], 4, 2, 64, 16, seed=13)
+    for most in (399, 48, 1):
+        sched = A.lora_attn_schedule(s.cu, s.kv_len, s.T, most, 4, 2, 64, s.ws)
+        o, lse = s.run(sched=sched)
+        assert L.lora_get_status(s.ws) == A.LORA_DEV_BAD_LENGTH
+        parts, t = [], 0
+        for n, length, k, v in zip(s.new, s.kv, s.keys, s.values):
+            lim = [max(0, min(length, most) - n + i + 1) for i in range(n)]
+            parts.append(reference(s.q_cpu[t:t + n], k, v, lim, s.scale))
+            t += n
+        assert_attn(o, lse, *[torch.cat(x) for x in zip(*parts)], f"at most {most}")
