@@ -174,8 +174,10 @@ typedef struct {
  * (LORA_DEV_BAD_LENGTH).
  * *out: HOST; passed to the attention calls with the same ws.  It stands until
  * another schedule is built in that ws (an attention call without one does so
- * too); an attention call that finds one of other sizes there runs nothing and
- * sets LORA_DEV_CHECK.  After LORA_DEV_TIMEOUT build it anew.
+ * too).  An attention call that finds one of other sizes there, of another max_kv,
+ * or of prompts for a cache (or the reverse), runs nothing and sets
+ * LORA_DEV_CHECK; one of the same sizes with other lengths is not told apart.
+ * After LORA_DEV_TIMEOUT build it anew.
  */
 typedef struct {
     void *plan;

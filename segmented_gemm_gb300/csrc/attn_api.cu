@@ -115,14 +115,15 @@ static int check_ws(const void *ws, size_t bytes, size_t need)
     return device_supported() ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 
-// What the places and the extents of a list in ws depend on, in 64 bits: a
-// workspace may have been given to a step of other sizes since.
+// What the places, the extents and the meaning of a list in ws depend on (but the
+// lengths themselves), in 64 bits: a workspace may have been given to a step of other
+// sizes since, to prompts instead of a cache, or to a cache of another bound.
 static uint64_t sched_stamp(const AttnLayout &L, int64_t T, int32_t R, int32_t kv_heads, int32_t head_dim, int32_t ctas,
-                            int32_t two)
+                            int32_t two, bool prompt, int64_t max_kv)
 {
     uint64_t h = 0x243f6a8885a308d3ull;
     for (const uint64_t v : {uint64_t(T), uint64_t(R), uint64_t(kv_heads), uint64_t(head_dim), uint64_t(L.tq),
-                             uint64_t(L.part_rows), uint64_t(ctas), uint64_t(two)}) {
+                             uint64_t(L.part_rows), uint64_t(ctas), uint64_t(two), uint64_t(prompt), uint64_t(max_kv)}) {
         h = (h ^ v) * 0x9e3779b97f4a7c15ull;   // odd: one value is told from another exactly
         h ^= h >> 29;
     }
@@ -158,7 +159,7 @@ static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R,
     p.T = T;
     p.max_kv = max_kv;
     p.max_blocks = L.max_blocks;
-    p.stamp = sched_stamp(L, T, R, kv_heads, head_dim, ctas, p.two);
+    p.stamp = sched_stamp(L, T, R, kv_heads, head_dim, ctas, p.two, !kv_len, max_kv);
     p.hdr = at<AttnHdr>(ws, L.hdr);
     p.first = at<AttnItem>(ws, L.first);
     p.blocks = at<AttnBlock>(ws, L.blocks);
@@ -209,7 +210,8 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     p->T = a->num_tokens;
     p->requests = a->num_requests;
     p->two = two_heads(a->num_tokens, a->num_requests, a->heads, a->kv_heads, kv_len != nullptr, ctas);
-    p->stamp = sched_stamp(L, a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, ctas, p->two);
+    p->stamp = sched_stamp(L, a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, ctas, p->two, !kv_len,
+                           sched ? sched->max_kv : max_kv);
     p->short_list = short_list;
     p->cu = a->cu;
     p->ctas = ctas;

@@ -59,3 +59,27 @@ def test_clamped_lengths_of_a_cache():
             parts.append(reference(s.q_cpu[t:t + n], k, v, lim, s.scale))
             t += n
         assert_attn(o, lse, *[torch.cat(x) for x in zip(*parts)], f"at most {most}")
+
+
+def test_a_list_of_the_other_kind_or_bound_runs_nothing():
+    s = Step([3] * 40, [3 + 5 * r for r in range(40)], 4, 2, 64, 16, seed=1)
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(s.T, 2, 64, generator=g).to(BF).cuda() for _ in range(2))
+    sched = s.schedule()
+    want, lse0 = s.run(sched=sched)
+    assert L.lora_get_status(s.ws) == 0
+    A.lora_attn_prompt(s.q, k, v, s.cu, s.scale, s.ws)   # more requests than a short list holds: builds its own
+    o, lse = s.run(sched=sched)
+    assert L.lora_get_status(s.ws) == L.LORA_DEV_CHECK
+    assert torch.isnan(o.float()).all() and torch.isnan(lse).all()
+    prompt = A.lora_attn_schedule(s.cu, None, s.T, s.T, 4, 2, 64, s.ws)
+    s.schedule()
+    A.lora_attn_prompt(s.q, k, v, s.cu, s.scale, s.ws, sched=prompt)
+    assert L.lora_get_status(s.ws) == L.LORA_DEV_CHECK
+    sched = s.schedule()
+    A.lora_attn_schedule(s.cu, s.kv_len, s.T, 100, 4, 2, 64, s.ws)   # clamps the longer requests
+    assert L.lora_get_status(s.ws) == A.LORA_DEV_BAD_LENGTH
+    s.run(sched=sched)
+    assert L.lora_get_status(s.ws) == L.LORA_DEV_CHECK
+    o, lse = s.run(sched=s.schedule())
+    assert L.lora_get_status(s.ws) == 0 and torch.equal(o, want) and torch.equal(lse, lse0)
