@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -87,6 +88,12 @@ def _lib():
             fn.argtypes = args
         _bound[_lora._active] = lib
     return lib
+
+
+def _on(stream):
+    """Where a call makes its outputs itself: memory of the stream that writes them, as with
+    torch.cuda.stream (the allocator reuses it in that stream's order)."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(code: int, where: str):
@@ -172,7 +179,8 @@ def lora_kv_plan(new_len: torch.Tensor, ctx_len: torch.Tensor, block_table: torc
     if out is None:
         if max_tokens is None:
             raise ValueError("lora_kv_plan: out or max_tokens")
-        out = KvPlan(max_tokens, R, new_len.device)
+        with _on(stream):
+            out = KvPlan(max_tokens, R, new_len.device)
     width, row = _table(block_table, R)
     if out.num_requests != R:
         raise ValueError("lora_kv_plan: out was made for another number of requests")
@@ -216,11 +224,12 @@ def lora_attn_schedule(cu: torch.Tensor, kv_len: Optional[torch.Tensor], T: int,
     return out
 
 
-def _attn(q, kv_heads, cu, R, scale, o, lse):
+def _attn(q, kv_heads, cu, R, scale, o, lse, stream):
     """The packed lora_attn_t, and o."""
     shape, qs = _rows(q, "q")
     if o is None:
-        o = torch.empty(shape, dtype=_BF16, device=q.device)
+        with _on(stream):
+            o = torch.empty(shape, dtype=_BF16, device=q.device)
     o_shape, os_ = _rows(o, "o")
     if o_shape != shape:
         raise ValueError("o: the shape of q")
@@ -243,7 +252,7 @@ def lora_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     causal.  ``lse``: fp32 [T, heads], written when given."""
     c, (_, kv_heads, _, dim) = _cache(k_cache, v_cache)
     R = cu.shape[0] - 1
-    a, o = _attn(q, kv_heads, cu, R, scale, o, lse)
+    a, o = _attn(q, kv_heads, cu, R, scale, o, lse, stream)
     width, row = _table(block_table, R)
     if q.shape[2] != dim:
         raise ValueError("lora_attn_paged: q and the cache have the same head dimension")
@@ -263,7 +272,7 @@ def lora_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torc
     v_shape, vs = _rows(v, "v")
     if v_shape != shape or shape[0] != q.shape[0] or shape[2] != q.shape[2]:
         raise ValueError("lora_attn_prompt: k and v are [T, kv_heads, head_dim] with q's tokens and head dimension")
-    a, o = _attn(q, shape[1], cu, cu.shape[0] - 1, scale, o, lse)
+    a, o = _attn(q, shape[1], cu, cu.shape[0] - 1, scale, o, lse, stream)
     _check(_lib().lora_attn_prompt(a, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
                                    None if sched is None else sched.addr, ws.addr, ws.nbytes,
                                    _raw_stream(q.get_device()) if stream is None else stream.cuda_stream),

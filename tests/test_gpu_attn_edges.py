@@ -83,3 +83,36 @@ def test_a_list_of_the_other_kind_or_bound_runs_nothing():
     assert L.lora_get_status(s.ws) == L.LORA_DEV_CHECK
     o, lse = s.run(sched=s.schedule())
     assert L.lora_get_status(s.ws) == 0 and torch.equal(o, want) and torch.equal(lse, lse0)
+
+
+def stream_of(t):
+    """The stream whose pool the caching allocator took t from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not of the caching allocator")
+
+
+def test_outputs_made_by_a_call_belong_to_its_stream():
+    s = Step([1, 20, 1], [700, 90, 33], 8, 2, 64, 16, seed=15)
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(s.T, 2, 64, generator=g).to(BF).cuda() for _ in range(2))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o = A.lora_attn_paged(s.q, s.k_cache, s.v_cache, s.table, s.cu, s.kv_len, s.scale, s.ws, stream=side)
+    assert stream_of(o) == side.cuda_stream
+    o = A.lora_attn_prompt(s.q, k, v, s.cu, s.scale, s.ws, stream=side)
+    assert stream_of(o) == side.cuda_stream
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = [torch.tensor([1, 2, 3], **i32), torch.tensor([0, 5, 9], **i32), torch.zeros(3, 4, **i32),
+            torch.arange(10, **i32), torch.zeros(1, **i32)]
+    torch.cuda.synchronize()
+    plan = A.lora_kv_plan(*args, 16, 20, s.ws, max_tokens=8, stream=side)
+    for t in (plan.cu_new, plan.kv_len, plan.free_head, plan.slot_map, plan.position, plan.lora_id_map):
+        assert stream_of(t) == side.cuda_stream
+    side.synchronize()
+    assert plan.cu_new.tolist() == [0, 1, 3, 6]
+    # and, where the call is on the current stream, to that one
+    o = A.lora_attn_paged(s.q, s.k_cache, s.v_cache, s.table, s.cu, s.kv_len, s.scale, s.ws)
+    assert stream_of(o) == torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
