@@ -16,13 +16,12 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from contextlib import nullcontext
 from typing import Optional
 
 import torch
 
 from . import lora as _lora
-from .lora import LORA_OK, LoraError, load_library
+from .lora import LORA_OK, LoraError, _on, load_library
 
 LORA_DEV_BAD_LENGTH, LORA_DEV_NO_PAGE, LORA_DEV_BAD_PAGE = 1 << 8, 1 << 9, 1 << 10
 LORA_MAX_REQUESTS, LORA_MAX_HEAD_DIM, LORA_MAX_GROUP = 4096, 128, 128
@@ -88,12 +87,6 @@ def _lib():
             fn.argtypes = args
         _bound[_lora._active] = lib
     return lib
-
-
-def _on(stream):
-    """Where a call makes its outputs itself: memory of the stream that writes them, as with
-    torch.cuda.stream (the allocator reuses it in that stream's order)."""
-    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(code: int, where: str):

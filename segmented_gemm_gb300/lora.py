@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -162,6 +163,12 @@ def _out_ptr(t: torch.Tensor):
     """An output the kernels write with plain stores: device memory, or a
     pinned host tensor through its device address."""
     return ctypes.c_void_p(t.data_ptr() if t.is_cuda else device_pointer(t))
+
+
+def _on(stream):
+    """Where a call makes its outputs itself: memory of the stream that writes them, as with
+    torch.cuda.stream (the allocator reuses it in that stream's order)."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def copy_async(pairs: Sequence[tuple], stream=None):
@@ -384,7 +391,8 @@ def lora_linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor], 
     ``y`` may be a pinned host tensor: the kernels store into it directly."""
     M = x.shape[0]
     if y is None:
-        y = torch.empty(M, W.shape[0], dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            y = torch.empty(M, W.shape[0], dtype=torch.bfloat16, device=x.device)
     _check(load_library().lora_linear_ex(
         _ptr(x), M, _ptr(W), _ptr(bias), _ptr(ids), ctypes.byref(pool.desc), float(scale),
         ctypes.byref(segs) if segs is not None else None, _out_ptr(y), ws.ptr, ws.nbytes,
@@ -414,8 +422,10 @@ def lora_linear_layers(layers: Sequence[tuple], ids: torch.Tensor, ws: Workspace
     outs, keep = [], []
     for i, ly in enumerate(layers):
         x, W, bias, pool, scale = ly[:5]
-        y = ly[5] if len(ly) > 5 and ly[5] is not None else torch.empty(x.shape[0], W.shape[0],
-                                                                        dtype=torch.bfloat16, device=x.device)
+        y = ly[5] if len(ly) > 5 else None
+        if y is None:
+            with _on(stream):
+                y = torch.empty(x.shape[0], W.shape[0], dtype=torch.bfloat16, device=x.device)
         arr[i].x, arr[i].W = x.data_ptr(), W.data_ptr()
         arr[i].bias = None if bias is None else bias.data_ptr()
         arr[i].pool = ctypes.addressof(pool.desc)
@@ -436,7 +446,8 @@ def lora_shrink(x: torch.Tensor, ids: torch.Tensor, pool: LoraPool, ws: Workspac
     M = x.shape[0]
     s_cols = s_cols or max(pool.desc.max_rank, 16)
     if S is None:
-        S = torch.empty(M, s_cols, dtype=torch.float32, device=x.device)
+        with _on(stream):
+            S = torch.empty(M, s_cols, dtype=torch.float32, device=x.device)
     _check(load_library().lora_shrink(
         _ptr(x), M, _ptr(ids), ctypes.byref(pool.desc),
         ctypes.byref(segs) if segs is not None else None, _ptr(S), s_cols, ws.ptr, ws.nbytes,
@@ -462,7 +473,8 @@ def lora_linear_noalloc(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.T
     library's own static scratch array is used instead of a workspace."""
     M = x.shape[0]
     if y is None:
-        y = torch.empty(M, W.shape[0], dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            y = torch.empty(M, W.shape[0], dtype=torch.bfloat16, device=x.device)
     _check(load_library().lora_linear_noalloc(
         _ptr(x), M, _ptr(W), _ptr(bias), _ptr(ids), ctypes.byref(pool.desc), float(scale), _ptr(y),
         _stream(stream)), "lora_linear_noalloc")
@@ -508,9 +520,11 @@ def lora_moe(x: torch.Tensor, W: torch.Tensor, expert: torch.Tensor, weight: tor
     E, N, _ = W.shape
     topk = expert.shape[1]
     if out is None:
-        out = torch.empty(M * topk, N, dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            out = torch.empty(M * topk, N, dtype=torch.bfloat16, device=x.device)
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
     _check(load_library().lora_moe(_ptr(x), M, K, _ptr(W), N, _ptr(expert), _ptr(weight), E, topk, _ptr(out),
                                    _ptr(y), ws.ptr, ws.nbytes, _stream(stream)), "lora_moe")
     return y
