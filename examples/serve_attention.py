@@ -85,7 +85,9 @@ class Model:
                 o = A.lora_attn_paged(q, kc, vc, self.table, plan.cu_new, plan.kv_len, scale, self.ws, sched=sched)
             x = x + L.lora_linear(o.flatten(1), out["W"], None, ids, out["pool"], self.lora_scale, self.lws,
                                   static_weights=True)
-        self.ctx.copy_(plan.kv_len)
+        # kv_len is 0 for a request that the plan could not give a page: none of its tokens were stored, its
+        # cached ones are still there, and the caller offers the same tokens again
+        self.ctx.copy_(torch.where(plan.kv_len > 0, plan.kv_len, self.ctx))
         self.steps += 1
         return x
 

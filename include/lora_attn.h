@@ -77,8 +77,10 @@ typedef struct {
  * order and entered in its table row; *free_head_out counts those taken.  If
  * the list runs short, the first request it cannot serve and every later one
  * that needs a page get none: kv_len 0 and slots -1 (their attention rows
- * come out as zeros), LORA_DEV_NO_PAGE.  Table entries that are not new stay
- * as they were; calling again with the same inputs gives the same result.
+ * come out as zeros), LORA_DEV_NO_PAGE.  Such a request keeps its ctx_len tokens
+ * and pages: a caller goes on from kv_len where that is not 0 and from ctx_len
+ * where it is, and offers the refused tokens again.  Table entries that are not
+ * new stay as they were; calling again with the same inputs gives the same result.
  *
  * Lengths are clamped to [0, table_width * page_size] in all and to
  * max_tokens packed tokens (LORA_DEV_BAD_LENGTH).  A page number outside

@@ -116,3 +116,36 @@ def test_outputs_made_by_a_call_belong_to_its_stream():
     o = A.lora_attn_paged(s.q, s.k_cache, s.v_cache, s.table, s.cu, s.kv_len, s.scale, s.ws)
     assert stream_of(o) == torch.cuda.current_stream().cuda_stream
     torch.cuda.synchronize()
+
+
+def test_a_refused_request_keeps_its_context():
+    """The serving example's bookkeeping where the free pages run short for a step."""
+    from test_gpu_attn_serving import _example
+    ex = _example()
+    R, hidden = 3, 256
+    m = ex.Model(R, 1, hidden, 4, 2, 64, 16, 64, 64, seed=3)
+    g = torch.Generator().manual_seed(4)
+    xs, ys = [[] for _ in range(R)], [[] for _ in range(R)]
+
+    def step(new, prompts, refused=()):
+        x = torch.randn(sum(new), hidden, generator=g).to(BF)
+        y = m.step(x.cuda(), new, prompts).cpu()
+        at = 0
+        for r, n in enumerate(new):
+            if r not in refused:
+                xs[r].append(x[at:at + n])
+                ys[r].append(y[at:at + n])
+            at += n
+    step([16, 20, 7], True)
+    assert m.ctx.tolist() == [16, 20, 7] and L.lora_get_status(m.ws) == 0
+    free, m.free = m.free, m.free[:4]          # all four pages are taken
+    step([1, 1, 1], False, refused=(0,))       # request 0 needs a fifth
+    assert L.lora_get_status(m.ws) == A.LORA_DEV_NO_PAGE
+    assert m.ctx.tolist() == [16, 21, 8]
+    m.free = free                              # pages came free again
+    step([2, 1, 3], False)
+    step([1, 1, 1], False)
+    assert m.ctx.tolist() == [19, 23, 12] and L.lora_get_status(m.ws) == 0
+    for r in range(R):
+        got, ref = torch.cat(ys[r]).double(), m.recompute(r, torch.cat(xs[r]))
+        assert float((got - ref).norm() / ref.norm()) <= 13 * 2.0 ** -8, r
