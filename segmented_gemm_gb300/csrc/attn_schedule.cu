@@ -8,12 +8,13 @@
 // The persistent attention kernel takes units from the list in one of two ways,
 // chosen here by which ends sooner:
 //   whole   a unit is one group, longest first, taken as CTAs come free: nothing
-//           is split, the end is ragged by about half of the units that run last
+//           is split, the end is ragged by about a third of the units that run last
 //   cut     all groups laid end to end and cut into one equal piece a CTA: they
 //           end together, but a group that spans pieces is written as partial
 //           results and joined
 // One token over 1000 takes 8.9 us cut and 12.3 whole, 32 requests of one token over up
-// to 8000 98 and 121; a 16384-token prompt 1460 cut and 1360 whole.
+// to 8000 98 and 121; a 16384-token prompt 1409 cut and 1347 whole (1 head of 128: 78 and
+// 177), one of 2048 tokens 56 and 30 (1 head: 72 and 27).
 // Whole groups run by sections of heads whose keys and values L2 holds together (a
 // 65536-token prompt of 8 kv heads: 21.1 ms, 22.4 with all heads at once).
 // One CTA, once a step.
@@ -30,9 +31,18 @@ namespace lora {
 constexpr int kSchedThreads = 1024;
 constexpr int kSchedBuckets = 1024;          // block costs told apart by the sort
 constexpr int kMinPiece = 2;                 // key tiles of a piece, at least (one token over 1000: 8.9 us, 9.2 with 1, 10.8 with 4)
-// what joining partial results costs, in a cut list's units (with 8 for pairs a
-// 16384-token prompt is cut, 1470 us against 1360)
-constexpr int kJoinSingle = 2, kJoinPair = 16;
+// What cutting costs, in a cut list's units.  A fixed part for writing and counting
+// partial results, less where their few rows are joined in place and CTAs are to spare.
+// And the join, which reads every piece's rows, one piece after another: kJoinElems
+// elements in the time of a unit.  256 tokens of one head over 4096, 36 pieces of 256 rows
+// of 128, take 126 us cut and 54 whole, one prompt of 2048 72 and 27; a fixed part alone (2
+// and 16) had both cut.  Both lists of 855 steps were timed, prompts, chunks, single tokens
+// and mixtures, heads 40 to 1 over 1 to 8, dimensions 64 to 128: this rule's choice takes
+// 0.3 % longer than the better list on average and 21 % at most, the fixed part alone 8 %
+// and 180 %.
+constexpr int kCutFew = 4, kCutSingle = 6, kCutPair = 24;
+constexpr int kFewElems = 1024;
+constexpr float kJoinElems = 8192.f;
 constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads that run together (L2 holds 126 MB)
 
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const AttnSchedParams p)
@@ -42,15 +52,15 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     __shared__ int64_t wsum[32];
     __shared__ int32_t hist[kSchedBuckets];
     __shared__ int32_t unit_blk[kAttnMaxCtas];
-    __shared__ int32_t s_max, s_pair, s_tail, s_ntok;
+    __shared__ int32_t s_max, s_tail, s_ntok, s_join;
     __shared__ unsigned long long s_shares;
     const int tid = threadIdx.x;
     const int R = p.R, tb = 2 * p.tq;
     if (tid == 0) {
         s_max = 0;
         s_tail = 1;
-        s_pair = 0;
         s_ntok = 0;
+        s_join = 0;
         s_shares = 0;
     }
     hist[tid] = 0;
@@ -116,25 +126,28 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     };
     auto bucket = [](int tiles) { return kSchedBuckets - min(tiles, kSchedBuckets); };
     int64_t tiles = 0, shares = 0;   // shares: in a list with pairs
-    int my_max = 0, my_pair = 0, my_ntok = 0;
+    int my_max = 0, my_ntok = 0, my_join = 0;   // my_join: most tokens times share
     for (int b = tid; b < nb; b += kSchedThreads) {
         const AttnBlock k = block_of(b);
         tiles += k.tiles;
-        shares += attn_share(k.tiles, k.ntok > p.tq, 2);
+        const int32_t share = attn_share(k.tiles, k.ntok > p.tq, 2);
+        shares += share;
+        my_join = max(my_join, static_cast<int>(min(static_cast<int64_t>(share) * k.ntok, static_cast<int64_t>(INT32_MAX))));
         my_max = max(my_max, k.tiles);
-        my_pair |= k.ntok > p.tq;
         my_ntok = max(my_ntok, k.ntok);
         atomicAdd(&hist[bucket(k.tiles)], 1);
     }
     if (my_max) atomicMax(&s_max, my_max);
-    if (my_pair) atomicOr(&s_pair, 1);
-    if (my_ntok) atomicMax(&s_ntok, my_ntok);
+    if (my_ntok) {
+        atomicMax(&s_ntok, my_ntok);
+        atomicMax(&s_join, my_join);
+    }
     if (bad) atomicOr(p.counters + CNT_STATUS, LORA_DEV_BAD_LENGTH);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) shares += __shfl_xor_sync(0xffffffffu, shares, d);
     if ((tid & 31) == 0 && shares) atomicAdd(&s_shares, static_cast<unsigned long long>(shares));
     int64_t all_tiles, total;
-    block_scan_i64(tiles, wsum, &all_tiles);   // also makes hist, s_max, s_pair and s_shares visible
+    block_scan_i64(tiles, wsum, &all_tiles);   // also makes hist and the shared maxima and sums visible
     const int32_t here = hist[tid];
     const int32_t before = static_cast<int32_t>(block_scan_i64(here, wsum, &total));
     hist[tid] = before;   // first place of each cost in the longest-first order
@@ -145,13 +158,18 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     __syncthreads();
 
     const int64_t groups = static_cast<int64_t>(nb) * p.kv_heads;
-    const int weight = s_pair ? 2 : 1;
-    const int64_t cost = (s_pair ? static_cast<int64_t>(s_shares) : all_tiles + static_cast<int64_t>(nb) * kAttnItemCost) * p.kv_heads;
+    const bool pairs = s_ntok > p.tq;
+    const int weight = pairs ? 2 : 1;
+    const int64_t cost = (pairs ? static_cast<int64_t>(s_shares) : all_tiles + static_cast<int64_t>(nb) * kAttnItemCost) * p.kv_heads;
     const int64_t even = (cost + p.ctas - 1) / p.ctas;
     const int64_t each = max((even + weight - 1) & -static_cast<int64_t>(weight), static_cast<int64_t>(kMinPiece));
-    const int64_t whole = weight * max(groups >= p.ctas ? each / weight + s_tail / 2 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
+    const int64_t whole = weight * max(groups >= p.ctas ? each / weight + s_tail * 3 / 8 : 0, static_cast<int64_t>(s_max + kAttnItemCost));
+    // a group's rows are joined as often as it has pieces, share / each and a first
+    const int elems = p.group * p.head_dim;   // of a token
+    const int fixed = pairs ? kCutPair : each == kMinPiece && s_ntok * elems <= kFewElems ? kCutFew : kCutSingle;
+    const float n = static_cast<float>(each), join = (static_cast<float>(s_join) + s_ntok * n) * elems;   // times n
     // (a list too long for 32-bit positions is never short of units)
-    const bool cut = each + (s_pair ? kJoinPair : kJoinSingle) < whole && cost + each < INT32_MAX;
+    const bool cut = join < static_cast<float>(whole - each - fixed) * n * kJoinElems && cost + each < INT32_MAX;
     AttnHdr h = {};
     h.stamp = p.stamp;
     h.nblocks = nb;

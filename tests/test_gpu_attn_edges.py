@@ -149,3 +149,37 @@ def test_a_refused_request_keeps_its_context():
     for r in range(R):
         got, ref = torch.cat(ys[r]).double(), m.recompute(r, torch.cat(xs[r]))
         assert float((got - ref).norm() / ref.norm()) <= 13 * 2.0 ** -8, r
+
+
+def work_list(ws):
+    """The header of the work list in a workspace: blocks, units, weight of a cut (0: whole groups), heads of a section."""
+    return dict(zip(("blocks", "units", "cut", "sec_heads"), ws.buf[768:784].view(torch.int32).tolist()))
+
+
+def list_of(new, kv, H, Hk, D):
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    T, R, i32 = cu[-1], len(new), dict(dtype=torch.int32, device="cuda")
+    ws = A.AttnWorkspace(T, R, H, Hk, D)
+    A.lora_attn_schedule(torch.tensor(cu, **i32), None if kv is None else torch.tensor(kv, **i32), T,
+                         T if kv is None else max(kv), H, Hk, D, ws)
+    assert L.lora_get_status(ws) == 0
+    return work_list(ws)
+
+
+@pytest.mark.parametrize("H,Hk,D", [(1, 1, 128), (4, 1, 128), (8, 1, 128), (16, 2, 128), (1, 1, 64), (8, 1, 64)])
+def test_groups_of_many_rows_are_cut_only_where_the_join_pays(H, Hk, D):
+    """Lists whose cut pieces took 1.2 to 3 times as long to run and join as the whole groups."""
+    for T in (1024, 2048):
+        assert list_of([T], None, H, Hk, D)["cut"] == 0, T
+    if H // Hk < 8:
+        assert list_of([256], [4352], H, Hk, D)["cut"] == 0
+    assert list_of([1024], [2024], H, Hk, D)["cut"] == 0
+    # and ones that take 2 to 5 times as long whole
+    assert list_of([1], [3000], H, Hk, D)["cut"] == 1
+    assert list_of([1] * 12, [250 * r + 90 for r in range(12)], H, Hk, D)["cut"] == 1
+    if H == 1:
+        assert list_of([16384], None, H, Hk, D)["cut"] == 2
+    else:
+        assert list_of([512], [16512], H, Hk, D)["cut"] == 2
