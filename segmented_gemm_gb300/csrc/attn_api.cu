@@ -141,6 +141,23 @@ static bool two_heads(int64_t T, int32_t R, int32_t heads, int32_t kv_heads, boo
            T * (heads / kv_heads) <= static_cast<int64_t>(R) * kAttnFewRows;
 }
 
+// Whether an attention over prompts makes its list itself (ShortList, attn.cu): whole
+// groups, without the launch that builds a list (5 us of 13 for a prompt of 77 tokens).  At
+// most 32 requests, a lane each, and two groups a CTA.  And no prompt may be so long that
+// its groups had better be cut, of which the host knows the tokens in all.  A lone prompt
+// that does not give every CTA a group: up to 6144 tokens with a head dimension of 128 (one
+// head: 4096 tokens 48 us so, 53 by a schedule; 6144 70 and 67; 12000 130 and 73) and 4096
+// with 64, whose pieces are joined faster (4096: 42 and 49; 6144 61 and 43; 12000 116 and
+// 51).  With a group for every CTA, or several prompts, taken to be alike, up to 8192 (8
+// heads on 1, 8000 tokens: 92 us, 98 by a schedule; 16 of 400 to 600 tokens, one head: 14
+// and 18; but 15 of 50 beside one of 6000 67 and 65, with 64 59 and 43).
+static bool makes_own_list(int64_t T, int32_t R, int32_t kv_heads, int32_t head_dim, const AttnLayout &L, int32_t ctas)
+{
+    if (R > 32 || L.max_blocks * kv_heads > 2 * ctas) return false;
+    const bool busy = T / (2 * L.tq) * kv_heads >= ctas;
+    return T <= (R > 1 || busy ? 8192 : 32 * (64 + head_dim));
+}
+
 static int enqueue_schedule(const int32_t *cu, const int32_t *kv_len, int32_t R, int64_t T, int64_t max_kv,
                             int32_t group, int32_t kv_heads, int32_t head_dim, const AttnLayout &L, void *ws,
                             cudaStream_t stream)
@@ -175,7 +192,8 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     const int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
     const int ctas = std::min(num_sms_current_device(), kAttnMaxCtas);
-    const bool short_list = !sched && !kv_len && a->num_requests <= 32 && L.max_blocks * a->kv_heads <= 2 * ctas;
+    const bool short_list = !sched && !kv_len &&
+                            makes_own_list(a->num_tokens, a->num_requests, a->kv_heads, a->head_dim, L, ctas);
     if (sched) {
         if (sched->plan != ws || sched->num_tokens != a->num_tokens || sched->num_requests != a->num_requests ||
             sched->heads != a->heads || sched->kv_heads != a->kv_heads || sched->head_dim != a->head_dim ||

@@ -183,3 +183,21 @@ def test_groups_of_many_rows_are_cut_only_where_the_join_pays(H, Hk, D):
         assert list_of([16384], None, H, Hk, D)["cut"] == 2
     else:
         assert list_of([512], [16512], H, Hk, D)["cut"] == 2
+
+
+@pytest.mark.parametrize("H,Hk,D,lens", [(1, 1, 128, [12000]), (4, 1, 64, [8000]), (2, 2, 64, [50] * 9 + [9000])])
+def test_long_prompts_of_few_heads_run_as_with_a_schedule(H, Hk, D, lens):
+    """Too long for the list that the attention kernel makes itself, though of few groups: whole groups
+    would take 1.2 to 2 times as long as the schedule's cut list, whose results these are to the bit."""
+    T, R = sum(lens), len(lens)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q = torch.randn(T, H, D, device="cuda", generator=g).to(BF)
+    k, v = (torch.randn(T, Hk, D, device="cuda", generator=g).to(BF) for _ in "kv")
+    cu = torch.tensor([sum(lens[:i]) for i in range(R + 1)], dtype=torch.int32, device="cuda")
+    ws = A.AttnWorkspace(T, R, H, Hk, D)
+    o = A.lora_attn_prompt(q, k, v, cu, D ** -0.5, ws)
+    sched = A.lora_attn_schedule(cu, None, T, T, H, Hk, D, ws)
+    assert work_list(ws)["cut"] == 2
+    with_sched = A.lora_attn_prompt(q, k, v, cu, D ** -0.5, ws, sched=sched)
+    assert L.lora_get_status(ws) == 0
+    assert torch.equal(o, with_sched)
