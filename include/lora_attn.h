@@ -142,6 +142,9 @@ int lora_kv_store(const lora_bf16_t *k, const lora_bf16_t *v, int64_t num_tokens
  * infinity in a value of the request itself may reach the request's other rows.
  * Scores, softmax sums and o accumulate in fp32; p is rounded to bf16 for the
  * second product (its sum is taken before that rounding), o once at the end.
+ * The p of a row are taken relative to a score that may lie up to 2^40 below its
+ * largest, so the unnormalised sums have that much less range: o is sure to be finite
+ * for values of up to 2^60 in magnitude; larger ones may give infinity or NaN.
  *
  * q, o: DEVICE bf16, head h of row t at t * token_stride + h * head_stride
  * elements (multiples of 8; 16-byte aligned bases); o must not overlap q, the

@@ -24,7 +24,9 @@
 // to 8000 97 and 103.
 // O stays in tensor memory.  Any m_i near the scores is as good as their maximum: p, l
 // and O are floating point (bf16 has fp32's range), so a larger p costs no precision,
-// and the division by l_i takes m_i out again.  So m_i is the first score that the row
+// and the division by l_i takes m_i out again.  It costs range: over all keys p may sum
+// to 2^66 (2^25 half tiles of 2^40, twice that where quads share rows), so O is finite for
+// |v| up to 2^60.  So m_i is the first score that the row
 // sees, and its own p = 1 keeps l_i from vanishing; it moves, to the maximum of the
 // half tile, only when half a tile's p sum to more than 2^40, and the softmax threads
 // rescale O then.  Otherwise no maximum is computed (with the first half tile's

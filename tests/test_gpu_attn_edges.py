@@ -201,3 +201,25 @@ def test_long_prompts_of_few_heads_run_as_with_a_schedule(H, Hk, D, lens):
     with_sched = A.lora_attn_prompt(q, k, v, cu, D ** -0.5, ws, sched=sched)
     assert L.lora_get_status(ws) == 0
     assert torch.equal(o, with_sched)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_values_that_the_header_promises(n, D):
+    """Values of 2^60, under scores that all lie just as far above each tile's first as leaves the row's reference alone."""
+    s = Step([n, n], [3000, 500], 4, 1, D, 16, seed=7)
+    s.q_cpu = torch.zeros(s.T, 4, D, dtype=torch.float64)
+    s.q_cpu[:, :, 0] = 1.0
+    s.q, s.scale = s.q_cpu.to(BF).cuda(), 0.25
+    kc, vc = s.k_cache.cpu(), s.v_cache.cpu()
+    for r, length in enumerate(s.kv):
+        for pos in range(length):
+            page, slot = int(s.table[r, pos // 16]), pos % 16
+            kc[page, 0, slot] = 0
+            kc[page, 0, slot, 0] = 0.0 if pos % 128 == 0 else 92.0   # scores 0 and 23: p of 2^33, 2^39 in half a tile
+            vc[page, 0, slot] = s.values[r][pos, 0].sign().to(BF) * 2.0 ** 60
+            s.keys[r][pos, 0] = kc[page, 0, slot].double()
+            s.values[r][pos, 0] = vc[page, 0, slot].double()
+    s.k_cache.copy_(kc)
+    s.v_cache.copy_(vc)
+    s.check("large values")
