@@ -44,13 +44,13 @@
 // What bounds it, and what it measured (32 query and 8 kv heads of 128 unless said;
 // peaks: a 6690 GB/s copy, 1867 TFLOP/s bf16):
 //   decode        the cache's bytes.  128 requests of 1000 to 16000 tokens, 4.14 GB:
-//                 608 to 617 us, 6.7 to 6.8 TB/s; 32 requests of up to 8000, 579 MB:
-//                 97 us, 6.0 TB/s (the start, 4 us, and the last pieces' join show)
+//                 608 to 621 us, 6.7 to 6.8 TB/s; 32 requests of up to 8000, 579 MB:
+//                 97 to 98 us, 5.9 to 6.0 TB/s (the start, 4 us, and the last pieces' join show)
 //   long prompts  16384 tokens, 2.2 TFLOP: 1260 to 1310 us (1.68 to 1.74 PFLOP/s, the
-//                 tensor cores busy for 76 % of the cycles), 1335 to 1400 back to back,
+//                 tensor cores busy for 76 % of the cycles), 1320 to 1400 back to back,
 //                 where the power cap bounds it (a plain product then has 1710 TFLOP/s)
 //   head dim 64   the softmax threads: the products take half as long for the same
-//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 133 us,
+//                 exponentials.  Chunks of up to 700 over 9000 tokens, 94 GFLOP: 132 us,
 //                 the special function units busy for 33 % of it and each warp
 //                 waiting mostly on its own chain of loads, exponentials and stores
 //   single calls  latency: one token over 1000 8.9 us, a prompt of 77 8.2 us
