@@ -263,7 +263,7 @@ def lora_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torc
     [T, kv_heads, head_dim], request r's rows [cu[r], cu[r+1])."""
     shape, ks = _rows(k, "k")
     v_shape, vs = _rows(v, "v")
-    if v_shape != shape or shape[0] != q.shape[0] or shape[2] != q.shape[2]:
+    if v_shape != shape or q.ndim != 3 or shape[0] != q.shape[0] or shape[2] != q.shape[2]:
         raise ValueError("lora_attn_prompt: k and v are [T, kv_heads, head_dim] with q's tokens and head dimension")
     a, o = _attn(q, shape[1], cu, cu.shape[0] - 1, scale, o, lse, stream)
     _check(_lib().lora_attn_prompt(a, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],

@@ -223,3 +223,20 @@ def test_the_largest_values_that_the_header_promises(n, D):
     s.k_cache.copy_(kc)
     s.v_cache.copy_(vc)
     s.check("large values")
+
+
+def test_shapes_that_do_not_fit_are_refused():
+    s = Step([2, 3], [40, 50], 4, 2, 64, 16, seed=13)
+    k = torch.zeros(5, 2, 64, dtype=BF, device="cuda")
+    flat = s.q.flatten(1)                      # a projection's rows, heads not told apart
+    for q, kk, v in ((flat, k, k), (s.q, flat, k), (s.q, k, flat), (s.q, k[:4], k[:4]), (s.q[..., :32], k, k),
+                     (s.q, k, k[:, :1]), (s.q.float(), k, k)):
+        with pytest.raises(ValueError):
+            A.lora_attn_prompt(q, kk, v, s.cu, s.scale, s.ws)
+    for q in (flat, s.q[..., :32], s.q.float()):
+        with pytest.raises(ValueError):
+            A.lora_attn_paged(q, s.k_cache, s.v_cache, s.table, s.cu, s.kv_len, s.scale, s.ws)
+    for q, kk in ((k[:, 0], k), (k, k[:, 0]), (k[:, :1], k[:, :1]), (k[..., :32], k[..., :32])):
+        with pytest.raises(ValueError):
+            A.lora_kv_store(q, kk, s.k_cache, s.v_cache, torch.zeros(5, dtype=torch.int32, device="cuda"), s.ws)
+    s.check()
