@@ -254,7 +254,7 @@ def prepare(c, seed):
         elif op in ("rope", "quant"):
             s["ws"] = A.AttnWorkspace(T, 1)
         else:
-            s["ws"] = KV.PagesWorkspace(s["pages"], s["table"].shape[0])
+            s["ws"] = KV.PagesWorkspace(s["pages"])
         if op in ("quant", "attn4"):
             s["cache4"] = KV.Kv4Cache(s["cache"], P, D)
     return s
