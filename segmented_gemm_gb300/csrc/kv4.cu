@@ -1,0 +1,190 @@
+// Writes into and reads of the 4-bit cache (include/lora_kv.h): lora_kv4_store
+// and lora_kv4_load.
+#include <cuda_runtime.h>
+
+#include "kv4.cuh"
+#include "kv_ops.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace lora {
+
+constexpr int kKv4Threads = 256;
+
+// The scale byte of 16 elements whose largest magnitude is amax (finite): amax / 6
+// rounded to 3 fraction bits.  Ties can be told in fp32: amax has 8 significant bits, so
+// a quotient that is not halfway between two scales is at least 2^-13 (relative) off.
+__device__ __forceinline__ uint32_t scale_byte(float amax)
+{
+    const float a = __fdiv_rn(amax, 6.f);
+    if (a < 6.103515625e-05f) return __float2uint_rn(a * 131072.f);   // below 2^-14: multiples of 2^-17
+    const uint32_t bits = __float_as_uint(a);
+    const uint32_t r = (bits + 0x7FFFFu + ((bits >> 20) & 1)) >> 20;  // exponent (bias 127) and 3 bits
+    return min(r - (112u << 3), 226u);                                // 226: 10240
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte)
+{
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
+}
+
+// Two codes, the first in the low half of the byte; nearest, ties to even, saturating.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 16 bf16 elements -> 16 codes (8 bytes) and the scale byte.
+__device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint32_t *scale)
+{
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    uint32_t top = 0;   // the largest magnitude's bits order as the magnitudes do, NaN above all
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        top = max(top, w[i] & 0x7FFF0000u);
+        top = max(top, (w[i] << 16) & 0x7FFF0000u);
+    }
+    if (top > 0x7F800000u) {
+        *scale = 0xFF;
+        return make_uint2(0, 0);
+    }
+    // an infinity counts as the largest bf16: the scale saturates, and x / s does
+    const uint32_t b = scale_byte(__uint_as_float(min(top, 0x7F7F0000u)));
+    *scale = b;
+    if (b == 0) return make_uint2(0, 0);
+    const float s = scale_value(b);
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // divided as the definition says: x / s falls on a tie exactly or clearly beside it
+        const uint32_t two = e2m1_pair(__fdiv_rn(bf16_lo(w[i]), s), __fdiv_rn(bf16_hi(w[i]), s));
+        c[i / 4] |= two << (8 * (i % 4));
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+// A thread takes 16 elements of a head's key row and of its value row, consecutive
+// threads consecutive elements; memory bounds it.
+template <int DP>
+__global__ void __launch_bounds__(kKv4Threads) kv4_store_kernel(const Kv4StoreParams p)
+{
+    pdl_launch_dependents();
+    using Tile = Kv4Tile<DP>;
+    const uint32_t per = static_cast<uint32_t>(p.kv_heads) * Tile::kGroups;
+    const int64_t total = p.T * per;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kKv4Threads;
+    pdl_wait();
+    int bad = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kKv4Threads + threadIdx.x; i < total; i += stride) {
+        const int64_t t = total < (int64_t(1) << 32) ? static_cast<uint32_t>(i) / per : i / per;
+        const int u = static_cast<int>(i - t * per), h = u / Tile::kGroups, g = u % Tile::kGroups;
+        const int32_t slot = p.slot_map[t];
+        uint4 k[2] = {}, v[2] = {};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = 16 * g + 8 * e;
+            if (d >= p.head_dim) continue;   // padding
+            k[e] = *reinterpret_cast<const uint4 *>(p.k + t * p.k_tok + h * p.k_head + d);
+            v[e] = *reinterpret_cast<const uint4 *>(p.v + t * p.v_tok + h * p.v_head + d);
+        }
+        if (slot < 0 || slot >= p.slots) {
+            bad |= slot != -1;
+            continue;
+        }
+        const int64_t page = slot >> p.page_shift;
+        const int line = slot & ((1 << p.page_shift) - 1), j = line & 15;
+        uint8_t *tile = p.data + page * p.page_stride + h * p.head_stride + (line >> 4) * Tile::kBytes;
+        uint32_t scale;
+        uint2 c = quantise(k[0], k[1], &scale);
+        *reinterpret_cast<uint2 *>(tile + j * (DP / 2) + g * 8) = c;
+        tile[Tile::kKeyScales + j * Tile::kGroups + g] = static_cast<uint8_t>(scale);
+        c = quantise(v[0], v[1], &scale);
+        *reinterpret_cast<uint32_t *>(tile + Tile::value_word(j, 16 * g)) = c.x;
+        *reinterpret_cast<uint32_t *>(tile + Tile::value_word(j, 16 * g + 8)) = c.y;
+        tile[Tile::value_scale(j, g)] = static_cast<uint8_t>(scale);
+    }
+    if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+}
+
+// 8 codes and their scale -> 8 bf16 values (exact: 6 significant bits).
+__device__ __forceinline__ uint4 values_of(uint32_t codes, uint32_t scale)
+{
+    uint32_t f[4];
+    e2m1x8_to_f16(codes, f);
+    const uint32_t s = scale_pair<0, 0>(scale);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = mul_f16x2(f[i], s);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+        o[i] = pack_bf16x2(x.x, x.y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The reverse, the same split; memory bounds it, three quarters of it the writes.
+template <int DP>
+__global__ void __launch_bounds__(kKv4Threads) kv4_load_kernel(const Kv4LoadParams p)
+{
+    pdl_launch_dependents();
+    using Tile = Kv4Tile<DP>;
+    const uint32_t groups = (p.head_dim + 15) / 16, per = static_cast<uint32_t>(p.kv_heads) * groups;
+    const int64_t total = p.n * per;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kKv4Threads;
+    pdl_wait();
+    int bad = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kKv4Threads + threadIdx.x; i < total; i += stride) {
+        const int64_t t = total < (int64_t(1) << 32) ? static_cast<uint32_t>(i) / per : i / per;
+        const int u = static_cast<int>(i - t * per), h = u / groups, g = u - h * groups;
+        const int32_t slot = p.slot_list[t];
+        const bool on = slot >= 0 && slot < p.slots;
+        bad |= !on && slot != -1;
+        uint2 kw = {}, vw = {};
+        uint32_t ks = 0, vs = 0;
+        if (on) {
+            const int64_t page = slot >> p.page_shift;
+            const int line = slot & ((1 << p.page_shift) - 1), j = line & 15;
+            const uint8_t *tile = p.data + page * p.page_stride + h * p.head_stride + (line >> 4) * Tile::kBytes;
+            kw = *reinterpret_cast<const uint2 *>(tile + j * (DP / 2) + g * 8);
+            ks = tile[Tile::kKeyScales + j * Tile::kGroups + g];
+            vw.x = *reinterpret_cast<const uint32_t *>(tile + Tile::value_word(j, 16 * g));
+            vw.y = *reinterpret_cast<const uint32_t *>(tile + Tile::value_word(j, 16 * g + 8));
+            vs = tile[Tile::value_scale(j, g)];
+        }
+        const bool second = 16 * g + 8 < p.head_dim;
+        if (p.k) {
+            uint16_t *k = p.k + t * p.k_tok + h * p.k_head + 16 * g;
+            *reinterpret_cast<uint4 *>(k) = values_of(kw.x, ks);
+            if (second) *reinterpret_cast<uint4 *>(k + 8) = values_of(kw.y, ks);
+        }
+        if (p.v) {
+            uint16_t *v = p.v + t * p.v_tok + h * p.v_head + 16 * g;
+            *reinterpret_cast<uint4 *>(v) = values_of(vw.x, vs);
+            if (second) *reinterpret_cast<uint4 *>(v + 8) = values_of(vw.y, vs);
+        }
+    }
+    if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+}
+
+static int64_t kv4_ctas(int64_t total)
+{
+    const int64_t ctas = (total + kKv4Threads - 1) / kKv4Threads, cap = 16ll * num_sms_current_device();
+    return ctas < cap ? ctas : cap;
+}
+
+cudaError_t launch_kv4_store(const Kv4StoreParams &p, cudaStream_t stream)
+{
+    const int dp = kv4_padded(p.head_dim);
+    return launch_pdl(dp == 64 ? kv4_store_kernel<64> : kv4_store_kernel<128>,
+                      kv4_ctas(p.T * p.kv_heads * (dp / 16)), kKv4Threads, 0, p, stream);
+}
+
+cudaError_t launch_kv4_load(const Kv4LoadParams &p, cudaStream_t stream)
+{
+    return launch_pdl(p.head_dim <= 64 ? kv4_load_kernel<64> : kv4_load_kernel<128>,
+                      kv4_ctas(p.n * p.kv_heads * ((p.head_dim + 15) / 16)), kKv4Threads, 0, p, stream);
+}
+
+}  // namespace lora

@@ -1,0 +1,415 @@
+// Host side of include/lora_kv.h: argument checks, workspace carving and
+// launches.  Nothing here allocates, synchronises or copies.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "attn_checks.h"
+#include "internal.h"
+#include "kv_ops.h"
+
+namespace lora {
+
+constexpr size_t kStatusBytes = 256;   // workspace of the calls that only report
+
+static bool page_size_ok(int32_t page_size, int32_t least)
+{
+    return page_size >= least && page_size <= 4096 && (page_size & (page_size - 1)) == 0;
+}
+
+// Bytes from one page or head of the 4-bit cache to the next.
+static bool kv4_stride_ok(int64_t s, int64_t extent)
+{
+    return extent <= 1 || (s > 0 && s % 16 == 0 && s < (int64_t(1) << 36));
+}
+
+static int check_cache4(const lora_kv4_cache_t *c)
+{
+    if (!c || !c->data) return LORA_ERR_NULL;
+    if (c->kv_heads <= 0 || c->head_dim <= 0 || c->head_dim > LORA_MAX_HEAD_DIM || c->head_dim % 8) return LORA_ERR_SHAPE;
+    if (!page_size_ok(c->page_size, 16)) return LORA_ERR_SHAPE;
+    if (c->num_pages <= 0 || static_cast<int64_t>(c->num_pages) * c->page_size >= (int64_t(1) << 31))
+        return LORA_ERR_SHAPE;
+    if (!kv4_stride_ok(c->page_stride, c->num_pages) || !kv4_stride_ok(c->head_stride, c->kv_heads)) return LORA_ERR_SHAPE;
+    return aligned(c->data, 16) ? LORA_OK : LORA_ERR_ALIGN;
+}
+
+static Kv4Layout kv4_layout(int32_t head_dim)
+{
+    // the widest blocks run one CTA an SM, so the product of slots and columns is the same for all but the widest
+    // multiple: 2 * kKv4MaxCtas slots of 16 columns hold kKv4MaxCtas of 32
+    Kv4Layout L;
+    const size_t dp = kv4_padded(head_dim), cells = 2 * static_cast<size_t>(kKv4MaxCtas) * 16;
+    L.counters = 0;
+    L.zeros = align256((kKv4CntGroup + kKv4MaxCtas) * 4);
+    L.part = L.zeros + align256(kv4_tile_bytes(128));
+    L.part_ml = L.part + align256(cells * dp * 4);
+    L.total = L.part_ml + align256(cells * 8);
+    return L;
+}
+
+static PagesLayout pages_layout(int32_t num_pages)
+{
+    PagesLayout L;
+    const size_t n = num_pages, chunks = (n + kPageChunk - 1) / kPageChunk;
+    L.counters = 0;
+    L.used = kStatusBytes;
+    L.free = L.used + align256(n);
+    L.counts = L.free + align256(n);
+    L.map = L.counts + align256(chunks * sizeof(int4));
+    L.total = L.map + align256(n * 4);
+    return L;
+}
+
+static bool num_pages_ok(int32_t n) { return n > 0 && n < (1 << 28); }
+
+// The checks of a lora_kv_pages_t, and the parameters that all calls share.
+static int prepare_pages(const lora_kv_pages_t *a, void *ws, size_t ws_bytes, KvPagesParams *p)
+{
+    if (!a) return LORA_ERR_NULL;
+    if (!page_size_ok(a->page_size, 8) || !num_pages_ok(a->num_pages) ||
+        static_cast<int64_t>(a->num_pages) * a->page_size >= (int64_t(1) << 31))
+        return LORA_ERR_SHAPE;
+    if (a->num_rows < 0 || a->num_rows > LORA_MAX_REQUESTS || a->table_width < 0 || a->num_free < 0 ||
+        static_cast<int64_t>(a->table_width) * a->page_size >= (int64_t(1) << 31))
+        return LORA_ERR_SHAPE;
+    if (a->num_rows > 1 && a->table_stride < a->table_width) return LORA_ERR_SHAPE;
+    if (!a->ref || !a->free_head || (a->num_free > 0 && !a->free_pages)) return LORA_ERR_NULL;
+    if (a->num_rows > 0 && (!a->ctx_len || (a->table_width > 0 && !a->block_table))) return LORA_ERR_NULL;
+    if (!ints_aligned({a->block_table, a->ctx_len, a->ref, a->free_pages, a->free_head})) return LORA_ERR_ALIGN;
+    const PagesLayout L = pages_layout(a->num_pages);
+    const int rc = check_ws(ws, ws_bytes, L.total);
+    if (rc) return rc;
+    std::memset(p, 0, sizeof *p);
+    p->a = *a;
+    p->counters = at<int32_t>(ws, L.counters);
+    p->used = at<uint8_t>(ws, L.used);
+    p->free = at<uint8_t>(ws, L.free);
+    p->counts = at<int4>(ws, L.counts);
+    p->map = at<int32_t>(ws, L.map);
+    return LORA_OK;
+}
+
+static int launched(cudaError_t e) { return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; }
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" int lora_qk_rope(const lora_qk_rope_t *rope, const lora_kv_cache_t *cache, void *ws, size_t ws_bytes,
+                            lora_stream_t stream)
+{
+    if (!rope) return LORA_ERR_NULL;
+    const lora_qk_rope_t &a = *rope;
+    if (cache) {
+        const int rc = check_cache(cache);
+        if (rc) return rc;
+        if (cache->kv_heads != a.kv_heads || cache->head_dim != a.head_dim) return LORA_ERR_SHAPE;
+    }
+    if (a.num_tokens < 0 || a.num_tokens > kMaxTokens || a.heads < 0 || a.kv_heads < 0 || a.heads > 65536 ||
+        a.kv_heads > 65536 || a.head_dim <= 0 || a.head_dim > LORA_MAX_HEAD_DIM || a.head_dim % 8 || a.rot_dim < 0 ||
+        a.rot_dim > a.head_dim || a.rot_dim % 8)
+        return LORA_ERR_SHAPE;
+    if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return LORA_ERR_SHAPE;
+    if (!stride_ok(a.q_token_stride, a.heads ? a.num_tokens : 0) || !stride_ok(a.q_head_stride, a.heads) ||
+        !stride_ok(a.qo_token_stride, a.heads ? a.num_tokens : 0) || !stride_ok(a.qo_head_stride, a.heads) ||
+        !stride_ok(a.k_token_stride, a.kv_heads ? a.num_tokens : 0) || !stride_ok(a.k_head_stride, a.kv_heads))
+        return LORA_ERR_SHAPE;
+    if (a.k_out && a.kv_heads &&
+        (!stride_ok(a.ko_token_stride, a.num_tokens) || !stride_ok(a.ko_head_stride, a.kv_heads)))
+        return LORA_ERR_SHAPE;
+    if (cache && (!stride_ok(a.v_token_stride, a.num_tokens) || !stride_ok(a.v_head_stride, a.kv_heads)))
+        return LORA_ERR_SHAPE;
+    if (a.num_tokens == 0 || (a.heads == 0 && a.kv_heads == 0)) return LORA_OK;
+    if ((a.heads && (!a.q || !a.q_out)) || (a.kv_heads && (!a.k || (!cache && !a.k_out)))) return LORA_ERR_NULL;
+    if ((cache && (!a.v || !a.slot_map)) || !a.position || (a.rot_dim && !a.inv_freq)) return LORA_ERR_NULL;
+    for (const void *x : {static_cast<const void *>(a.q), static_cast<const void *>(a.k), static_cast<const void *>(a.v),
+                          static_cast<const void *>(a.q_out), static_cast<const void *>(a.k_out),
+                          static_cast<const void *>(a.q_weight), static_cast<const void *>(a.k_weight)})
+        if (!aligned(x, 16)) return LORA_ERR_ALIGN;
+    if (!ints_aligned({a.position, a.inv_freq, a.slot_map})) return LORA_ERR_ALIGN;
+    // in place means row by row
+    if ((a.heads && a.q_out == a.q && ((a.num_tokens > 1 && a.qo_token_stride != a.q_token_stride) ||
+                                       (a.heads > 1 && a.qo_head_stride != a.q_head_stride))) ||
+        (a.kv_heads && a.k_out == a.k && ((a.num_tokens > 1 && a.ko_token_stride != a.k_token_stride) ||
+                                          (a.kv_heads > 1 && a.ko_head_stride != a.k_head_stride))))
+        return LORA_ERR_SHAPE;
+    const int rc = check_ws(ws, ws_bytes, kStatusBytes);
+    if (rc) return rc;
+    QkRopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.a = a;
+    p.status = at<int32_t>(ws, 0) + CNT_STATUS;
+    if (cache) {
+        p.kc = cache->k;
+        p.vc = cache->v;
+        p.page_stride = cache->page_stride;
+        p.head_stride = cache->head_stride;
+        p.slot_stride = cache->slot_stride;
+        p.slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+        p.page_shift = page_shift(cache->page_size);
+    }
+    return launched(launch_qk_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lora_kv4_block_size(int32_t page_size, int32_t head_dim)
+{
+    if (!page_size_ok(page_size, 16) || head_dim <= 0 || head_dim > LORA_MAX_HEAD_DIM || head_dim % 8) return 0;
+    return static_cast<size_t>(page_size / 16) * kv4_tile_bytes(kv4_padded(head_dim));
+}
+
+extern "C" int lora_kv4_store(const lora_bf16_t *k, const lora_bf16_t *v, int64_t num_tokens, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                              const lora_kv4_cache_t *cache, const int32_t *slot_map, void *ws, size_t ws_bytes,
+                              lora_stream_t stream)
+{
+    int rc = check_cache4(cache);
+    if (rc) return rc;
+    if (num_tokens < 0 || num_tokens > kMaxTokens) return LORA_ERR_SHAPE;
+    if (!stride_ok(k_token_stride, num_tokens) || !stride_ok(v_token_stride, num_tokens) ||
+        !stride_ok(k_head_stride, cache->kv_heads) || !stride_ok(v_head_stride, cache->kv_heads))
+        return LORA_ERR_SHAPE;
+    if (num_tokens == 0) return LORA_OK;
+    if (!k || !v || !slot_map) return LORA_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4)) return LORA_ERR_ALIGN;
+    rc = check_ws(ws, ws_bytes, kStatusBytes);
+    if (rc) return rc;
+    Kv4StoreParams p;
+    p.k = k;
+    p.v = v;
+    p.k_tok = k_token_stride;
+    p.k_head = k_head_stride;
+    p.v_tok = v_token_stride;
+    p.v_head = v_head_stride;
+    p.data = cache->data;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+    p.page_shift = page_shift(cache->page_size);
+    p.kv_heads = cache->kv_heads;
+    p.head_dim = cache->head_dim;
+    p.T = num_tokens;
+    p.slot_map = slot_map;
+    p.status = at<int32_t>(ws, 0) + CNT_STATUS;
+    return launched(launch_kv4_store(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int lora_kv4_load(const lora_kv4_cache_t *cache, const int32_t *slots, int64_t num_slots, lora_bf16_t *k,
+                             lora_bf16_t *v, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    int rc = check_cache4(cache);
+    if (rc) return rc;
+    if (num_slots < 0 || num_slots > kMaxTokens) return LORA_ERR_SHAPE;
+    if ((k && (!stride_ok(k_token_stride, num_slots) || !stride_ok(k_head_stride, cache->kv_heads))) ||
+        (v && (!stride_ok(v_token_stride, num_slots) || !stride_ok(v_head_stride, cache->kv_heads))))
+        return LORA_ERR_SHAPE;
+    if (num_slots == 0 || (!k && !v)) return LORA_OK;
+    if (!slots) return LORA_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return LORA_ERR_ALIGN;
+    rc = check_ws(ws, ws_bytes, kStatusBytes);
+    if (rc) return rc;
+    Kv4LoadParams p;
+    p.k = k;
+    p.v = v;
+    p.k_tok = k_token_stride;
+    p.k_head = k_head_stride;
+    p.v_tok = v_token_stride;
+    p.v_head = v_head_stride;
+    p.data = cache->data;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+    p.page_shift = page_shift(cache->page_size);
+    p.kv_heads = cache->kv_heads;
+    p.head_dim = cache->head_dim;
+    p.n = num_slots;
+    p.slot_list = slots;
+    p.status = at<int32_t>(ws, 0) + CNT_STATUS;
+    return launched(launch_kv4_load(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t heads, int32_t kv_heads,
+                                          int32_t head_dim)
+{
+    if (!step_ok(num_tokens, num_requests) || !heads_ok(heads, kv_heads, head_dim)) return 0;
+    return kv4_layout(head_dim).total;
+}
+
+extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *cache, const int32_t *block_table,
+                             int32_t table_width, int64_t table_stride, const int32_t *kv_len, void *ws,
+                             size_t ws_bytes, lora_stream_t stream)
+{
+    int rc = check_attn(attn);
+    if (rc) return rc;
+    rc = check_cache4(cache);
+    if (rc) return rc;
+    if (cache->kv_heads != attn->kv_heads || cache->head_dim != attn->head_dim) return LORA_ERR_SHAPE;
+    if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > kMaxTokens) return LORA_ERR_SHAPE;
+    if (attn->num_requests > 1 && table_stride < table_width) return LORA_ERR_SHAPE;
+    if (attn->num_tokens * (attn->heads / attn->kv_heads) > kMaxTokens) return LORA_ERR_SHAPE;   // rows of a key head
+    if (attn->num_tokens == 0 || attn->num_requests == 0) return LORA_OK;
+    if (!kv_len || (table_width > 0 && !block_table)) return LORA_ERR_NULL;
+    if (!ints_aligned({kv_len, block_table})) return LORA_ERR_ALIGN;
+    const Kv4Layout L = kv4_layout(attn->head_dim);
+    rc = check_ws(ws, ws_bytes, L.total);
+    if (rc) return rc;
+    Kv4AttnParams p;
+    p.q = attn->q;
+    p.o = attn->o;
+    p.lse = attn->lse;
+    p.q_tok = attn->q_token_stride;
+    p.q_head = attn->q_head_stride;
+    p.o_tok = attn->o_token_stride;
+    p.o_head = attn->o_head_stride;
+    p.cu = attn->cu;
+    p.kv_len = kv_len;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.max_kv = static_cast<int64_t>(table_width) * cache->page_size;
+    p.data = cache->data;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.num_pages = cache->num_pages;
+    p.page_shift = page_shift(cache->page_size);
+    p.T = static_cast<int32_t>(attn->num_tokens);
+    p.R = attn->num_requests;
+    p.heads = attn->heads;
+    p.kv_heads = attn->kv_heads;
+    p.group = attn->heads / attn->kv_heads;
+    p.head_dim = attn->head_dim;
+    p.scale = attn->scale;
+    p.zeros = at<uint8_t>(ws, L.zeros);
+    p.counters = at<int32_t>(ws, L.counters);
+    p.part = at<float>(ws, L.part);
+    p.part_ml = at<float2>(ws, L.part_ml);
+    p.wait_cycles = tc_wait_cycles();
+    return launched(launch_kv4_attn(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lora_kv_pages_workspace_size(int32_t num_pages)
+{
+    return num_pages_ok(num_pages) ? pages_layout(num_pages).total : 0;
+}
+
+extern "C" int lora_kv_release(const lora_kv_pages_t *pages, const int32_t *rows, int32_t num, void *ws, size_t ws_bytes,
+                               lora_stream_t stream)
+{
+    KvPagesParams p;
+    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
+    if (num < 0 || num > LORA_MAX_REQUESTS) return LORA_ERR_SHAPE;
+    if (num == 0) return LORA_OK;
+    if (!rows) return LORA_ERR_NULL;
+    if (!aligned(rows, 4)) return LORA_ERR_ALIGN;
+    p.rows = rows;
+    p.num = num;
+    return launched(launch_kv_release(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int lora_kv_fork(const lora_kv_pages_t *pages, const int32_t *parent, const int32_t *child, int32_t num,
+                            int32_t *copy_src, int32_t *copy_dst, void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    KvPagesParams p;
+    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
+    if (num < 0 || num > LORA_MAX_REQUESTS) return LORA_ERR_SHAPE;
+    if (num == 0) return LORA_OK;
+    if (!parent || !child || !copy_src || !copy_dst) return LORA_ERR_NULL;
+    if (!ints_aligned({parent, child, copy_src, copy_dst})) return LORA_ERR_ALIGN;
+    p.parent = parent;
+    p.child = child;
+    p.num = num;
+    p.src = copy_src;
+    p.dst = copy_dst;
+    return launched(launch_kv_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int lora_kv_compact(const lora_kv_pages_t *pages, int32_t limit, int32_t *copy_src, int32_t *copy_dst,
+                               int32_t max_copies, int32_t *table_out, int32_t *ref_out, int32_t *free_out,
+                               int32_t *head_out, void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    KvPagesParams p;
+    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
+    if (limit < 0 || max_copies < 0) return LORA_ERR_SHAPE;
+    if (max_copies > 0 && (!copy_src || !copy_dst)) return LORA_ERR_NULL;
+    if (!ints_aligned({copy_src, copy_dst, table_out, ref_out, free_out, head_out})) return LORA_ERR_ALIGN;
+    p.limit = limit;
+    p.max_copies = max_copies;
+    p.src = copy_src;
+    p.dst = copy_dst;
+    p.table_out = table_out ? table_out : pages->block_table;
+    p.ref_out = ref_out ? ref_out : pages->ref;
+    p.free_out = free_out ? free_out : pages->free_pages;
+    p.head_out = head_out ? head_out : pages->free_head;
+    return launched(launch_kv_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+// The common part of both copies.
+static int copy_pages(const int32_t *src, const int32_t *dst, int32_t num, PageCopyParams *p, void *ws, size_t ws_bytes,
+                      lora_stream_t stream)
+{
+    if (num < 0) return LORA_ERR_SHAPE;
+    if (num == 0) return LORA_OK;
+    if (!src || !dst) return LORA_ERR_NULL;
+    if (!ints_aligned({src, dst})) return LORA_ERR_ALIGN;
+    const int rc = check_ws(ws, ws_bytes, kStatusBytes);
+    if (rc) return rc;
+    p->src = src;
+    p->dst = dst;
+    p->num = num;
+    p->status = at<int32_t>(ws, 0) + CNT_STATUS;
+    return launched(launch_page_copy(*p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int lora_kv_copy(const int32_t *src, const int32_t *dst, int32_t num, const lora_kv_cache_t *cache, void *ws,
+                            size_t ws_bytes, lora_stream_t stream)
+{
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    PageCopyParams p;
+    std::memset(&p, 0, sizeof p);
+    p.base[0] = reinterpret_cast<uint4 *>(cache->k);
+    p.base[1] = reinterpret_cast<uint4 *>(cache->v);
+    p.num_pages = cache->num_pages;
+    p.page_stride = cache->page_stride / 8;
+    p.heads = cache->kv_heads;
+    p.rows = cache->page_size;
+    p.vecs = cache->head_dim / 8;
+    p.head_stride = cache->head_stride / 8;
+    p.slot_stride = cache->slot_stride / 8;
+    // a page's units without gaps, in either order of heads and slots: one run
+    const bool heads_outer = p.slot_stride == p.vecs && (p.heads == 1 || p.head_stride == static_cast<int64_t>(p.rows) * p.vecs);
+    const bool rows_outer = (p.heads == 1 || p.head_stride == p.vecs) && p.slot_stride == static_cast<int64_t>(p.heads) * p.vecs;
+    if (static_cast<int64_t>(p.heads) * p.rows * p.vecs > (1 << 30)) return LORA_ERR_SHAPE;
+    if (heads_outer || rows_outer) {
+        p.vecs *= p.heads * p.rows;
+        p.heads = p.rows = 1;
+    }
+    return copy_pages(src, dst, num, &p, ws, ws_bytes, stream);
+}
+
+extern "C" int lora_kv4_copy(const int32_t *src, const int32_t *dst, int32_t num, const lora_kv4_cache_t *cache,
+                             void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    const int rc = check_cache4(cache);
+    if (rc) return rc;
+    PageCopyParams p;
+    std::memset(&p, 0, sizeof p);
+    p.base[0] = reinterpret_cast<uint4 *>(cache->data);
+    p.num_pages = cache->num_pages;
+    p.page_stride = cache->page_stride / 16;
+    p.heads = cache->kv_heads;
+    p.rows = 1;
+    p.vecs = static_cast<int32_t>(lora_kv4_block_size(cache->page_size, cache->head_dim) / 16);
+    p.head_stride = cache->head_stride / 16;
+    if (static_cast<int64_t>(p.heads) * p.vecs > (1 << 30)) return LORA_ERR_SHAPE;
+    if (p.heads == 1 || p.head_stride == p.vecs) {
+        p.vecs *= p.heads;
+        p.heads = 1;
+    }
+    return copy_pages(src, dst, num, &p, ws, ws_bytes, stream);
+}

@@ -1,0 +1,138 @@
+// Internal declarations of the cache operators (include/lora_kv.h).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "attn.h"
+#include "lora_kv.h"
+
+namespace lora {
+
+// Elements of a head's row in the 4-bit cache, and bytes of a tile of 16 keys.
+constexpr int kv4_padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
+constexpr int kv4_tile_bytes(int padded) { return 18 * padded; }
+
+struct QkRopeParams {
+    lora_qk_rope_t a;
+    uint16_t *kc, *vc;                       // the cache, or NULL
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t slots;
+    int32_t page_shift;
+    int32_t *status;
+};
+
+struct Kv4StoreParams {
+    const uint16_t *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;
+    uint8_t *data;
+    int64_t page_stride, head_stride;
+    int64_t slots;
+    int32_t page_shift, kv_heads, head_dim;
+    int64_t T;
+    const int32_t *slot_map;
+    int32_t *status;
+};
+
+struct Kv4LoadParams {
+    uint16_t *k, *v;                         // either may be NULL
+    int64_t k_tok, k_head, v_tok, v_head;
+    const uint8_t *data;
+    int64_t page_stride, head_stride;
+    int64_t slots;
+    int32_t page_shift, kv_heads, head_dim;
+    int64_t n;
+    const int32_t *slot_list;
+    int32_t *status;
+};
+
+constexpr int kKv4MaxCtas = 2 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
+
+// Workspace of the 4-bit attention (offsets 256-byte aligned): the status word and
+// the arrival counters of split groups (zero at rest but the status), a tile of zeros
+// that stands for pages outside the cache, and the partial results.
+struct Kv4Layout {
+    size_t counters, zeros, part, part_ml, total;
+};
+constexpr int kKv4CntGroup = 32;                // first arrival counter; one for each CTA
+
+struct Kv4AttnParams {
+    const uint16_t *q;
+    uint16_t *o;
+    float *lse;
+    int64_t q_tok, q_head, o_tok, o_head;       // element strides
+    const int32_t *cu, *kv_len, *table;
+    int64_t table_stride;
+    int64_t max_kv;                             // table_width * page_size
+    const uint8_t *data;
+    int64_t page_stride, head_stride;           // bytes
+    int32_t num_pages, page_shift;
+    int32_t T, R;
+    int32_t heads, kv_heads, group, head_dim;
+    float scale;
+    const uint8_t *zeros;
+    int32_t *counters;
+    float *part;                                // [2 * CTAs][columns][padded head_dim] partial O
+    float2 *part_ml;                            // [2 * CTAs][columns] partial (m, l)
+    int64_t wait_cycles;
+};
+
+// Workspace of the calls on pages (offsets 256-byte aligned; all of it zero at
+// rest but the status, the counts and the map).
+struct PagesLayout {
+    size_t counters, used, free, counts, map, total;
+};
+constexpr int kPagesArrived = 2;                // counter: CTAs done with their reading
+constexpr int kPageChunk = 4096;                // pages that one CTA counts and lists
+
+struct KvPagesParams {
+    lora_kv_pages_t a;
+    int32_t *counters;
+    uint8_t *used, *free;                       // [num_pages] marks
+    int4 *counts;                               // [chunks]
+    int32_t *map;                               // [num_pages] place + 1 of a page that moves, or 0
+    // release: rows; fork: parent and child
+    const int32_t *rows, *parent, *child;
+    int32_t num;
+    int32_t *src, *dst;
+    // compact
+    int32_t limit, max_copies;
+    int32_t *table_out, *ref_out, *free_out, *head_out;
+};
+
+struct PageCopyParams {
+    const int32_t *src, *dst;
+    int32_t num;
+    int32_t num_pages;
+    uint4 *base[2];                             // keys and values; the 4-bit cache has one
+    int64_t page_stride;                        // in 16-byte units, as all below
+    int64_t head_stride, slot_stride;
+    int32_t rows, heads, vecs;                  // a page: heads x rows x vecs units (heads = rows = 1: contiguous)
+    int32_t *status;
+};
+
+cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_store(const Kv4StoreParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_load(const Kv4LoadParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream);
+cudaError_t launch_kv_release(const KvPagesParams &p, cudaStream_t stream);
+cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvPagesParams &p, cudaStream_t stream);
+cudaError_t launch_page_copy(const PageCopyParams &p, cudaStream_t stream);
+
+// A launch that may start its prologue while the one ahead finishes.
+template <typename P>
+inline cudaError_t launch_pdl(void (*kernel)(P), int64_t ctas, int threads, size_t smem, const P &p, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    pdl_attribute(cfg, at);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace lora
