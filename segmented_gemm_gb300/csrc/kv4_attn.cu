@@ -21,10 +21,12 @@
 //   - a warp is on its own: it takes tiles of 16 keys from its own ring of bulk
 //     copies, so nothing but the ends of pieces is synchronised.
 //
-// The groups (request, key head, block of columns) in a row, a tile of each a
-// unit, are cut evenly over the CTAs; a CTA's warps split each piece.  Pieces of a
-// group cut by a CTA boundary go to the workspace, and the CTA that stores the
-// last of them joins them in order.
+// The groups (request, key head, block of columns) in a row, with what beginning one
+// costs (kGap) ahead of its tiles, are cut evenly over all warps.  Whole groups are
+// written by their warp.  The pieces of a cut one meet in shared memory at the end,
+// once for a CTA; those of a group that CTAs share in the workspace, where the
+// CTA that stores the last of them joins them in order, so that results do not depend
+// on timing.
 #include <cuda_runtime.h>
 
 #include "block_scan.cuh"
@@ -38,11 +40,11 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 4;          // tiles of a warp's ring
-constexpr int kSlots = 4;           // results of warps in shared memory at a time
+constexpr int kGap = 3;             // what a group costs beside its tiles, in tiles
+constexpr int kMinShare = 2;        // least share of a warp, in tiles
+constexpr int kBatch = 2;           // most tiles of a stage of a warp's ring
 constexpr float kSlack = 8.f;       // log2 of the largest p
 constexpr float kNone = -1e30f;     // m of a column that has seen no key
-constexpr int kMinTiles = 16;       // least tiles of a CTA's share, two a warp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -72,6 +74,22 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
     return r;
 }
 
+// mbar_wait, with what it does when the barrier is not there yet out of line.
+__device__ __noinline__ bool wait_loop(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status, int64_t budget)
+{
+    return mbar_wait(bar, parity, abort, status, LORA_DEV_TIMEOUT, budget);
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status, int64_t budget)
+{
+    return mbar_try_wait(smem_u32(bar), parity) || wait_loop(bar, parity, abort, status, budget);
+}
+
+// a / b; most quotients here fit 32 bits, where a division takes a quarter of the time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // Packed tokens of request r and its keys, clamped.
 struct Request {
     int tok0, n, keys;
@@ -89,13 +107,21 @@ __device__ __forceinline__ Request request(const Kv4AttnParams &p, int r, int *b
     return q;
 }
 
-// The pieces of a CTA's share, one after another: tiles [t0, t1) of block b of key head h
-// of request r.  A request has kv_heads * blocks groups of `tiles` tiles.
+// A group, as far as its rows and its place among the units go.
+struct Group {
+    int64_t start;      // its first unit
+    int cost;           // its units: kGap and its tiles
+    int tok0, h, first_row, cols;   // first token of the request, key head, first row of the block, rows of the block
+};
+
+// The pieces of a warp's share, one after another: tiles [t0, t1) of block b of key head
+// h of request r.  A request has kv_heads * blocks groups of kGap + tiles units, and a
+// warp begins or ends inside one only behind its gap.
 template <int NC>
 struct Pieces {
     int r, h, b, t0, t1, tiles, blocks;
     Request q;
-    int64_t left;
+    int64_t at, left;   // place in the group, units left from there
 
     __device__ __forceinline__ void take(const Kv4AttnParams &p)
     {
@@ -104,275 +130,314 @@ struct Pieces {
         blocks = (q.n * p.group + NC - 1) / NC;
         tiles = max(1, (q.keys + 15) >> 4);
     }
-    // the piece that starts at unit `at` of request r, of at most `share` units
-    __device__ __forceinline__ void start(const Kv4AttnParams &p, int r_, int64_t at, int64_t share)
+    // the first piece of a share of `units` that begins at unit u of request r_; false if there is none
+    __device__ __forceinline__ bool start(const Kv4AttnParams &p, int r_, int64_t u, int64_t units)
     {
         r = r_;
         take(p);
-        const int64_t g = at / tiles;
-        t0 = static_cast<int>(at - g * tiles);
-        h = static_cast<int>(g / blocks);
+        const int64_t g = quotient(u, tiles + kGap);
+        at = u - g * (tiles + kGap);
+        h = static_cast<int>(blocks == 1 ? g : quotient(g, blocks));
         b = static_cast<int>(g - static_cast<int64_t>(h) * blocks);
-        left = share;
-        cut();
+        left = units;
+        return cut();
     }
-    __device__ __forceinline__ void cut()
+    __device__ __forceinline__ bool cut()
     {
-        t1 = left < tiles - t0 ? t0 + static_cast<int>(left) : tiles;
-        left -= t1 - t0;
+        if (left <= 0) return false;
+        t0 = static_cast<int>(at > kGap ? at - kGap : 0);
+        const int64_t end = at + left, cost = tiles + kGap;
+        if (end < cost && end <= kGap) {   // not behind the gap: the next warp's
+            left = 0;
+            return false;
+        }
+        t1 = end < cost ? static_cast<int>(end) - kGap : tiles;
+        left = end - cost;
+        return true;
     }
     __device__ __forceinline__ bool next(const Kv4AttnParams &p)
     {
         if (left <= 0) return false;
-        t0 = t1;
-        if (t0 == tiles) {
-            t0 = 0;
-            if (++b == blocks) {
-                b = 0;
-                if (++h == p.kv_heads) {
-                    h = 0;
-                    do {
-                        if (++r >= p.R) return false;
-                        take(p);
-                    } while (q.n == 0);
-                }
+        at = 0;
+        if (++b == blocks) {
+            b = 0;
+            if (++h == p.kv_heads) {
+                h = 0;
+                do {
+                    if (++r >= p.R) return false;
+                    take(p);
+                } while (q.n == 0);
             }
         }
-        cut();
-        return true;
+        return cut();
     }
-    // keys that the block's last row sees, and a warp's tiles of the piece
-    __device__ __forceinline__ int seen(int group) const
+    // tiles of the piece that some row of the block sees: [t0, this)
+    __device__ __forceinline__ int end(int group) const
     {
         const int last = min(q.n - 1, (b * NC + NC - 1) / group);
-        return max(0, q.keys - q.n + last + 1);
+        return min(t1, (max(0, q.keys - q.n + last + 1) + 15) >> 4);
     }
-    __device__ __forceinline__ void share(int group, int warp, int *a, int *e) const
-    {
-        const int end = min(t1, (seen(group) + 15) >> 4), len = max(0, end - t0);
-        *a = t0 + len * warp / kWarps;
-        *e = t0 + len * (warp + 1) / kWarps;
-    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
+// A warp's last piece takes its ring's place; a first one that others follow goes to
+// the workspace.  NT 1: queries in registers, else in shared memory.
 template <int DP, int NT>
 struct Smem {
     static constexpr int NC = 8 * NT;
     static constexpr int kPad = DP + 4;                                  // floats from a column of results to the next
     static constexpr int kTile = Kv4Tile<DP>::kBytes;
-    static constexpr int kRing = kWarps * kStages * kTile;
-    static constexpr int kQ = kRing;                                     // [NT][DP / 16][32] uint2
-    static constexpr int kOut = kQ + NT * (DP / 16) * 32 * 8;            // [kSlots][NC][kPad] fp32
-    static constexpr int kMl = kOut + kSlots * NC * kPad * 4;            // [kSlots][NC] (m, l)
-    static constexpr int kFactor = kMl + kSlots * NC * 8;                // [NC] score factors
-    static constexpr int kBars = kFactor + NC * 4;                       // [kWarps][kStages]
-    static constexpr int kMisc = kBars + kWarps * kStages * 8;           // scan, share, flags
-    static constexpr int kTotal = kMisc + 512;
+    static constexpr int kSlot = NC * kPad * 4;                          // a piece's results
+    static constexpr int kStages = NT == 4 ? 4 : NT == 2 ? (DP == 128 ? 2 : 4) : (DP == 128 ? 3 : 4);   // of a warp's ring
+    static constexpr int kRing = kStages * kBatch * kTile;
+    static_assert(kRing >= kSlot, "a warp's last piece takes its ring's place");
+    static constexpr int kQ = kWarps * kRing;                            // [kWarps][NT][DP / 16][32] uint2
+    static constexpr int kQWarp = NT == 1 ? 0 : NT * (DP / 16) * 32 * 8;
+    static constexpr int kMl = kQ + kWarps * kQWarp;                     // [2][kWarps][NC] (m, l): first and last pieces
+    static constexpr int kGroups = kMl + 2 * kWarps * NC * 8;            // [2][kWarps] their groups
+    static constexpr int kNow = kGroups + 2 * kWarps * static_cast<int>(sizeof(Group));     // [kWarps] Group
+    static constexpr int kPieces = kNow + kWarps * static_cast<int>(sizeof(Group));         // [kWarps][2] Pieces
+    static constexpr int kBars = kPieces + 2 * kWarps * static_cast<int>(sizeof(Pieces<NC>));   // [kWarps][kStages]
+    static constexpr int kMisc = kBars + kWarps * kStages * 8;           // scan, flags
+    static constexpr int kTotal = kMisc + 32 * 8 + 32;
+    static constexpr int kCtas = NT == 4 ? 1 : 2;                        // of an SM
 };
 
+enum { kHasFirst = 1, kFirstGoesOn = 2, kHasLast = 4, kFirstInRing = 8 };   // a warp's pieces of cut groups
+
 template <int DP, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p)
+__global__ void __launch_bounds__(kThreads, (Smem<DP, NT>::kCtas)) kv4_attn_kernel(const Kv4AttnParams p)
 {
     pdl_launch_dependents();
     using S = Smem<DP, NT>;
     using Tile = Kv4Tile<DP>;
     constexpr int NC = S::NC, KB = DP / 16, W = DP / 32;   // W: words of 8 codes of a lane's share of a key
+    constexpr int kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t sm[];
-    float *out = reinterpret_cast<float *>(sm + S::kOut);
     float2 *ml = reinterpret_cast<float2 *>(sm + S::kMl);
-    float *factor = reinterpret_cast<float *>(sm + S::kFactor);
+    Group *groups = reinterpret_cast<Group *>(sm + S::kGroups);
     int64_t *scan = reinterpret_cast<int64_t *>(sm + S::kMisc);          // [32]
-    int64_t *found = scan + 32;                                          // request, unit in it
-    volatile int *abort = reinterpret_cast<volatile int *>(found + 2);
-    int *last = const_cast<int *>(abort) + 1;
+    int64_t *bases = reinterpret_cast<int64_t *>(sm);                    // [kThreads] units before a thread's requests, in place of rings
+    volatile int *abort = reinterpret_cast<volatile int *>(scan + 32);
+    uint32_t *cuts = reinterpret_cast<uint32_t *>(scan + 32) + 1;        // the warps' pieces of cut groups, 4 bits each
+    int *joins = reinterpret_cast<int *>(cuts + 1);                      // [2][3]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    uint8_t *ring = sm + warp * kStages * S::kTile;
+    uint8_t *ring = sm + warp * S::kRing;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::kBars) + warp * kStages;
-    if (tid == 0) *abort = 0;
+    if (tid == 0) {
+        *abort = 0;
+        *cuts = 0;
+    }
     if (lane == 0)
         for (int i = 0; i < kStages; ++i) mbar_init(full + i, 1);
     fence_mbarrier_init();
     int32_t *status = p.counters;
     pdl_wait();
 
-    // this CTA's share of all units: every CTA counts them for itself
+    // ---- the warps' shares of all units: every CTA counts them for itself
     const int run = (p.R + kThreads - 1) / kThreads, r0 = min(p.R, tid * run), r1 = min(p.R, r0 + run);
     auto units = [&](int r, int *bad) {
         const Request q = request(p, r, bad);
         const int64_t blocks = (q.n * p.group + NC - 1) / NC;
-        return blocks * p.kv_heads * max(1, (q.keys + 15) >> 4);
+        return blocks * p.kv_heads * (kGap + max(1, (q.keys + 15) >> 4));
     };
     int bad = 0;
     int64_t mine = 0, total;
     for (int r = r0; r < r1; ++r) mine += units(r, &bad);
     const int64_t base = block_scan_i64(mine, scan, &total);
     if (bad) atomicOr(status, LORA_DEV_BAD_LENGTH);
-    const int64_t most = (total + kMinTiles - 1) / kMinTiles;
-    const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-    const int cta = blockIdx.x;
-    if (cta >= ctas) return;
-    const int64_t u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-    if (u0 >= base && u0 < base + mine) {
-        int64_t at = u0 - base;
-        for (int r = r0; r < r1; ++r) {
-            const int64_t n = units(r, &bad);
-            if (at < n) {
-                found[0] = r;
-                found[1] = at;
-                break;
-            }
-            at -= n;
-        }
-    }
+    if (total == 0) return;
+    const int64_t most = total / kMinShare;   // at least 1: a group has kGap + 1 units, and no share is empty
+    const int warps = static_cast<int>(most < gridDim.x * kWarps ? most : gridDim.x * kWarps), cta = blockIdx.x;
+    if (cta * kWarps >= warps) return;
+    const int64_t quot = quotient(total, warps), rem = total - quot * warps;
+    auto share_of = [&](int w) { return w * quot + min(static_cast<int64_t>(w), rem); };        // first unit of warp w
+    auto warp_of = [&](int64_t u) {                                                             // whose share has unit u
+        const int64_t longer = rem * (quot + 1);
+        return static_cast<int>(u < longer ? quotient(u, quot + 1) : rem + quotient(u - longer, quot));
+    };
+    bases[tid] = base;
     __syncthreads();
 
-    Pieces<NC> piece, ahead;   // the one in work, and the one whose tiles are being fetched
-    piece.start(p, static_cast<int>(found[0]), found[1], u1 - u0);
-    ahead = piece;
-    int64_t unit = u0;         // of the piece's first tile
+    const int me = cta * kWarps + warp;
+    const int64_t u0 = share_of(me), u1 = share_of(me + 1);
+    Pieces<NC> piece = {};
+    bool going = false;
+    if (me < warps) {
+        // the thread whose requests have the first unit: the last one of a base up to there
+        static_assert(kThreads == 256, "two ballots");
+        const int j8 = (31 - __clz(__ballot_sync(0xffffffffu, bases[8 * lane] <= u0))) * 8;
+        const int j = j8 + 31 - __clz(__ballot_sync(0xffffffffu, lane < 8 && bases[j8 + (lane & 7)] <= u0));
+        int r = j * run;
+        int64_t in = u0 - bases[j];
+        if (run > 1)
+            for (int64_t n; in >= (n = units(r, &bad)); ++r) in -= n;
+        going = piece.start(p, r, in, u1 - u0);
+    }
+    bool more = going;
 
-    // ---- the warp's ring: tiles [fetch_t, fetch_e) of `ahead`, then of the pieces after it
-    int fetch_t, fetch_e, issued = 0, pages = 0, pages_at = 0;
-    bool more = true;
-    ahead.share(p.group, warp, &fetch_t, &fetch_e);
-    pages_at = fetch_t - 32;   // nothing loaded yet
+    // What only the ends of pieces need stays in shared memory (the loop over tiles has no registers for it): the
+    // piece in work with its group, and the one whose tiles are being fetched.
+    Pieces<NC> *cur = reinterpret_cast<Pieces<NC> *>(sm + S::kPieces) + 2 * warp, *ahead = cur + 1;
+    Group *now = reinterpret_cast<Group *>(sm + S::kNow) + warp;
+    if (lane == 0) {
+        *cur = *ahead = piece;
+        now->start = u0 - piece.at;
+        now->cost = 0;
+    }
+    __syncthreads();   // everybody is done with `bases`
+
+    // ---- the warp's ring: tiles [fetch_t, fetch_e) of the piece `ahead`, then of those after it, up to
+    // kBatch of a piece a stage.  The lanes have the addresses of 32 tiles from fetch_0 on, and each issues its own.
+    int fetch_t = piece.t0, fetch_e = more ? piece.end(p.group) : fetch_t, fetch_0 = fetch_t - 32;
+    int put = 0, flying = 0;   // the stage that is filled next, and stages filled and not used up
+    const uint8_t *src = nullptr;
     const int in_page = p.page_shift - 4;   // log2 of the tiles of a page
-    auto fetch = [&]() {       // one more tile, if there is one
-        while (more && fetch_t >= fetch_e) {
-            more = ahead.next(p);
-            if (more) {
-                ahead.share(p.group, warp, &fetch_t, &fetch_e);
-                pages_at = fetch_t - 32;
-            }
+    auto fetch = [&]() {       // one more stage, if there is anything
+        while (fetch_t >= fetch_e) {
+            if (!more) return;
+            Pieces<NC> x = *ahead;
+            more = x.next(p);
+            __syncwarp();
+            if (lane == 0) *ahead = x;
+            __syncwarp();
+            if (!more) return;
+            fetch_t = x.t0;
+            fetch_e = x.end(p.group);
+            fetch_0 = fetch_t - 32;
         }
-        if (!more) return;
-        if (fetch_t - pages_at >= 32) {   // the pages of 32 tiles, one a lane
-            pages_at = fetch_t;
+        if (fetch_t - fetch_0 >= 32) {
+            fetch_0 = fetch_t;
             const int t = fetch_t + lane;
-            pages = t < fetch_e ? p.table[ahead.r * p.table_stride + (t >> in_page)] : 0;
-            const bool none = pages < 0 || pages >= p.num_pages;
-            if (none) {
-                atomicOr(status, LORA_DEV_BAD_PAGE);
-                pages = -1;
+            if (t < fetch_e) {
+                const int page = p.table[ahead->r * p.table_stride + (t >> in_page)];
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(status, LORA_DEV_BAD_PAGE);
+                    src = p.zeros;
+                } else {
+                    src = p.data + page * p.page_stride + ahead->h * p.head_stride +
+                          (t & ((1 << in_page) - 1)) * static_cast<int64_t>(S::kTile);
+                }
             }
         }
-        const int page = __shfl_sync(0xffffffffu, pages, fetch_t - pages_at);
-        if (lane == 0) {
-            const uint8_t *src = page < 0 ? p.zeros
-                                          : p.data + page * p.page_stride + ahead.h * p.head_stride +
-                                                (fetch_t & ((1 << in_page) - 1)) * static_cast<int64_t>(S::kTile);
-            const int s = issued % kStages;
-            mbar_expect_tx(full + s, S::kTile);
-            bulk_load(ring + s * S::kTile, src, S::kTile, full + s);
-        }
-        ++issued;
-        ++fetch_t;
+        static_assert(32 % kBatch == 0, "a stage's addresses are there together");
+        const int n = min(kBatch, fetch_e - fetch_t), i = lane - (fetch_t - fetch_0);
+        if (i == 0) mbar_expect_tx(full + put, n * S::kTile);
+        __syncwarp();
+        if (i >= 0 && i < n) bulk_load(ring + (put * kBatch + i) * S::kTile, src, S::kTile, full + put);
+        put = put + 1 == kStages ? 0 : put + 1;
+        ++flying;
+        fetch_t += n;
     };
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) fetch();
-    int taken = 0;
+    int stage = 0, parity = 0;
+    bool live = true;   // until a wait gives up
 
-    bool going = true;
-    while (going) {
-        // ---- queries: columns of fp16, scaled by a power of two, in the order of the B operand
-        const int cols = min(NC, piece.q.n * p.group - piece.b * NC);   // columns with a row
-        {
-            constexpr int kLanes = DP / 8;                               // lanes of a column, 8 elements each
-            const int sub = tid % kLanes;
+    // a row of the output; by: 1 / l
+    auto row_of = [&](const Group &gr, int n, int *h) {
+        const int row = gr.first_row + n, i = row / p.group;
+        *h = gr.h * p.group + row - i * p.group;
+        return static_cast<int64_t>(gr.tok0 + i);
+    };
+    auto store_lse = [&](int64_t t, int h, float m, float l) {
+        p.lse[t * p.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    };
+
 #pragma unroll 1
-            for (int n = tid / kLanes; n < NC; n += kThreads / kLanes) {
-                uint4 x = {};
-                if (n < cols && sub * 8 < p.head_dim) {
-                    const int row = piece.b * NC + n, i = row / p.group, hg = row - i * p.group;
-                    x = *reinterpret_cast<const uint4 *>(p.q + (piece.q.tok0 + i) * p.q_tok +
-                                                         (piece.h * p.group + hg) * p.q_head + sub * 8);
-                }
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                float f[8], top = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[2 * i] = bf16_lo(w[i]);
-                    f[2 * i + 1] = bf16_hi(w[i]);
-                    top = fmaxf(top, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-                }
-#pragma unroll   // whole warps have a column or none
-                for (int d = kLanes / 2; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                // 2^(12 - e) for a largest magnitude in [2^e, 2^(e + 1)); rows of zeros or infinities stay as they are
-                const int e = __float_as_uint(top) >> 23;
-                const bool as_is = e < 13 || e > 254;
-                const float by = as_is ? 1.f : __uint_as_float((266 - e) << 23);
-                if (sub == 0) factor[n] = p.scale * 1.4426950408889634f * (as_is ? 1.f : __uint_as_float((e - 12) << 23));
-                uint2 *to = reinterpret_cast<uint2 *>(sm + S::kQ) + (n / 8) * KB * 32;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int u = 2 * sub + i, cc = u / KB, kb = u % KB;   // 4 elements: part kb of lane cc's share
-                    to[kb * 32 + (n % 8) * 4 + cc] = make_uint2(pack_f16x2(f[4 * i] * by, f[4 * i + 1] * by),
-                                                                pack_f16x2(f[4 * i + 2] * by, f[4 * i + 3] * by));
-                }
-            }
-        }
-        __syncthreads();
-        const uint2 *qs = reinterpret_cast<const uint2 *>(sm + S::kQ) + lane;
-        uint2 qf[NT == 1 ? KB : 1];
-        if (NT == 1)
-#pragma unroll
-            for (int i = 0; i < KB; ++i) qf[NT == 1 ? i : 0] = qs[i * 32];
+    while (going) {
+        piece = *cur;
+        Group gr;
+        gr.start = now->start + now->cost;   // after the group before
+        gr.cost = piece.tiles + kGap;
+        gr.tok0 = piece.q.tok0;
+        gr.h = piece.h;
+        gr.first_row = piece.b * NC;
+        gr.cols = min(NC, piece.q.n * p.group - piece.b * NC);
+        __syncwarp();
+        if (lane == 0) *now = gr;
 
+        // ---- queries: lane (g, c) has elements [c * DP / 4, (c + 1) * DP / 4) of column g, as fp16
+        // scaled by a power of two, four at a time in the order of the B operand
+        uint2 qf[NT == 1 ? KB : 1];
+        uint2 *qs = reinterpret_cast<uint2 *>(sm + S::kQ + warp * S::kQWarp) + lane;
         float fac[NT][2], m[NT][2], l[NT][2], o[NT][KB][4];
-        int lim[NT][2], first_limit = 0x7fffffff;   // keys that a column sees; the fewest of any column
+        int lim[NT][2];   // keys that a column sees
+        if (NT > 1) __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            uint4 x[KB / 2];
+            int h;
+            const int n = nt * 8 + g;
+            const int64_t t = row_of(gr, n, &h);
+            const uint16_t *from = p.q + t * p.q_tok + h * p.q_head + c * (DP / 4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = nt * 8 + 2 * c + e, i = (piece.b * NC + n) / p.group;
-                fac[nt][e] = factor[n];
-                lim[nt][e] = n < cols ? max(0, piece.q.keys - piece.q.n + i + 1) : 0x7fffffff;
-                m[nt][e] = kNone;
-                l[nt][e] = 0.f;
+            for (int i = 0; i < KB / 2; ++i) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (n < gr.cols && c * (DP / 4) + 8 * i < p.head_dim) x[i] = *reinterpret_cast<const uint4 *>(from + 8 * i);
+            }
+            uint32_t top = 0;   // the largest magnitude, by its bits
+#pragma unroll
+            for (int i = 0; i < KB / 2; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(12 - e) for a largest magnitude in [2^e, 2^(e + 1)); rows of zeros or infinities stay as they are
+            const int e = top >> 7;
+            const bool as_is = e < 13 || e > 254;
+            const float by = as_is ? 1.f : __uint_as_float((266 - e) << 23);
+            const float f = p.scale * 1.4426950408889634f * (as_is ? 1.f : __uint_as_float((e - 12) << 23));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fac[nt][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+                const uint32_t a = i & 1 ? x[i / 2].z : x[i / 2].x, b = i & 1 ? x[i / 2].w : x[i / 2].y;
+                const uint2 v = make_uint2(pack_f16x2(bf16_lo(a) * by, bf16_hi(a) * by), pack_f16x2(bf16_lo(b) * by, bf16_hi(b) * by));
+                if (NT == 1) qf[NT == 1 ? i : 0] = v;
+                else qs[(nt * KB + i) * 32] = v;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = nt * 8 + 2 * c + i;
+                lim[nt][i] = col < gr.cols ? max(0, piece.q.keys - piece.q.n + (gr.first_row + col) / p.group + 1) : 0x7fffffff;
+                m[nt][i] = kNone;
+                l[nt][i] = 0.f;
             }
 #pragma unroll
             for (int j = 0; j < KB; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+                for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
         }
-        first_limit = max(0, piece.q.keys - piece.q.n + (piece.b * NC) / p.group + 1);
+        if (NT > 1) __syncwarp();
+        const int first_limit = max(0, piece.q.keys - piece.q.n + gr.first_row / p.group + 1);   // of the first column, the fewest
 
-        int t, te;
-        piece.share(p.group, warp, &t, &te);
-#pragma unroll 1
-        for (; t < te; ++t) {
-            const int s = taken % kStages;
-            if (!mbar_wait(full + s, (taken / kStages) & 1, abort, status, LORA_DEV_TIMEOUT, p.wait_cycles)) break;
-            const uint8_t *tile = ring + s * S::kTile;
-
-            // ---- S^T: rows are the keys g and g + 8, columns 2c and 2c + 1
-            float sc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-            uint32_t kw[2][W];
+        // S^T of a tile: rows are the keys g and g + 8, columns 2c and 2c + 1
+        auto scores = [&](const uint8_t *tile, float (&sc)[NT][4]) {
+            uint32_t kw[2][W], ks[2][W / 2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint8_t *at = tile + e * (4 * DP) + lane * (4 * W);
                 if (W == 4) *reinterpret_cast<uint4 *>(kw[e]) = *reinterpret_cast<const uint4 *>(at);
                 else *reinterpret_cast<uint2 *>(kw[e]) = *reinterpret_cast<const uint2 *>(at);
-            }
-            uint32_t ks[2];
+                at = tile + Tile::kKeyScales + (8 * e + g) * Tile::kGroups + c * (W / 2);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint8_t *at = tile + Tile::kKeyScales + (8 * e + g) * Tile::kGroups + c * (W / 2);
-                ks[e] = W == 4 ? *reinterpret_cast<const uint16_t *>(at) : *at;
+                for (int i = 0; i < W / 2; ++i) ks[e][i] = at[i] * 0x00800080u;   // the scale as an fp16 pair
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
 #pragma unroll
             for (int w = 0; w < W; ++w) {   // 8 elements of each key, of one scale
                 uint32_t f[2][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t s2 = w < 2 ? scale_pair<0, 0>(ks[e]) : scale_pair<1, 1>(ks[e]);
                     e2m1x8_to_f16(kw[e][w], f[e]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[e][i] = mul_f16x2(f[e][i], s2);
+                    for (int i = 0; i < 4; ++i) f[e][i] = mul_f16x2(f[e][i], ks[e][w / 2]);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -384,53 +449,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) kv4_attn_kernel(con
                     }
                 }
             }
-
-            // ---- p, and its sums
-            const int key = t * 16 + g;
-            const bool edge = t * 16 + 16 > first_limit;
-            float rise = kNone;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[nt][e] * fac[nt][e & 1];
-                    if (edge && key + 8 * (e >> 1) >= lim[nt][e & 1]) x = -INFINITY;
-                    sc[nt][e] = x;
-                    rise = fmaxf(rise, x - m[nt][e & 1]);
-                }
-            if (__any_sync(0xffffffffu, rise > kSlack)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(sc[nt][e], sc[nt][e + 2]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        top = fmaxf(top, m[nt][e]);
-                        const float by = exp2_approx(m[nt][e] - top);
-                        m[nt][e] = top;
-                        l[nt][e] *= by;
-#pragma unroll
-                        for (int j = 0; j < KB; ++j) {
-                            o[nt][j][e] *= by;
-                            o[nt][j][e + 2] *= by;
-                        }
-                    }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = exp2_approx(sc[nt][e] - m[nt][e & 1]);
-                    l[nt][e & 1] += x[e];   // before the rounding to fp16
-                }
-                pb[nt][0] = transposed(pack_f16x2(x[0], x[1]));
-                pb[nt][1] = transposed(pack_f16x2(x[2], x[3]));
-            }
-
-            // ---- O^T: rows are elements of the values, inner dimension the keys 2c, 2c + 1 and 2c + 8, 2c + 9
+        };
+        // O^T += V^T P^T: rows are elements of the values, inner dimension the keys 2c, 2c + 1 and 2c + 8, 2c + 9
+        auto values = [&](const uint8_t *tile, const uint32_t (&pb)[NT][2], int keys) {
             uint32_t vw[2][W];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -439,14 +460,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) kv4_attn_kernel(con
                 else *reinterpret_cast<uint2 *>(vw[e]) = *reinterpret_cast<const uint2 *>(at);
             }
             uint32_t vs = *reinterpret_cast<const uint32_t *>(tile + Tile::kValueScales + ((DP == 128 ? g : g / 2) * 4 + c) * 4);
-            if (t * 16 + 16 > piece.q.keys) {   // keys past the request: whatever they hold, their scales may be NaN
-                const int k0 = t * 16 + 2 * c;
+            if (keys < 16) {   // keys past the request: whatever they hold, their scales may be NaN
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (k0 + (e & 1) + 8 * (e >> 1) >= piece.q.keys) vs &= ~(0xFFu << (8 * e));
+                    if (2 * c + (e & 1) + 8 * (e >> 1) >= keys) vs &= ~(0xFFu << (8 * e));
             }
-            __syncwarp();
-            ++taken;
             const uint32_t vs2[2] = {scale_pair<0, 1>(vs), scale_pair<2, 3>(vs)};
 #pragma unroll
             for (int w = 0; w < W / 2; ++w) {   // 8 elements of the four keys
@@ -468,157 +486,250 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) kv4_attn_kernel(con
                     for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], a, pb[nt][0], pb[nt][1]);
                 }
             }
+        };
+        // ---- the tiles
+        const int te = piece.end(p.group), keys = piece.q.keys;
+#pragma unroll 1
+        for (int t = piece.t0; t < te && live;) {
+            live = __all_sync(0xffffffffu, wait(full + stage, parity, abort, status, p.wait_cycles));
+            if (!live) break;
+            const uint8_t *tile = ring + stage * (kBatch * S::kTile);
+            const int t_end = min(t + kBatch, te);
+#pragma unroll 1
+            for (; t < t_end; ++t, tile += S::kTile) {
+                float sc[NT][4];
+                scores(tile, sc);
+                // x - m, and -infinity for what is not seen
+                float y[NT][4];
+                auto shift = [&]() {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(sc[nt][e], fac[nt][e & 1], -m[nt][e & 1]);
+                    if (t * 16 + 16 > first_limit) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (t * 16 + g + 8 * (e >> 1) >= lim[nt][e & 1]) y[nt][e] = -INFINITY;
+                    }
+                };
+                shift();
+                float rise = kNone;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) rise = fmaxf(fmaxf(rise, fmaxf(y[nt][0], y[nt][1])), fmaxf(y[nt][2], y[nt][3]));
+                if (__any_sync(0xffffffffu, rise > kSlack)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = m[nt][e];
+#pragma unroll
+                            for (int q = 0; q < 4; q += 2)
+                                if (y[nt][e + q] != -INFINITY) top = fmaxf(top, sc[nt][e + q] * fac[nt][e]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            const float by = exp2_approx(m[nt][e] - top);
+                            m[nt][e] = top;
+                            l[nt][e] *= by;
+#pragma unroll
+                            for (int j = 0; j < KB; ++j) {
+                                o[nt][j][e] *= by;
+                                o[nt][j][e + 2] *= by;
+                            }
+                        }
+                    shift();
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = exp2_approx(y[nt][e]);
+                        l[nt][e & 1] += x[e];   // before the rounding to fp16
+                    }
+                    pb[nt][0] = transposed(pack_f16x2(x[0], x[1]));
+                    pb[nt][1] = transposed(pack_f16x2(x[2], x[3]));
+                }
+                values(tile, pb, keys - t * 16);
+            }
+            __syncwarp();   // every lane is done with the stage
+            --flying;
             fetch();
+            parity = stage + 1 == kStages ? parity ^ 1 : parity;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
 
-        // ---- the warps' results: four at a time through shared memory
+        // ---- results
+        __syncwarp();
+        piece = *cur;
+        gr = *now;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-        const int slot = warp % kSlots;
-        float *mine_o = out + slot * NC * S::kPad;
         // a lane's elements of a column are consecutive: d = g * DP / 8 + 2j, + 1
-        auto put = [&]() {
+        if (piece.whole()) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int n = nt * 8 + 2 * c + e;
-                    float4 *to = reinterpret_cast<float4 *>(mine_o + n * S::kPad + g * (DP / 8));
+                    if (n >= gr.cols) continue;
+                    int h;
+                    const int64_t t = row_of(gr, n, &h);
+                    const float by = l[nt][e] != 0.f ? 1.f / l[nt][e] : 0.f;   // no key: zeros
+                    uint16_t *to = p.o + t * p.o_tok + h * p.o_head + g * (DP / 8);
+                    uint32_t v[KB];
+#pragma unroll
+                    for (int j = 0; j < KB; ++j) v[j] = pack_bf16x2(o[nt][j][e] * by, o[nt][j][e + 2] * by);
+#pragma unroll
+                    for (int j = 0; j < KB; j += 4)
+                        if (g * (DP / 8) + 2 * j < p.head_dim)
+                            *reinterpret_cast<uint4 *>(to + 2 * j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (g == 0 && p.lse) store_lse(t, h, m[nt][e], l[nt][e]);
+                }
+        } else {
+            const int last = piece.t0 == 0;   // begins here and goes on elsewhere; else it comes from elsewhere
+            const bool in_ring = last || piece.left <= 0;   // nothing after it
+            float *to = in_ring ? reinterpret_cast<float *>(ring) : p.first + static_cast<int64_t>(me) * NC * S::kPad;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = nt * 8 + 2 * c + e;
+                    float4 *v = reinterpret_cast<float4 *>(to + n * S::kPad + g * (DP / 8));
 #pragma unroll
                     for (int j = 0; j < KB / 2; ++j)
-                        to[j] = make_float4(o[nt][2 * j][e], o[nt][2 * j][e + 2], o[nt][2 * j + 1][e], o[nt][2 * j + 1][e + 2]);
-                    if (g == 0) ml[slot * NC + n] = make_float2(m[nt][e], l[nt][e]);
+                        v[j] = make_float4(o[nt][2 * j][e], o[nt][2 * j][e + 2], o[nt][2 * j + 1][e], o[nt][2 * j + 1][e + 2]);
+                    if (g == 0) ml[(last * kWarps + warp) * NC + n] = make_float2(m[nt][e], l[nt][e]);
                 }
-        };
-        if (warp >= kSlots) put();
-        __syncthreads();
-        if (warp < kSlots) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int n = nt * 8 + 2 * c + e;
-                    const float2 other = ml[slot * NC + n];
-                    const float top = fmaxf(m[nt][e], other.x);
-                    const float by = exp2_approx(m[nt][e] - top), by2 = exp2_approx(other.x - top);
-                    m[nt][e] = top;
-                    l[nt][e] = l[nt][e] * by + other.y * by2;
-                    const float4 *from = reinterpret_cast<const float4 *>(mine_o + n * S::kPad + g * (DP / 8));
-#pragma unroll
-                    for (int j = 0; j < KB / 2; ++j) {
-                        const float4 v = from[j];
-                        o[nt][2 * j][e] = o[nt][2 * j][e] * by + v.x * by2;
-                        o[nt][2 * j][e + 2] = o[nt][2 * j][e + 2] * by + v.y * by2;
-                        o[nt][2 * j + 1][e] = o[nt][2 * j + 1][e] * by + v.z * by2;
-                        o[nt][2 * j + 1][e + 2] = o[nt][2 * j + 1][e + 2] * by + v.w * by2;
-                    }
-                }
-            __syncwarp();
-            put();
+            if (lane == 0) {
+                groups[last * kWarps + warp] = gr;
+                const uint32_t mark = last ? kHasLast
+                                           : kHasFirst | (piece.t1 < piece.tiles ? kFirstGoesOn : 0) | (in_ring ? kFirstInRing : 0);
+                atomicOr(cuts, mark << (4 * warp));
+            }
         }
-        __syncthreads();
+        going = piece.next(p);
+        __syncwarp();
+        if (lane == 0) *cur = piece;
+        __syncwarp();
+    }
+    // after a timeout: nothing may be in flight when the CTA ends
+    for (; flying > 0; --flying) {
+        wait_loop(full + stage, parity, abort, status, p.wait_cycles < kWaitShort ? kWaitShort : p.wait_cycles);
+        parity = stage + 1 == kStages ? parity ^ 1 : parity;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    __syncthreads();
 
-        // ---- their sum: the rows, or a part of a cut group
-        const bool whole = piece.t0 == 0 && piece.t1 == piece.tiles;
-        constexpr int kUnits = NC * (DP / 4);   // four elements of a column
-        auto store = [&](int n, int d, float4 v, float top, float sum) {
-            const int row = piece.b * NC + n, i = row / p.group, h = piece.h * p.group + row - i * p.group;
-            const float by = sum != 0.f ? 1.f / sum : 0.f;   // no key: zeros
-            if (sum == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (d < p.head_dim)
-                *reinterpret_cast<uint2 *>(p.o + (piece.q.tok0 + i) * p.o_tok + h * p.o_head + d) =
-                    make_uint2(pack_bf16x2(v.x * by, v.y * by), pack_bf16x2(v.z * by, v.w * by));
-            if (d == 0 && p.lse)
-                p.lse[static_cast<int64_t>(piece.q.tok0 + i) * p.heads + h] =
-                    sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-        };
-        const int at = 2 * cta + (piece.t0 == 0);
+    // ---- cut groups.  A chain of pieces: the last of a warp (or, at the CTA's start, one that
+    // comes from the CTA before), then the first of the warps after it as long as they go on.
+    constexpr int kUnits = NC * (DP / 4);   // four elements of a column
+    auto store = [&](const Group &gr, int n, int d, float4 v, float top, float sum) {
+        int h;
+        const int64_t t = row_of(gr, n, &h);
+        const float by = sum != 0.f ? 1.f / sum : 0.f;   // no key: zeros
+        if (d < p.head_dim)
+            *reinterpret_cast<uint2 *>(p.o + t * p.o_tok + h * p.o_head + d) =
+                make_uint2(pack_bf16x2(v.x * by, v.y * by), pack_bf16x2(v.z * by, v.w * by));
+        if (d == 0 && p.lse) store_lse(t, h, top, sum);
+    };
+    auto add = [](float4 &v, float &top, float &sum, float4 y, float2 x) {
+        const float next = fmaxf(top, x.x), by = exp2_approx(top - next), by2 = exp2_approx(x.x - next);
+        top = next;
+        sum = sum * by + x.y * by2;
+        v.x = v.x * by + y.x * by2;
+        v.y = v.y * by + y.y * by2;
+        v.z = v.z * by + y.z * by2;
+        v.w = v.w * by + y.w * by2;
+    };
+    const uint32_t marks = *cuts;
+    int shared_groups = 0, tail = 0;   // bit 0: with the CTA before, bit 1: with the CTA after, by this warp's last piece
+    // begins: bit 4 + 4w for a chain that begins with warp w's last piece, bit 0 for one with warp 0's first
+    for (uint64_t begins = (static_cast<uint64_t>(marks / kHasLast & 0x11111111u) << 4) | (marks & kHasFirst); begins;
+         begins &= begins - 1) {
+        const int w = (__ffsll(begins) - 1) / 4 - 1;
+        int to = w;   // last warp of the chain
+        bool goes_on = true;
+        while (goes_on && to + 1 < kWarps) goes_on = marks >> (4 * ++to) & kFirstGoesOn;
+        const Group gr = groups[w < 0 ? 0 : kWarps + w];
+        const bool whole = w >= 0 && !goes_on;
+        const int64_t part = 2 * cta + (w >= 0);
+        if (!whole) shared_groups |= w < 0 ? 1 : 2;
+        if (w >= 0) tail = kWarps + w;
 #pragma unroll 1
         for (int u = tid; u < kUnits; u += kThreads) {
             const int n = u / (DP / 4), d = u % (DP / 4) * 4;
-            if (n >= cols) break;
-            float top = kNone;
-#pragma unroll
-            for (int w = 0; w < kSlots; ++w) top = fmaxf(top, ml[w * NC + n].x);
+            if (n >= gr.cols) break;
+            float top = kNone, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kSlots; ++w) {
-                const float2 x = ml[w * NC + n];
-                const float by = exp2_approx(x.x - top);
-                const float4 y = *reinterpret_cast<const float4 *>(out + (w * NC + n) * S::kPad + d);
-                sum += x.y * by;
-                v.x += y.x * by;
-                v.y += y.y * by;
-                v.z += y.z * by;
-                v.w += y.w * by;
+            if (w >= 0)
+                add(v, top, sum, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm + w * S::kRing) + n * S::kPad + d),
+                    ml[(kWarps + w) * NC + n]);
+            for (int i = w + 1; i <= to; ++i) {
+                const float *from = marks >> (4 * i) & kFirstInRing ? reinterpret_cast<const float *>(sm + i * S::kRing)
+                                                            : p.first + static_cast<int64_t>(cta * kWarps + i) * NC * S::kPad;
+                add(v, top, sum, *reinterpret_cast<const float4 *>(from + n * S::kPad + d), ml[i * NC + n]);
             }
             if (whole) {
-                store(n, d, v, top, sum);
+                store(gr, n, d, v, top, sum);
             } else {
-                *reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(at) * NC + n) * DP + d) = v;
-                if (d == 0) p.part_ml[at * NC + n] = make_float2(top, sum);
+                *reinterpret_cast<float4 *>(p.part + (part * NC + n) * DP + d) = v;
+                if (d == 0) p.part_ml[part * NC + n] = make_float2(top, sum);
             }
         }
-        if (!whole) {
-            // the CTA that stores the last part joins them, in their order
-            const int64_t from = unit - piece.t0, to = from + piece.tiles - 1;
-            const int c0 = static_cast<int>(((from + 1) * ctas - 1) / total), c1 = static_cast<int>(((to + 1) * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = atom_acq_rel_gpu_add(p.counters + kKv4CntGroup + c0, 1);
-                *last = n == c1 - c0;
-                if (n == c1 - c0) p.counters[kKv4CntGroup + c0] = 0;
-            }
-            __syncthreads();
-            if (*last) {
-                __threadfence();
-#pragma unroll 1
-                for (int u = tid; u < kUnits; u += kThreads) {
-                    const int n = u / (DP / 4), d = u % (DP / 4) * 4;
-                    if (n >= cols) break;
-                    float top = kNone, sum = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int i = c0; i <= c1; ++i) {
-                        const int part = 2 * i + (i == c0);
-                        const float2 x = __ldcg(p.part_ml + part * NC + n);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + (static_cast<int64_t>(part) * NC + n) * DP + d));
-                        const float next = fmaxf(top, x.x), by = exp2_approx(top - next), by2 = exp2_approx(x.x - next);
-                        top = next;
-                        sum = sum * by + x.y * by2;
-                        v.x = v.x * by + y.x * by2;
-                        v.y = v.y * by + y.y * by2;
-                        v.z = v.z * by + y.z * by2;
-                        v.w = v.w * by + y.w * by2;
-                    }
-                    store(n, d, v, top, sum);
-                }
-            }
-        }
-        unit += piece.t1 - piece.t0;
-        going = piece.next(p);
-        // `out` is written again only after the next piece's first barrier
     }
-    // after a timeout: nothing may be in flight when the CTA ends
-    for (; taken < issued; ++taken)
-        mbar_wait(full + taken % kStages, (taken / kStages) & 1, abort, status, LORA_DEV_TIMEOUT,
-                  p.wait_cycles < kWaitShort ? kWaitShort : p.wait_cycles);
+    if (!shared_groups) return;
+    // the CTA that stores the last part of a group joins them, in their order
+    __threadfence();
+    __syncthreads();
+    if (tid < 2 && (shared_groups >> tid & 1)) {
+        const Group &gr = groups[tid == 0 ? 0 : tail];
+        const int c0 = warp_of(gr.start + kGap) / kWarps, c1 = warp_of(gr.start + gr.cost - 1) / kWarps;
+        const int n = atom_acq_rel_gpu_add(p.counters + kKv4CntGroup + c0, 1);
+        joins[3 * tid] = n == c1 - c0;
+        joins[3 * tid + 1] = c0;
+        joins[3 * tid + 2] = c1;
+        if (n == c1 - c0) p.counters[kKv4CntGroup + c0] = 0;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (!(shared_groups >> which & 1) || !joins[3 * which]) continue;
+        __threadfence();
+        const Group gr = groups[which == 0 ? 0 : tail];
+        const int c0 = joins[3 * which + 1], c1 = joins[3 * which + 2];
+#pragma unroll 1
+        for (int u = tid; u < kUnits; u += kThreads) {
+            const int n = u / (DP / 4), d = u % (DP / 4) * 4;
+            if (n >= gr.cols) break;
+            float top = kNone, sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = c0; i <= c1; ++i) {
+                const int64_t part = 2 * i + (i == c0);
+                add(v, top, sum, __ldcg(reinterpret_cast<const float4 *>(p.part + (part * NC + n) * DP + d)),
+                    __ldcg(p.part_ml + part * NC + n));
+            }
+            store(gr, n, d, v, top, sum);
+        }
+    }
 }
 
 template <int DP, int NT>
 cudaError_t launch_variant(const Kv4AttnParams &p, cudaStream_t stream)
 {
-    constexpr int smem = Smem<DP, NT>::kTotal;
-    static_assert(smem <= (NT <= 2 ? 113 : 227) * 1024, "shared memory");
+    using S = Smem<DP, NT>;
+    constexpr int smem = S::kTotal;
+    static_assert(S::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t ctas = (NT <= 2 ? 2 : 1) * static_cast<int64_t>(num_sms_current_device());
+    int64_t ctas = S::kCtas * static_cast<int64_t>(num_sms_current_device());
     ctas = ctas < kKv4MaxCtas ? ctas : kKv4MaxCtas;
     return launch_pdl(kv4_attn_kernel<DP, NT>, ctas, kThreads, smem, p, stream);
 }

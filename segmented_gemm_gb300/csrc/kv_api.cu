@@ -44,7 +44,8 @@ static Kv4Layout kv4_layout(int32_t head_dim)
     const size_t dp = kv4_padded(head_dim), cells = 2 * static_cast<size_t>(kKv4MaxCtas) * 16;
     L.counters = 0;
     L.zeros = align256((kKv4CntGroup + kKv4MaxCtas) * 4);
-    L.part = L.zeros + align256(kv4_tile_bytes(128));
+    L.first = L.zeros + align256(kv4_tile_bytes(128));
+    L.part = L.first + align256(8 * cells / 2 * (dp + 4) * 4);
     L.part_ml = L.part + align256(cells * dp * 4);
     L.total = L.part_ml + align256(cells * 8);
     return L;
@@ -283,6 +284,7 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     p.scale = attn->scale;
     p.zeros = at<uint8_t>(ws, L.zeros);
     p.counters = at<int32_t>(ws, L.counters);
+    p.first = at<float>(ws, L.first);
     p.part = at<float>(ws, L.part);
     p.part_ml = at<float2>(ws, L.part_ml);
     p.wait_cycles = tc_wait_cycles();

@@ -47,13 +47,13 @@ struct Kv4LoadParams {
     int32_t *status;
 };
 
-constexpr int kKv4MaxCtas = 2 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
+constexpr int kKv4MaxCtas = 3 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
 
 // Workspace of the 4-bit attention (offsets 256-byte aligned): the status word and
 // the arrival counters of split groups (zero at rest but the status), a tile of zeros
-// that stands for pages outside the cache, and the partial results.
+// that stands for pages outside the cache, and the partial results, of warps and of CTAs.
 struct Kv4Layout {
-    size_t counters, zeros, part, part_ml, total;
+    size_t counters, zeros, first, part, part_ml, total;
 };
 constexpr int kKv4CntGroup = 32;                // first arrival counter; one for each CTA
 
@@ -73,6 +73,7 @@ struct Kv4AttnParams {
     float scale;
     const uint8_t *zeros;
     int32_t *counters;
+    float *first;                               // [warps][columns][padded head_dim + 4] first pieces of wide blocks
     float *part;                                // [2 * CTAs][columns][padded head_dim] partial O
     float2 *part_ml;                            // [2 * CTAs][columns] partial (m, l)
     int64_t wait_cycles;
