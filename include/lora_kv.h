@@ -133,23 +133,31 @@ int lora_kv4_load(const lora_kv4_cache_t *cache, const int32_t *slots, int64_t n
                   lora_bf16_t *v, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
                   int64_t v_head_stride, void *ws, size_t ws_bytes, lora_stream_t stream);
 
-/* Bytes of workspace for lora_kv4_attn (0 for arguments out of range); zero-filled once. */
+/* Bytes of workspace for lora_kv4_attn over steps of up to num_tokens tokens and num_requests requests with
+ * this unpack_tokens (0 for arguments out of range); zero-filled once. */
 size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t heads, int32_t kv_heads,
-                               int32_t head_dim);
+                               int32_t head_dim, int64_t unpack_tokens);
 
 /*
  * lora_attn_paged over a 4-bit cache: the same arguments, the same rows, over
  * the values that the cache stands for.  Needs no schedule.  q keeps its bf16
  * values (elements below 2^-26 of their row's largest lose bits), p is rounded to
- * fp16 for the second product, o to bf16 once; scores, statistics and sums are
+ * 16 bits for the second product, o to bf16 once; scores, statistics and sums are
  * fp32.  Keys and values past a row's request are never mixed in, whatever
  * they hold.  kv_len is clamped to [0, table_width * page_size], offsets to [0,
  * num_tokens] (LORA_DEV_BAD_LENGTH).  A page outside the cache reads as zeros
  * (LORA_DEV_BAD_PAGE).
+ *
+ * unpack_tokens: keys and values that the workspace has room for in bf16 (0: none).
+ * In steps with chunks of prompts, requests of more than 64 rows (new tokens times
+ * heads / kv_heads), in order as long as they fit, are unpacked there and go through
+ * lora_attn_paged's kernel: 512 tokens over 8000 take a third of the time so.  A
+ * multiple of 128 up to 2^24 (others are rounded down); the tokens are those of the cache that such
+ * requests attend over, each request's rounded up to 128.
  */
 int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *cache, const int32_t *block_table,
-                  int32_t table_width, int64_t table_stride, const int32_t *kv_len, void *ws, size_t ws_bytes,
-                  lora_stream_t stream);
+                  int32_t table_width, int64_t table_stride, const int32_t *kv_len, int64_t unpack_tokens, void *ws,
+                  size_t ws_bytes, lora_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Pages

@@ -26,7 +26,8 @@ DEBUG_LIB_PATH = os.path.join(PKG, "liblora_debug.so")
 
 SOURCES = ["lora_api.cu", "seg_build.cu", "fused_tc.cu", "fused_splitk.cu", "fused_cluster.cu",
            "lora_noalloc.cu", "moe.cu", "widen.cu", "seg_check.cu", "stage.cu", "moe_pair.cu", "attn_api.cu",
-           "attn_schedule.cu", "attn.cu", "kv.cu", "kv_api.cu", "qk_rope.cu", "kv4.cu", "kv4_attn.cu", "kv_pages.cu"]
+           "attn_schedule.cu", "attn.cu", "kv.cu", "kv_api.cu", "qk_rope.cu", "kv4.cu", "kv4_attn.cu", "kv4_wide.cu",
+           "kv_pages.cu"]
 VARIANTS = ((LIB_PATH, "", []), (DEBUG_LIB_PATH, "debug", ["-DLORA_DEBUG"]))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -36,6 +36,13 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
     return r;
 }
 
+// x * inv to a multiple of 2^-12 (for |x * inv| < 1024; a larger one keeps what precision there is)
+__device__ __forceinline__ float rounded_product(float x, float inv)
+{
+    constexpr float kRound = 3072.f;   // fp32 numbers near it are 2^-12 apart
+    return __fadd_rn(__fmaf_rn(x, inv, kRound), -kRound);
+}
+
 // 16 bf16 elements -> 16 codes (8 bytes) and the scale byte.
 __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint32_t *scale)
 {
@@ -54,12 +61,15 @@ __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint
     const uint32_t b = scale_byte(__uint_as_float(min(top, 0x7F7F0000u)));
     *scale = b;
     if (b == 0) return make_uint2(0, 0);
-    const float s = scale_value(b);
+    // x / s as x * (1 / s), rounded to a multiple of 2^-12 on the way.  A quotient halfway
+    // between two values is x = half * s: the product is within 2^-22 of it and rounds to it.  Any
+    // other one is at least 2^-8 (relative) from there, x having 8 and half * s 7
+    // significant bits, and stays on its side.
+    const float inv = __frcp_rn(scale_value(b));
     uint32_t c[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // divided as the definition says: x / s falls on a tie exactly or clearly beside it
-        const uint32_t two = e2m1_pair(__fdiv_rn(bf16_lo(w[i]), s), __fdiv_rn(bf16_hi(w[i]), s));
+        const uint32_t two = e2m1_pair(rounded_product(bf16_lo(w[i]), inv), rounded_product(bf16_hi(w[i]), inv));
         c[i / 4] |= two << (8 * (i % 4));
     }
     return make_uint2(c[0], c[1]);
@@ -108,22 +118,6 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_store_kernel(const Kv4StorePa
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
 }
 
-// 8 codes and their scale -> 8 bf16 values (exact: 6 significant bits).
-__device__ __forceinline__ uint4 values_of(uint32_t codes, uint32_t scale)
-{
-    uint32_t f[4];
-    e2m1x8_to_f16(codes, f);
-    const uint32_t s = scale_pair<0, 0>(scale);
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t two = mul_f16x2(f[i], s);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&two));
-        o[i] = pack_bf16x2(x.x, x.y);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // The reverse, the same split; memory bounds it, three quarters of it the writes.
 template <int DP>
 __global__ void __launch_bounds__(kKv4Threads) kv4_load_kernel(const Kv4LoadParams p)
@@ -156,13 +150,13 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_load_kernel(const Kv4LoadPara
         const bool second = 16 * g + 8 < p.head_dim;
         if (p.k) {
             uint16_t *k = p.k + t * p.k_tok + h * p.k_head + 16 * g;
-            *reinterpret_cast<uint4 *>(k) = values_of(kw.x, ks);
-            if (second) *reinterpret_cast<uint4 *>(k + 8) = values_of(kw.y, ks);
+            *reinterpret_cast<uint4 *>(k) = kv4_values(kw.x, ks);
+            if (second) *reinterpret_cast<uint4 *>(k + 8) = kv4_values(kw.y, ks);
         }
         if (p.v) {
             uint16_t *v = p.v + t * p.v_tok + h * p.v_head + 16 * g;
-            *reinterpret_cast<uint4 *>(v) = values_of(vw.x, vs);
-            if (second) *reinterpret_cast<uint4 *>(v + 8) = values_of(vw.y, vs);
+            *reinterpret_cast<uint4 *>(v) = kv4_values(vw.x, vs);
+            if (second) *reinterpret_cast<uint4 *>(v + 8) = kv4_values(vw.y, vs);
         }
     }
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace lora {
 
 // Eight 4-bit codes -> four pairs of fp16 values; codes 2i and 2i + 1 (byte i) give o[i].
@@ -32,6 +34,22 @@ template <int I, int J>
 __device__ __forceinline__ uint32_t scale_pair(uint32_t v)
 {
     return __byte_perm(v, 0u, I | 0x40 | (J << 8) | 0x4000) << 7;
+}
+
+// 8 codes and their scale -> 8 bf16 values (exact: 6 significant bits).
+__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale)
+{
+    uint32_t f[4];
+    e2m1x8_to_f16(codes, f);
+    const uint32_t s = scale_pair<0, 0>(scale);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = mul_f16x2(f[i], s);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+        o[i] = pack_bf16x2(x.x, x.y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Offsets in a tile.

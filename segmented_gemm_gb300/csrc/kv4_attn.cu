@@ -31,6 +31,7 @@
 
 #include "block_scan.cuh"
 #include "kv4.cuh"
+#include "kv4_request.cuh"
 #include "kv_ops.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -90,20 +91,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
-// Packed tokens of request r and its keys, clamped.
-struct Request {
-    int tok0, n, keys;
-};
-
-__device__ __forceinline__ Request request(const Kv4AttnParams &p, int r, int *bad)
+// The same, without what the attention over a bf16 cache has done (a wide request).
+__device__ __forceinline__ Kv4Request request(const Kv4AttnParams &p, int r, int *bad)
 {
-    const int a0 = p.cu[r], b0 = p.cu[r + 1], k0 = p.kv_len[r];
-    const int a = max(0, min(a0, p.T)), b = max(0, min(b0, p.T));
-    Request q;
-    q.tok0 = a;
-    q.n = max(0, b - a);
-    q.keys = static_cast<int>(k0 < 0 ? 0 : k0 > p.max_kv ? p.max_kv : k0);
-    *bad |= (a != a0) | (b != b0) | (b < a) | (q.keys != k0);
+    Kv4Request q = kv4_request(p, r, bad);
+    if (p.wide && p.wide[r]) q.n = 0;
     return q;
 }
 
@@ -120,7 +112,7 @@ struct Group {
 template <int NC>
 struct Pieces {
     int r, h, b, t0, t1, tiles, blocks;
-    Request q;
+    Kv4Request q;
     int64_t at, left;   // place in the group, units left from there
 
     __device__ __forceinline__ void take(const Kv4AttnParams &p)
@@ -234,10 +226,15 @@ __global__ void __launch_bounds__(kThreads, (Smem<DP, NT>::kCtas)) kv4_attn_kern
     int32_t *status = p.counters;
     pdl_wait();
 
+    if (p.wide_status && blockIdx.x == 0 && tid == 0) {   // what the attention over a bf16 cache has to report
+        if (const int32_t bits = *p.wide_status) atomicOr(status, bits);
+        *p.wide_status = 0;
+    }
+
     // ---- the warps' shares of all units: every CTA counts them for itself
     const int run = (p.R + kThreads - 1) / kThreads, r0 = min(p.R, tid * run), r1 = min(p.R, r0 + run);
     auto units = [&](int r, int *bad) {
-        const Request q = request(p, r, bad);
+        const Kv4Request q = request(p, r, bad);
         const int64_t blocks = (q.n * p.group + NC - 1) / NC;
         return blocks * p.kv_heads * (kGap + max(1, (q.keys + 15) >> 4));
     };

@@ -1,0 +1,156 @@
+// The wide requests of a step over the 4-bit cache (lora_kv4_attn): chunks of
+// prompts, whose many rows share each key, so that the tensor cores bound them and
+// not the cache's bytes.  Their keys and values are unpacked to bf16 once (exactly),
+// and the attention over a bf16 cache (attn.cu) runs over that.
+#include <cuda_runtime.h>
+
+#include "block_scan.cuh"
+#include "kv4.cuh"
+#include "kv4_request.cuh"
+#include "kv_ops.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kUnpackThreads = 256;
+constexpr int kPageTiles = kKv4WidePage / 16;
+
+// One CTA: which requests are wide, and where each goes.  In request order as long as there
+// is room for their keys.  What the attention is given are the wide requests and, in
+// between, everything else as requests without keys, whose rows it writes as zeros
+// and the kernel for the other requests (after it) as they are.
+__global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4WideParams w, const Kv4AttnParams p)
+{
+    pdl_launch_dependents();
+    __shared__ int64_t scan[32];
+    const int tid = threadIdx.x;
+    const int run = (p.R + kPlanThreads - 1) / kPlanThreads, r0 = min(p.R, tid * run), r1 = min(p.R, r0 + run);
+    pdl_wait();
+    int bad = 0;
+    // pages in the low half, requests in the high one
+    auto need = [&](const Kv4Request &q) {
+        const bool wide = static_cast<int64_t>(q.n) * p.group > kKv4WideRows && q.keys > 0;
+        return wide ? (int64_t(1) << 32) + (q.keys + kKv4WidePage - 1) / kKv4WidePage : int64_t(0);
+    };
+    int64_t sum = 0, total;
+    for (int r = r0; r < r1; ++r) sum += need(kv4_request(p, r, &bad));
+    int64_t at = block_scan_i64(sum, scan, &total);
+    int64_t served = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Kv4Request q = kv4_request(p, r, &bad);
+        const int64_t n = need(q);
+        const int pages = static_cast<int>(n), first = static_cast<int>(at & 0xFFFFFFFF), i = static_cast<int>(at >> 32);
+        const bool wide = n != 0 && static_cast<int64_t>(first) + pages <= w.pages && i < w.max_wide;
+        w.wide[r] = wide;
+        if (wide) {
+            served += n;
+            w.cu[2 * i + 1] = q.tok0;
+            w.cu[2 * i + 2] = q.tok0 + q.n;
+            w.kv_len[2 * i] = 0;
+            w.kv_len[2 * i + 1] = q.keys;
+            w.first[i] = first;
+            w.request[i] = r;
+        }
+        at += n;
+    }
+    // the served ones are the first: n and the pages of all of them
+    block_scan_i64(served, scan, &total);
+    const int count = static_cast<int>(total >> 32);
+    // rows of no request, in front and behind, stay out
+    const int begin = max(0, min(p.cu[0], p.T)), end = max(begin, min(p.cu[p.R], p.T));
+    if (tid == 0) {
+        w.cu[0] = begin;
+        w.kv_len[2 * count] = 0;
+        w.count[0] = count;
+        w.count[1] = static_cast<int>(total & 0xFFFFFFFF);
+    }
+    for (int i = 2 * count + 1 + tid; i <= 2 * w.max_wide + 1; i += kPlanThreads) {
+        w.cu[i] = end;
+        if (i <= 2 * w.max_wide) w.kv_len[i] = 0;
+    }
+}
+
+// A warp a tile: a lane has 8 (4) words of key codes and as many of value codes, as in the attention.
+template <int DP>
+__global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4WideParams w, const Kv4AttnParams p)
+{
+    pdl_launch_dependents();
+    using Tile = Kv4Tile<DP>;
+    constexpr int W = DP / 32;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int in_page = p.page_shift - 4;
+    pdl_wait();
+    const int count = w.count[0];
+    // the tables of the pages that the attention sees, and the tiles behind them
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kUnpackThreads / 32);
+    const int64_t tiles = static_cast<int64_t>(w.count[1]) * kPageTiles * p.kv_heads;
+    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kUnpackThreads + threadIdx.x) >> 5; u < tiles; u += warps) {
+        const int64_t per_page = static_cast<int64_t>(kPageTiles) * p.kv_heads;
+        const int page = static_cast<int>(u / per_page), rest = static_cast<int>(u - page * per_page);
+        const int h = rest / kPageTiles, in = rest % kPageTiles;
+        const int i = last_le(w.first, count, page), r = w.request[i];
+        const int t = (page - w.first[i]) * kPageTiles + in;   // of the request's tiles
+        if (h == 0 && in == 0 && lane == 0) w.table[(2 * i + 1) * static_cast<int64_t>(w.pages) + page - w.first[i]] = page;
+        int bad = 0;
+        const int keys = kv4_request(p, r, &bad).keys;
+        if (t * 16 >= keys) continue;
+        const int from = p.table[r * p.table_stride + (t >> in_page)];
+        const uint8_t *tile = p.zeros;
+        if (from >= 0 && from < p.num_pages)
+            tile = p.data + from * p.page_stride + h * p.head_stride + (t & ((1 << in_page) - 1)) * static_cast<int64_t>(Tile::kBytes);
+        else if (lane == 0)
+            atomicOr(p.counters, LORA_DEV_BAD_PAGE);
+        const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + h) * kKv4WidePage + in * 16) * p.head_dim;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {   // keys g and g + 8, elements from c * DP / 4 on
+            uint32_t k[W];
+            const uint8_t *at = tile + e * (4 * DP) + lane * (4 * W);
+            if (W == 4) *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<const uint4 *>(at);
+            else *reinterpret_cast<uint2 *>(k) = *reinterpret_cast<const uint2 *>(at);
+            uint16_t *to = w.k + row + (8 * e + g) * p.head_dim + c * (DP / 4);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const uint32_t scale = tile[Tile::kKeyScales + (8 * e + g) * Tile::kGroups + (c * (DP / 4) + 8 * j) / 16];
+                if (c * (DP / 4) + 8 * j < p.head_dim) *reinterpret_cast<uint4 *>(to + 8 * j) = kv4_values(k[j], scale);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {   // keys 2c, 2c + 1 and 8 more, elements from g * DP / 8 on
+            uint32_t v[W];
+            const uint8_t *at = tile + Tile::kValues + e * (4 * DP) + lane * (4 * W);
+            if (W == 4) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(at);
+            else *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(at);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {   // words: 8 elements of the even key, of the odd one, the next 8
+                const int key = 8 * e + 2 * c + (j & 1), d = g * (DP / 8) + (j >> 1) * 8;
+                const uint32_t scale = tile[Tile::value_scale(key, d / 16)];
+                if (d < p.head_dim) *reinterpret_cast<uint4 *>(w.v + row + key * p.head_dim + d) = kv4_values(v[j], scale);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    pdl_attribute(cfg, at);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_wide_plan_kernel, w, p);
+    if (e != cudaSuccess) return e;
+    const int64_t most = static_cast<int64_t>(w.pages) * kPageTiles * p.kv_heads / (kUnpackThreads / 32) + 1;
+    const int64_t cap = 8ll * num_sms_current_device();
+    cfg.gridDim = dim3(static_cast<unsigned>(most < cap ? most : cap));
+    cfg.blockDim = dim3(kUnpackThreads);
+    return cudaLaunchKernelEx(&cfg, p.head_dim <= 64 ? kv4_unpack_kernel<64> : kv4_unpack_kernel<128>, w, p);
+}
+
+}  // namespace lora

@@ -36,18 +36,52 @@ static int check_cache4(const lora_kv4_cache_t *c)
     return aligned(c->data, 16) ? LORA_OK : LORA_ERR_ALIGN;
 }
 
-static Kv4Layout kv4_layout(int32_t head_dim)
+// Whether a step of T tokens of R requests is likely to have wide ones that are worth the launches they
+// need (12 us): many rows a request, or many beyond one token each.
+static bool maybe_wide(int64_t T, int32_t R, int32_t group)
 {
-    // the widest blocks run one CTA an SM, so the product of slots and columns is the same for all but the widest
-    // multiple: 2 * kKv4MaxCtas slots of 16 columns hold kKv4MaxCtas of 32
+    return T * group > static_cast<int64_t>(R) * kKv4WideRows / 2 || (T - R) * group >= 16 * kKv4WideRows;
+}
+
+static bool unpack_ok(int64_t tokens) { return tokens >= 0 && tokens <= (int64_t(1) << 24); }
+
+static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t unpack)
+{
     Kv4Layout L;
-    const size_t dp = kv4_padded(head_dim), cells = 2 * static_cast<size_t>(kKv4MaxCtas) * 16;
-    L.counters = 0;
-    L.zeros = align256((kKv4CntGroup + kKv4MaxCtas) * 4);
-    L.first = L.zeros + align256(kv4_tile_bytes(128));
-    L.part = L.first + align256(8 * cells / 2 * (dp + 4) * 4);
-    L.part_ml = L.part + align256(cells * dp * 4);
-    L.total = L.part_ml + align256(cells * 8);
+    std::memset(&L, 0, sizeof L);
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t a = o;
+        o = align256(o + bytes);
+        return a;
+    };
+    L.counters = take((kKv4CntGroup + kKv4MaxCtas) * 4);
+    L.zeros = take(kv4_tile_bytes(128));
+    // wide requests: no more than the rows allow, or than lists have places
+    L.max_wide = static_cast<int32_t>(
+        std::min<int64_t>({R, T * (heads / kv_heads) / (kKv4WideRows + 1), LORA_MAX_REQUESTS / 2 - 1}));
+    L.pages = static_cast<int32_t>(unpack / kKv4WidePage);
+    if (L.max_wide == 0 || L.pages == 0) L.max_wide = L.pages = 0;
+    L.attn_bytes = lora_attn_workspace_size(T, 2 * L.max_wide + 1, heads, kv_heads, head_dim);
+    L.attn = take(L.max_wide ? L.attn_bytes : ACNT_WORDS * 4);
+    // as many warps, and as many columns of CTAs, as the narrowest blocks have; wider ones have fewer CTAs
+    const size_t dp = kv4_padded(head_dim), columns = static_cast<size_t>(kAttnMaxCtas) * 32;
+    L.first = take(8 * columns * (dp + 4) * 4);
+    L.part = take(2 * columns * dp * 4);
+    L.part_ml = take(2 * columns * 8);
+    if (L.max_wide) {
+        const size_t lists = 2 * static_cast<size_t>(L.max_wide) + 2, rows = static_cast<size_t>(L.pages) * kv_heads * kKv4WidePage;
+        L.cu = take(lists * 4);
+        L.kv_len = take(lists * 4);
+        L.wide = take(R);
+        L.wide_first = take(lists * 4);
+        L.request = take(lists * 4);
+        L.count = take(2 * 4);
+        L.table = take((lists - 1) * L.pages * 4);
+        L.k = take(rows * head_dim * 2);
+        L.v = take(rows * head_dim * 2);
+    }
+    L.total = o;
     return L;
 }
 
@@ -233,15 +267,15 @@ extern "C" int lora_kv4_load(const lora_kv4_cache_t *cache, const int32_t *slots
 }
 
 extern "C" size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t heads, int32_t kv_heads,
-                                          int32_t head_dim)
+                                          int32_t head_dim, int64_t unpack_tokens)
 {
-    if (!step_ok(num_tokens, num_requests) || !heads_ok(heads, kv_heads, head_dim)) return 0;
-    return kv4_layout(head_dim).total;
+    if (!step_ok(num_tokens, num_requests) || !heads_ok(heads, kv_heads, head_dim) || !unpack_ok(unpack_tokens)) return 0;
+    return kv4_layout(num_tokens, num_requests, heads, kv_heads, head_dim, unpack_tokens).total;
 }
 
 extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *cache, const int32_t *block_table,
-                             int32_t table_width, int64_t table_stride, const int32_t *kv_len, void *ws,
-                             size_t ws_bytes, lora_stream_t stream)
+                             int32_t table_width, int64_t table_stride, const int32_t *kv_len, int64_t unpack_tokens,
+                             void *ws, size_t ws_bytes, lora_stream_t stream)
 {
     int rc = check_attn(attn);
     if (rc) return rc;
@@ -251,10 +285,12 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > kMaxTokens) return LORA_ERR_SHAPE;
     if (attn->num_requests > 1 && table_stride < table_width) return LORA_ERR_SHAPE;
     if (attn->num_tokens * (attn->heads / attn->kv_heads) > kMaxTokens) return LORA_ERR_SHAPE;   // rows of a key head
+    if (!unpack_ok(unpack_tokens)) return LORA_ERR_SHAPE;
     if (attn->num_tokens == 0 || attn->num_requests == 0) return LORA_OK;
     if (!kv_len || (table_width > 0 && !block_table)) return LORA_ERR_NULL;
     if (!ints_aligned({kv_len, block_table})) return LORA_ERR_ALIGN;
-    const Kv4Layout L = kv4_layout(attn->head_dim);
+    const Kv4Layout L = kv4_layout(attn->num_tokens, attn->num_requests, attn->heads, attn->kv_heads, attn->head_dim,
+                                   unpack_tokens);
     rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
     Kv4AttnParams p;
@@ -288,6 +324,32 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     p.part = at<float>(ws, L.part);
     p.part_ml = at<float2>(ws, L.part_ml);
     p.wait_cycles = tc_wait_cycles();
+    p.wide = nullptr;
+    p.wide_status = nullptr;
+    if (L.max_wide && maybe_wide(p.T, p.R, p.group)) {   // the wide requests, by the attention over a bf16 cache; then the others
+        Kv4WideParams w;
+        w.cu = at<int32_t>(ws, L.cu);
+        w.kv_len = at<int32_t>(ws, L.kv_len);
+        w.wide = at<uint8_t>(ws, L.wide);
+        w.first = at<int32_t>(ws, L.wide_first);
+        w.request = at<int32_t>(ws, L.request);
+        w.count = at<int32_t>(ws, L.count);
+        w.table = at<int32_t>(ws, L.table);
+        w.k = at<uint16_t>(ws, L.k);
+        w.v = at<uint16_t>(ws, L.v);
+        w.max_wide = L.max_wide;
+        w.pages = L.pages;
+        if (launch_kv4_wide(w, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LORA_ERR_CUDA;
+        lora_attn_t a = *attn;
+        a.cu = w.cu;
+        a.num_requests = 2 * L.max_wide + 1;
+        const int64_t slot = a.head_dim, head = slot * kKv4WidePage;
+        const lora_kv_cache_t c = {w.k, w.v, head * a.kv_heads, head, slot, w.pages, kKv4WidePage, a.kv_heads, a.head_dim};
+        rc = lora_attn_paged(&a, &c, w.table, w.pages, w.pages, w.kv_len, nullptr, at<void>(ws, L.attn), L.attn_bytes, stream);
+        if (rc) return rc;
+        p.wide = w.wide;
+        p.wide_status = at<int32_t>(ws, L.attn) + CNT_STATUS;
+    }
     return launched(launch_kv4_attn(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -49,13 +49,19 @@ struct Kv4LoadParams {
 
 constexpr int kKv4MaxCtas = 3 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
 
-// Workspace of the 4-bit attention (offsets 256-byte aligned): the status word and
-// the arrival counters of split groups (zero at rest but the status), a tile of zeros
-// that stands for pages outside the cache, and the partial results, of warps and of CTAs.
+// Workspace of the 4-bit attention (offsets 256-byte aligned).  In front, at the same places in
+// every call's layout, what is zero at rest: the status word and the arrival counters of
+// split groups, a tile of zeros that stands for pages outside the cache, and the counters of the
+// attention over a bf16 cache, whose workspace begins there.  Then partial results, of warps
+// and of CTAs, and the wide requests' lists and unpacked pages.
 struct Kv4Layout {
-    size_t counters, zeros, first, part, part_ml, total;
+    size_t counters, zeros, attn, first, part, part_ml, cu, kv_len, wide, wide_first, request, count, table, k, v, total;
+    size_t attn_bytes;
+    int32_t max_wide, pages;
 };
 constexpr int kKv4CntGroup = 32;                // first arrival counter; one for each CTA
+constexpr int kKv4WidePage = 128;               // keys of a page of the unpacked cache
+constexpr int kKv4WideRows = 64;                // most rows (tokens times a group's heads) of a request that is not wide
 
 struct Kv4AttnParams {
     const uint16_t *q;
@@ -63,6 +69,8 @@ struct Kv4AttnParams {
     float *lse;
     int64_t q_tok, q_head, o_tok, o_head;       // element strides
     const int32_t *cu, *kv_len, *table;
+    const uint8_t *wide;                        // [R] what is left out, or NULL
+    int32_t *wide_status;                       // its status word, or NULL
     int64_t table_stride;
     int64_t max_kv;                             // table_width * page_size
     const uint8_t *data;
@@ -79,13 +87,23 @@ struct Kv4AttnParams {
     int64_t wait_cycles;
 };
 
+struct Kv4WideParams {
+    int32_t *cu, *kv_len;                       // [2 max_wide + 2], [2 max_wide + 1]: request 2i + 1 is the i-th wide one
+    uint8_t *wide;                              // [R]
+    int32_t *first, *request;                   // [max_wide] first unpacked page, request
+    int32_t *count;                             // wide requests, their pages
+    int32_t *table;                             // [2 max_wide + 1][pages]
+    uint16_t *k, *v;                            // [pages][kv_heads][kKv4WidePage][head_dim]
+    int32_t max_wide, pages;
+};
+
 // Workspace of the calls on pages (offsets 256-byte aligned; all of it zero at
 // rest but the status, the counts and the map).
 struct PagesLayout {
     size_t counters, used, free, counts, map, total;
 };
 constexpr int kPagesArrived = 2;                // counter: CTAs done with their reading
-constexpr int kPageChunk = 4096;                // pages that one CTA counts and lists
+constexpr int kPageChunk = 1024;                // pages that one CTA counts and lists
 
 struct KvPagesParams {
     lora_kv_pages_t a;
@@ -116,6 +134,7 @@ struct PageCopyParams {
 cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_store(const Kv4StoreParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_load(const Kv4LoadParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream);
 cudaError_t launch_kv_release(const KvPagesParams &p, cudaStream_t stream);
 cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream);

@@ -244,8 +244,6 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const KvPagesParams p)
 // below the limit (holes), the held ones from it on (movers) and the free ones from it on;
 // list: with the counts before a chunk, every page's place among its kind is known, so
 // the pairs and the new free list are written in one pass; and the tables follow.
-__device__ __forceinline__ bool is_held(const KvPagesParams &p, int64_t page) { return p.used[page]; }
-
 __global__ void __launch_bounds__(kThreads) compact_mark_kernel(const KvPagesParams p)
 {
     pdl_launch_dependents();
@@ -399,46 +397,60 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
 // ---------------------------------------------------------------------------
 // lora_kv_copy, lora_kv4_copy
 // ---------------------------------------------------------------------------
-// 16-byte units, a block a run of one page's; HBM bounds it, so a thread has four
-// loads in flight.
-constexpr int kCopyUnits = 4;
+// 16-byte units, a block a run of one page's; HBM bounds it, so a thread has eight
+// loads in flight.  Lists may be mostly empty pairs (compaction pads its own), so a
+// block looks at the pairs of several rounds at once.
+constexpr int kCopyUnits = 8, kCopyRounds = 4;
 
 template <bool ROWS>   // ROWS: a page's units go by head and slot strides
 __global__ void __launch_bounds__(kThreads) page_copy_kernel(const PageCopyParams p)
 {
     pdl_launch_dependents();
-    const int units = p.heads * p.rows * p.vecs, runs = (units + kCopyUnits * kThreads - 1) / (kCopyUnits * kThreads);
-    const int parts = p.base[1] ? 2 : 1;
-    const int64_t work = static_cast<int64_t>(p.num) * runs * parts;
+    const int units = p.heads * p.rows * p.vecs;
+    const uint32_t runs = (units + kCopyUnits * kThreads - 1) / (kCopyUnits * kThreads), each = runs * (p.base[1] ? 2 : 1);
+    const int64_t work = static_cast<int64_t>(p.num) * each, step = gridDim.x;
     pdl_wait();
     int bad = 0;
-    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
-        const int64_t i = w / (runs * parts);
-        const int rest = static_cast<int>(w - i * (runs * parts)), part = rest / runs, run = rest - part * runs;
-        const int src = p.src[i], dst = p.dst[i];
-        if (src < 0 || dst < 0 || src >= p.num_pages || dst >= p.num_pages) {
-            bad |= src != -1 || dst != -1;
-            continue;
-        }
-        const uint4 *from = p.base[part] + src * p.page_stride;
-        uint4 *to = p.base[part] + dst * p.page_stride;
-        uint4 v[kCopyUnits];
-        int64_t at[kCopyUnits];
+    for (int64_t w0 = blockIdx.x; w0 < work; w0 += kCopyRounds * step) {
+        int src[kCopyRounds], dst[kCopyRounds];
+        uint32_t rest[kCopyRounds];
 #pragma unroll
-        for (int u = 0; u < kCopyUnits; ++u) {
-            const int k = (run * kCopyUnits + u) * kThreads + threadIdx.x;
-            at[u] = -1;
-            if (k >= units) continue;
-            at[u] = k;
-            if (ROWS) {
-                const int row = k / p.vecs, h = row / p.rows;
-                at[u] = h * p.head_stride + (row - h * p.rows) * p.slot_stride + (k - row * p.vecs);
+        for (int q = 0; q < kCopyRounds; ++q) {
+            const int64_t w = w0 + q * step;
+            src[q] = dst[q] = -1;
+            if (w >= work) continue;
+            const int64_t i = work < (int64_t(1) << 32) ? static_cast<uint32_t>(w) / each : w / each;
+            rest[q] = static_cast<uint32_t>(w - i * each);
+            src[q] = p.src[i];
+            dst[q] = p.dst[i];
+        }
+#pragma unroll
+        for (int q = 0; q < kCopyRounds; ++q) {
+            if (src[q] < 0 || dst[q] < 0 || src[q] >= p.num_pages || dst[q] >= p.num_pages) {
+                bad |= src[q] != -1 || dst[q] != -1;
+                continue;
             }
-            v[u] = __ldcs(from + at[u]);
-        }
+            const uint32_t part = rest[q] >= runs, run = rest[q] - part * runs;
+            const uint4 *from = p.base[part] + src[q] * p.page_stride;
+            uint4 *to = p.base[part] + dst[q] * p.page_stride;
+            uint4 v[kCopyUnits];
+            int64_t at[kCopyUnits];
 #pragma unroll
-        for (int u = 0; u < kCopyUnits; ++u)
-            if (at[u] >= 0) to[at[u]] = v[u];
+            for (int u = 0; u < kCopyUnits; ++u) {
+                const int k = (run * kCopyUnits + u) * kThreads + threadIdx.x;
+                at[u] = -1;
+                if (k >= units) continue;
+                at[u] = k;
+                if (ROWS) {
+                    const int row = k / p.vecs, h = row / p.rows;
+                    at[u] = h * p.head_stride + (row - h * p.rows) * p.slot_stride + (k - row * p.vecs);
+                }
+                v[u] = __ldcs(from + at[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kCopyUnits; ++u)
+                if (at[u] >= 0) __stcs(to + at[u], v[u]);
+        }
     }
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
 }

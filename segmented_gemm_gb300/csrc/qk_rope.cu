@@ -13,166 +13,263 @@ namespace lora {
 // neighbours (interleaved pairs, and what is not rotated).  So a pair never leaves
 // its lane, and a row's sum of squares is a few lane exchanges away.
 //
-// The angle of (position p, frequency w) in turns is p * w / 2pi modulo 1.  With
-// w / 2pi modulo 1 as a 64-bit fixed-point fraction the product with p wraps as
-// it should in integer arithmetic, exactly at any position; only its top 32 bits
-// become an fp32 angle.  A CTA does that once for its tokens, into shared memory.
-//
-// HBM bounds large calls: every row is read and written once, U rows of a lane in
-// flight.
+// A group of lanes has one head's row of each of the CTA's tokens, then the next head's
+// that is its turn, so what goes by the head (addresses, weights, what is
+// done) is settled once for all tokens, and a token's rows are in flight together.
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ float2 turn_of(float inv_freq, int32_t pos)
+// inv_freq / 2pi, modulo 1, in units of 2^-64: what a position turns by.  inv_freq is m * 2^e, so it is
+// m * (2^88 / 2pi) * 2^(e - 24), in integers: fp64 would cost more than the rest of the kernel.
+__device__ __forceinline__ unsigned long long turns_of(float inv_freq)
 {
-    const double t = static_cast<double>(inv_freq) * 0.15915494309189535;   // 1 / 2pi
-    const unsigned long long step = __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+    constexpr unsigned long long kHi = 0x28BE60ull, kLo = 0xDB9391054A7F09D5ull;   // 2^88 / 2pi
+    const uint32_t bits = __float_as_uint(inv_freq), field = bits >> 23 & 0xFF;
+    const unsigned long long m = (bits & 0x7FFFFF) | (field ? 0x800000 : 0);
+    const int shift = 174 - static_cast<int>(field ? field : 1);     // 24 - e
+    const unsigned long long lo = m * kLo, hi = m * kHi + __umul64hi(m, kLo);
+    unsigned long long step;
+    if (shift >= 128) step = 0;
+    else if (shift >= 64) step = hi >> (shift - 64);
+    else if (shift > 0) step = hi << (64 - shift) | lo >> shift;
+    else {   // from 2^24 on: not what these frequencies are, and not exact
+        const double w = static_cast<double>(fabsf(inv_freq)) * 0.15915494309189535;
+        step = __double2ull_rz((w - floor(w)) * 18446744073709551616.0);
+    }
+    return bits >> 31 ? 0 - step : step;
+}
+
+// The cosine and sine of position * inv_freq.  The product wraps as an angle in turns should, exactly at
+// any position; only its top 32 bits become an fp32 angle.
+__device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos)
+{
     const unsigned long long at = step * static_cast<unsigned>(pos);
-    // the top 32 bits as a signed fraction of a turn, [-1/2, 1/2)
+    // a signed fraction of a turn, [-1/2, 1/2), in half turns
     const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * 4.656612873077393e-10f;   // 2^-31
     float2 r;
     sincospif(half_turns, &r.y, &r.x);
     return r;
 }
 
-template <int LANES, int TOKENS, int U>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const QkRopeParams p)
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t both(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t widen2(uint32_t v) { return both(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ uint32_t narrow2(uint64_t v)
+{
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return pack_bf16x2(lo, hi);
+}
+
+// TOKENS of a CTA, up to four of them in flight at a time
+template <int LANES, int TOKENS, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopeParams p)
 {
     pdl_launch_dependents();
-    __shared__ __align__(16) float2 turn[TOKENS][LORA_MAX_HEAD_DIM / 2];
-    __shared__ int32_t position[TOKENS], slot[TOKENS];
     constexpr int kGroups = kRopeThreads / LANES;   // rows at a time
+    constexpr int U = TOKENS < 4 ? TOKENS : 4;
+    constexpr int kPairs = LORA_MAX_HEAD_DIM / 2;
+    // cosines and sines by quarters of pairs, as the lanes want them: (c, c, c, c), (s, s, s, s)
+    __shared__ __align__(16) float turn[TOKENS][kPairs / 4][2][4];
+    __shared__ int32_t position[TOKENS];
+    __shared__ int64_t place[TOKENS];               // of the token in the cache, or -1
     const lora_qk_rope_t &a = p.a;
     const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
     const int half = a.rot_dim / 2;
     const bool rotated = lane < a.rot_dim / 8, on = lane < a.head_dim / 8;
-    const bool halves = rotated && !a.interleaved;
+    const bool halves = rotated && !INTERLEAVED;
     const int off0 = halves ? 4 * lane : 8 * lane, off1 = halves ? half + 4 * lane : 8 * lane + 4;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
     const int tokens = static_cast<int>(a.num_tokens - t0 < TOKENS ? a.num_tokens - t0 : TOKENS);
     const int heads = a.heads, k_end = heads + a.kv_heads, per = k_end + (p.kc ? a.kv_heads : 0);
-    const int rows = tokens * per;
-    const bool norm = a.q_weight || a.k_weight;
+    const bool norms = a.q_weight || a.k_weight;
+    const float mean = 1.f / static_cast<float>(a.head_dim);
     pdl_wait();
 
-    // weights of this lane's elements
-    uint2 w[2][2] = {};
-    if (on && a.q_weight) {
-        w[0][0] = *reinterpret_cast<const uint2 *>(a.q_weight + off0);
-        w[0][1] = *reinterpret_cast<const uint2 *>(a.q_weight + off1);
-    }
-    if (on && a.k_weight) {
-        w[1][0] = *reinterpret_cast<const uint2 *>(a.k_weight + off0);
-        w[1][1] = *reinterpret_cast<const uint2 *>(a.k_weight + off1);
-    }
-
+    // row r of a token: a query head, a key head, or a value head that is only copied
+    struct Row {
+        const uint16_t *from;
+        uint16_t *to, *cache;        // either may be NULL
+        int64_t step, to_step;       // from token to token
+        const uint16_t *weight;
+        bool on, turned;
+    };
+    auto row = [&](int r) {
+        Row w = {};
+        w.on = r < per && on;
+        w.turned = r < k_end;
+        if (r < heads) {
+            w.from = a.q + r * a.q_head_stride + t0 * a.q_token_stride;
+            w.step = a.q_token_stride;
+            w.to = a.q_out + r * a.qo_head_stride + t0 * a.qo_token_stride;
+            w.to_step = a.qo_token_stride;
+            w.weight = a.q_weight;
+        } else {
+            const int h = r - (w.turned ? heads : k_end);
+            w.from = w.turned ? a.k + h * a.k_head_stride + t0 * a.k_token_stride : a.v + h * a.v_head_stride + t0 * a.v_token_stride;
+            w.step = w.turned ? a.k_token_stride : a.v_token_stride;
+            if (w.turned && a.k_out) w.to = a.k_out + h * a.ko_head_stride + t0 * a.ko_token_stride;
+            w.to_step = a.ko_token_stride;
+            if (p.kc) w.cache = (w.turned ? p.kc : p.vc) + h * p.head_stride;
+            w.weight = w.turned ? a.k_weight : nullptr;
+        }
+        return w;
+    };
     uint2 x[U][2];
-    auto load = [&](int base) {
+    auto load = [&](const Row &w, int i0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + u * kGroups + group;
-            x[u][0] = x[u][1] = make_uint2(0, 0);
-            if (i >= rows || !on) continue;
-            const int tok = TOKENS == 1 ? 0 : i / per, r = i - tok * per;
-            const int64_t t = t0 + tok;
-            const uint16_t *row = r < heads ? a.q + t * a.q_token_stride + r * a.q_head_stride
-                                  : r < k_end ? a.k + t * a.k_token_stride + (r - heads) * a.k_head_stride
-                                              : a.v + t * a.v_token_stride + (r - k_end) * a.v_head_stride;
-            x[u][0] = *reinterpret_cast<const uint2 *>(row + off0);
-            x[u][1] = *reinterpret_cast<const uint2 *>(row + off1);
+        for (int i = 0; i < U; ++i) {
+            x[i][0] = x[i][1] = make_uint2(0, 0);
+            if (!w.on || i0 + i >= tokens) continue;
+            const uint16_t *at = w.from + (i0 + i) * w.step;
+            x[i][0] = *reinterpret_cast<const uint2 *>(at + off0);
+            x[i][1] = *reinterpret_cast<const uint2 *>(at + off1);
         }
     };
-    load(0);
+    Row w = row(blockIdx.y * kGroups + group);
+    load(w, 0);
 
     if (tid < tokens) {
-        position[tid] = a.position ? a.position[t0 + tid] : 0;
-        slot[tid] = p.kc ? a.slot_map[t0 + tid] : -1;
+        const int32_t at = a.position[t0 + tid], s = p.kc ? a.slot_map[t0 + tid] : -1;
+        const bool known = s >= 0 && s < p.slots;
+        if (at >= 0 && s != -1 && !known) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+        position[tid] = at;
+        place[tid] = known ? (s >> p.page_shift) * p.page_stride + (s & ((1 << p.page_shift) - 1)) * p.slot_stride : -1;
     }
-    for (int i = tid; i < tokens * half; i += kRopeThreads) {
-        const int tok = TOKENS == 1 ? 0 : i / half, j = i - tok * half;
-        turn[tok][j] = turn_of(a.inv_freq[j], a.position[t0 + tok]);
+    static_assert(kRopeThreads % kPairs == 0, "a thread has one frequency");
+    {   // what is not rotated turns by nothing, so that no lane has a branch
+        const int j = tid % kPairs;
+        const unsigned long long step = j < half ? turns_of(a.inv_freq[j]) : 0;
+        for (int i = tid / kPairs; i < tokens; i += kRopeThreads / kPairs) {
+            const float2 cs = turn_of(step, j < half ? a.position[t0 + i] : 0);
+            turn[i][j / 4][0][j % 4] = cs.x;
+            turn[i][j / 4][1][j % 4] = cs.y;
+        }
     }
     __syncthreads();
-    if (tid < tokens && slot[tid] != -1 && position[tid] >= 0 && (slot[tid] < 0 || slot[tid] >= p.slots))
-        atomicOr(p.status, LORA_DEV_BAD_PAGE);
 
-    for (int base = 0; base < rows; base += U * kGroups) {
-        if (base) load(base);
+    // the same rounds for a whole warp: rows are summed by lane exchanges
+    for (int first = blockIdx.y * kGroups; first < per; first += gridDim.y * kGroups) {
+        const bool again = first != static_cast<int>(blockIdx.y) * kGroups;
+        if (again) w = row(first + group);
+        const bool weighted = w.on && w.weight;
+        uint64_t wt[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + u * kGroups + group;
-            const bool row_on = i < rows;
-            const int tok = TOKENS == 1 || !row_on ? 0 : i / per, r = i - tok * per;
-            const bool is_q = r < heads, is_v = r >= k_end;
-            float y[8] = {bf16_lo(x[u][0].x), bf16_hi(x[u][0].x), bf16_lo(x[u][0].y), bf16_hi(x[u][0].y),
-                          bf16_lo(x[u][1].x), bf16_hi(x[u][1].x), bf16_lo(x[u][1].y), bf16_hi(x[u][1].y)};
-            if (norm) {
-                float sum = 0.f;
+        for (int j = 0; j < 4; ++j) wt[j] = both(1.f, 1.f);
+        if (weighted) {
+            const uint2 w0 = *reinterpret_cast<const uint2 *>(w.weight + off0), w1 = *reinterpret_cast<const uint2 *>(w.weight + off1);
+            wt[0] = widen2(w0.x);
+            wt[1] = widen2(w0.y);
+            wt[2] = widen2(w1.x);
+            wt[3] = widen2(w1.y);
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < tokens; i0 += U) {
+            if (again || i0) load(w, i0);
+            float f[U];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum += y[j] * y[j];
+            for (int i = 0; i < U; ++i) f[i] = 1.f;
+            if (norms) {
 #pragma unroll
-                for (int d = LANES / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-                    const float f = rsqrtf(sum / static_cast<float>(a.head_dim) + a.eps);
-                    const uint2 w0 = is_q ? w[0][0] : w[1][0], w1 = is_q ? w[0][1] : w[1][1];
-                    const float wf[8] = {bf16_lo(w0.x), bf16_hi(w0.x), bf16_lo(w0.y), bf16_hi(w0.y),
-                                         bf16_lo(w1.x), bf16_hi(w1.x), bf16_lo(w1.y), bf16_hi(w1.y)};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] *= f * wf[j];
+                for (int i = 0; i < U; ++i) {
+                    const uint64_t y0 = widen2(x[i][0].x), y1 = widen2(x[i][0].y), y2 = widen2(x[i][1].x), y3 = widen2(x[i][1].y);
+                    const uint64_t s2 = fma2(y3, y3, fma2(y2, y2, fma2(y1, y1, mul2(y0, y0))));
+                    float s0, s1;
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s2));
+                    f[i] = s0 + s1;
                 }
-            }
-            if (!row_on || !on || position[tok] < 0) continue;
-            if (rotated) {
-                const float4 c01 = *reinterpret_cast<const float4 *>(&turn[tok][4 * lane]);
-                const float4 c23 = *reinterpret_cast<const float4 *>(&turn[tok][4 * lane + 2]);
-                const float c[4] = {c01.x, c01.z, c23.x, c23.z}, s[4] = {c01.y, c01.w, c23.y, c23.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a0 = a.interleaved ? y[2 * j] : y[j], b0 = a.interleaved ? y[2 * j + 1] : y[4 + j];
-                    const float a1 = a0 * c[j] - b0 * s[j], b1 = b0 * c[j] + a0 * s[j];
-                    if (a.interleaved) {
-                        y[2 * j] = a1;
-                        y[2 * j + 1] = b1;
-                    } else {
-                        y[j] = a1;
-                        y[4 + j] = b1;
+                for (int d = LANES / 2; d; d >>= 1)
+#pragma unroll
+                    for (int i = 0; i < U; ++i) f[i] += __shfl_xor_sync(0xffffffffu, f[i], d);
+#pragma unroll
+                for (int i = 0; i < U; ++i) f[i] = weighted ? rsqrtf(fmaf(f[i], mean, a.eps)) : 1.f;
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int tok = i0 + i;
+                uint64_t y[4] = {widen2(x[i][0].x), widen2(x[i][0].y), widen2(x[i][1].x), widen2(x[i][1].y)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(y[j], wt[j]), both(f[i], f[i]));
+                const float4 c = *reinterpret_cast<const float4 *>(turn[tok][lane][0]);
+                const float4 s = *reinterpret_cast<const float4 *>(turn[tok][lane][1]);
+                if (!INTERLEAVED) {   // pairs (y[0], y[2]) and (y[1], y[3])
+                    const uint64_t c2[2] = {both(c.x, c.y), both(c.z, c.w)}, s2[2] = {both(s.x, s.y), both(s.z, s.w)};
+                    const uint64_t n2[2] = {both(-s.x, -s.y), both(-s.z, -s.w)};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint64_t u = y[j], v = y[2 + j];
+                        y[j] = fma2(v, n2[j], mul2(u, c2[j]));
+                        y[2 + j] = fma2(u, s2[j], mul2(v, c2[j]));
+                    }
+                } else {              // each y[j] is a pair
+                    const float cf[4] = {c.x, c.y, c.z, c.w}, sf[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float u, v;
+                        asm("mov.b64 {%0, %1}, %2;" : "=f"(u), "=f"(v) : "l"(y[j]));
+                        y[j] = both(fmaf(v, -sf[j], u * cf[j]), fmaf(u, sf[j], v * cf[j]));
                     }
                 }
-            }
-            uint2 o0 = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-            uint2 o1 = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            const int64_t t = t0 + tok;
-            uint16_t *out = nullptr;
-            if (is_q) {
-                out = a.q_out + t * a.qo_token_stride + r * a.qo_head_stride;
-            } else if (!is_v && a.k_out) {
-                out = a.k_out + t * a.ko_token_stride + (r - heads) * a.ko_head_stride;
-            }
-            if (is_v) {   // copied as it is
-                o0 = x[u][0];
-                o1 = x[u][1];
-            }
-            if (out) {
-                *reinterpret_cast<uint2 *>(out + off0) = o0;
-                *reinterpret_cast<uint2 *>(out + off1) = o1;
-            }
-            if (!is_q && p.kc && slot[tok] >= 0 && slot[tok] < p.slots) {
-                const int64_t page = slot[tok] >> p.page_shift, line = slot[tok] & ((1 << p.page_shift) - 1);
-                const int64_t h = r - (is_v ? k_end : heads);
-                uint16_t *to = (is_v ? p.vc : p.kc) + page * p.page_stride + h * p.head_stride + line * p.slot_stride;
-                *reinterpret_cast<uint2 *>(to + off0) = o0;
-                *reinterpret_cast<uint2 *>(to + off1) = o1;
+                uint2 o0 = x[i][0], o1 = x[i][1];   // values are copied as they are
+                if (w.turned) {
+                    o0 = make_uint2(narrow2(y[0]), narrow2(y[1]));
+                    o1 = make_uint2(narrow2(y[2]), narrow2(y[3]));
+                }
+                const bool ok = w.on && tok < tokens && position[tok] >= 0;
+                if (ok && w.to) {
+                    uint16_t *to = w.to + tok * w.to_step;
+                    *reinterpret_cast<uint2 *>(to + off0) = o0;
+                    *reinterpret_cast<uint2 *>(to + off1) = o1;
+                }
+                if (ok && w.cache && place[tok] >= 0) {
+                    uint16_t *to = w.cache + place[tok];
+                    *reinterpret_cast<uint2 *>(to + off0) = o0;
+                    *reinterpret_cast<uint2 *>(to + off1) = o1;
+                }
             }
         }
     }
 }
 
-cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream)
+template <int LANES, bool INTERLEAVED>
+static cudaError_t launch_rope(const QkRopeParams &p, cudaStream_t stream)
 {
     const int64_t T = p.a.num_tokens;
-    const bool wide = p.a.head_dim > 64;
-    if (T <= 4ll * num_sms_current_device())   // few tokens: spread over the SMs
-        return launch_pdl(wide ? qk_rope_kernel<16, 1, 4> : qk_rope_kernel<8, 1, 4>, T, kRopeThreads, 0, p, stream);
-    return launch_pdl(wide ? qk_rope_kernel<16, 4, 4> : qk_rope_kernel<8, 4, 4>, (T + 3) / 4, kRopeThreads, 0, p, stream);
+    constexpr int kGroups = kRopeThreads / LANES, kTokens = 8;
+    const int per = p.a.heads + (p.kc ? 2 : 1) * p.a.kv_heads;
+    // few tokens: a CTA for each group of heads too, one token each
+    const bool few = T <= 2ll * num_sms_current_device();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = few ? dim3(static_cast<unsigned>(T), (per + kGroups - 1) / kGroups)
+                      : dim3(static_cast<unsigned>((T + kTokens - 1) / kTokens));
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    pdl_attribute(cfg, at);
+    return cudaLaunchKernelEx(&cfg, few ? qk_rope_kernel<LANES, 1, INTERLEAVED> : qk_rope_kernel<LANES, kTokens, INTERLEAVED>, p);
+}
+
+cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream)
+{
+    if (p.a.head_dim <= 64) return p.a.interleaved ? launch_rope<8, true>(p, stream) : launch_rope<8, false>(p, stream);
+    return p.a.interleaved ? launch_rope<16, true>(p, stream) : launch_rope<16, false>(p, stream);
 }
 
 }  // namespace lora

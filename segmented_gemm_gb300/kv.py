@@ -75,8 +75,8 @@ def _lib():
             "lora_kv4_block_size": (_SZ, [_I32, _I32]),
             "lora_kv4_store": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64, VP, _P, _P, _SZ, _P]),
             "lora_kv4_load": (ctypes.c_int, [VP, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
-            "lora_kv4_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
-            "lora_kv4_attn": (ctypes.c_int, [VP, VP, _P, _I32, _I64, _P, _P, _SZ, _P]),
+            "lora_kv4_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I64]),
+            "lora_kv4_attn": (ctypes.c_int, [VP, VP, _P, _I32, _I64, _P, _I64, _P, _SZ, _P]),
             "lora_kv_pages_workspace_size": (_SZ, [_I32]),
             "lora_kv_release": (ctypes.c_int, [VP, _P, _I32, _P, _SZ, _P]),
             "lora_kv_fork": (ctypes.c_int, [VP, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
@@ -234,11 +234,20 @@ class _Workspace:
 
 
 class Kv4Workspace(_Workspace):
-    """A zero-initialised device workspace for lora_kv4_attn; serves the small
-    calls (lora_qk_rope, lora_kv4_store, lora_kv4_load) too."""
+    """A zero-initialised device workspace for lora_kv4_attn over steps of T packed
+    tokens and R requests; serves the small calls (lora_qk_rope, lora_kv4_store,
+    lora_kv4_load) too.  unpack_tokens: how many cached tokens of chunks of
+    prompts it has room for in bf16; by default what 256 MiB hold if T tokens of R requests
+    have chunks among them, else none."""
 
-    def __init__(self, T: int, R: int, heads: int, kv_heads: int, head_dim: int, device="cuda"):
-        super().__init__(int(_lib().lora_kv4_workspace_size(T, R, heads, kv_heads, head_dim)),
+    def __init__(self, T: int, R: int, heads: int, kv_heads: int, head_dim: int, unpack_tokens: Optional[int] = None,
+                 device="cuda"):
+        if unpack_tokens is None:
+            group = heads // max(1, kv_heads)
+            chunks = T * group > 32 * R or (T - R) * group >= 1024
+            unpack_tokens = (256 << 20) // max(1, 4 * kv_heads * head_dim) if chunks else 0
+        self.unpack_tokens = unpack_tokens
+        super().__init__(int(_lib().lora_kv4_workspace_size(T, R, heads, kv_heads, head_dim, unpack_tokens)),
                          "Kv4Workspace: token, request or head counts out of range", device)
 
 
@@ -262,8 +271,8 @@ def lora_kv4_attn(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, c
     width, row = _table(block_table, R)
     if q.shape[2] != cache.head_dim:
         raise ValueError("lora_kv4_attn: q and the cache have the same head dimension")
-    _check(_lib().lora_kv4_attn(a, cache.packed, block_table.data_ptr(), width, row, _ints(kv_len, R, "kv_len"), ws.addr,
-                                ws.nbytes, _stream(q, stream)), "lora_kv4_attn")
+    _check(_lib().lora_kv4_attn(a, cache.packed, block_table.data_ptr(), width, row, _ints(kv_len, R, "kv_len"),
+                                ws.unpack_tokens, ws.addr, ws.nbytes, _stream(q, stream)), "lora_kv4_attn")
     return o
 
 
