@@ -149,9 +149,10 @@ size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t
  * (LORA_DEV_BAD_PAGE).
  *
  * unpack_tokens: keys and values that the workspace has room for in bf16 (0: none).
- * In steps with chunks of prompts, requests of more than 64 rows (new tokens times
- * heads / kv_heads), in order as long as they fit, are unpacked there and go through
- * lora_attn_paged's kernel: 512 tokens over 8000 take a third of the time so.  A
+ * In steps with chunks of prompts, requests of more than 96 rows (new tokens times
+ * heads / kv_heads; 160 for a head_dim up to 64), in order as long as they fit, are
+ * unpacked there and go through lora_attn_paged's kernel: 512 tokens over 8000 take a third
+ * of the time so.  A
  * multiple of 128 up to 2^24 (others are rounded down); the tokens are those of the cache that such
  * requests attend over, each request's rounded up to 128.
  */

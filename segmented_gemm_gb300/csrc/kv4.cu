@@ -36,11 +36,12 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
     return r;
 }
 
-// x * inv to a multiple of 2^-12 (for |x * inv| < 1024; a larger one keeps what precision there is)
+// x * inv to a multiple of 2^-12 (for |x * inv| < 1024; a larger one keeps what precision there is), with the
+// sign of x where that is 0 (of 0 itself a positive one)
 __device__ __forceinline__ float rounded_product(float x, float inv)
 {
     constexpr float kRound = 3072.f;   // fp32 numbers near it are 2^-12 apart
-    return __fadd_rn(__fmaf_rn(x, inv, kRound), -kRound);
+    return copysignf(__fadd_rn(__fmaf_rn(x, inv, kRound), -kRound), __fadd_rn(x, 0.f));
 }
 
 // 16 bf16 elements -> 16 codes (8 bytes) and the scale byte.

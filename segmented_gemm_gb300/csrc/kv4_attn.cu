@@ -180,7 +180,7 @@ struct Smem {
     static constexpr int kPad = DP + 4;                                  // floats from a column of results to the next
     static constexpr int kTile = Kv4Tile<DP>::kBytes;
     static constexpr int kSlot = NC * kPad * 4;                          // a piece's results
-    static constexpr int kStages = NT == 4 ? 4 : NT == 2 ? (DP == 128 ? 2 : 4) : (DP == 128 ? 3 : 4);   // of a warp's ring
+    static constexpr int kStages = DP == 128 ? 3 : 4;   // of a warp's ring
     static constexpr int kRing = kStages * kBatch * kTile;
     static_assert(kRing >= kSlot, "a warp's last piece takes its ring's place");
     static constexpr int kQ = kWarps * kRing;                            // [kWarps][NT][DP / 16][32] uint2
@@ -192,13 +192,12 @@ struct Smem {
     static constexpr int kBars = kPieces + 2 * kWarps * static_cast<int>(sizeof(Pieces<NC>));   // [kWarps][kStages]
     static constexpr int kMisc = kBars + kWarps * kStages * 8;           // scan, flags
     static constexpr int kTotal = kMisc + 32 * 8 + 32;
-    static constexpr int kCtas = NT == 4 ? 1 : 2;                        // of an SM
 };
 
 enum { kHasFirst = 1, kFirstGoesOn = 2, kHasLast = 4, kFirstInRing = 8 };   // a warp's pieces of cut groups
 
 template <int DP, int NT>
-__global__ void __launch_bounds__(kThreads, (Smem<DP, NT>::kCtas)) kv4_attn_kernel(const Kv4AttnParams p)
+__global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnParams p)
 {
     pdl_launch_dependents();
     using S = Smem<DP, NT>;
@@ -723,25 +722,26 @@ cudaError_t launch_variant(const Kv4AttnParams &p, cudaStream_t stream)
 {
     using S = Smem<DP, NT>;
     constexpr int smem = S::kTotal;
-    static_assert(S::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
     const cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t ctas = S::kCtas * static_cast<int64_t>(num_sms_current_device());
+    int64_t ctas = 2 * static_cast<int64_t>(num_sms_current_device());
     ctas = ctas < kKv4MaxCtas ? ctas : kKv4MaxCtas;
     return launch_pdl(kv4_attn_kernel<DP, NT>, ctas, kThreads, smem, p, stream);
 }
 
 }  // namespace
 
-// Columns of a block: as many as an average request has rows.
+// Blocks of 8 columns: a request of more rows has several, which read its tiles again (from L2)
+// and unpack them again, but 8 more columns of a block would take as long on the matrix
+// units as that, and the registers of a second CTA an SM: 48 requests of up to 5 tokens of 28/4 heads
+// over 300 to 6000 take 54 us so, 61 with 16 columns, 87 with 32; 64 requests of 16 rows 118 and
+// 106.  With a head dimension of 64 the registers are there: 8 requests of 64 rows 65 us, 53 with 16.
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream)
 {
-    const int64_t rows = (static_cast<int64_t>(p.T) * p.group + p.R - 1) / p.R;
-    if (p.head_dim <= 64)
-        return rows <= 8 ? launch_variant<64, 1>(p, stream) : rows <= 16 ? launch_variant<64, 2>(p, stream)
-                                                                        : launch_variant<64, 4>(p, stream);
-    return rows <= 8 ? launch_variant<128, 1>(p, stream) : rows <= 16 ? launch_variant<128, 2>(p, stream)
-                                                                     : launch_variant<128, 4>(p, stream);
+    if (p.head_dim > 64) return launch_variant<128, 1>(p, stream);
+    return static_cast<int64_t>(p.T) * p.group <= 8 * static_cast<int64_t>(p.R) ? launch_variant<64, 1>(p, stream)
+                                                                              : launch_variant<64, 2>(p, stream);
 }
 
 }  // namespace lora

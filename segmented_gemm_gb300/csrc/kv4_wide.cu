@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
     int bad = 0;
     // pages in the low half, requests in the high one
     auto need = [&](const Kv4Request &q) {
-        const bool wide = static_cast<int64_t>(q.n) * p.group > kKv4WideRows && q.keys > 0;
+        const bool wide = static_cast<int64_t>(q.n) * p.group > kv4_wide_rows(p.head_dim) && q.keys > 0;
         return wide ? (int64_t(1) << 32) + (q.keys + kKv4WidePage - 1) / kKv4WidePage : int64_t(0);
     };
     int64_t sum = 0, total;

@@ -38,9 +38,10 @@ static int check_cache4(const lora_kv4_cache_t *c)
 
 // Whether a step of T tokens of R requests is likely to have wide ones that are worth the launches they
 // need (12 us): many rows a request, or many beyond one token each.
-static bool maybe_wide(int64_t T, int32_t R, int32_t group)
+static bool maybe_wide(int64_t T, int32_t R, int32_t group, int32_t head_dim)
 {
-    return T * group > static_cast<int64_t>(R) * kKv4WideRows / 2 || (T - R) * group >= 16 * kKv4WideRows;
+    const int64_t rows = kv4_wide_rows(head_dim);
+    return T * group > R * rows || (T - R) * group >= 16 * rows;
 }
 
 static bool unpack_ok(int64_t tokens) { return tokens >= 0 && tokens <= (int64_t(1) << 24); }
@@ -59,13 +60,12 @@ static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_head
     L.zeros = take(kv4_tile_bytes(128));
     // wide requests: no more than the rows allow, or than lists have places
     L.max_wide = static_cast<int32_t>(
-        std::min<int64_t>({R, T * (heads / kv_heads) / (kKv4WideRows + 1), LORA_MAX_REQUESTS / 2 - 1}));
+        std::min<int64_t>({R, T * (heads / kv_heads) / (kv4_wide_rows(head_dim) + 1), LORA_MAX_REQUESTS / 2 - 1}));
     L.pages = static_cast<int32_t>(unpack / kKv4WidePage);
     if (L.max_wide == 0 || L.pages == 0) L.max_wide = L.pages = 0;
     L.attn_bytes = lora_attn_workspace_size(T, 2 * L.max_wide + 1, heads, kv_heads, head_dim);
     L.attn = take(L.max_wide ? L.attn_bytes : ACNT_WORDS * 4);
-    // as many warps, and as many columns of CTAs, as the narrowest blocks have; wider ones have fewer CTAs
-    const size_t dp = kv4_padded(head_dim), columns = static_cast<size_t>(kAttnMaxCtas) * 32;
+    const size_t dp = kv4_padded(head_dim), columns = static_cast<size_t>(kKv4MaxCtas) * (dp == 64 ? 16 : 8);
     L.first = take(8 * columns * (dp + 4) * 4);
     L.part = take(2 * columns * dp * 4);
     L.part_ml = take(2 * columns * 8);
@@ -100,8 +100,7 @@ static PagesLayout pages_layout(int32_t num_pages)
 
 static bool num_pages_ok(int32_t n) { return n > 0 && n < (1 << 28); }
 
-// The checks of a lora_kv_pages_t, and the parameters that all calls share.
-static int prepare_pages(const lora_kv_pages_t *a, void *ws, size_t ws_bytes, KvPagesParams *p)
+static int check_pages(const lora_kv_pages_t *a)
 {
     if (!a) return LORA_ERR_NULL;
     if (!page_size_ok(a->page_size, 8) || !num_pages_ok(a->num_pages) ||
@@ -113,7 +112,12 @@ static int prepare_pages(const lora_kv_pages_t *a, void *ws, size_t ws_bytes, Kv
     if (a->num_rows > 1 && a->table_stride < a->table_width) return LORA_ERR_SHAPE;
     if (!a->ref || !a->free_head || (a->num_free > 0 && !a->free_pages)) return LORA_ERR_NULL;
     if (a->num_rows > 0 && (!a->ctx_len || (a->table_width > 0 && !a->block_table))) return LORA_ERR_NULL;
-    if (!ints_aligned({a->block_table, a->ctx_len, a->ref, a->free_pages, a->free_head})) return LORA_ERR_ALIGN;
+    return ints_aligned({a->block_table, a->ctx_len, a->ref, a->free_pages, a->free_head}) ? LORA_OK : LORA_ERR_ALIGN;
+}
+
+// The workspace, and the parameters that all calls on pages share.
+static int prepare_pages(const lora_kv_pages_t *a, void *ws, size_t ws_bytes, KvPagesParams *p)
+{
     const PagesLayout L = pages_layout(a->num_pages);
     const int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
@@ -326,7 +330,7 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     p.wait_cycles = tc_wait_cycles();
     p.wide = nullptr;
     p.wide_status = nullptr;
-    if (L.max_wide && maybe_wide(p.T, p.R, p.group)) {   // the wide requests, by the attention over a bf16 cache; then the others
+    if (L.max_wide && maybe_wide(p.T, p.R, p.group, p.head_dim)) {   // the wide requests, by the attention over a bf16 cache; then the others
         Kv4WideParams w;
         w.cu = at<int32_t>(ws, L.cu);
         w.kv_len = at<int32_t>(ws, L.kv_len);
@@ -361,13 +365,15 @@ extern "C" size_t lora_kv_pages_workspace_size(int32_t num_pages)
 extern "C" int lora_kv_release(const lora_kv_pages_t *pages, const int32_t *rows, int32_t num, void *ws, size_t ws_bytes,
                                lora_stream_t stream)
 {
-    KvPagesParams p;
-    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    int rc = check_pages(pages);
     if (rc) return rc;
     if (num < 0 || num > LORA_MAX_REQUESTS) return LORA_ERR_SHAPE;
     if (num == 0) return LORA_OK;
     if (!rows) return LORA_ERR_NULL;
     if (!aligned(rows, 4)) return LORA_ERR_ALIGN;
+    KvPagesParams p;
+    rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
     p.rows = rows;
     p.num = num;
     return launched(launch_kv_release(p, static_cast<cudaStream_t>(stream)));
@@ -376,13 +382,15 @@ extern "C" int lora_kv_release(const lora_kv_pages_t *pages, const int32_t *rows
 extern "C" int lora_kv_fork(const lora_kv_pages_t *pages, const int32_t *parent, const int32_t *child, int32_t num,
                             int32_t *copy_src, int32_t *copy_dst, void *ws, size_t ws_bytes, lora_stream_t stream)
 {
-    KvPagesParams p;
-    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    int rc = check_pages(pages);
     if (rc) return rc;
     if (num < 0 || num > LORA_MAX_REQUESTS) return LORA_ERR_SHAPE;
     if (num == 0) return LORA_OK;
     if (!parent || !child || !copy_src || !copy_dst) return LORA_ERR_NULL;
     if (!ints_aligned({parent, child, copy_src, copy_dst})) return LORA_ERR_ALIGN;
+    KvPagesParams p;
+    rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
     p.parent = parent;
     p.child = child;
     p.num = num;
@@ -395,12 +403,14 @@ extern "C" int lora_kv_compact(const lora_kv_pages_t *pages, int32_t limit, int3
                                int32_t max_copies, int32_t *table_out, int32_t *ref_out, int32_t *free_out,
                                int32_t *head_out, void *ws, size_t ws_bytes, lora_stream_t stream)
 {
-    KvPagesParams p;
-    const int rc = prepare_pages(pages, ws, ws_bytes, &p);
+    int rc = check_pages(pages);
     if (rc) return rc;
     if (limit < 0 || max_copies < 0) return LORA_ERR_SHAPE;
     if (max_copies > 0 && (!copy_src || !copy_dst)) return LORA_ERR_NULL;
     if (!ints_aligned({copy_src, copy_dst, table_out, ref_out, free_out, head_out})) return LORA_ERR_ALIGN;
+    KvPagesParams p;
+    rc = prepare_pages(pages, ws, ws_bytes, &p);
+    if (rc) return rc;
     p.limit = limit;
     p.max_copies = max_copies;
     p.src = copy_src;

@@ -47,7 +47,7 @@ struct Kv4LoadParams {
     int32_t *status;
 };
 
-constexpr int kKv4MaxCtas = 3 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
+constexpr int kKv4MaxCtas = 2 * kAttnMaxCtas;   // upper bound on the 4-bit attention's grid
 
 // Workspace of the 4-bit attention (offsets 256-byte aligned).  In front, at the same places in
 // every call's layout, what is zero at rest: the status word and the arrival counters of
@@ -61,7 +61,10 @@ struct Kv4Layout {
 };
 constexpr int kKv4CntGroup = 32;                // first arrival counter; one for each CTA
 constexpr int kKv4WidePage = 128;               // keys of a page of the unpacked cache
-constexpr int kKv4WideRows = 64;                // most rows (tokens times a group's heads) of a request that is not wide
+// Most rows (tokens times a group's heads) of a request that is not wide.  8 requests over 1000 to 8000 take, 32/8
+// heads of 128, with 64, 96 and 128 rows each 71, 97 and 124 us by blocks of 8 columns, 99, 103 and 108
+// unpacked; with heads of 64, 64, 128 and 256 rows: 37, 61 and 106, and 68, 71 and 89.
+constexpr int kv4_wide_rows(int head_dim) { return head_dim <= 64 ? 160 : 96; }
 
 struct Kv4AttnParams {
     const uint16_t *q;
