@@ -2,6 +2,7 @@
 // and lora_kv4_load.
 #include <cuda_runtime.h>
 
+#include "attn_ptx.cuh"
 #include "kv4.cuh"
 #include "kv_ops.h"
 #include "internal.h"
@@ -28,32 +29,41 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// Two codes, the first in the low half of the byte; nearest, ties to even, saturating.
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+// Eight codes of four pairs of fp32, the first in the lowest bits; nearest, ties to even, saturating.
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&y)[4])
 {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .f32 lo, hi;\n\t"
+        "mov.b64 {lo, hi}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, hi, lo;\n\t"
+        "mov.b64 {lo, hi}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, hi, lo;\n\t"
+        "mov.b64 {lo, hi}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, hi, lo;\n\t"
+        "mov.b64 {lo, hi}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, hi, lo;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "l"(y[0]), "l"(y[1]), "l"(y[2]), "l"(y[3]));
     return r;
 }
 
-// x * inv to a multiple of 2^-12 (for |x * inv| < 1024; a larger one keeps what precision there is), with the
-// sign of x where that is 0 (of 0 itself a positive one)
-__device__ __forceinline__ float rounded_product(float x, float inv)
+// For two elements x (bf16): x * inv to a multiple of 2^-12 (for |x * inv| < 1024; a larger one keeps what precision
+// there is), with the sign of x where that is 0 (of 0 itself a positive one).
+__device__ __forceinline__ uint64_t rounded_products(uint32_t x, uint64_t inv)
 {
     constexpr float kRound = 3072.f;   // fp32 numbers near it are 2^-12 apart
-    return copysignf(__fadd_rn(__fmaf_rn(x, inv, kRound), -kRound), __fadd_rn(x, 0.f));
+    const uint64_t x2 = pack_f2(bf16_lo(x), bf16_hi(x)), y2 = add_f2(fma_f2(x2, inv, pack_f2(kRound, kRound)), pack_f2(-kRound, -kRound));
+    float x0, x1, y0, y1;
+    unpack_f2(add_f2(x2, 0), x0, x1);  // -0 becomes 0
+    unpack_f2(y2, y0, y1);
+    return pack_f2(copysignf(y0, x0), copysignf(y1, x1));
 }
 
 // 16 bf16 elements -> 16 codes (8 bytes) and the scale byte.
 __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint32_t *scale)
 {
     const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-    uint32_t top = 0;   // the largest magnitude's bits order as the magnitudes do, NaN above all
+    uint32_t top2 = 0;   // the largest magnitudes' bits, which order as the magnitudes do, NaN above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        top = max(top, w[i] & 0x7FFF0000u);
-        top = max(top, (w[i] << 16) & 0x7FFF0000u);
-    }
+    for (int i = 0; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[i] & 0x7FFF7FFFu));
+    const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16) << 16;
     if (top > 0x7F800000u) {
         *scale = 0xFF;
         return make_uint2(0, 0);
@@ -67,13 +77,29 @@ __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint
     // other one is at least 2^-8 (relative) from there, x having 8 and half * s 7
     // significant bits, and stays on its side.
     const float inv = __frcp_rn(scale_value(b));
-    uint32_t c[2] = {0, 0};
+    const uint64_t inv2 = pack_f2(inv, inv);
+    uint32_t c[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t two = e2m1_pair(rounded_product(bf16_lo(w[i]), inv), rounded_product(bf16_hi(w[i]), inv));
-        c[i / 4] |= two << (8 * (i % 4));
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t y[4] = {rounded_products(w[4 * i], inv2), rounded_products(w[4 * i + 1], inv2),
+                               rounded_products(w[4 * i + 2], inv2), rounded_products(w[4 * i + 3], inv2)};
+        c[i] = e2m1x8(y);
     }
     return make_uint2(c[0], c[1]);
+}
+
+// 32 bytes at once, a whole sector, where rows start on 32 bytes and are whole groups.
+__device__ __forceinline__ void load32(const uint16_t *from, uint4 (&x)[2])
+{
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
+                 : "l"(from));
+}
+__device__ __forceinline__ void store32(uint16_t *to, const uint4 &a, const uint4 &b)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
 }
 
 // A thread takes 16 elements of a head's key row and of its value row, consecutive
@@ -93,12 +119,19 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_store_kernel(const Kv4StorePa
         const int u = static_cast<int>(i - t * per), h = u / Tile::kGroups, g = u % Tile::kGroups;
         const int32_t slot = p.slot_map[t];
         uint4 k[2] = {}, v[2] = {};
+        const uint16_t *kr = p.k + t * p.k_tok + h * p.k_head + 16 * g, *vr = p.v + t * p.v_tok + h * p.v_head + 16 * g;
+        if (p.sectors) {
+            if (16 * g < p.head_dim) {
+                load32(kr, k);
+                load32(vr, v);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int d = 16 * g + 8 * e;
-            if (d >= p.head_dim) continue;   // padding
-            k[e] = *reinterpret_cast<const uint4 *>(p.k + t * p.k_tok + h * p.k_head + d);
-            v[e] = *reinterpret_cast<const uint4 *>(p.v + t * p.v_tok + h * p.v_head + d);
+            for (int e = 0; e < 2; ++e) {
+                if (16 * g + 8 * e >= p.head_dim) continue;   // padding
+                k[e] = *reinterpret_cast<const uint4 *>(kr + 8 * e);
+                v[e] = *reinterpret_cast<const uint4 *>(vr + 8 * e);
+            }
         }
         if (slot < 0 || slot >= p.slots) {
             bad |= slot != -1;
@@ -149,15 +182,18 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_load_kernel(const Kv4LoadPara
             vs = tile[Tile::value_scale(j, g)];
         }
         const bool second = 16 * g + 8 < p.head_dim;
-        if (p.k) {
-            uint16_t *k = p.k + t * p.k_tok + h * p.k_head + 16 * g;
-            *reinterpret_cast<uint4 *>(k) = kv4_values(kw.x, ks);
-            if (second) *reinterpret_cast<uint4 *>(k + 8) = kv4_values(kw.y, ks);
-        }
-        if (p.v) {
-            uint16_t *v = p.v + t * p.v_tok + h * p.v_head + 16 * g;
-            *reinterpret_cast<uint4 *>(v) = kv4_values(vw.x, vs);
-            if (second) *reinterpret_cast<uint4 *>(v + 8) = kv4_values(vw.y, vs);
+        uint16_t *const rows[2] = {p.k ? p.k + t * p.k_tok + h * p.k_head + 16 * g : nullptr,
+                                   p.v ? p.v + t * p.v_tok + h * p.v_head + 16 * g : nullptr};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (!rows[e]) continue;
+            const uint4 lo = kv4_values(e ? vw.x : kw.x, e ? vs : ks), hi = kv4_values(e ? vw.y : kw.y, e ? vs : ks);
+            if (p.sectors) {
+                store32(rows[e], lo, hi);
+            } else {
+                *reinterpret_cast<uint4 *>(rows[e]) = lo;
+                if (second) *reinterpret_cast<uint4 *>(rows[e] + 8) = hi;
+            }
         }
     }
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);

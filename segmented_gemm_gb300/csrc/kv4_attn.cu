@@ -635,14 +635,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
                 make_uint2(pack_bf16x2(v.x * by, v.y * by), pack_bf16x2(v.z * by, v.w * by));
         if (d == 0 && p.lse) store_lse(t, h, top, sum);
     };
-    auto add = [](float4 &v, float &top, float &sum, float4 y, float2 x) {
-        const float next = fmaxf(top, x.x), by = exp2_approx(top - next), by2 = exp2_approx(x.x - next);
-        top = next;
-        sum = sum * by + x.y * by2;
-        v.x = v.x * by + y.x * by2;
-        v.y = v.y * by + y.y * by2;
-        v.z = v.z * by + y.z * by2;
-        v.w = v.w * by + y.w * by2;
+    auto add = [](float4 &v, float &sum, float top, float4 y, float2 x) {
+        const float by = exp2_approx(x.x - top);
+        sum += x.y * by;
+        v.x += y.x * by;
+        v.y += y.y * by;
+        v.z += y.z * by;
+        v.w += y.w * by;
     };
     const uint32_t marks = *cuts;
     int shared_groups = 0, tail = 0;   // bit 0: with the CTA before, bit 1: with the CTA after, by this warp's last piece
@@ -662,15 +661,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         for (int u = tid; u < kUnits; u += kThreads) {
             const int n = u / (DP / 4), d = u % (DP / 4) * 4;
             if (n >= gr.cols) break;
+            // the largest m first: then the pieces' loads and factors do not wait for one another
             float top = kNone, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w >= 0) top = ml[(kWarps + w) * NC + n].x;
+            for (int i = w + 1; i <= to; ++i) top = fmaxf(top, ml[i * NC + n].x);
             if (w >= 0)
-                add(v, top, sum, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm + w * S::kRing) + n * S::kPad + d),
+                add(v, sum, top, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm + w * S::kRing) + n * S::kPad + d),
                     ml[(kWarps + w) * NC + n]);
             for (int i = w + 1; i <= to; ++i) {
                 const float *from = marks >> (4 * i) & kFirstInRing ? reinterpret_cast<const float *>(sm + i * S::kRing)
-                                                            : p.first + static_cast<int64_t>(cta * kWarps + i) * NC * S::kPad;
-                add(v, top, sum, *reinterpret_cast<const float4 *>(from + n * S::kPad + d), ml[i * NC + n]);
+                                                                    : p.first + static_cast<int64_t>(cta * kWarps + i) * NC * S::kPad;
+                add(v, sum, top, *reinterpret_cast<const float4 *>(from + n * S::kPad + d), ml[i * NC + n]);
             }
             if (whole) {
                 store(gr, n, d, v, top, sum);
@@ -681,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         }
     }
     if (!shared_groups) return;
-    // the CTA that stores the last part of a group joins them, in their order
-    __threadfence();
+    // the CTA that stores the last part of a group joins them, in their order (the barrier
+    // and the release behind it put every thread's part before the count)
     __syncthreads();
     if (tid < 2 && (shared_groups >> tid & 1)) {
         const Group &gr = groups[tid == 0 ? 0 : tail];
@@ -697,7 +699,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         if (!(shared_groups >> which & 1) || !joins[3 * which]) continue;
-        __threadfence();
         const Group gr = groups[which == 0 ? 0 : tail];
         const int c0 = joins[3 * which + 1], c1 = joins[3 * which + 2];
 #pragma unroll 1
@@ -706,11 +707,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
             if (n >= gr.cols) break;
             float top = kNone, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            // (two passes would cost a second round trip to L2)
 #pragma unroll 4
             for (int i = c0; i <= c1; ++i) {
                 const int64_t part = 2 * i + (i == c0);
-                add(v, top, sum, __ldcg(reinterpret_cast<const float4 *>(p.part + (part * NC + n) * DP + d)),
-                    __ldcg(p.part_ml + part * NC + n));
+                const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + (part * NC + n) * DP + d));
+                const float2 x = __ldcg(p.part_ml + part * NC + n);
+                const float next = fmaxf(top, x.x), by = exp2_approx(top - next);
+                sum *= by;
+                v = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+                top = next;
+                add(v, sum, top, y, x);
             }
             store(gr, n, d, v, top, sum);
         }

@@ -25,6 +25,12 @@ static bool kv4_stride_ok(int64_t s, int64_t extent)
     return extent <= 1 || (s > 0 && s % 16 == 0 && s < (int64_t(1) << 36));
 }
 
+// Whether groups of 16 elements of every row start on 32 bytes, and none is half a group.
+static bool whole_sectors(const void *base, int64_t token, int64_t tokens, int64_t head, int32_t heads, int32_t head_dim)
+{
+    return aligned(base, 32) && head_dim % 16 == 0 && (tokens == 1 || token % 16 == 0) && (heads == 1 || head % 16 == 0);
+}
+
 static int check_cache4(const lora_kv4_cache_t *c)
 {
     if (!c || !c->data) return LORA_ERR_NULL;
@@ -229,6 +235,8 @@ extern "C" int lora_kv4_store(const lora_bf16_t *k, const lora_bf16_t *v, int64_
     p.page_shift = page_shift(cache->page_size);
     p.kv_heads = cache->kv_heads;
     p.head_dim = cache->head_dim;
+    p.sectors = whole_sectors(k, k_token_stride, num_tokens, k_head_stride, cache->kv_heads, cache->head_dim) &&
+                whole_sectors(v, v_token_stride, num_tokens, v_head_stride, cache->kv_heads, cache->head_dim);
     p.T = num_tokens;
     p.slot_map = slot_map;
     p.status = at<int32_t>(ws, 0) + CNT_STATUS;
@@ -264,6 +272,8 @@ extern "C" int lora_kv4_load(const lora_kv4_cache_t *cache, const int32_t *slots
     p.page_shift = page_shift(cache->page_size);
     p.kv_heads = cache->kv_heads;
     p.head_dim = cache->head_dim;
+    p.sectors = whole_sectors(k, k_token_stride, num_slots, k_head_stride, cache->kv_heads, cache->head_dim) &&
+                whole_sectors(v, v_token_stride, num_slots, v_head_stride, cache->kv_heads, cache->head_dim);
     p.n = num_slots;
     p.slot_list = slots;
     p.status = at<int32_t>(ws, 0) + CNT_STATUS;

@@ -30,6 +30,7 @@ struct Kv4StoreParams {
     int64_t page_stride, head_stride;
     int64_t slots;
     int32_t page_shift, kv_heads, head_dim;
+    int32_t sectors;                         // groups of 16 elements start on 32 bytes
     int64_t T;
     const int32_t *slot_map;
     int32_t *status;
@@ -42,6 +43,7 @@ struct Kv4LoadParams {
     int64_t page_stride, head_stride;
     int64_t slots;
     int32_t page_shift, kv_heads, head_dim;
+    int32_t sectors;
     int64_t n;
     const int32_t *slot_list;
     int32_t *status;

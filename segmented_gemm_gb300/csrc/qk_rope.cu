@@ -2,6 +2,7 @@
 // the rotation by position, and the keys' and values' way into the paged cache.
 #include <cuda_runtime.h>
 
+#include "attn_ptx.cuh"
 #include "kv_ops.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -50,30 +51,11 @@ __device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos)
     return r;
 }
 
-// Two fp32 at a time.
-__device__ __forceinline__ uint64_t both(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t widen2(uint32_t v) { return both(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ uint64_t widen2(uint32_t v) { return pack_f2(bf16_lo(v), bf16_hi(v)); }
 __device__ __forceinline__ uint32_t narrow2(uint64_t v)
 {
     float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    unpack_f2(v, lo, hi);
     return pack_bf16x2(lo, hi);
 }
 
@@ -171,7 +153,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
         const bool weighted = w.on && w.weight;
         uint64_t wt[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wt[j] = both(1.f, 1.f);
+        for (int j = 0; j < 4; ++j) wt[j] = pack_f2(1.f, 1.f);
         if (weighted) {
             const uint2 w0 = *reinterpret_cast<const uint2 *>(w.weight + off0), w1 = *reinterpret_cast<const uint2 *>(w.weight + off1);
             wt[0] = widen2(w0.x);
@@ -189,9 +171,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const uint64_t y0 = widen2(x[i][0].x), y1 = widen2(x[i][0].y), y2 = widen2(x[i][1].x), y3 = widen2(x[i][1].y);
-                    const uint64_t s2 = fma2(y3, y3, fma2(y2, y2, fma2(y1, y1, mul2(y0, y0))));
+                    const uint64_t s2 = fma_f2(y3, y3, fma_f2(y2, y2, fma_f2(y1, y1, mul_f2(y0, y0))));
                     float s0, s1;
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s2));
+                    unpack_f2(s2, s0, s1);
                     f[i] = s0 + s1;
                 }
 #pragma unroll
@@ -206,25 +188,25 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
                 const int tok = i0 + i;
                 uint64_t y[4] = {widen2(x[i][0].x), widen2(x[i][0].y), widen2(x[i][1].x), widen2(x[i][1].y)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(y[j], wt[j]), both(f[i], f[i]));
+                for (int j = 0; j < 4; ++j) y[j] = mul_f2(mul_f2(y[j], wt[j]), pack_f2(f[i], f[i]));
                 const float4 c = *reinterpret_cast<const float4 *>(turn[tok][lane][0]);
                 const float4 s = *reinterpret_cast<const float4 *>(turn[tok][lane][1]);
                 if (!INTERLEAVED) {   // pairs (y[0], y[2]) and (y[1], y[3])
-                    const uint64_t c2[2] = {both(c.x, c.y), both(c.z, c.w)}, s2[2] = {both(s.x, s.y), both(s.z, s.w)};
-                    const uint64_t n2[2] = {both(-s.x, -s.y), both(-s.z, -s.w)};
+                    const uint64_t c2[2] = {pack_f2(c.x, c.y), pack_f2(c.z, c.w)}, s2[2] = {pack_f2(s.x, s.y), pack_f2(s.z, s.w)};
+                    const uint64_t n2[2] = {pack_f2(-s.x, -s.y), pack_f2(-s.z, -s.w)};
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint64_t u = y[j], v = y[2 + j];
-                        y[j] = fma2(v, n2[j], mul2(u, c2[j]));
-                        y[2 + j] = fma2(u, s2[j], mul2(v, c2[j]));
+                        y[j] = fma_f2(v, n2[j], mul_f2(u, c2[j]));
+                        y[2 + j] = fma_f2(u, s2[j], mul_f2(v, c2[j]));
                     }
                 } else {              // each y[j] is a pair
                     const float cf[4] = {c.x, c.y, c.z, c.w}, sf[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float u, v;
-                        asm("mov.b64 {%0, %1}, %2;" : "=f"(u), "=f"(v) : "l"(y[j]));
-                        y[j] = both(fmaf(v, -sf[j], u * cf[j]), fmaf(u, sf[j], v * cf[j]));
+                        unpack_f2(y[j], u, v);
+                        y[j] = pack_f2(fmaf(v, -sf[j], u * cf[j]), fmaf(u, sf[j], v * cf[j]));
                     }
                 }
                 uint2 o0 = x[i][0], o1 = x[i][1];   // values are copied as they are
