@@ -141,6 +141,69 @@ __global__ void __launch_bounds__(kThreads) release_list_kernel(const KvPagesPar
     }
 }
 
+// For caches of up to kSmallPages one CTA counts and lists, 32 pages a thread; and takes the rows before, a
+// warp each, where these are few (ROWS): one launch.  8 rows of 49 pages 4 us so, 192 of up to 94
+// pages 15, 10 by a launch of their own for the rows.
+constexpr int kSmallThreads = 1024, kSmallPages = 32 * kSmallThreads, kSmallEntries = 4096;
+
+template <bool ROWS>
+__global__ void __launch_bounds__(kSmallThreads) release_small_kernel(const KvPagesParams p)
+{
+    pdl_launch_dependents();
+    __shared__ uint32_t named[LORA_MAX_REQUESTS / 32];
+    __shared__ int64_t scan[32];
+    const lora_kv_pages_t &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (ROWS)
+        for (int i = tid; i < LORA_MAX_REQUESTS / 32; i += kSmallThreads) named[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    const int head0 = *a.free_head, head = max(0, min(head0, a.num_free));
+    int flags = head != head0 ? LORA_DEV_BAD_LENGTH : 0;
+    for (int i = ROWS ? tid >> 5 : p.num; i < p.num; i += kSmallThreads / 32) {
+        const int r = p.rows[i];
+        bool skip = r < 0 || r >= a.num_rows;
+        if (!skip) {
+            uint32_t old = 0;
+            if (lane == 0) old = atomicOr(named + r / 32, 1u << (r % 32));
+            skip = __shfl_sync(0xffffffffu, old, 0) >> (r % 32) & 1;   // by another i; which one does not matter
+        }
+        if (skip) {
+            flags |= LORA_DEV_BAD_ROW;
+            continue;
+        }
+        const int n = held_pages(a, a.ctx_len[r], &flags);
+        for (int j = lane; j < n; j += 32) {
+            const int page = a.block_table[r * a.table_stride + j];
+            if (page >= 0 && page < a.num_pages) atomicSub(a.ref + page, 1);
+            else flags |= LORA_DEV_BAD_PAGE;
+        }
+        __syncwarp();
+        if (lane == 0) a.ctx_len[r] = 0;
+    }
+    __syncthreads();
+    const int each = (a.num_pages + kSmallThreads - 1) / kSmallThreads, base = tid * each;
+    uint32_t freed = 0;
+#pragma unroll 8
+    for (int i = 0; i < each; ++i)
+        if (base + i < a.num_pages && __ldcg(a.ref + base + i) < 0) freed |= 1u << i;
+    int64_t total;
+    const int64_t before = block_scan_i64(__popc(freed), scan, &total);
+    const int first = max(0, head - static_cast<int>(total));
+    int at = first + static_cast<int>(before);
+    for (; freed; freed &= freed - 1) {
+        const int page = base + __ffs(freed) - 1;
+        a.ref[page] = 0;
+        if (at < head) a.free_pages[at] = page;
+        ++at;
+    }
+    if (tid == 0) {
+        *a.free_head = first;
+        if (total > head) flags |= LORA_DEV_NO_PAGE;
+    }
+    if (flags) atomicOr(p.counters, flags);
+}
+
 // ---------------------------------------------------------------------------
 // lora_kv_fork
 // ---------------------------------------------------------------------------
@@ -394,6 +457,90 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
     if (gid == 0) *p.head_out = first;
 }
 
+// The same in one launch, for small caches with few entries: one CTA, 32 pages a thread as bits.  94 pages of 5
+// rows 6 us so, 10 by four launches; 7554 pages of 90 rows 15 and 12.
+__global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const KvPagesParams p)
+{
+    pdl_launch_dependents();
+    __shared__ uint32_t used[kSmallThreads], free[kSmallThreads];   // a bit a page; then `used` the movers
+    __shared__ int before[kSmallThreads];                           // movers in the words before
+    __shared__ int64_t scan[32];
+    const lora_kv_pages_t &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    used[tid] = free[tid] = 0;
+    __syncthreads();
+    pdl_wait();
+    const int head0 = *a.free_head, head = max(0, min(head0, a.num_free));
+    int flags = head != head0 ? LORA_DEV_BAD_LENGTH : 0;
+    for (int r = warp; r < a.num_rows; r += kSmallThreads / 32) {
+        const int n = held_pages(a, a.ctx_len[r], &flags);
+        for (int j = lane; j < n; j += 32) {
+            const int page = a.block_table[r * a.table_stride + j];
+            if (page >= 0 && page < a.num_pages) atomicOr(used + page / 32, 1u << (page % 32));
+            else flags |= LORA_DEV_BAD_PAGE;
+        }
+    }
+    for (int i = head + tid; i < a.num_free; i += kSmallThreads) {
+        const int page = a.free_pages[i];
+        if (page >= 0 && page < a.num_pages) atomicOr(free + page / 32, 1u << (page % 32));
+        else flags |= LORA_DEV_BAD_PAGE;
+    }
+    __syncthreads();
+    const int base = 32 * tid, below = max(0, min(32, p.limit - base));
+    const uint32_t low = below == 32 ? ~0u : (1u << below) - 1, u = used[tid], f = free[tid] & ~u;
+    if (free[tid] & u) flags |= LORA_DEV_BAD_PAGE;
+    uint32_t holes = f & low, movers = u & ~low, high = f & ~low;
+    int64_t total;
+    const int64_t at = block_scan_i64(__popc(holes) | static_cast<int64_t>(__popc(movers)) << 20 | static_cast<int64_t>(__popc(high)) << 40,
+                                      scan, &total);
+    used[tid] = movers;
+    int hole = static_cast<int>(at & 0xFFFFF), mover = static_cast<int>(at >> 20 & 0xFFFFF), up = static_cast<int>(at >> 40);
+    before[tid] = mover;
+    const int all_holes = static_cast<int>(total & 0xFFFFF), all_movers = static_cast<int>(total >> 20 & 0xFFFFF);
+    const int moved = min(min(all_holes, all_movers), p.max_copies);
+    const int first = a.num_free - all_holes - static_cast<int>(total >> 40);
+    // the list's old entries have all been read
+    for (; holes; holes &= holes - 1, ++hole) {
+        const int page = base + __ffs(holes) - 1;
+        if (hole < moved) p.dst[hole] = page;
+        else p.free_out[first + hole - moved] = page;
+    }
+    for (uint32_t left = movers | high; left; left &= left - 1) {
+        const int page = base + __ffs(left) - 1;
+        const bool moves = left & (0u - left) & movers;
+        if (moves && mover < moved) p.src[mover] = page;
+        if (!moves || mover < moved) p.free_out[first + (all_holes - moved) + up + min(mover, moved)] = page;
+        if (moves) ++mover;
+        else ++up;
+    }
+    for (int i = moved + tid; i < p.max_copies; i += kSmallThreads) p.src[i] = p.dst[i] = -1;
+    if (p.ref_out != a.ref)
+        for (int i = tid; i < a.num_pages; i += kSmallThreads) p.ref_out[i] = a.ref[i];
+    if (p.free_out != a.free_pages)
+        for (int i = tid; i < first; i += kSmallThreads) p.free_out[i] = a.free_pages[i];
+    __syncthreads();
+    for (int i = tid; i < moved; i += kSmallThreads) {
+        const int src = __ldcg(p.src + i), n = a.ref[src];
+        p.ref_out[__ldcg(p.dst + i)] = n;
+        p.ref_out[src] = 0;
+    }
+    const bool in_place = p.table_out == a.block_table;
+    for (int r = warp; r < a.num_rows; r += kSmallThreads / 32) {
+        int ignored = 0;
+        const int n = held_pages(a, a.ctx_len[r], &ignored);
+        for (int j = lane; j < (in_place ? n : a.table_width); j += 32) {
+            int page = a.block_table[r * a.table_stride + j];
+            if (j < n && page >= 0 && page < a.num_pages && used[page / 32] >> (page % 32) & 1) {
+                const int i = before[page / 32] + __popc(used[page / 32] & ((1u << (page % 32)) - 1));
+                if (i < moved) page = __ldcg(p.dst + i);
+            }
+            p.table_out[r * a.table_stride + j] = page;
+        }
+    }
+    if (tid == 0) *p.head_out = first;
+    if (flags) atomicOr(p.counters, flags);
+}
+
 // ---------------------------------------------------------------------------
 // lora_kv_copy, lora_kv4_copy
 // ---------------------------------------------------------------------------
@@ -465,7 +612,11 @@ int64_t capped(int64_t n, int64_t per_sm)
 
 cudaError_t launch_kv_release(const KvPagesParams &p, cudaStream_t stream)
 {
+    const bool small = p.a.num_pages <= kSmallPages;
+    if (small && static_cast<int64_t>(p.num) * p.a.table_width <= kSmallEntries)
+        return launch_pdl(release_small_kernel<true>, 1, kSmallThreads, 0, p, stream);
     cudaError_t e = launch_pdl(release_rows_kernel, capped(p.num, 8), kThreads, 0, p, stream);
+    if (small) return e == cudaSuccess ? launch_pdl(release_small_kernel<false>, 1, kSmallThreads, 0, p, stream) : e;
     const int chunks = (p.a.num_pages + kPageChunk - 1) / kPageChunk;
     if (e == cudaSuccess) e = launch_pdl(release_count_kernel, chunks, kThreads, 0, p, stream);
     if (e == cudaSuccess) e = launch_pdl(release_list_kernel, chunks, kThreads, 0, p, stream);
@@ -480,6 +631,8 @@ cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream)
 
 cudaError_t launch_kv_compact(const KvPagesParams &p, cudaStream_t stream)
 {
+    if (p.a.num_pages <= kSmallPages && static_cast<int64_t>(p.a.num_rows) * p.a.table_width <= kSmallEntries)
+        return launch_pdl(compact_small_kernel, 1, kSmallThreads, 0, p, stream);
     const int chunks = (p.a.num_pages + kPageChunk - 1) / kPageChunk;
     const int64_t lists = (static_cast<int64_t>(p.a.num_free) + kThreads - 1) / kThreads;
     const int64_t rows = p.a.num_rows > lists ? p.a.num_rows : lists;
