@@ -405,3 +405,26 @@ def test_the_operators_in_use(bits):
             KV.lora_kv4_copy(src, dst, cache4, wsp)
         assert ctx.tolist() == [len(h) for h in history]
         assert L.lora_get_status(ws) == 0 and L.lora_get_status(wsp) == 0 and L.lora_get_status(aws) == 0
+
+
+@pytest.mark.parametrize("cfg", [dict(rope=True), dict(bits=4), dict(rope=True, bits=4, head_dim=128, kv_heads=1, page=32)])
+def test_serving_example_runs_with_the_cache_operators(cfg):
+    from test_gpu_attn_serving import _example
+    status, errors = _example().serve(requests=4, layers=1, steps=5, **cfg)
+    assert status == 0 and all(math.isfinite(e) for e in errors)
+
+
+def test_rows_that_start_on_16_bytes_only():
+    # the cache's writes and reads take 32 bytes at once where they can
+    wide = torch.randn(20, 2, 3 * 64 + 8, device="cuda").to(BF)
+    a, b = KV.Kv4Cache.zeros(2, 2, 16, 64), KV.Kv4Cache.zeros(2, 2, 16, 64)
+    ws, slots = A.AttnWorkspace(1, 1), torch.arange(20, dtype=torch.int32, device="cuda")
+    k, v = wide[..., 8:72], wide[..., 72:136]
+    KV.lora_kv4_store(k, v, a, slots, ws)
+    KV.lora_kv4_store(k.contiguous(), v.contiguous(), b, slots, ws)
+    assert torch.equal(a.data, b.data)
+    out = torch.full_like(wide, 3.0)
+    KV.lora_kv4_load(a, slots, ws, k=out[..., 8:72], v=out[..., 136:200])
+    k1, v1 = KV.lora_kv4_load(a, slots, ws)
+    assert torch.equal(out[..., 8:72], k1) and torch.equal(out[..., 136:200], v1)
+    assert (out[..., :8] == 3).all() and (out[..., 72:136] == 3).all()
