@@ -625,7 +625,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
 
     // ---- cut groups.  A chain of pieces: the last of a warp (or, at the CTA's start, one that
     // comes from the CTA before), then the first of the warps after it as long as they go on.
-    constexpr int kUnits = NC * (DP / 4);   // four elements of a column
     auto store = [&](const Group &gr, int n, int d, float4 v, float top, float sum) {
         int h;
         const int64_t t = row_of(gr, n, &h);
@@ -644,41 +643,64 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         v.w += y.w * by;
     };
     const uint32_t marks = *cuts;
+    // bit 4 + 4w for a chain that begins with warp w's last piece, bit 0 for one with warp 0's first
+    const uint64_t begins = (static_cast<uint64_t>(marks / kHasLast & 0x11111111u) << 4) | (marks & kHasFirst);
+    const int chains = __popcll(begins);
+    // The chains side by side, some warps each: a chain is a few dependent loads, and there may be nine.
+    const int each = chains > 4 ? 1 : chains > 2 ? 2 : chains > 1 ? 4 : 8;   // warps of a chain
     int shared_groups = 0, tail = 0;   // bit 0: with the CTA before, bit 1: with the CTA after, by this warp's last piece
-    // begins: bit 4 + 4w for a chain that begins with warp w's last piece, bit 0 for one with warp 0's first
-    for (uint64_t begins = (static_cast<uint64_t>(marks / kHasLast & 0x11111111u) << 4) | (marks & kHasFirst); begins;
-         begins &= begins - 1) {
-        const int w = (__ffsll(begins) - 1) / 4 - 1;
+    int k = 0;
+    for (uint64_t left = begins; left; left &= left - 1, ++k) {
+        const int w = (__ffsll(left) - 1) / 4 - 1;
         int to = w;   // last warp of the chain
         bool goes_on = true;
         while (goes_on && to + 1 < kWarps) goes_on = marks >> (4 * ++to) & kFirstGoesOn;
-        const Group gr = groups[w < 0 ? 0 : kWarps + w];
         const bool whole = w >= 0 && !goes_on;
-        const int64_t part = 2 * cta + (w >= 0);
         if (!whole) shared_groups |= w < 0 ? 1 : 2;
         if (w >= 0) tail = kWarps + w;
+        if (k % (kWarps / each) != warp / each) continue;
+        const Group gr = groups[w < 0 ? 0 : kWarps + w];
+        const int64_t part = 2 * cta + (w >= 0);
+        constexpr int kAtOnce = 4;   // elements of four of a thread
 #pragma unroll 1
-        for (int u = tid; u < kUnits; u += kThreads) {
-            const int n = u / (DP / 4), d = u % (DP / 4) * 4;
-            if (n >= gr.cols) break;
-            // the largest m first: then the pieces' loads and factors do not wait for one another
-            float top = kNone, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w >= 0) top = ml[(kWarps + w) * NC + n].x;
-            for (int i = w + 1; i <= to; ++i) top = fmaxf(top, ml[i * NC + n].x);
-            if (w >= 0)
-                add(v, sum, top, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm + w * S::kRing) + n * S::kPad + d),
-                    ml[(kWarps + w) * NC + n]);
-            for (int i = w + 1; i <= to; ++i) {
-                const float *from = marks >> (4 * i) & kFirstInRing ? reinterpret_cast<const float *>(sm + i * S::kRing)
-                                                                    : p.first + static_cast<int64_t>(cta * kWarps + i) * NC * S::kPad;
-                add(v, sum, top, *reinterpret_cast<const float4 *>(from + n * S::kPad + d), ml[i * NC + n]);
+        for (int u0 = tid % (32 * each); u0 < gr.cols * (DP / 4); u0 += kAtOnce * 32 * each) {
+            float top[kAtOnce], sum[kAtOnce];
+            float4 v[kAtOnce];
+            int n[kAtOnce], d[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int u = min(u0 + q * 32 * each, gr.cols * (DP / 4) - 1);   // past the end: the last one again
+                n[q] = u / (DP / 4);
+                d[q] = u % (DP / 4) * 4;
+                top[q] = w >= 0 ? ml[(kWarps + w) * NC + n[q]].x : kNone;
+                sum[q] = 0.f;
+                v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (whole) {
-                store(gr, n, d, v, top, sum);
-            } else {
-                *reinterpret_cast<float4 *>(p.part + (part * NC + n) * DP + d) = v;
-                if (d == 0) p.part_ml[part * NC + n] = make_float2(top, sum);
+            // the largest m first: then the pieces' factors do not wait for one another
+            for (int i = w + 1; i <= to; ++i)
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) top[q] = fmaxf(top[q], ml[i * NC + n[q]].x);
+            for (int i = w; i <= to; ++i) {
+                if (i < 0) continue;
+                const bool last = i == w;   // the chain's first piece is its warp's last
+                const float *from = last || marks >> (4 * i) & kFirstInRing
+                                        ? reinterpret_cast<const float *>(sm + i * S::kRing)
+                                        : p.first + static_cast<int64_t>(cta * kWarps + i) * NC * S::kPad;
+                float4 y[kAtOnce];
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) y[q] = *reinterpret_cast<const float4 *>(from + n[q] * S::kPad + d[q]);
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) add(v[q], sum[q], top[q], y[q], ml[(last * kWarps + i) * NC + n[q]]);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                if (u0 + q * 32 * each >= gr.cols * (DP / 4)) continue;
+                if (whole) {
+                    store(gr, n[q], d[q], v[q], top[q], sum[q]);
+                } else {
+                    *reinterpret_cast<float4 *>(p.part + (part * NC + n[q]) * DP + d[q]) = v[q];
+                    if (d[q] == 0) p.part_ml[part * NC + n[q]] = make_float2(top[q], sum[q]);
+                }
             }
         }
     }
@@ -696,31 +718,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         if (n == c1 - c0) p.counters[kKv4CntGroup + c0] = 0;
     }
     __syncthreads();
+    // two groups side by side, half of the CTA each
+    const bool join0 = (shared_groups & 1) && joins[0], join1 = (shared_groups & 2) && joins[3];
+    if (!join0 && !join1) return;
+    const bool halves = join0 && join1;
+    const int which = halves ? warp >= kWarps / 2 : join1, threads = halves ? kThreads / 2 : kThreads;
+    const Group gr = groups[which == 0 ? 0 : tail];
+    const int c0 = joins[3 * which + 1], c1 = joins[3 * which + 2];
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        if (!(shared_groups >> which & 1) || !joins[3 * which]) continue;
-        const Group gr = groups[which == 0 ? 0 : tail];
-        const int c0 = joins[3 * which + 1], c1 = joins[3 * which + 2];
-#pragma unroll 1
-        for (int u = tid; u < kUnits; u += kThreads) {
-            const int n = u / (DP / 4), d = u % (DP / 4) * 4;
-            if (n >= gr.cols) break;
-            float top = kNone, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            // (two passes would cost a second round trip to L2)
+    for (int u = tid % threads; u < gr.cols * (DP / 4); u += threads) {
+        const int n = u / (DP / 4), d = u % (DP / 4) * 4;
+        float top = kNone, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        // (a first pass for the largest m would cost a second round trip to L2)
 #pragma unroll 4
-            for (int i = c0; i <= c1; ++i) {
-                const int64_t part = 2 * i + (i == c0);
-                const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + (part * NC + n) * DP + d));
-                const float2 x = __ldcg(p.part_ml + part * NC + n);
-                const float next = fmaxf(top, x.x), by = exp2_approx(top - next);
-                sum *= by;
-                v = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
-                top = next;
-                add(v, sum, top, y, x);
-            }
-            store(gr, n, d, v, top, sum);
+        for (int i = c0; i <= c1; ++i) {
+            const int64_t part = 2 * i + (i == c0);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + (part * NC + n) * DP + d));
+            const float2 x = __ldcg(p.part_ml + part * NC + n);
+            const float next = fmaxf(top, x.x), by = exp2_approx(top - next);
+            sum *= by;
+            v = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+            top = next;
+            add(v, sum, top, y, x);
         }
+        store(gr, n, d, v, top, sum);
     }
 }
 
