@@ -88,20 +88,6 @@ __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint
     return make_uint2(c[0], c[1]);
 }
 
-// 32 bytes at once, a whole sector, where rows start on 32 bytes and are whole groups.
-__device__ __forceinline__ void load32(const uint16_t *from, uint4 (&x)[2])
-{
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
-                 : "l"(from));
-}
-__device__ __forceinline__ void store32(uint16_t *to, const uint4 &a, const uint4 &b)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
-                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-}
-
 // A thread takes 16 elements of a head's key row and of its value row, consecutive
 // threads consecutive elements; memory bounds it.
 template <int DP>

@@ -261,9 +261,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
     bool going = false;
     if (me < warps) {
         // the thread whose requests have the first unit: the last one of a base up to there
-        static_assert(kThreads == 256, "two ballots");
-        const int j8 = (31 - __clz(__ballot_sync(0xffffffffu, bases[8 * lane] <= u0))) * 8;
-        const int j = j8 + 31 - __clz(__ballot_sync(0xffffffffu, lane < 8 && bases[j8 + (lane & 7)] <= u0));
+        const int j0 = (31 - __clz(__ballot_sync(0xffffffffu, bases[kWarps * lane] <= u0))) * kWarps;
+        const int j = j0 + 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && bases[j0 + lane % kWarps] <= u0));
         int r = j * run;
         int64_t in = u0 - bases[j];
         if (run > 1)

@@ -52,8 +52,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
             w.cu[2 * i + 2] = q.tok0 + q.n;
             w.kv_len[2 * i] = 0;
             w.kv_len[2 * i + 1] = q.keys;
-            w.first[i] = first;
-            w.request[i] = r;
+            for (int j = 0; j < pages; ++j) {   // what the unpacking takes, and what the attention sees
+                w.pages_of[first + j] = make_int4(r, j, q.keys, 0);
+                w.table[(2 * i + 1) * static_cast<int64_t>(w.pages) + j] = first + j;
+            }
         }
         at += n;
     }
@@ -65,8 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
     if (tid == 0) {
         w.cu[0] = begin;
         w.kv_len[2 * count] = 0;
-        w.count[0] = count;
-        w.count[1] = static_cast<int>(total & 0xFFFFFFFF);
+        *w.used = static_cast<int>(total & 0xFFFFFFFF);
     }
     for (int i = 2 * count + 1 + tid; i <= 2 * w.max_wide + 1; i += kPlanThreads) {
         w.cu[i] = end;
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
     }
 }
 
-// A warp a tile: a lane has 8 (4) words of key codes and as many of value codes, as in the attention.
+// A warp a tile, as a lane takes it in the attention.  Memory bounds it: 8512 tokens of 8 heads of 128 are 45 MB.
 template <int DP>
 __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4WideParams w, const Kv4AttnParams p)
 {
@@ -83,54 +84,75 @@ __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4Wid
     constexpr int W = DP / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int in_page = p.page_shift - 4;
+    const bool sectors = p.head_dim % 16 == 0;
     pdl_wait();
-    const int count = w.count[0];
-    // the tables of the pages that the attention sees, and the tiles behind them
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kUnpackThreads / 32);
-    const int64_t tiles = static_cast<int64_t>(w.count[1]) * kPageTiles * p.kv_heads;
+    const int per_page = kPageTiles * p.kv_heads;
+    const int64_t tiles = static_cast<int64_t>(*w.used) * per_page;
     for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kUnpackThreads + threadIdx.x) >> 5; u < tiles; u += warps) {
-        const int64_t per_page = static_cast<int64_t>(kPageTiles) * p.kv_heads;
-        const int page = static_cast<int>(u / per_page), rest = static_cast<int>(u - page * per_page);
+        const int page = static_cast<int>(u / per_page), rest = static_cast<int>(u - static_cast<int64_t>(page) * per_page);
         const int h = rest / kPageTiles, in = rest % kPageTiles;
-        const int i = last_le(w.first, count, page), r = w.request[i];
-        const int t = (page - w.first[i]) * kPageTiles + in;   // of the request's tiles
-        if (h == 0 && in == 0 && lane == 0) w.table[(2 * i + 1) * static_cast<int64_t>(w.pages) + page - w.first[i]] = page;
-        int bad = 0;
-        const int keys = kv4_request(p, r, &bad).keys;
-        if (t * 16 >= keys) continue;
-        const int from = p.table[r * p.table_stride + (t >> in_page)];
+        const int4 whose = w.pages_of[page];   // request, page of the request, its keys
+        const int t = whose.y * kPageTiles + in;
+        if (t * 16 >= whose.z) continue;
+        const int from = p.table[whose.x * p.table_stride + (t >> in_page)];
         const uint8_t *tile = p.zeros;
         if (from >= 0 && from < p.num_pages)
             tile = p.data + from * p.page_stride + h * p.head_stride + (t & ((1 << in_page) - 1)) * static_cast<int64_t>(Tile::kBytes);
         else if (lane == 0)
             atomicOr(p.counters, LORA_DEV_BAD_PAGE);
+        uint32_t k[2][W], v[2][W], ks[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint8_t *at = tile + e * (4 * DP) + lane * (4 * W);
+            if (W == 4) {
+                *reinterpret_cast<uint4 *>(k[e]) = *reinterpret_cast<const uint4 *>(at);
+                *reinterpret_cast<uint4 *>(v[e]) = *reinterpret_cast<const uint4 *>(at + Tile::kValues);
+            } else {
+                *reinterpret_cast<uint2 *>(k[e]) = *reinterpret_cast<const uint2 *>(at);
+                *reinterpret_cast<uint2 *>(v[e]) = *reinterpret_cast<const uint2 *>(at + Tile::kValues);
+            }
+            at = tile + Tile::kKeyScales + (8 * e + g) * Tile::kGroups + c * (W / 2);
+            ks[e] = W == 4 ? *reinterpret_cast<const uint16_t *>(at) : *at;
+        }
+        const uint32_t vs = *reinterpret_cast<const uint32_t *>(tile + Tile::kValueScales + ((DP == 128 ? g : g / 2) * 4 + c) * 4);
         const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + h) * kKv4WidePage + in * 16) * p.head_dim;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {   // keys g and g + 8, elements from c * DP / 4 on
-            uint32_t k[W];
-            const uint8_t *at = tile + e * (4 * DP) + lane * (4 * W);
-            if (W == 4) *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<const uint4 *>(at);
-            else *reinterpret_cast<uint2 *>(k) = *reinterpret_cast<const uint2 *>(at);
+        for (int e = 0; e < 2; ++e) {   // keys g and g + 8, elements from c * DP / 4 on: a scale for two words
             uint16_t *to = w.k + row + (8 * e + g) * p.head_dim + c * (DP / 4);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const uint32_t scale = tile[Tile::kKeyScales + (8 * e + g) * Tile::kGroups + (c * (DP / 4) + 8 * j) / 16];
-                if (c * (DP / 4) + 8 * j < p.head_dim) *reinterpret_cast<uint4 *>(to + 8 * j) = kv4_values(k[j], scale);
+            for (int j = 0; j < W; j += 2) {
+                const int d = c * (DP / 4) + 8 * j;
+                const uint32_t scale = ks[e] >> (4 * j) & 0xFF;
+                const uint4 lo = kv4_values(k[e][j], scale), hi = kv4_values(k[e][j + 1], scale);
+                if (sectors) {
+                    if (d < p.head_dim) store32(to + 8 * j, lo, hi);
+                } else {
+                    if (d < p.head_dim) *reinterpret_cast<uint4 *>(to + 8 * j) = lo;
+                    if (d + 8 < p.head_dim) *reinterpret_cast<uint4 *>(to + 8 * j + 8) = hi;
+                }
             }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {   // keys 2c, 2c + 1 and 8 more, elements from g * DP / 8 on
-            uint32_t v[W];
-            const uint8_t *at = tile + Tile::kValues + e * (4 * DP) + lane * (4 * W);
-            if (W == 4) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(at);
-            else *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(at);
+        for (int e = 0; e < 2; ++e)     // keys 2c, 2c + 1 and 8 more, elements from g * DP / 8 on
 #pragma unroll
-            for (int j = 0; j < W; ++j) {   // words: 8 elements of the even key, of the odd one, the next 8
-                const int key = 8 * e + 2 * c + (j & 1), d = g * (DP / 8) + (j >> 1) * 8;
-                const uint32_t scale = tile[Tile::value_scale(key, d / 16)];
-                if (d < p.head_dim) *reinterpret_cast<uint4 *>(w.v + row + key * p.head_dim + d) = kv4_values(v[j], scale);
+            for (int o = 0; o < 2; ++o) {
+                const int d = g * (DP / 8);
+                const uint32_t scale = vs >> (8 * (2 * e + o)) & 0xFF;
+                uint16_t *to = w.v + row + (8 * e + 2 * c + o) * p.head_dim + d;
+                const uint4 lo = kv4_values(v[e][o], scale);
+                if (DP == 64) {
+                    if (d < p.head_dim) *reinterpret_cast<uint4 *>(to) = lo;
+                    continue;
+                }
+                const uint4 hi = kv4_values(v[e][DP == 64 ? o : o + 2], scale);
+                if (sectors) {
+                    if (d < p.head_dim) store32(to, lo, hi);
+                } else {
+                    if (d < p.head_dim) *reinterpret_cast<uint4 *>(to) = lo;
+                    if (d + 8 < p.head_dim) *reinterpret_cast<uint4 *>(to + 8) = hi;
+                }
             }
-        }
     }
 }
 

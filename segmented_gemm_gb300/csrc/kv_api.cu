@@ -80,9 +80,8 @@ static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_head
         L.cu = take(lists * 4);
         L.kv_len = take(lists * 4);
         L.wide = take(R);
-        L.wide_first = take(lists * 4);
-        L.request = take(lists * 4);
-        L.count = take(2 * 4);
+        L.pages_of = take(static_cast<size_t>(L.pages) * sizeof(int4));
+        L.used = take(4);
         L.table = take((lists - 1) * L.pages * 4);
         L.k = take(rows * head_dim * 2);
         L.v = take(rows * head_dim * 2);
@@ -345,9 +344,8 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
         w.cu = at<int32_t>(ws, L.cu);
         w.kv_len = at<int32_t>(ws, L.kv_len);
         w.wide = at<uint8_t>(ws, L.wide);
-        w.first = at<int32_t>(ws, L.wide_first);
-        w.request = at<int32_t>(ws, L.request);
-        w.count = at<int32_t>(ws, L.count);
+        w.pages_of = at<int4>(ws, L.pages_of);
+        w.used = at<int32_t>(ws, L.used);
         w.table = at<int32_t>(ws, L.table);
         w.k = at<uint16_t>(ws, L.k);
         w.v = at<uint16_t>(ws, L.v);

@@ -57,7 +57,7 @@ constexpr int kKv4MaxCtas = 2 * kAttnMaxCtas;   // upper bound on the 4-bit atte
 // attention over a bf16 cache, whose workspace begins there.  Then partial results, of warps
 // and of CTAs, and the wide requests' lists and unpacked pages.
 struct Kv4Layout {
-    size_t counters, zeros, attn, first, part, part_ml, cu, kv_len, wide, wide_first, request, count, table, k, v, total;
+    size_t counters, zeros, attn, first, part, part_ml, cu, kv_len, wide, pages_of, used, table, k, v, total;
     size_t attn_bytes;
     int32_t max_wide, pages;
 };
@@ -95,8 +95,8 @@ struct Kv4AttnParams {
 struct Kv4WideParams {
     int32_t *cu, *kv_len;                       // [2 max_wide + 2], [2 max_wide + 1]: request 2i + 1 is the i-th wide one
     uint8_t *wide;                              // [R]
-    int32_t *first, *request;                   // [max_wide] first unpacked page, request
-    int32_t *count;                             // wide requests, their pages
+    int4 *pages_of;                             // [pages] request, page of the request, its keys
+    int32_t *used;                              // unpacked pages
     int32_t *table;                             // [2 max_wide + 1][pages]
     uint16_t *k, *v;                            // [pages][kv_heads][kKv4WidePage][head_dim]
     int32_t max_wide, pages;
