@@ -141,7 +141,8 @@ size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t
 /*
  * lora_attn_paged over a 4-bit cache: the same arguments, the same rows, over
  * the values that the cache stands for.  Needs no schedule.  q keeps its bf16
- * values (elements below 2^-26 of their row's largest lose bits), p is rounded to
+ * values (elements below 2^-26 of their row's largest lose bits, rows below 2^-114
+ * are zeros), p is rounded to
  * 16 bits for the second product, o to bf16 once; scores, statistics and sums are
  * fp32.  Keys and values past a row's request are never mixed in, whatever
  * they hold.  kv_len is clamped to [0, table_width * page_size], offsets to [0,

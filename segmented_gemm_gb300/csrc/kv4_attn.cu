@@ -751,8 +751,14 @@ cudaError_t launch_variant(const Kv4AttnParams &p, cudaStream_t stream)
     using S = Smem<DP, NT>;
     constexpr int smem = S::kTotal;
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static int configured[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev >= 64 || !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = 1;
+    }
     int64_t ctas = 2 * static_cast<int64_t>(num_sms_current_device());
     ctas = ctas < kKv4MaxCtas ? ctas : kKv4MaxCtas;
     return launch_pdl(kv4_attn_kernel<DP, NT>, ctas, kThreads, smem, p, stream);
