@@ -89,7 +89,8 @@ __device__ __forceinline__ uint2 quantise(const uint4 &x0, const uint4 &x1, uint
 }
 
 // A thread takes 16 elements of a head's key row and of its value row, consecutive
-// threads consecutive elements; memory bounds it.
+// threads consecutive elements.  Memory bounds it, and the arithmetic of 32 elements a thread: 7300 tokens
+// of 8 heads of 128, 38 MB, 10.3 us (13.9 with divisions, 11.4 without packed arithmetic); 32 tokens 2.6 us.
 template <int DP>
 __global__ void __launch_bounds__(kKv4Threads) kv4_store_kernel(const Kv4StoreParams p)
 {
@@ -138,7 +139,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_store_kernel(const Kv4StorePa
     if (bad) atomicOr(p.status, LORA_DEV_BAD_PAGE);
 }
 
-// The reverse, the same split; memory bounds it, three quarters of it the writes.
+// The reverse, the same split; memory bounds it, three quarters of it the writes: 8192 slots of 8 heads of
+// 128, 43 MB, 9.0 us (12.0 with 16-byte stores, half sectors each).
 template <int DP>
 __global__ void __launch_bounds__(kKv4Threads) kv4_load_kernel(const Kv4LoadParams p)
 {

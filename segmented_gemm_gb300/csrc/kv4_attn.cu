@@ -27,6 +27,18 @@
 // once for a CTA; those of a group that CTAs share in the workspace, where the
 // CTA that stores the last of them joins them in order, so that results do not depend
 // on timing.
+//
+// What bounds it, and what it measured (32 query and 8 kv heads of 128 unless said; a copy has 6780 GB/s):
+//   128 requests of one token over 1000 to 16000, 1.17 GB: 201 us, 5.8 TB/s; the tiles at
+//     6.7 TB/s, then one of an SM's two CTAs ends 15 % before the other, and the joins (7 us)
+//   32 over 100 to 8000, 163 MB: 42 us; the tiles take 27, the lists and the first loads 4, the ends of
+//     shares and the joins 6 to 10
+//   one over 1000: 12 us, all latency (counts, table, tiles, two tiles a warp, two joins)
+// The integer pipe is the busiest unit (it converts the codes, 16 lanes a cycle), so whatever could
+// went elsewhere: scales become fp16 pairs by a multiplication, masks have a branch of their own, addresses
+// are made 32 tiles at a time.  That took the first case from 242 to 201 us.  No gain: two tiles a round
+// (235 us where one took 223), three CTAs of 80 registers (259), four or sixteen warps a CTA (207, 196,
+// but 15 us for one token), more units for the CTA that runs ahead (200 to 224).
 #include <cuda_runtime.h>
 
 #include "block_scan.cuh"
@@ -41,8 +53,8 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kGap = 3;             // what a group costs beside its tiles, in tiles
-constexpr int kMinShare = 2;        // least share of a warp, in tiles
+constexpr int kGap = 3;             // what a group costs beside its tiles, in tiles (48 requests of up to 5 tokens: 68 us, 71 with 2)
+constexpr int kMinShare = 2;        // least share of a warp, in tiles (one token over 1000: 14 us, 16 with 4, 20 with 8)
 constexpr int kBatch = 2;           // most tiles of a stage of a warp's ring
 constexpr float kSlack = 8.f;       // log2 of the largest p
 constexpr float kNone = -1e30f;     // m of a column that has seen no key
