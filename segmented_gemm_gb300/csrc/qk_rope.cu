@@ -56,6 +56,13 @@ __device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos)
     return r;
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t widen2(uint32_t v) { return pack_f2(bf16_lo(v), bf16_hi(v)); }
 __device__ __forceinline__ uint32_t narrow2(uint64_t v)
 {
@@ -64,8 +71,9 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v)
     return pack_bf16x2(lo, hi);
 }
 
-// TOKENS of a CTA, up to four of them in flight at a time
-template <int LANES, int TOKENS, bool INTERLEAVED>
+// TOKENS of a CTA, up to four of them in flight at a time.  PARTIAL: rows have elements that are not rotated
+// (an angle of 0 would do for them, but for an infinity among those beside them).
+template <int LANES, int TOKENS, bool INTERLEAVED, bool PARTIAL>
 __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopeParams p)
 {
     pdl_launch_dependents();
@@ -204,6 +212,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
                         const uint64_t u = y[j], v = y[2 + j];
                         y[j] = fma_f2(v, n2[j], mul_f2(u, c2[j]));
                         y[2 + j] = fma_f2(u, s2[j], mul_f2(v, c2[j]));
+                        if (PARTIAL) {
+                            y[j] = rotated ? y[j] : u;
+                            y[2 + j] = rotated ? y[2 + j] : v;
+                        }
                     }
                 } else {              // each y[j] is a pair
                     const float cf[4] = {c.x, c.y, c.z, c.w}, sf[4] = {s.x, s.y, s.z, s.w};
@@ -211,7 +223,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
                     for (int j = 0; j < 4; ++j) {
                         float u, v;
                         unpack_f2(y[j], u, v);
-                        y[j] = pack_f2(fmaf(v, -sf[j], u * cf[j]), fmaf(u, sf[j], v * cf[j]));
+                        const uint64_t z = pack_f2(fmaf(v, -sf[j], u * cf[j]), fmaf(u, sf[j], v * cf[j]));
+                        y[j] = PARTIAL && !rotated ? y[j] : z;
                     }
                 }
                 uint2 o0 = x[i][0], o1 = x[i][1];   // values are copied as they are
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
     }
 }
 
-template <int LANES, bool INTERLEAVED>
+template <int LANES, bool INTERLEAVED, bool PARTIAL>
 static cudaError_t launch_rope(const QkRopeParams &p, cudaStream_t stream)
 {
     const int64_t T = p.a.num_tokens;
@@ -250,13 +263,22 @@ static cudaError_t launch_rope(const QkRopeParams &p, cudaStream_t stream)
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     pdl_attribute(cfg, at);
-    return cudaLaunchKernelEx(&cfg, few ? qk_rope_kernel<LANES, 1, INTERLEAVED> : qk_rope_kernel<LANES, kTokens, INTERLEAVED>, p);
+    return cudaLaunchKernelEx(
+        &cfg, few ? qk_rope_kernel<LANES, 1, INTERLEAVED, PARTIAL> : qk_rope_kernel<LANES, kTokens, INTERLEAVED, PARTIAL>, p);
 }
 
+template <int LANES>
+static cudaError_t launch_lanes(const QkRopeParams &p, cudaStream_t stream)
+{
+    const bool partial = p.a.rot_dim < p.a.head_dim;
+    if (p.a.interleaved) return partial ? launch_rope<LANES, true, true>(p, stream) : launch_rope<LANES, true, false>(p, stream);
+    return partial ? launch_rope<LANES, false, true>(p, stream) : launch_rope<LANES, false, false>(p, stream);
+}
+
+// Runs of 4 elements: with 8, for rows that allow it, 8100 tokens of 128 took 55 to 62 us instead of 38.5.
 cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream)
 {
-    if (p.a.head_dim <= 64) return p.a.interleaved ? launch_rope<8, true>(p, stream) : launch_rope<8, false>(p, stream);
-    return p.a.interleaved ? launch_rope<16, true>(p, stream) : launch_rope<16, false>(p, stream);
+    return p.a.head_dim <= 64 ? launch_lanes<8>(p, stream) : launch_lanes<16>(p, stream);
 }
 
 }  // namespace lora

@@ -153,6 +153,20 @@ def test_a_row_of_nans_or_zeros_stays_alone(ws):
     assert torch.equal(got, want)
 
 
+def test_infinities_beside_what_is_rotated(ws):
+    # elements that are not rotated keep their own, and pairs that are do not reach beyond themselves
+    for D, rot, inter in ((128, 64, False), (128, 64, True), (64, 0, False), (80, 40, False)):
+        (_, _, _), (q, k, _), _ = rope_inputs(5, 2, 1, D, 4)
+        pos, inv = i32([0, 3, 5, 70, 1000]), None if rot == 0 else freqs(rot).cuda()
+        want, _ = KV.lora_qk_rope(q, k, pos, inv, ws, interleaved=inter)
+        q[1, 0, D - 1], q[2, 1, D - 8], q[3, 1, rot] = float("inf"), -float("inf"), float("nan")
+        got, _ = KV.lora_qk_rope(q, k, pos, inv, ws, interleaved=inter)
+        for t, h, d in ((1, 0, D - 1), (2, 1, D - 8), (3, 1, rot)):
+            assert torch.equal(got[t, h, d].isnan(), q[t, h, d].isnan()) and (got[t, h, d].isnan() or got[t, h, d] == q[t, h, d])
+            got[t, h, d] = want[t, h, d]
+        assert torch.equal(got, want)
+
+
 def test_slots_outside_the_cache_are_reported(ws):
     (_, _, _), (q, k, v), _ = rope_inputs(6, 2, 1, 64, 2)
     kc, vc = (torch.zeros(2, 1, 16, 64, dtype=BF, device="cuda") for _ in range(2))
