@@ -103,7 +103,13 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
-// The same, without what the attention over a bf16 cache has done (a wide request).
+// row / group (the token of a row): exact, as row * group < 2^64, and a division takes several times as long.
+__device__ __forceinline__ int token_of(const Kv4AttnParams &p, int row)
+{
+    return p.group == 1 ? row : static_cast<int>(__umul64hi(static_cast<uint64_t>(row), p.group_inverse));
+}
+
+// A request without what the attention over a bf16 cache has done (a wide request).
 __device__ __forceinline__ Kv4Request request(const Kv4AttnParams &p, int r, int *bad)
 {
     Kv4Request q = kv4_request(p, r, bad);
@@ -176,9 +182,9 @@ struct Pieces {
         return cut();
     }
     // tiles of the piece that some row of the block sees: [t0, this)
-    __device__ __forceinline__ int end(int group) const
+    __device__ __forceinline__ int end(const Kv4AttnParams &p) const
     {
-        const int last = min(q.n - 1, (b * NC + NC - 1) / group);
+        const int last = min(q.n - 1, token_of(p, b * NC + NC - 1));
         return min(t1, (max(0, q.keys - q.n + last + 1) + 15) >> 4);
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
 
     // ---- the warp's ring: tiles [fetch_t, fetch_e) of the piece `ahead`, then of those after it, up to
     // kBatch of a piece a stage.  The lanes have the addresses of 32 tiles from fetch_0 on, and each issues its own.
-    int fetch_t = piece.t0, fetch_e = more ? piece.end(p.group) : fetch_t, fetch_0 = fetch_t - 32;
+    int fetch_t = piece.t0, fetch_e = more ? piece.end(p) : fetch_t, fetch_0 = fetch_t - 32;
     int put = 0, flying = 0;   // the stage that is filled next, and stages filled and not used up
     const uint8_t *src = nullptr;
     const int in_page = p.page_shift - 4;   // log2 of the tiles of a page
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
             __syncwarp();
             if (!more) return;
             fetch_t = x.t0;
-            fetch_e = x.end(p.group);
+            fetch_e = x.end(p);
             fetch_0 = fetch_t - 32;
         }
         if (fetch_t - fetch_0 >= 32) {
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
 
     // a row of the output; by: 1 / l
     auto row_of = [&](const Group &gr, int n, int *h) {
-        const int row = gr.first_row + n, i = row / p.group;
+        const int row = gr.first_row + n, i = token_of(p, row);
         *h = gr.h * p.group + row - i * p.group;
         return static_cast<int64_t>(gr.tok0 + i);
     };
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = nt * 8 + 2 * c + i;
-                lim[nt][i] = col < gr.cols ? max(0, piece.q.keys - piece.q.n + (gr.first_row + col) / p.group + 1) : 0x7fffffff;
+                lim[nt][i] = col < gr.cols ? max(0, piece.q.keys - piece.q.n + token_of(p, gr.first_row + col) + 1) : 0x7fffffff;
                 m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
                 for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
         }
         if (NT > 1) __syncwarp();
-        const int first_limit = max(0, piece.q.keys - piece.q.n + gr.first_row / p.group + 1);   // of the first column, the fewest
+        const int first_limit = max(0, piece.q.keys - piece.q.n + token_of(p, gr.first_row) + 1);   // of the first column, the fewest
 
         // S^T of a tile: rows are the keys g and g + 8, columns 2c and 2c + 1
         auto scores = [&](const uint8_t *tile, float (&sc)[NT][4]) {
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
             }
         };
         // ---- the tiles
-        const int te = piece.end(p.group), keys = piece.q.keys;
+        const int te = piece.end(p), keys = piece.q.keys;
 #pragma unroll 1
         for (int t = piece.t0; t < te && live;) {
             live = __all_sync(0xffffffffu, wait(full + stage, parity, abort, status, p.wait_cycles));

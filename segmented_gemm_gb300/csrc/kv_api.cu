@@ -329,6 +329,7 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     p.heads = attn->heads;
     p.kv_heads = attn->kv_heads;
     p.group = attn->heads / attn->kv_heads;
+    p.group_inverse = p.group > 1 ? ~uint64_t(0) / p.group + 1 : 0;
     p.head_dim = attn->head_dim;
     p.scale = attn->scale;
     p.zeros = at<uint8_t>(ws, L.zeros);

@@ -83,6 +83,7 @@ struct Kv4AttnParams {
     int32_t num_pages, page_shift;
     int32_t T, R;
     int32_t heads, kv_heads, group, head_dim;
+    uint64_t group_inverse;                     // 2^64 / group, rounded up (group > 1)
     float scale;
     const uint8_t *zeros;
     int32_t *counters;
