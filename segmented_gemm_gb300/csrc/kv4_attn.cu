@@ -53,7 +53,7 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kGap = 3;             // what a group costs beside its tiles, in tiles (48 requests of up to 5 tokens: 68 us, 71 with 2)
+constexpr int kGap = 4;             // what a group costs beside its tiles, in tiles (48 requests of up to 5 tokens: 53 us, 55 with 2)
 constexpr int kMinShare = 2;        // least share of a warp, in tiles (one token over 1000: 14 us, 16 with 4, 20 with 8)
 constexpr int kBatch = 2;           // most tiles of a stage of a warp's ring
 constexpr float kSlack = 8.f;       // log2 of the largest p
@@ -101,6 +101,22 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
     return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// bulk_load of what is read once: the first to leave L2, before the parts of cut groups, tables and queries (32
+// requests over 100 to 8000 40.0 us so, 40.9 without; 512 over 50 to 300 38 and 40; 128 over 1000 to 16000 the same).
+__device__ __forceinline__ uint64_t read_once_policy()
+{
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+                 : "memory");
 }
 
 // row / group (the token of a row): exact, as row * group < 2^64, and a division takes several times as long.
@@ -305,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
     int fetch_t = piece.t0, fetch_e = more ? piece.end(p) : fetch_t, fetch_0 = fetch_t - 32;
     int put = 0, flying = 0;   // the stage that is filled next, and stages filled and not used up
     const uint8_t *src = nullptr;
+    const uint64_t policy = read_once_policy();
     const int in_page = p.page_shift - 4;   // log2 of the tiles of a page
     auto fetch = [&]() {       // one more stage, if there is anything
         while (fetch_t >= fetch_e) {
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         const int n = min(kBatch, fetch_e - fetch_t), i = lane - (fetch_t - fetch_0);
         if (i == 0) mbar_expect_tx(full + put, n * S::kTile);
         __syncwarp();
-        if (i >= 0 && i < n) bulk_load(ring + (put * kBatch + i) * S::kTile, src, S::kTile, full + put);
+        if (i >= 0 && i < n) bulk_load_once(ring + (put * kBatch + i) * S::kTile, src, S::kTile, full + put, policy);
         put = put + 1 == kStages ? 0 : put + 1;
         ++flying;
         fetch_t += n;
@@ -697,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
             for (int i = w + 1; i <= to; ++i)
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) top[q] = fmaxf(top[q], ml[i * NC + n[q]].x);
+#pragma unroll 4
             for (int i = w; i <= to; ++i) {
                 if (i < 0) continue;
                 const bool last = i == w;   // the chain's first piece is its warp's last
