@@ -33,10 +33,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
     const int run = (p.R + kPlanThreads - 1) / kPlanThreads, r0 = min(p.R, tid * run), r1 = min(p.R, r0 + run);
     pdl_wait();
     int bad = 0;
-    // pages in the low half, requests in the high one
+    // pages in the low half (one more than there are for what cannot fit, so that they add up), requests in the high one
     auto need = [&](const Kv4Request &q) {
         const bool wide = static_cast<int64_t>(q.n) * p.group > kv4_wide_rows(p.head_dim) && q.keys > 0;
-        return wide ? (int64_t(1) << 32) + (q.keys + kKv4WidePage - 1) / kKv4WidePage : int64_t(0);
+        const int pages = min(w.pages + 1, (q.keys - 1) / kKv4WidePage + 1);
+        return wide ? (int64_t(1) << 32) + pages : int64_t(0);
     };
     int64_t sum = 0, total;
     for (int r = r0; r < r1; ++r) sum += need(kv4_request(p, r, &bad));
