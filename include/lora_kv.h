@@ -117,7 +117,8 @@ typedef struct {
 /* Bytes of one head of one page (0 for arguments out of range). */
 size_t lora_kv4_block_size(int32_t page_size, int32_t head_dim);
 
-/* lora_kv_store into a 4-bit cache; k, v, strides, slot_map and ws as there. */
+/* lora_kv_store into a 4-bit cache; k, v, strides, slot_map and ws as there (of two tokens with one slot
+ * groups of either may stay). */
 int lora_kv4_store(const lora_bf16_t *k, const lora_bf16_t *v, int64_t num_tokens, int64_t k_token_stride,
                    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const lora_kv4_cache_t *cache,
                    const int32_t *slot_map, void *ws, size_t ws_bytes, lora_stream_t stream);
