@@ -129,6 +129,8 @@ KERNEL_SOURCES = {   # the sources each kernel is compiled from (besides interna
     "seg_build_kernel": ("seg_build.cu", "seg_build_body.cuh"),
     "moe_pair_kernel": ("moe_pair.cu", "moe_pair.h"),
     "attn_kernel": ("attn.cu", "attn.h", "attn_piece.cuh", "attn_ptx.cuh"),
+    "kv4_attn_kernel": ("kv4_attn.cu", "kv4.cuh", "kv4_request.cuh", "block_scan.cuh", "kv_ops.h"),
+    "qk_rope_kernel": ("qk_rope.cu", "kv_ops.h", "attn_ptx.cuh"),
 }
 
 

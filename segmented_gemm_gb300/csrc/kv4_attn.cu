@@ -29,14 +29,14 @@
 // on timing.
 //
 // What bounds it, and what it measured (32 query and 8 kv heads of 128 unless said; a copy has 6780 GB/s):
-//   128 requests of one token over 1000 to 16000, 1.17 GB: 201 us, 5.8 TB/s; the tiles at
+//   128 requests of one token over 1000 to 16000, 1.17 GB: 197 us, 5.9 TB/s; the tiles at
 //     6.7 TB/s, then one of an SM's two CTAs ends 15 % before the other, and the joins (7 us)
-//   32 over 100 to 8000, 163 MB: 42 us; the tiles take 27, the lists and the first loads 4, the ends of
-//     shares and the joins 6 to 10
+//   32 over 100 to 8000, 163 MB: 40 us; the tiles take 27, the lists and the first loads 4, the ends of
+//     shares and the joins 5 to 9
 //   one over 1000: 12 us, all latency (counts, table, tiles, two tiles a warp, two joins)
 // The integer pipe is the busiest unit (it converts the codes, 16 lanes a cycle), so whatever could
 // went elsewhere: scales become fp16 pairs by a multiplication, masks have a branch of their own, addresses
-// are made 32 tiles at a time.  That took the first case from 242 to 201 us.  No gain: two tiles a round
+// are made 32 tiles at a time.  That took the first case from 242 to 197 us.  No gain: two tiles a round
 // (235 us where one took 223), three CTAs of 80 registers (259), four or sixteen warps a CTA (207, 196,
 // but 15 us for one token), more units for the CTA that runs ahead (200 to 224).
 #include <cuda_runtime.h>
@@ -805,7 +805,7 @@ cudaError_t launch_variant(const Kv4AttnParams &p, cudaStream_t stream)
 // Blocks of 8 columns: a request of more rows has several, which read its tiles again (from L2)
 // and unpack them again, but 8 more columns of a block would take as long on the matrix
 // units as that, and the registers of a second CTA an SM: 48 requests of up to 5 tokens of 28/4 heads
-// over 300 to 6000 take 54 us so, 61 with 16 columns, 87 with 32; 64 requests of 16 rows 118 and
+// over 300 to 6000 take 52 us so, 61 with 16 columns, 87 with 32; 64 requests of 16 rows 118 and
 // 106.  With a head dimension of 64 the registers are there: 8 requests of 64 rows 65 us, 53 with 16.
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream)
 {
