@@ -283,10 +283,19 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const KvPagesParams p)
             else flags |= LORA_DEV_BAD_PAGE;
         }
         if (tid == 0) {
-            const int fresh = need && served ? a.free_pages[head + place] : -1;
-            if (fresh != -1) to[whole] = fresh;
-            p.src[i] = fresh != -1 ? from[whole] : -1;
-            p.dst[i] = fresh;
+            int old = -1, fresh = -1;
+            if (need && served) {
+                auto page_or_none = [&](int page) {
+                    if (page >= 0 && page < a.num_pages) return page;
+                    flags |= LORA_DEV_BAD_PAGE;
+                    return -1;
+                };
+                old = page_or_none(from[whole]);
+                to[whole] = fresh = page_or_none(a.free_pages[head + place]);
+            }
+            const bool pair = old >= 0 && fresh >= 0;
+            p.src[i] = pair ? old : -1;
+            p.dst[i] = pair ? fresh : -1;
             a.ctx_len[c] = served ? n : 0;
         }
     }

@@ -459,6 +459,28 @@ def test_forks_run_out_of_pages():
     assert_state(d, s)
 
 
+def test_forks_onto_bad_pages():
+    """A page of the list outside the cache is nobody's: the child's entry is -1, never what stood there before."""
+    s = small()
+    s.free, s.head = [99, -1, 10], 0
+    s.table += [[7] * 4 for _ in range(3)]
+    s.ctx += [0] * 3
+    d, ws = device_state(s), KV.PagesWorkspace(12)
+    src, dst = KV.lora_kv_fork(i32([0, 0, 0]), i32([4, 5, 6]), ws=ws, **d)
+    assert L.lora_get_status(ws) == A.LORA_DEV_BAD_PAGE
+    old = s.table[0][2]
+    assert list(zip(src.tolist(), dst.tolist())) == [(-1, -1), (-1, -1), (old, 10)]
+    assert [t[2] for t in d["block_table"].tolist()[4:]] == [-1, -1, 10] and d["free_head"].item() == 3
+    assert d["ctx_len"].tolist()[4:] == [20] * 3
+    # so is the parent's unfinished page
+    s = small()
+    s.table[0][2] = 12
+    d = device_state(s)
+    src, dst = KV.lora_kv_fork(i32([0]), i32([2]), ws=ws, **d)
+    assert L.lora_get_status(ws) == A.LORA_DEV_BAD_PAGE and (src.item(), dst.item()) == (-1, -1)
+    assert d["block_table"].tolist()[2][2] == s.free[s.head] and d["free_head"].item() == s.head + 1
+
+
 def test_compaction_of_bad_states():
     s = small()
     s.free, s.head = [7, 0, 9, 0, 99, -4], 0              # a held page, one twice, two outside
