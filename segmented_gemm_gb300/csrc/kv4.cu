@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&y)[4])
 // there is), with the sign of x where that is 0 (of 0 itself a positive one).
 __device__ __forceinline__ uint64_t rounded_products(uint32_t x, uint64_t inv)
 {
-    constexpr float kRound = 3072.f;   // fp32 numbers near it are 2^-12 apart
+    constexpr float kRound = 1.5f * 2048.f;   // fp32 numbers around it, from 2^11 to 2^12, are 2^-12 apart
     const uint64_t x2 = pack_f2(bf16_lo(x), bf16_hi(x)), y2 = add_f2(fma_f2(x2, inv, pack_f2(kRound, kRound)), pack_f2(-kRound, -kRound));
     float x0, x1, y0, y1;
     unpack_f2(add_f2(x2, 0), x0, x1);  // -0 becomes 0
