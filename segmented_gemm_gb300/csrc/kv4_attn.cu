@@ -56,7 +56,8 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kGap = 4;             // what a group costs beside its tiles, in tiles (48 requests of up to 5 tokens: 53 us, 55 with 2)
 constexpr int kMinShare = 2;        // least share of a warp, in tiles (one token over 1000: 14 us, 16 with 4, 20 with 8)
 constexpr int kBatch = 2;           // most tiles of a stage of a warp's ring
-constexpr float kSlack = 8.f;       // log2 of the largest p
+constexpr float kLift = 7.f;        // m is this far below the largest score where it is set: fp16 has p down to 2^-31 of the largest
+constexpr float kSlack = 15.f;      // log2 of the largest p; m is set again past it
 constexpr float kNone = -1e30f;     // m of a column that has seen no key
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
                             float top = m[nt][e];
 #pragma unroll
                             for (int q = 0; q < 4; q += 2)
-                                if (y[nt][e + q] != -INFINITY) top = fmaxf(top, sc[nt][e + q] * fac[nt][e]);
+                                if (y[nt][e + q] != -INFINITY) top = fmaxf(top, fmaf(sc[nt][e + q], fac[nt][e], -kLift));
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                             const float by = exp2_approx(m[nt][e] - top);

@@ -428,3 +428,30 @@ def test_rows_that_start_on_16_bytes_only():
     k1, v1 = KV.lora_kv4_load(a, slots, ws)
     assert torch.equal(out[..., 8:72], k1) and torch.equal(out[..., 136:200], v1)
     assert (out[..., :8] == 3).all() and (out[..., 72:136] == 3).all()
+
+
+def test_many_small_weights_beside_a_large_one():
+    """2^20 keys whose weights are 2^-25.5 of the first one's: together 2 % of it, each below what fp16 has beside 1.
+    Pages repeat, and there are enough groups that a warp has most of one.  With n = 2^16 tiles, adding equal numbers
+    in fp32 loses up to n / 2 * 2^-23 of o (truncated in a product) and as much of l; o itself is rounded by U, p by 2^-11,
+    and x = 25.5 by 2^-22 of itself.  l is summed by lanes, an eighth of the keys each; in the one that has the
+    first key, its 1 absorbs what is added one by one: 2^-25.5 is below half of fp32's last place there, 2^-24."""
+    R, Hk, D, page, N = 320, 8, 128, 4096, 1 << 20
+    k = torch.zeros(2 * page, Hk, D, dtype=BF, device="cuda")
+    v = torch.full_like(k, 6.0)              # a scale of 1: exact
+    k[0, :, 0], v[0] = 6.0, 0.0
+    cache = KV.Kv4Cache.zeros(2, Hk, page, D)
+    ws = KV.Kv4Workspace(R, R, Hk, Hk, D)
+    KV.lora_kv4_store(k, v, cache, torch.arange(2 * page, dtype=torch.int32, device="cuda"), ws)
+    table = torch.ones(R, N // page, dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    q = torch.zeros(R, Hk, D, dtype=BF, device="cuda")
+    q[..., 0] = 2.0
+    lse = torch.empty(R, Hk, device="cuda")
+    o = KV.lora_kv4_attn(q, cache, table, i32(list(range(R + 1))), i32([N] * R), 25.5 / 12 * math.log(2.0), ws, lse=lse)
+    rest = (N - 1) * 2.0 ** -25.5
+    want = 6.0 * rest / (1.0 + rest)
+    tol = (U + 2.0 ** -11 + 2 * 2.0 ** 15 * 2.0 ** -23 + 2.0 ** -16) * want
+    assert float((o.double() - want).abs().max()) <= tol
+    want = 25.5 * math.log(2.0) + math.log1p(rest)
+    assert float((lse.double() - want).abs().max()) <= rest / 8 + 2 * 2.0 ** -8 * rest + 25 * 2.0 ** -22
