@@ -466,88 +466,140 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
     if (gid == 0) *p.head_out = first;
 }
 
-// The same in one launch, for small caches with few entries: one CTA, 32 pages a thread as bits.  94 pages of 5
-// rows 6 us so, 10 by four launches; 7554 pages of 90 rows 15 and 12.
-__global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const KvPagesParams p)
+// The same in one launch, for small caches: the CTAs of a cluster mark the pages in shared memory, every one takes
+// all CTAs' marks together and counts for itself, and they share what is to be written.  7554 pages of 90
+// rows 8.7 us by eight CTAs, 12.3 by four launches; 94 pages of 5 rows 7 by eight and 4.3 by one; with 32768 pages and
+// as many entries eight CTAs and four launches take the same 14.
+constexpr int64_t kClusterEntries = 1 << 15;
+constexpr int kClusterCtas = 8;
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// *mine of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t of_rank(const uint32_t *mine, uint32_t rank)
+{
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+struct CompactShared {
+    uint32_t used[kSmallThreads], free[kSmallThreads];                           // this CTA's marks, a bit a page
+    uint32_t hole[kSmallThreads], mover[kSmallThreads], high[kSmallThreads];     // all CTAs'
+    int64_t before[kSmallThreads], scan[32];   // holes, movers and high ones in the words before, 20 bits each
+    uint16_t to[kSmallPages / 2];              // where a mover goes: no more than half of the pages do
+};
+
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kSmallThreads) compact_small_kernel(const KvPagesParams p)
 {
     pdl_launch_dependents();
-    __shared__ uint32_t used[kSmallThreads], free[kSmallThreads];   // a bit a page; then `used` the movers
-    __shared__ int before[kSmallThreads];                           // movers in the words before
-    __shared__ int64_t scan[32];
+    extern __shared__ __align__(16) uint8_t shared[];
+    CompactShared &s = *reinterpret_cast<CompactShared *>(shared);
     const lora_kv_pages_t &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    used[tid] = free[tid] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x, warp = (tid >> 5) * CTAS + rank;
+    constexpr int kWarps = kSmallThreads / 32 * CTAS, kAll = kSmallThreads * CTAS;   // the cluster's
+    s.used[tid] = s.free[tid] = 0;
     __syncthreads();
     pdl_wait();
     const int head0 = *a.free_head, head = max(0, min(head0, a.num_free));
     int flags = head != head0 ? LORA_DEV_BAD_LENGTH : 0;
-    for (int r = warp; r < a.num_rows; r += kSmallThreads / 32) {
+    for (int r = warp; r < a.num_rows; r += kWarps) {
         const int n = held_pages(a, a.ctx_len[r], &flags);
+#pragma unroll 4
         for (int j = lane; j < n; j += 32) {
             const int page = a.block_table[r * a.table_stride + j];
-            if (page >= 0 && page < a.num_pages) atomicOr(used + page / 32, 1u << (page % 32));
+            if (page >= 0 && page < a.num_pages) atomicOr(s.used + page / 32, 1u << (page % 32));
             else flags |= LORA_DEV_BAD_PAGE;
         }
     }
-    for (int i = head + tid; i < a.num_free; i += kSmallThreads) {
+    for (int i = head + rank * kSmallThreads + tid; i < a.num_free; i += kAll) {
         const int page = a.free_pages[i];
-        if (page >= 0 && page < a.num_pages) atomicOr(free + page / 32, 1u << (page % 32));
+        if (page >= 0 && page < a.num_pages) atomicOr(s.free + page / 32, 1u << (page % 32));
         else flags |= LORA_DEV_BAD_PAGE;
     }
-    __syncthreads();
+    uint32_t u = 0, f = 0;
+    if (CTAS > 1) {
+        cluster_arrive();
+        cluster_wait();
+#pragma unroll
+        for (int c = 0; c < CTAS; ++c) {
+            u |= of_rank(s.used + tid, c);
+            f |= of_rank(s.free + tid, c);
+        }
+        cluster_arrive();   // until everybody has read the marks, nobody leaves
+    } else {
+        __syncthreads();
+        u = s.used[tid];
+        f = s.free[tid];
+    }
+    if (f & u) flags |= LORA_DEV_BAD_PAGE;
+    f &= ~u;
     const int base = 32 * tid, below = max(0, min(32, p.limit - base));
-    const uint32_t low = below == 32 ? ~0u : (1u << below) - 1, u = used[tid], f = free[tid] & ~u;
-    if (free[tid] & u) flags |= LORA_DEV_BAD_PAGE;
-    uint32_t holes = f & low, movers = u & ~low, high = f & ~low;
+    const uint32_t low = below == 32 ? ~0u : (1u << below) - 1, holes = f & low, movers = u & ~low, high = f & ~low;
     int64_t total;
-    const int64_t at = block_scan_i64(__popc(holes) | static_cast<int64_t>(__popc(movers)) << 20 | static_cast<int64_t>(__popc(high)) << 40,
-                                      scan, &total);
-    used[tid] = movers;
-    int hole = static_cast<int>(at & 0xFFFFF), mover = static_cast<int>(at >> 20 & 0xFFFFF), up = static_cast<int>(at >> 40);
-    before[tid] = mover;
+    const int64_t before = block_scan_i64(
+        __popc(holes) | static_cast<int64_t>(__popc(movers)) << 20 | static_cast<int64_t>(__popc(high)) << 40, s.scan, &total);
     const int all_holes = static_cast<int>(total & 0xFFFFF), all_movers = static_cast<int>(total >> 20 & 0xFFFFF);
     const int moved = min(min(all_holes, all_movers), p.max_copies);
     const int first = a.num_free - all_holes - static_cast<int>(total >> 40);
-    // the list's old entries have all been read
-    for (; holes; holes &= holes - 1, ++hole) {
-        const int page = base + __ffs(holes) - 1;
-        if (hole < moved) p.dst[hole] = page;
-        else p.free_out[first + hole - moved] = page;
-    }
-    for (uint32_t left = movers | high; left; left &= left - 1) {
-        const int page = base + __ffs(left) - 1;
-        const bool moves = left & (0u - left) & movers;
-        if (moves && mover < moved) p.src[mover] = page;
-        if (!moves || mover < moved) p.free_out[first + (all_holes - moved) + up + min(mover, moved)] = page;
-        if (moves) ++mover;
-        else ++up;
-    }
-    for (int i = moved + tid; i < p.max_copies; i += kSmallThreads) p.src[i] = p.dst[i] = -1;
-    if (p.ref_out != a.ref)
-        for (int i = tid; i < a.num_pages; i += kSmallThreads) p.ref_out[i] = a.ref[i];
-    if (p.free_out != a.free_pages)
-        for (int i = tid; i < first; i += kSmallThreads) p.free_out[i] = a.free_pages[i];
+    s.hole[tid] = holes;
+    s.mover[tid] = movers;
+    s.high[tid] = high;
+    s.before[tid] = before;
+    int n = static_cast<int>(before & 0xFFFFF);
+    for (uint32_t left = holes; left && n < moved; left &= left - 1, ++n) s.to[n] = static_cast<uint16_t>(base + __ffs(left) - 1);
     __syncthreads();
-    for (int i = tid; i < moved; i += kSmallThreads) {
-        const int src = __ldcg(p.src + i), n = a.ref[src];
-        p.ref_out[__ldcg(p.dst + i)] = n;
-        p.ref_out[src] = 0;
+
+    // the list's old entries have all been read
+    for (int w = warp; w < (a.num_pages + 31) / 32; w += kWarps) {
+        const int page = 32 * w + lane;
+        const uint32_t bit = 1u << lane, less = bit - 1;
+        const int64_t at = s.before[w];
+        const int hole = static_cast<int>(at & 0xFFFFF) + __popc(s.hole[w] & less);
+        const int mover = static_cast<int>(at >> 20 & 0xFFFFF) + __popc(s.mover[w] & less);
+        int32_t *high_out = p.free_out + first + (all_holes - moved) + static_cast<int>(at >> 40) + __popc(s.high[w] & less);
+        bool pair = false;                                   // its count is the other one's, or 0
+        if (s.hole[w] & bit) {
+            pair = hole < moved;
+            if (pair) p.dst[hole] = page;
+            else p.free_out[first + hole - moved] = page;
+        } else if (s.mover[w] & bit) {
+            pair = mover < moved;
+            if (pair) {
+                p.src[mover] = page;
+                high_out[mover] = page;
+                p.ref_out[s.to[mover]] = a.ref[page];
+                p.ref_out[page] = 0;
+            }
+        } else if (s.high[w] & bit) {
+            high_out[min(mover, moved)] = page;
+        }
+        if (!pair && p.ref_out != a.ref && page < a.num_pages) p.ref_out[page] = a.ref[page];
     }
+    for (int i = moved + rank * kSmallThreads + tid; i < p.max_copies; i += kAll) p.src[i] = p.dst[i] = -1;
+    if (p.free_out != a.free_pages)
+        for (int i = rank * kSmallThreads + tid; i < first; i += kAll) p.free_out[i] = a.free_pages[i];
     const bool in_place = p.table_out == a.block_table;
-    for (int r = warp; r < a.num_rows; r += kSmallThreads / 32) {
+    for (int r = warp; r < a.num_rows; r += kWarps) {
         int ignored = 0;
-        const int n = held_pages(a, a.ctx_len[r], &ignored);
-        for (int j = lane; j < (in_place ? n : a.table_width); j += 32) {
+        const int held = held_pages(a, a.ctx_len[r], &ignored);
+#pragma unroll 4
+        for (int j = lane; j < (in_place ? held : a.table_width); j += 32) {
             int page = a.block_table[r * a.table_stride + j];
-            if (j < n && page >= 0 && page < a.num_pages && used[page / 32] >> (page % 32) & 1) {
-                const int i = before[page / 32] + __popc(used[page / 32] & ((1u << (page % 32)) - 1));
-                if (i < moved) page = __ldcg(p.dst + i);
+            if (j < held && page >= 0 && page < a.num_pages && s.mover[page / 32] >> (page % 32) & 1) {
+                const int i = static_cast<int>(s.before[page / 32] >> 20 & 0xFFFFF) +
+                              __popc(s.mover[page / 32] & ((1u << (page % 32)) - 1));
+                if (i < moved) page = s.to[i];
             }
             p.table_out[r * a.table_stride + j] = page;
         }
     }
-    if (tid == 0) *p.head_out = first;
+    if (rank == 0 && tid == 0) *p.head_out = first;
     if (flags) atomicOr(p.counters, flags);
+    if (CTAS > 1) cluster_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -618,6 +670,21 @@ int64_t capped(int64_t n, int64_t per_sm)
     return n < 1 ? 1 : n < cap ? n : cap;
 }
 
+template <int CTAS>
+cudaError_t launch_compact_small(const KvPagesParams &p, cudaStream_t stream)
+{
+    static bool configured[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev >= 64 || !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(compact_small_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   sizeof(CompactShared));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    return launch_pdl(compact_small_kernel<CTAS>, CTAS, kSmallThreads, sizeof(CompactShared), p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_release(const KvPagesParams &p, cudaStream_t stream)
@@ -641,8 +708,9 @@ cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream)
 
 cudaError_t launch_kv_compact(const KvPagesParams &p, cudaStream_t stream)
 {
-    if (p.a.num_pages <= kSmallPages && static_cast<int64_t>(p.a.num_rows) * p.a.table_width <= kSmallEntries)
-        return launch_pdl(compact_small_kernel, 1, kSmallThreads, 0, p, stream);
+    const int64_t entries = static_cast<int64_t>(p.a.num_rows) * p.a.table_width;
+    if (p.a.num_pages <= kSmallPages && entries <= kSmallEntries) return launch_compact_small<1>(p, stream);
+    if (p.a.num_pages <= kSmallPages && entries <= kClusterEntries) return launch_compact_small<kClusterCtas>(p, stream);
     const int chunks = (p.a.num_pages + kPageChunk - 1) / kPageChunk;
     const int64_t lists = (static_cast<int64_t>(p.a.num_free) + kThreads - 1) / kThreads;
     const int64_t rows = p.a.num_rows > lists ? p.a.num_rows : lists;

@@ -568,3 +568,31 @@ def test_many_pages_and_rows():
     assert L.lora_get_status(ws) == 0
     assert int(d["free_head"]) == 0 and int(d["ctx_len"].max()) == 0 and int(d["ref"].abs().max()) == 0
     assert torch.equal(d["free_pages"][:total], used)
+
+
+@pytest.mark.parametrize("pages,rows,width", [(32768, 256, 128), (32769, 256, 128), (32768, 256, 129), (32768, 4, 1024), (32768, 16, 1025)])
+def test_compaction_that_moves_half_of_all_pages(pages, rows, width):
+    """Every held page has to move: around the most pages and entries that one launch takes."""
+    page, half = 16, pages // 2
+    rng = random.Random(pages + rows)
+    used = min(half, rows * width)
+    order = rng.sample(range(half, pages), used)
+    table, ctx, at = [], [], 0
+    for r in range(rows):
+        n = min(width, used - at) if r % 2 == 0 else 0
+        table.append(order[at:at + n] + [-1] * (width - n))
+        ctx.append(n * page)
+        at += n
+    for r in range(1, rows, 2):
+        n = min(width, used - at)
+        table[r], ctx[r], at = order[at:at + n] + [-1] * (width - n), n * page, at + n
+    held = set(order)
+    free = [p for p in range(pages) if p not in held]
+    rng.shuffle(free)
+    s = ref.Pages(table, ctx, [rng.randrange(3) if p in held else 0 for p in range(pages)], [-1] * used + free, used, page)
+    d, ws = device_state(s), KV.PagesWorkspace(pages)
+    src, dst = KV.lora_kv_compact(limit=half, ws=ws, **d)
+    assert L.lora_get_status(ws) == 0
+    pairs = s.compact(half, len(s.free))
+    assert list(zip(src.tolist(), dst.tolist())) == pairs and sum(a >= 0 for a, _ in pairs) == used
+    assert_state(d, s)
