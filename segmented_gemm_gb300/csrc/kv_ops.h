@@ -15,6 +15,7 @@ constexpr int kv4_padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
 constexpr int kv4_tile_bytes(int padded) { return 18 * padded; }
 
 struct QkRopeParams {
+    int32_t cta_tokens;                         // of a CTA, set by the launch
     lora_qk_rope_t a;
     uint16_t *kc, *vc;                       // the cache, or NULL
     int64_t page_stride, head_stride, slot_stride;
@@ -137,7 +138,7 @@ struct PageCopyParams {
     int32_t *status;
 };
 
-cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream);
+cudaError_t launch_qk_rope(QkRopeParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_store(const Kv4StoreParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_load(const Kv4LoadParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream);

@@ -22,7 +22,7 @@ namespace lora {
 //
 // HBM bounds it.  8100 tokens of 32 + 8 + 8 heads of 128 into the cache, 199 MB: 38.5 us, 5.2 TB/s (64 us with
 // branches and a division a row, 47 with branches alone, 44 with three CTAs an SM instead of four).  32 tokens: 2.6 us, the launch and two loads in a row.
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kCtas = 4;   // of an SM
 
 // inv_freq / 2pi, modulo 1, in units of 2^-64: what a position turns by.  inv_freq is m * 2^e, so it is
 // m * (2^88 / 2pi) * 2^(e - 24), in integers: fp64 would cost more than the rest of the kernel.
@@ -71,10 +71,10 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v)
     return pack_bf16x2(lo, hi);
 }
 
-// TOKENS of a CTA, up to four of them in flight at a time.  PARTIAL: rows have elements that are not rotated
+// Up to TOKENS of a CTA (p.cta_tokens), up to four of them in flight at a time.  PARTIAL: rows have elements that are not rotated
 // (an angle of 0 would do for them, but for an infinity among those beside them).
 template <int LANES, int TOKENS, bool INTERLEAVED, bool PARTIAL>
-__global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, kCtas) qk_rope_kernel(const QkRopeParams p)
 {
     pdl_launch_dependents();
     constexpr int kGroups = kRopeThreads / LANES;   // rows at a time
@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
     const bool rotated = lane < a.rot_dim / 8, on = lane < a.head_dim / 8;
     const bool halves = rotated && !INTERLEAVED;
     const int off0 = halves ? 4 * lane : 8 * lane, off1 = halves ? half + 4 * lane : 8 * lane + 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
-    const int tokens = static_cast<int>(a.num_tokens - t0 < TOKENS ? a.num_tokens - t0 : TOKENS);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.cta_tokens;
+    const int tokens = static_cast<int>(a.num_tokens - t0 < p.cta_tokens ? a.num_tokens - t0 : p.cta_tokens);
     const int heads = a.heads, k_end = heads + a.kv_heads, per = k_end + (p.kc ? a.kv_heads : 0);
     const bool norms = a.q_weight || a.k_weight;
     const float mean = 1.f / static_cast<float>(a.head_dim);
@@ -249,16 +249,20 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const QkRopePa
 }
 
 template <int LANES, bool INTERLEAVED, bool PARTIAL>
-static cudaError_t launch_rope(const QkRopeParams &p, cudaStream_t stream)
+static cudaError_t launch_rope(QkRopeParams &p, cudaStream_t stream)
 {
     const int64_t T = p.a.num_tokens;
     constexpr int kGroups = kRopeThreads / LANES, kTokens = 8;
     const int per = p.a.heads + (p.kc ? 2 : 1) * p.a.kv_heads;
-    // few tokens: a CTA for each group of heads too, one token each
-    const bool few = T <= 2ll * num_sms_current_device();
+    // few tokens: a CTA for each group of heads too, one token each (400 tokens 5.5 us so, 6.0 without; 600 7.4 and 6.6)
+    const int64_t sms = num_sms_current_device();
+    const bool few = T <= 3 * sms;
+    // CTAs of 8 tokens from a wave and a half of them on (8100 tokens: 38.6 us, 40.1 with 4), else of 4 (600: 6.6 us, 9.0
+    // with 8; 2000: 13.5 and 18.2; 6000: 31.3 and 33.1)
+    p.cta_tokens = few ? 1 : T < 12 * kCtas * sms ? 4 : kTokens;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = few ? dim3(static_cast<unsigned>(T), (per + kGroups - 1) / kGroups)
-                      : dim3(static_cast<unsigned>((T + kTokens - 1) / kTokens));
+                      : dim3(static_cast<unsigned>((T + p.cta_tokens - 1) / p.cta_tokens));
     cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -268,7 +272,7 @@ static cudaError_t launch_rope(const QkRopeParams &p, cudaStream_t stream)
 }
 
 template <int LANES>
-static cudaError_t launch_lanes(const QkRopeParams &p, cudaStream_t stream)
+static cudaError_t launch_lanes(QkRopeParams &p, cudaStream_t stream)
 {
     const bool partial = p.a.rot_dim < p.a.head_dim;
     if (p.a.interleaved) return partial ? launch_rope<LANES, true, true>(p, stream) : launch_rope<LANES, true, false>(p, stream);
@@ -276,7 +280,7 @@ static cudaError_t launch_lanes(const QkRopeParams &p, cudaStream_t stream)
 }
 
 // Runs of 4 elements: with 8, for rows that allow it, 8100 tokens of 128 took 55 to 62 us instead of 38.5.
-cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t stream)
+cudaError_t launch_qk_rope(QkRopeParams &p, cudaStream_t stream)
 {
     return p.a.head_dim <= 64 ? launch_lanes<8>(p, stream) : launch_lanes<16>(p, stream);
 }

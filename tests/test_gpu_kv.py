@@ -79,6 +79,21 @@ def test_rotation_to_rows(ws, T, H, Hk, D, rot, inter, norms):
     assert q2 is qd and torch.equal(qd, qo) and torch.equal(kd, ko)
 
 
+@pytest.mark.parametrize("per_sm,more", [(3, 0), (3, 1), (48, -1), (48, 5), (96, 3)])
+def test_rotation_around_the_splits(ws, per_sm, more):
+    """Numbers of tokens around which the tokens of a CTA change, and where the last CTA has few."""
+    T = per_sm * torch.cuda.get_device_properties(0).multi_processor_count + more
+    (q, k, _), (qd, kd, _), (wq, wk) = rope_inputs(T, 3, 1, 24, per_sm)
+    position = torch.randint(0, 100000, (T,), generator=torch.Generator().manual_seed(T))
+    position[-2] = -1
+    qo, ko = torch.full_like(qd, 5.0), torch.full_like(kd, 5.0)
+    KV.lora_qk_rope(qd, kd, i32(position.tolist()), freqs(16).cuda(), ws, wq.cuda(), wk.cuda(), q_out=qo, k_out=ko)
+    on = position >= 0
+    assert_rope(qo, q, wq, position, freqs(16), False, rows=on)
+    assert_rope(ko, k, wk, position, freqs(16), False, rows=on)
+    assert (qo[-2] == 5).all() and (ko[-2] == 5).all()
+
+
 @pytest.mark.parametrize("order", ["phsd", "pshd"])
 @pytest.mark.parametrize("T,H,Hk,D,page,k_rows", [(1, 8, 2, 128, 16, False), (50, 4, 4, 64, 8, True),
                                                   (700, 6, 2, 80, 64, False)])
