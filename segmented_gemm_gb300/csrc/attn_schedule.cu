@@ -47,7 +47,6 @@ constexpr int64_t kSectionBytes = 64 << 20;  // keys and values of the heads tha
 
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const AttnSchedParams p)
 {
-    pdl_launch_dependents();
     extern __shared__ int32_t blk_start[];   // [R + 1] first block of each request
     __shared__ int64_t wsum[32];
     __shared__ int32_t hist[kSchedBuckets];
@@ -65,6 +64,7 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(const Attn
     }
     hist[tid] = 0;
     pdl_wait();
+    pdl_launch_dependents();   // not before: a kernel behind this one may count on what lies ahead of it (kv4_wide.cu)
     // a call whose waits gave up may have left counters behind
     for (int i = tid; i < ACNT_WORDS; i += kSchedThreads)
         if (i != CNT_STATUS) p.counters[i] = 0;

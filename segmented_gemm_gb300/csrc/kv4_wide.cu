@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_wide_plan_kernel(const Kv4Wi
 }
 
 // A warp a tile, as a lane takes it in the attention.  Memory bounds it: 8512 tokens of 8 heads of 128 are 45 MB.
+// It runs beside the attention's list of work (one CTA, 9 us), the launch ahead of it, which lets others start only when
+// the plan is done: so it takes the plan's results at once and waits for the list at its end.
 template <int DP>
 __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4WideParams w, const Kv4AttnParams p)
 {
@@ -88,14 +90,13 @@ __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4Wid
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int in_page = p.page_shift - 4;
     const bool sectors = p.head_dim % 16 == 0;
-    pdl_wait();
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kUnpackThreads / 32);
     const int per_page = kPageTiles * p.kv_heads;
-    const int64_t tiles = static_cast<int64_t>(*w.used) * per_page;
+    const int64_t tiles = static_cast<int64_t>(__ldcg(w.used)) * per_page;
     for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kUnpackThreads + threadIdx.x) >> 5; u < tiles; u += warps) {
         const int page = static_cast<int>(u / per_page), rest = static_cast<int>(u - static_cast<int64_t>(page) * per_page);
         const int h = rest / kPageTiles, in = rest % kPageTiles;
-        const int4 whose = w.pages_of[page];   // request, page of the request, its keys
+        const int4 whose = __ldcg(w.pages_of + page);   // request, page of the request, its keys
         const int t = whose.y * kPageTiles + in;
         if (t * 16 >= whose.z) continue;
         const int from = p.table[whose.x * p.table_stride + (t >> in_page)];
@@ -157,11 +158,12 @@ __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4Wid
                 }
             }
     }
+    pdl_wait();   // the list: the attention waits for this kernel alone
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream)
+cudaError_t launch_kv4_wide_plan(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
@@ -169,12 +171,19 @@ cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cuda
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     pdl_attribute(cfg, at);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_wide_plan_kernel, w, p);
-    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, kv4_wide_plan_kernel, w, p);
+}
+
+cudaError_t launch_kv4_unpack(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream)
+{
     const int64_t most = static_cast<int64_t>(w.pages) * kPageTiles * p.kv_heads / (kUnpackThreads / 32) + 1;
     const int64_t cap = 8ll * num_sms_current_device();
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(most < cap ? most : cap));
     cfg.blockDim = dim3(kUnpackThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    pdl_attribute(cfg, at);
     return cudaLaunchKernelEx(&cfg, p.head_dim <= 64 ? kv4_unpack_kernel<64> : kv4_unpack_kernel<128>, w, p);
 }
 

@@ -352,13 +352,18 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
         w.v = at<uint16_t>(ws, L.v);
         w.max_wide = L.max_wide;
         w.pages = L.pages;
-        if (launch_kv4_wide(w, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LORA_ERR_CUDA;
+        if (launch_kv4_wide_plan(w, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LORA_ERR_CUDA;
         lora_attn_t a = *attn;
         a.cu = w.cu;
         a.num_requests = 2 * L.max_wide + 1;
         const int64_t slot = a.head_dim, head = slot * kKv4WidePage;
         const lora_kv_cache_t c = {w.k, w.v, head * a.kv_heads, head, slot, w.pages, kKv4WidePage, a.kv_heads, a.head_dim};
-        rc = lora_attn_paged(&a, &c, w.table, w.pages, w.pages, w.kv_len, nullptr, at<void>(ws, L.attn), L.attn_bytes, stream);
+        lora_attn_sched_t list;
+        rc = lora_attn_schedule(w.cu, w.kv_len, a.num_requests, a.num_tokens, static_cast<int64_t>(w.pages) * kKv4WidePage, a.heads,
+                                a.kv_heads, a.head_dim, &list, at<void>(ws, L.attn), L.attn_bytes, stream);
+        if (rc) return rc;
+        if (launch_kv4_unpack(w, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LORA_ERR_CUDA;
+        rc = lora_attn_paged(&a, &c, w.table, w.pages, w.pages, w.kv_len, &list, at<void>(ws, L.attn), L.attn_bytes, stream);
         if (rc) return rc;
         p.wide = w.wide;
         p.wide_status = at<int32_t>(ws, L.attn) + CNT_STATUS;

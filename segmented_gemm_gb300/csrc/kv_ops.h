@@ -141,7 +141,8 @@ struct PageCopyParams {
 cudaError_t launch_qk_rope(QkRopeParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_store(const Kv4StoreParams &p, cudaStream_t stream);
 cudaError_t launch_kv4_load(const Kv4LoadParams &p, cudaStream_t stream);
-cudaError_t launch_kv4_wide(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_wide_plan(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_unpack(const Kv4WideParams &w, const Kv4AttnParams &p, cudaStream_t stream);   // behind the list
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream);
 cudaError_t launch_kv_release(const KvPagesParams &p, cudaStream_t stream);
 cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream);
