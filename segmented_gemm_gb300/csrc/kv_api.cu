@@ -42,12 +42,14 @@ static int check_cache4(const lora_kv4_cache_t *c)
     return aligned(c->data, 16) ? LORA_OK : LORA_ERR_ALIGN;
 }
 
-// Whether a step of T tokens of R requests is likely to have wide ones that are worth the launches they
-// need (12 us): many rows a request, or many beyond one token each.
-static bool maybe_wide(int64_t T, int32_t R, int32_t group, int32_t head_dim)
+// Whether a step of T tokens of R requests is likely to have wide ones that are worth it: many rows a request, or
+// many beyond one token each; and enough of them altogether, as the bf16 kernel is slow over a few long rows.
+// One request of 48 tokens of 32/8 heads of 128 over 8000 takes 49 us by blocks of 8 columns, 90 unpacked, 400 tokens
+// 160 and 97; over 1000 keys 48 tokens 18 and 33; 4 requests of 48 over 1000 to 8000 71 and 83; 8 of 32 119 and 87.
+static bool maybe_wide(int64_t T, int32_t R, int32_t group, int32_t kv_heads, int32_t head_dim)
 {
     const int64_t rows = kv4_wide_rows(head_dim);
-    return T * group > R * rows || (T - R) * group >= 16 * rows;
+    return T * group * kv_heads >= kKv4WideTotal && (T * group > R * rows || (T - R) * group >= 16 * rows);
 }
 
 static bool unpack_ok(int64_t tokens) { return tokens >= 0 && tokens <= (int64_t(1) << 24); }
@@ -340,7 +342,7 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
     p.wait_cycles = tc_wait_cycles();
     p.wide = nullptr;
     p.wide_status = nullptr;
-    if (L.max_wide && maybe_wide(p.T, p.R, p.group, p.head_dim)) {   // the wide requests, by the attention over a bf16 cache; then the others
+    if (L.max_wide && maybe_wide(p.T, p.R, p.group, p.kv_heads, p.head_dim)) {   // the wide requests, by the attention over a bf16 cache; then the others
         Kv4WideParams w;
         w.cu = at<int32_t>(ws, L.cu);
         w.kv_len = at<int32_t>(ws, L.kv_len);

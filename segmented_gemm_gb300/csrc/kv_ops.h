@@ -65,9 +65,10 @@ struct Kv4Layout {
 constexpr int kKv4CntGroup = 32;                // first arrival counter; one for each CTA
 constexpr int kKv4WidePage = 128;               // keys of a page of the unpacked cache
 // Most rows (tokens times a group's heads) of a request that is not wide.  8 requests over 1000 to 8000 take, 32/8
-// heads of 128, with 64, 96 and 128 rows each 71, 97 and 124 us by blocks of 8 columns, 99, 103 and 108
-// unpacked; with heads of 64, 64, 128 and 256 rows: 37, 61 and 106, and 68, 71 and 89.
+// heads of 128, with 64, 96 and 128 rows each 68, 93 and 119 us by blocks of 8 columns, 79, 83 and 87
+// unpacked; with heads of 64, 64, 128 and 256 rows: 36, 58 and 102, and 50, 54 and 71.
 constexpr int kv4_wide_rows(int head_dim) { return head_dim <= 64 ? 160 : 96; }
+constexpr int kKv4WideTotal = 6400;             // least rows of all heads of a step with wide requests
 
 struct Kv4AttnParams {
     const uint16_t *q;

@@ -244,7 +244,7 @@ class Kv4Workspace(_Workspace):
                  device="cuda"):
         if unpack_tokens is None:
             group = heads // max(1, kv_heads)
-            chunks = T * group > 96 * R or (T - R) * group >= 1536
+            chunks = T * heads >= 6400 and (T * group > 96 * R or (T - R) * group >= 1536)
             unpack_tokens = (256 << 20) // max(1, 4 * kv_heads * head_dim) if chunks else 0
         self.unpack_tokens = unpack_tokens
         super().__init__(int(_lib().lora_kv4_workspace_size(T, R, heads, kv_heads, head_dim, unpack_tokens)),

@@ -91,7 +91,7 @@ class Step:
         self.cu, self.kv_len = i32(cu), i32(kv)
         self.scale = 1.0 / math.sqrt(D) / scale_q
         rows = 160 if D <= 64 else 96
-        self.any_wide = self.ws.unpack_tokens > 0 and any(x * H // Hk > rows for x in new)
+        self.any_wide = self.ws.unpack_tokens > 0 and T * H >= 6400 and any(x * H // Hk > rows for x in new)
 
     def run(self):
         o = torch.full((self.T, self.H, self.D), float("nan"), dtype=BF, device="cuda")
@@ -125,24 +125,28 @@ def test_single_tokens(H, Hk, D, page):
 
 
 @pytest.mark.parametrize("unpack", [0, None, 512])   # never, all, only the first ones fit
-@pytest.mark.parametrize("H,Hk,D,page", [(8, 2, 128, 16), (14, 2, 64, 32), (3, 3, 96, 64)])
+@pytest.mark.parametrize("H,Hk,D,page", [(8, 2, 128, 16), (14, 2, 64, 32), (3, 3, 96, 64),
+                                         (16, 4, 128, 16), (32, 2, 64, 32), (18, 3, 96, 64)])   # these have wide requests
 def test_chunks_and_single_tokens_mixed(H, Hk, D, page, unpack):
     new, kv = [1, 200, 0, 5, 33, 1, 130, 2, 64], [300, 450, 77, 5, 33, 1, 600, 129, 64]
     Step(new, kv, H, Hk, D, page, seed=H, unpack=unpack, q_pad=16).check(f"{H}/{Hk} d{D} unpack {unpack}")
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(12, 3), (80, 20)])
 @pytest.mark.parametrize("n", [2, 3, 8, 9, 24, 25, 41])
-def test_a_few_tokens_a_request(n, D):
+def test_a_few_tokens_a_request(n, H, Hk, D):
     # around the most rows that a request may have and not be wide, and blocks that end inside a token's heads
-    Step([n, 1, n, 0, n], [n, 90, 400, 20, n + 130], 12, 3, D, 16, seed=n).check(f"{n} tokens")
+    Step([n, 1, n, 0, n], [n, 90, 400, 20, n + 130], H, Hk, D, 16, seed=n).check(f"{n} tokens")
 
 
 def test_rows_that_see_nothing():
     # more new tokens than keys, none at all, and a request that got no pages
-    s = Step([5, 3, 1, 4, 120], [2, 0, 0, 4, 7], 4, 2, 128, 16, seed=3)
-    o, lse = s.check()
-    assert (o[:3] == 0).all() and torch.isinf(lse[:3]).all() and (o[5:9] == 0).all()
+    for H, Hk in ((4, 2), (64, 4)):
+        s = Step([5, 3, 1, 4, 120], [2, 0, 0, 4, 7], H, Hk, 128, 16, seed=3)
+        o, lse = s.check()
+        assert (o[:3] == 0).all() and torch.isinf(lse[:3]).all() and (o[5:9] == 0).all()
+        assert s.any_wide == (H == 64)
     s = Step([5, 3, 1, 4, 120], [2, 0, 0, 4, 7], 4, 2, 128, 16, seed=3, unpack=0)
     s.check()
 
@@ -171,9 +175,10 @@ def test_queries_of_any_size():
     s.check("a row of zeros")
 
 
-@pytest.mark.parametrize("unpack", [0, None])
-def test_nans_and_infinities_stay_in_their_rows(unpack):
-    s = Step([3, 1, 60], [90, 40, 200], 8, 2, 128, 16, seed=9, unpack=unpack)
+@pytest.mark.parametrize("H,unpack", [(8, 0), (8, None), (128, None)])
+def test_nans_and_infinities_stay_in_their_rows(H, unpack):
+    s = Step([3, 1, 60], [90, 40, 200], H, max(2, H // 8), 128, 16, seed=9, unpack=unpack)
+    assert s.any_wide == (H == 128)
     want, _ = s.run()
     s.q[1, 5, 7] = float("nan")
     s.q[3, 0, 0] = float("inf")
@@ -186,9 +191,9 @@ def test_nans_and_infinities_stay_in_their_rows(unpack):
 
 
 def test_rows_of_no_request_and_lengths_out_of_range():
-    for unpack in (0, None):
-        s = Step([1, 60, 2], [50, 90, 20], 8, 2, 128, 16, seed=2, unpack=unpack)
-        o = torch.full((s.T, 8, 128), 3.0, dtype=BF, device="cuda")
+    for H, unpack in ((8, 0), (8, None), (128, None)):
+        s = Step([1, 60, 2], [50, 90, 20], H, max(2, H // 8), 128, 16, seed=2, unpack=unpack)
+        o = torch.full((s.T, H, 128), 3.0, dtype=BF, device="cuda")
         want, _ = s.run()
         s.cu[3], s.cu[0] = s.T - 2, 1          # the first row and the last two belong to nobody now
         KV.lora_kv4_attn(s.q, s.cache, s.table, s.cu, s.kv_len, s.scale, s.ws, o=o)
@@ -208,9 +213,9 @@ def test_rows_of_no_request_and_lengths_out_of_range():
     assert (o[0] == 0).all() and torch.isinf(lse[0]).all() and near(o[1], want[1], 6.0)
 
 
-@pytest.mark.parametrize("unpack", [0, None])
-def test_pages_outside_the_cache_read_as_zeros(unpack):
-    s = Step([1, 64], [60, 130], 8, 2, 128, 16, seed=4, unpack=unpack)
+@pytest.mark.parametrize("H,unpack", [(8, 0), (8, None), (128, None)])
+def test_pages_outside_the_cache_read_as_zeros(H, unpack):
+    s = Step([1, 64], [60, 130], H, max(2, H // 8), 128, 16, seed=4, unpack=unpack)
     for r, j, page in ((0, 1, s.num_pages), (1, 3, -1), (1, 8, 1 << 30)):
         s.table[r, j] = page
         s.keys[r][16 * j:16 * j + 16] = 0
@@ -221,11 +226,13 @@ def test_pages_outside_the_cache_read_as_zeros(unpack):
     assert_attn4(o, lse, *s.reference(), vmax, s.any_wide)
 
 
-def test_strides_streams_and_captured_calls():
-    s = Step([1, 70, 1], [500, 300, 9], 8, 2, 64, 32, seed=6, q_pad=64)
+@pytest.mark.parametrize("H", [8, 96])
+def test_strides_streams_and_captured_calls(H):
+    s = Step([1, 70, 1], [500, 300, 9], H, max(2, H // 8), 64, 32, seed=6, q_pad=64)
+    assert s.any_wide == (H == 96)
     want, lse0 = s.run()
     # o as rows of a wider tensor, heads apart; the table's rows apart; another stream
-    o = torch.full((s.T, 8, 3, 64), 2.0, dtype=BF, device="cuda")
+    o = torch.full((s.T, H, 3, 64), 2.0, dtype=BF, device="cuda")
     table = torch.full((3, s.table.shape[1] + 5), 12345, dtype=torch.int32, device="cuda")
     table[:, :s.table.shape[1]] = s.table
     stream = torch.cuda.Stream()
@@ -234,7 +241,7 @@ def test_strides_streams_and_captured_calls():
     stream.synchronize()
     assert torch.equal(o[:, :, 1], want) and (o[:, :, 0] == 2).all() and (o[:, :, 2] == 2).all()
     # two captured graphs over one workspace, replayed in turn
-    t = Step([1, 2], [90, 700], 8, 2, 64, 32, seed=7)
+    t = Step([1, 2], [90, 700], H, max(2, H // 8), 64, 32, seed=7)
     t.ws = s.ws
     want_t, _ = t.run()
     out = [torch.empty_like(want), torch.empty_like(want_t)]
@@ -282,7 +289,7 @@ def test_a_cache_past_32_bit_offsets():
 
 @pytest.mark.parametrize("budget", [100, 3000])
 def test_waits_that_run_out_are_reported_and_the_next_call_is_right(budget):
-    s = Step([1] * 20 + [300, 7], [2000 - 90 * i for i in range(20)] + [900, 40], 8, 2, 128, 16, seed=5)
+    s = Step([1] * 20 + [300, 7], [2000 - 90 * i for i in range(20)] + [900, 40], 32, 8, 128, 16, seed=5)
     want, _ = s.run()
     statuses = []
     L.lora_set_wait_budget(budget)
@@ -298,9 +305,9 @@ def test_waits_that_run_out_are_reported_and_the_next_call_is_right(budget):
 
 
 def test_workspace_of_a_large_step_serves_smaller_ones():
-    ws = KV.Kv4Workspace(600, 40, 8, 2, 128, unpack_tokens=2048)
+    ws = KV.Kv4Workspace(600, 40, 16, 4, 128, unpack_tokens=2048)
     for new, kv in (([1] * 40, list(range(1, 41))), ([600], [700]), ([1, 64], [9, 300]), ([3], [3]), ([200, 200], [200, 900])):
-        s = Step(new, kv, 8, 2, 128, 16, seed=len(new), unpack=2048)
+        s = Step(new, kv, 16, 4, 128, 16, seed=len(new), unpack=2048)
         s.ws = ws
         s.check(str(new))
     for kw in (dict(o=torch.empty(1, 8, 64, dtype=BF, device="cuda")), dict(lse=torch.empty(3, 8, device="cuda"))):
@@ -314,8 +321,10 @@ def test_workspace_of_a_large_step_serves_smaller_ones():
         KV.lora_kv4_attn(s.q, s.cache, s.table, s.cu, s.kv_len, s.scale, small)
 
 
-def test_debug_library_gives_the_same():
-    s = Step([1, 60, 2], [300, 90, 20], 8, 2, 128, 16, seed=12)
+@pytest.mark.parametrize("H", [8, 128])
+def test_debug_library_gives_the_same(H):
+    s = Step([1, 60, 2], [300, 90, 20], H, max(2, H // 8), 128, 16, seed=12)
+    assert s.any_wide == (H == 128)
     want, _ = s.run()
     L.use_debug_library(True)
     try:
