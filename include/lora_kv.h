@@ -153,7 +153,7 @@ size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t
  * In steps with chunks of prompts (of 6400 rows of all heads), requests of more than 96 rows (new tokens times
  * heads / kv_heads; 160 for a head_dim up to 64), in order as long as they fit, are
  * unpacked there and go through lora_attn_paged's kernel (8 chunks of 64 tokens over
- * 1000 to 8000, 32/8 heads of 128: 134 us so, 226 without).  Up to 2^24, in units of 128 (others are
+ * 1000 to 8000, 32/8 heads of 128: 113 us so, 224 without).  Up to 2^24, in units of 128 (others are
  * rounded down); each such request needs its cached tokens, rounded up to 128.
  */
 int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *cache, const int32_t *block_table,

@@ -2,7 +2,7 @@
 // prompts, whose many rows share each key, so that the tensor cores bound them and
 // not the cache's bytes.  Their keys and values are unpacked to bf16 once (exactly),
 // and the attention over a bf16 cache (attn.cu) runs over that: 8 chunks of 64 tokens over
-// 1000 to 8000 take 134 us so and 226 by blocks of 8 columns, one of 512 over 8000 110 us (87 of them that
+// 1000 to 8000 take 113 us so and 224 by blocks of 8 columns, one of 512 over 8000 102 us (87 of them that
 // kernel, 9 its list, 4 the plan).
 #include <cuda_runtime.h>
 
