@@ -193,7 +193,8 @@ typedef struct {
     int32_t num_pages;
 } lora_kv_pages_t;
 
-/* Bytes of workspace for the calls below (0 for arguments out of range); zero-filled once. */
+/* Bytes of workspace for the calls below (0 for arguments out of range); zero-filled once.  One for a cache of
+ * num_pages serves smaller ones too, in any order. */
 size_t lora_kv_pages_workspace_size(int32_t num_pages);
 
 /*

@@ -92,17 +92,9 @@ static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_head
     return L;
 }
 
-static PagesLayout pages_layout(int32_t num_pages)
+static size_t pages_workspace(int32_t num_pages)
 {
-    PagesLayout L;
-    const size_t n = num_pages, chunks = (n + kPageChunk - 1) / kPageChunk;
-    L.counters = 0;
-    L.used = kStatusBytes;
-    L.free = L.used + align256(n);
-    L.counts = L.free + align256(n);
-    L.map = L.counts + align256(chunks * sizeof(int4));
-    L.total = L.map + align256(n * 4);
-    return L;
+    return kStatusBytes + (static_cast<size_t>(num_pages) + kPageChunk - 1) / kPageChunk * kPagesBlock;
 }
 
 static bool num_pages_ok(int32_t n) { return n > 0 && n < (1 << 28); }
@@ -125,16 +117,12 @@ static int check_pages(const lora_kv_pages_t *a)
 // The workspace, and the parameters that all calls on pages share.
 static int prepare_pages(const lora_kv_pages_t *a, void *ws, size_t ws_bytes, KvPagesParams *p)
 {
-    const PagesLayout L = pages_layout(a->num_pages);
-    const int rc = check_ws(ws, ws_bytes, L.total);
+    const int rc = check_ws(ws, ws_bytes, pages_workspace(a->num_pages));
     if (rc) return rc;
     std::memset(p, 0, sizeof *p);
     p->a = *a;
-    p->counters = at<int32_t>(ws, L.counters);
-    p->used = at<uint8_t>(ws, L.used);
-    p->free = at<uint8_t>(ws, L.free);
-    p->counts = at<int4>(ws, L.counts);
-    p->map = at<int32_t>(ws, L.map);
+    p->counters = at<int32_t>(ws, 0);
+    p->blocks = at<uint8_t>(ws, kStatusBytes);
     return LORA_OK;
 }
 
@@ -375,7 +363,7 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
 
 extern "C" size_t lora_kv_pages_workspace_size(int32_t num_pages)
 {
-    return num_pages_ok(num_pages) ? pages_layout(num_pages).total : 0;
+    return num_pages_ok(num_pages) ? pages_workspace(num_pages) : 0;
 }
 
 extern "C" int lora_kv_release(const lora_kv_pages_t *pages, const int32_t *rows, int32_t num, void *ws, size_t ws_bytes,

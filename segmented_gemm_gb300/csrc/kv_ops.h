@@ -105,20 +105,19 @@ struct Kv4WideParams {
     int32_t max_wide, pages;
 };
 
-// Workspace of the calls on pages (offsets 256-byte aligned; all of it zero at
-// rest but the status, the counts and the map).
-struct PagesLayout {
-    size_t counters, used, free, counts, map, total;
-};
+// Workspace of the calls on pages: the status and the counters, then a block for every kPageChunk pages with what is
+// kept of them: their marks (used, free), the chunk's counts and the map.  A page's place
+// does not depend on how many there are, so a workspace may serve caches of different sizes in turn: the
+// marks are zero at rest, counts and map are written before they are read.
 constexpr int kPagesArrived = 2;                // counter: CTAs done with their reading
 constexpr int kPageChunk = 1024;                // pages that one CTA counts and lists
+constexpr int kPagesFree = kPageChunk, kPagesCounts = 2 * kPageChunk, kPagesMap = kPagesCounts + 256;   // in a block
+constexpr int kPagesBlock = kPagesMap + 4 * kPageChunk;
 
 struct KvPagesParams {
     lora_kv_pages_t a;
     int32_t *counters;
-    uint8_t *used, *free;                       // [num_pages] marks
-    int4 *counts;                               // [chunks]
-    int32_t *map;                               // [num_pages] place + 1 of a page that moves, or 0
+    uint8_t *blocks;                            // [chunks][kPagesBlock]
     // release: rows; fork: parent and child
     const int32_t *rows, *parent, *child;
     int32_t num;
@@ -126,6 +125,16 @@ struct KvPagesParams {
     // compact
     int32_t limit, max_copies;
     int32_t *table_out, *ref_out, *free_out, *head_out;
+
+    __host__ __device__ uint8_t *block(int64_t chunk) const { return blocks + chunk * kPagesBlock; }
+    __host__ __device__ uint8_t *used(int64_t page) const { return block(page / kPageChunk) + page % kPageChunk; }
+    __host__ __device__ uint8_t *free(int64_t page) const { return used(page) + kPagesFree; }
+    __host__ __device__ int4 *counts(int64_t chunk) const { return reinterpret_cast<int4 *>(block(chunk) + kPagesCounts); }
+    // place + 1 of a page that moves, or 0
+    __host__ __device__ int32_t *map(int64_t page) const
+    {
+        return reinterpret_cast<int32_t *>(block(page / kPageChunk) + kPagesMap) + page % kPageChunk;
+    }
 };
 
 struct PageCopyParams {

@@ -30,13 +30,13 @@ __device__ __forceinline__ int held_pages(const lora_kv_pages_t &a, int len, int
 __device__ __forceinline__ int4 add4(int4 a, int4 b) { return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
 // Sum of the chunks' counts before chunk `to`, and of all of them, by the whole block.
-__device__ __forceinline__ int4 sum_counts(const int4 *counts, int chunks, int to, int4 *all, int4 *sm /* [2] */)
+__device__ __forceinline__ int4 sum_counts(const KvPagesParams &p, int chunks, int to, int4 *all, int4 *sm /* [2] */)
 {
     if (threadIdx.x < 2) sm[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
     int4 a = make_int4(0, 0, 0, 0), b = a;
     for (int i = threadIdx.x; i < chunks; i += kThreads) {
-        const int4 c = __ldcg(counts + i);
+        const int4 c = __ldcg(p.counts(i));
         a = add4(a, c);
         if (i < to) b = add4(b, c);
     }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) release_count_kernel(const KvPagesPa
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0 && n) atomicAdd(&sum, n);
     __syncthreads();
-    if (threadIdx.x == 0) p.counts[blockIdx.x] = make_int4(sum, 0, 0, 0);
+    if (threadIdx.x == 0) *p.counts(blockIdx.x) = make_int4(sum, 0, 0, 0);
 }
 
 __global__ void __launch_bounds__(kThreads) release_list_kernel(const KvPagesParams p)
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) release_list_kernel(const KvPagesPar
     const lora_kv_pages_t &a = p.a;
     pdl_wait();
     int4 all;
-    const int before = sum_counts(p.counts, gridDim.x, blockIdx.x, &all, sm).x;
+    const int before = sum_counts(p, gridDim.x, blockIdx.x, &all, sm).x;
     const int head0 = *a.free_head, head = max(0, min(head0, a.num_free)), first = max(0, head - all.x);
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPerThread;
     uint32_t freed = 0;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) compact_mark_kernel(const KvPagesPar
         const int n = held_pages(a, a.ctx_len[r], &flags);
         for (int j = threadIdx.x; j < n; j += kThreads) {
             const int page = a.block_table[r * a.table_stride + j];
-            if (page >= 0 && page < a.num_pages) p.used[page] = 1;
+            if (page >= 0 && page < a.num_pages) *p.used(page) = 1;
             else flags |= LORA_DEV_BAD_PAGE;
         }
     }
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) compact_mark_kernel(const KvPagesPar
     for (int64_t i = head + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < a.num_free;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
         const int page = a.free_pages[i];
-        if (page >= 0 && page < a.num_pages) p.free[page] = 1;
+        if (page >= 0 && page < a.num_pages) *p.free(page) = 1;
         else flags |= LORA_DEV_BAD_PAGE;
     }
     if (flags) atomicOr(p.counters, flags);
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(kThreads) compact_mark_kernel(const KvPagesPar
 // What a page is: bit 0 a hole, bit 8 a mover, bit 16 free from the limit on (so that 16 of a thread add up without carries).
 __device__ __forceinline__ uint32_t kind_of(const KvPagesParams &p, int64_t page, int *both)
 {
-    const bool held = p.used[page], free = p.free[page] && !held;
-    *both |= held && p.free[page];
+    const bool held = *p.used(page), listed = *p.free(page), free = listed && !held;
+    *both |= held && listed;
     return held ? (page >= p.limit ? 1u << 8 : 0u) : free ? (page < p.limit ? 1u : 1u << 16) : 0u;
 }
 
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) compact_count_kernel(const KvPagesPa
         if ((threadIdx.x & 31) == 0 && w) atomicAdd(sum + i, w);
     }
     __syncthreads();
-    if (threadIdx.x == 0) p.counts[blockIdx.x] = make_int4(sum[0], sum[1], sum[2], 0);
+    if (threadIdx.x == 0) *p.counts(blockIdx.x) = make_int4(sum[0], sum[1], sum[2], 0);
     if (both) atomicOr(p.counters, LORA_DEV_BAD_PAGE);
 }
 
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
     const lora_kv_pages_t &a = p.a;
     pdl_wait();
     int4 all;
-    const int4 before = sum_counts(p.counts, gridDim.x, blockIdx.x, &all, sm);
+    const int4 before = sum_counts(p, gridDim.x, blockIdx.x, &all, sm);
     const int moved = min(min(all.x, all.y), p.max_copies);
     const int first = a.num_free - (all.x + all.z);          // the new head: as many are free as before
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPerThread;
@@ -422,9 +422,9 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
             p.free_out[first + (all.x - moved) + high + min(mover, moved)] = id;
             ++high;
         }
-        p.map[page] = map;
+        *p.map(page) = map;
         if (!pair && p.ref_out != a.ref) p.ref_out[page] = a.ref[page];
-        p.used[page] = p.free[page] = 0;
+        *p.used(page) = *p.free(page) = 0;
     }
     for (int64_t i = moved + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < p.max_copies;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
     pdl_wait();
     int4 all;
     const int chunks = (a.num_pages + kPageChunk - 1) / kPageChunk;
-    sum_counts(p.counts, chunks, 0, &all, sm);
+    sum_counts(p, chunks, 0, &all, sm);
     const int moved = min(min(all.x, all.y), p.max_copies), first = a.num_free - (all.x + all.z);
     const bool in_place = p.table_out == a.block_table;
     int flags = 0;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
         for (int j = threadIdx.x; j < (in_place ? n : a.table_width); j += kThreads) {
             int page = a.block_table[r * a.table_stride + j];
             if (j < n && page >= 0 && page < a.num_pages) {
-                const int m = p.map[page];
+                const int m = *p.map(page);
                 if (m) page = p.dst[m - 1];
             }
             p.table_out[r * a.table_stride + j] = page;

@@ -252,7 +252,7 @@ class Kv4Workspace(_Workspace):
 
 
 class PagesWorkspace(_Workspace):
-    """A zero-initialised device workspace for the calls on the pages of a cache of num_pages."""
+    """A zero-initialised device workspace for the calls on the pages of a cache of num_pages, or of fewer."""
 
     def __init__(self, num_pages: int, device="cuda"):
         self.num_pages = num_pages
