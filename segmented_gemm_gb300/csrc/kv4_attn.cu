@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnPara
         now->start = u0 - piece.at;
         now->cost = 0;
     }
+    fence_proxy_async_smem();   // `bases` was written and read as ordinary memory; the ring's copies go there next
     __syncthreads();   // everybody is done with `bases`
 
     // ---- the warp's ring: tiles [fetch_t, fetch_e) of the piece `ahead`, then of those after it, up to
