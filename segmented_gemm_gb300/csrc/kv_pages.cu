@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(const KvPagesP
 // rows 8.7 us by eight CTAs, 12.3 by four launches; 94 pages of 5 rows 7 by eight and 4.3 by one; with 32768 pages and
 // as many entries eight CTAs and four launches take the same 14.
 constexpr int64_t kClusterEntries = 1 << 15;
+constexpr int32_t kSmallList = 4 * kSmallPages;   // longest lists: a CTA goes through them with 32-bit places
 constexpr int kClusterCtas = 8;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -709,8 +710,9 @@ cudaError_t launch_kv_fork(const KvPagesParams &p, cudaStream_t stream)
 cudaError_t launch_kv_compact(const KvPagesParams &p, cudaStream_t stream)
 {
     const int64_t entries = static_cast<int64_t>(p.a.num_rows) * p.a.table_width;
-    if (p.a.num_pages <= kSmallPages && entries <= kSmallEntries) return launch_compact_small<1>(p, stream);
-    if (p.a.num_pages <= kSmallPages && entries <= kClusterEntries) return launch_compact_small<kClusterCtas>(p, stream);
+    const bool small = p.a.num_pages <= kSmallPages && p.a.num_free <= kSmallList && p.max_copies <= kSmallList;
+    if (small && entries <= kSmallEntries) return launch_compact_small<1>(p, stream);
+    if (small && entries <= kClusterEntries) return launch_compact_small<kClusterCtas>(p, stream);
     const int chunks = (p.a.num_pages + kPageChunk - 1) / kPageChunk;
     const int64_t lists = (static_cast<int64_t>(p.a.num_free) + kThreads - 1) / kThreads;
     const int64_t rows = p.a.num_rows > lists ? p.a.num_rows : lists;

@@ -61,3 +61,39 @@ def test_one_workspace_serves_caches_of_several_sizes(sizes):
         s.release(rows)
         assert_state(d, s, f"{pages} pages: release")
         L.lora_get_status(ws)                       # (a list without room for what comes back)
+
+
+@pytest.mark.parametrize("rows,width", [(4, 40), (100, 60)])
+@pytest.mark.parametrize("extra", [0, 4 * 32768, (1 << 31) - 1 - 3000])
+def test_lists_longer_than_the_cache(rows, width, extra):
+    """A free list whose taken part is long, up to the longest there may be (8.6 GB), and as many places for pairs as
+    fit: places past 2^31 - 2^13 in it once wrapped to negative ones."""
+    pages, page = 3000, 16
+    s = random_state(pages, rows, width, page, random.Random(rows))
+    tail = s.free
+    wide = torch.empty(extra + len(tail), dtype=torch.int32, device="cuda")
+    wide[extra:] = i32(tail)
+    d = device_state(s)
+    d["free_pages"], d["free_head"] = wide, i32([extra + s.head])
+    ws = KV.PagesWorkspace(pages)
+    src, dst = KV.lora_kv_compact(limit=pages // 2, ws=ws, max_copies=pages, **d)
+    assert L.lora_get_status(ws) == 0
+    assert list(zip(src.tolist(), dst.tolist())) == s.compact(pages // 2, pages)
+    for name, want in (("ctx_len", s.ctx), ("block_table", s.table), ("ref", s.ref), ("free_head", [extra + s.head])):
+        assert d[name].tolist() == want, name
+    assert wide[extra + s.head:].tolist() == s.free[s.head:]
+
+
+def test_places_for_more_pairs_than_32_bits_step_over():
+    """max_copies of 2^31 - 1 (two arrays of 8.6 GB): the places behind the last pair are all -1."""
+    pages, page, most = 3000, 16, (1 << 31) - 1
+    s = random_state(pages, 4, 40, page, random.Random(2))
+    d, ws = device_state(s), KV.PagesWorkspace(pages)
+    src, dst = KV.lora_kv_compact(limit=pages // 2, ws=ws, max_copies=most, **d)
+    assert L.lora_get_status(ws) == 0
+    pairs = s.compact(pages // 2, pages)
+    assert list(zip(src[:pages].tolist(), dst[:pages].tolist())) == pairs
+    n = sum(a >= 0 for a, _ in pairs)
+    for x in (src, dst):
+        for part in x[n:].split(1 << 28):
+            assert int(part.min()) == -1 and int(part.max()) == -1
