@@ -42,14 +42,14 @@ static int check_cache4(const lora_kv4_cache_t *c)
     return aligned(c->data, 16) ? LORA_OK : LORA_ERR_ALIGN;
 }
 
-// Whether a step of T tokens of R requests is likely to have wide ones that are worth it: many rows a request, or
-// many beyond one token each; and enough of them altogether, as the bf16 kernel is slow over a few long rows.
+// Whether a step of T tokens of R requests, with room for wide ones (kv4_layout: rows enough altogether, as the bf16
+// kernel is slow over a few long rows), is likely to have some: many rows a request, or many beyond one token each.
 // One request of 48 tokens of 32/8 heads of 128 over 8000 takes 49 us by blocks of 8 columns, 90 unpacked, 400 tokens
 // 160 and 97; over 1000 keys 48 tokens 18 and 33; 4 requests of 48 over 1000 to 8000 71 and 83; 8 of 32 119 and 87.
 static bool maybe_wide(int64_t T, int32_t R, int32_t group, int32_t kv_heads, int32_t head_dim)
 {
     const int64_t rows = kv4_wide_rows(head_dim);
-    return T * group * kv_heads >= kKv4WideTotal && (T * group > R * rows || (T - R) * group >= 16 * rows);
+    return T * group > R * rows || (T - R) * group >= 16 * rows;
 }
 
 static bool unpack_ok(int64_t tokens) { return tokens >= 0 && tokens <= (int64_t(1) << 24); }
@@ -66,8 +66,8 @@ static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_head
     };
     L.counters = take((kKv4CntGroup + kKv4MaxCtas) * 4);
     L.zeros = take(kv4_tile_bytes(128));
-    // wide requests: no more than the rows allow, or than lists have places
-    L.max_wide = static_cast<int32_t>(
+    // wide requests: none in steps of few rows, and no more than the rows allow, or than lists have places
+    L.max_wide = T * heads < kKv4WideTotal ? 0 : static_cast<int32_t>(
         std::min<int64_t>({R, T * (heads / kv_heads) / (kv4_wide_rows(head_dim) + 1), LORA_MAX_REQUESTS / 2 - 1}));
     L.pages = static_cast<int32_t>(unpack / kKv4WidePage);
     if (L.max_wide == 0 || L.pages == 0) L.max_wide = L.pages = 0;

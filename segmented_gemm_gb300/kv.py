@@ -234,20 +234,21 @@ class _Workspace:
 
 
 class Kv4Workspace(_Workspace):
-    """A zero-initialised device workspace for lora_kv4_attn over steps of T packed
-    tokens and R requests; serves the small calls (lora_qk_rope, lora_kv4_store,
+    """A zero-initialised device workspace for lora_kv4_attn over steps of up to T
+    packed tokens and R requests; serves the small calls (lora_qk_rope, lora_kv4_store,
     lora_kv4_load) too.  unpack_tokens: how many cached tokens of chunks of
-    prompts it has room for in bf16; by default what 256 MiB hold if T tokens of R requests
-    have chunks among them, else none."""
+    prompts it has room for in bf16; by default what 256 MiB hold if a step of T tokens of any number of
+    requests may have chunks that take them, else none.  0 for steps of single tokens saves that."""
 
     def __init__(self, T: int, R: int, heads: int, kv_heads: int, head_dim: int, unpack_tokens: Optional[int] = None,
                  device="cuda"):
+        size = _lib().lora_kv4_workspace_size
         if unpack_tokens is None:
-            group = heads // max(1, kv_heads)
-            chunks = T * heads >= 6400 and (T * group > 96 * R or (T - R) * group >= 1536)
-            unpack_tokens = (256 << 20) // max(1, 4 * kv_heads * head_dim) if chunks else 0
+            unpack_tokens = (256 << 20) // max(1, 4 * kv_heads * head_dim)
+            if size(T, R, heads, kv_heads, head_dim, unpack_tokens) == size(T, R, heads, kv_heads, head_dim, 0):
+                unpack_tokens = 0
         self.unpack_tokens = unpack_tokens
-        super().__init__(int(_lib().lora_kv4_workspace_size(T, R, heads, kv_heads, head_dim, unpack_tokens)),
+        super().__init__(int(size(T, R, heads, kv_heads, head_dim, unpack_tokens)),
                          "Kv4Workspace: token, request or head counts out of range", device)
 
 
