@@ -143,16 +143,16 @@ size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t
  * lora_attn_paged over a 4-bit cache: the same arguments, the same rows, over
  * the values that the cache stands for.  Needs no schedule.  q keeps its bf16
  * values (elements below 2^-26 of their row's largest lose bits, rows below 2^-114
- * are zeros), p is rounded to 16 bits for the second product, o to bf16 once; scores,
- * statistics and sums are fp32.  Keys and values past a row's request are never mixed in, whatever
- * they hold.  kv_len is clamped to [0, table_width * page_size], offsets to [0,
+ * are zeros), p is rounded to fp16 (11 bits) for the second product whichever way a request
+ * takes, o to bf16 once; scores, statistics and sums are fp32.  Keys and values past a row's
+ * request are never mixed in, whatever they hold.  kv_len is clamped to [0, table_width * page_size], offsets to [0,
  * num_tokens] (LORA_DEV_BAD_LENGTH).  A page outside the cache reads as zeros
  * (LORA_DEV_BAD_PAGE).
  *
- * unpack_tokens: keys and values that the workspace has room for in bf16 (0: none).
+ * unpack_tokens: keys and values that the workspace has room for in 16 bits (0: none).
  * In steps with chunks of prompts (of 6400 rows of all heads), requests of more than 96 rows (new tokens times
  * heads / kv_heads; 160 for a head_dim up to 64), in order as long as they fit, are
- * unpacked there and go through lora_attn_paged's kernel (8 chunks of 64 tokens over
+ * unpacked there, exactly, and go through lora_attn_paged's kernel in a form with p in fp16 (8 chunks of 64 tokens over
  * 1000 to 8000, 32/8 heads of 128: 113 us so, 224 without).  Up to 2^24, in units of 128 (others are
  * rounded down); each such request needs its cached tokens, rounded up to 128.
  */

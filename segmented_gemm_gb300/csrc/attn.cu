@@ -66,6 +66,12 @@ namespace lora {
 constexpr int kAttnThreads = 384;
 constexpr int kItems = 4;             // work items in flight between the loader and the others
 constexpr float kMostP = 0x1p40f;     // half a tile whose p sum to more than this moves m_i
+// Values of a 4-bit cache (kv4_wide.cu; kF16): fp16 has them exactly, and p with three bits more than bf16: the outputs are 0.0017
+// of their norm off fp64, 0.0023 with p in bf16.  What it lacks is bf16's range: p is 2^kLiftF16 where the score is m_i, at most
+// kMostPF16, and has all its bits down to 2^-21, some to 2^-31, of what it is at m_i (kv4_attn.cu has the same
+// range).  So that m_i need not move soon it starts as the largest of eight scores: chunks of up to 700 over 9000
+// take 152 us so, 154 with the first one, 157 with the largest of 64; 150 with p in bf16.
+constexpr float kMostPF16 = 65504.f, kLiftF16 = 7.f;
 
 // tensor memory columns (512 in all): S of stream s at s * 128, O at 256 + s * DP.
 // With a head dimension of 128 that is all of them, and P lies over S's first 64:
@@ -213,6 +219,13 @@ __device__ __forceinline__ bool attn_wait_count(const int *count, int n, volatil
     return ld_volatile_shared(count) > n || attn_wait_count_loop(count, n, abort_flag, limit);
 }
 
+// log2 of a sum of p, as if p were 1 where the score is m_i
+template <bool kF16>
+__device__ __forceinline__ float log2_sum(float l)
+{
+    return kF16 ? log2f(l) - kLiftF16 : log2f(l);
+}
+
 // First row of the partial results of a group's piece k, of the group that starts in
 // unit unit0: the last piece of that unit, then the first of the units after it.
 __device__ __forceinline__ int64_t join_slot(const AttnParams &p, int unit0, int k)
@@ -228,6 +241,7 @@ __device__ __forceinline__ int64_t join_slot(const AttnParams &p, int unit0, int
 // its own: inlined it costs the softmax loop registers.  A few rows (at most one
 // element a thread, often of many pieces) are joined where it is called instead, with
 // four pieces in flight: one decoded token takes 9.0 us so, 10.6 through this function.
+template <bool kF16>
 __device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0, int kvh, int parts, int unit0, float c)
 {
     const int G = p.group, D = p.head_dim, rows = ntok * G, d4 = D / 4;
@@ -278,20 +292,21 @@ __device__ __noinline__ void join_pieces(const AttnParams &p, int ntok, int tok0
             *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col[j]) =
                 make_uint2(pack_bf16x2(a[j][0] * inv, a[j][1] * inv), pack_bf16x2(a[j][2] * inv, a[j][3] * inv));
             if (p.lse && col[j] == 0)
-                p.lse[row * p.heads + hd] =
-                    ll[j] == 0.f ? -INFINITY : (mm[j] * c + log2f(ll[j])) * 0.6931471805599453f;
+                p.lse[row * p.heads + hd] = ll[j] == 0.f ? -INFINITY : (mm[j] * c + log2_sum<kF16>(ll[j])) * 0.6931471805599453f;
         }
     }
 }
 
-// kTwo: lists whose units are two heads of few rows are run too
-template <int DP, bool kPaged, bool kTwo>
+// kTwo: lists whose units are two heads of few rows are run too.  kF16: p and the values are fp16
+template <int DP, bool kPaged, bool kTwo, bool kF16>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
 {
     using Sm = AttnSmem<DP>;
     constexpr int kStages = Sm::kStages, kTile = Sm::kTile, kHalves = Sm::kHalves;
     constexpr bool kOwnP = Sm::kOwnP;
+    constexpr float kMost = kF16 ? kMostPF16 : kMostP;
+    auto pack_p = [](float a, float b) { return kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b); };
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qbuf = smem, *ring = smem + 2 * kTile;
@@ -560,7 +575,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t qlo = umma_lo(smem_u32(qbuf), 16);
         const uint32_t klo = umma_lo(smem_u32(ring), 16), vlo = umma_lo(smem_u32(ring), kAttnTileK * 128);
         const int dsteps = (p.head_dim + 15) / 16;
-        const uint32_t idesc_pv = umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
+        const uint32_t idesc_pv = kF16 ? umma_idesc_f16_bn(kAttnTileQ, dsteps * 16) : umma_idesc_bf16_bn(kAttnTileQ, dsteps * 16);
         const uint32_t s_cells = tmem_u + s * kColS, o_cells = tmem_u + kColO + s * DP;
         const uint32_t p_cells = kOwnP ? tmem_u + kColP + s * 64 : s_cells;
         auto commit = [&](uint64_t *bar) { umma_commit_if(elect_one(), bar); };
@@ -696,6 +711,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t t_p = kOwnP ? tmem + lanes + kColP + s * 64 : t_s;
         const int G = p.group, D = p.head_dim;
         const float c = p.scale * 1.4426950408889634f;
+        auto offset = [&](float m) {   // p = 2^(c x + offset(m))
+            if (kF16) return m == -INFINITY ? 0.f : fmaf(-m, c, kLiftF16);
+            return m == -INFINITY ? 0.f : -m * c;
+        };
         uint32_t nitem = 0, ns = 0, no = 0, nx = 0, nt = 0;
         auto meet = [&] {   // all 256 threads
             __syncwarp();
@@ -814,7 +833,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 for (int j = 0; j < 16; ++j) pk[2 * j + 1] = 0;
                                 continue;
                             }
-                            const float off = nm[h] == -INFINITY ? 0.f : -nm[h] * c;
+                            const float off = offset(nm[h]);
                             const uint64_t off2 = pack_f2(off, off);
                             uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -824,13 +843,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 a = ex2(a);
                                 b = ex2(b);
                                 sum[j & 1] = add_f2(sum[j & 1], pack_f2(a, b));
-                                pk[2 * j + h] = pack_bf16x2(a, b);
+                                pk[2 * j + h] = pack_p(a, b);
                             }
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
                             part[h] = a + b;
                         }
-                        move = part[0] > kMostP || part[1] > kMostP;
+                        move = part[0] > kMost || part[1] > kMost;
                         if (round == 1 || !__any_sync(0xffffffffu, move)) {
                             nl[0] += part[0];
                             nl[1] += part[1];
@@ -870,11 +889,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 64; ++e) x[e] = e < seen ? x[e] : -INFINITY;
                         }
-                        if (h == 0) m = m == -INFINITY ? x[0] : m;   // the first score (-infinity if it is not seen)
+                        if (h == 0) {   // the first score (-infinity if it is not seen), or the largest of the first few
+                            float first = x[0];
+                            if (kF16 && k == 0) {
+#pragma unroll
+                                for (int e = 1; e < 8; ++e) first = fmaxf(first, x[e]);
+                            }
+                            m = m == -INFINITY ? first : m;
+                        }
                         uint32_t pk[32];
                         float total;
                         auto exps = [&] {
-                            const float off = m == -INFINITY ? 0.f : -m * c;
+                            const float off = offset(m);
                             const uint64_t off2 = pack_f2(off, off);
                             uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -884,14 +910,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 a = ex2(a);
                                 b = ex2(b);
                                 sum[e & 1] = add_f2(sum[e & 1], pack_f2(a, b));
-                                pk[e] = pack_bf16x2(a, b);
+                                pk[e] = pack_p(a, b);
                             }
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
                             total = a + b;
                         };
                         exps();
-                        if (__any_sync(0xffffffffu, total > kMostP || (m == -INFINITY && seen > 0))) {
+                        if (__any_sync(0xffffffffu, total > kMost || (m == -INFINITY && seen > 0))) {
                             if (h == 0) {
                                 products_done();
                             } else {
@@ -1046,7 +1072,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 p.part_ml[static_cast<int64_t>(w.slot) * p.part_rows + row] = make_float2(nm[h], nl[h]);
                             else if (p.lse)
                                 p.lse[at * p.heads + head] =
-                                    nl[h] == 0.f ? -INFINITY : (nm[h] * c + log2f(nl[h])) * 0.6931471805599453f;
+                                    nl[h] == 0.f ? -INFINITY : (nm[h] * c + log2_sum<kF16>(nl[h])) * 0.6931471805599453f;
                         }
                     }
                 }
@@ -1104,7 +1130,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (!whole)
                         p.part_ml[static_cast<int64_t>(w.slot) * p.part_rows + rho] = make_float2(m, l);
                     else if (p.lse)
-                        p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+                        p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (m * c + log2_sum<kF16>(l)) * 0.6931471805599453f;
                 }
             }
             if (w.parts > 1) {
@@ -1116,7 +1142,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (*join_flag) {
                     const int d4 = D / 4, all = w.ntok * G * d4;
                     if (all > 256) {
-                        join_pieces(p, w.ntok, w.tok0, w.kvh, w.parts, w.unit0, c);
+                        join_pieces<kF16>(p, w.ntok, w.tok0, w.kvh, w.parts, w.unit0, c);
                     } else if (threadIdx.x < all) {   // a thread's element, four pieces in flight
                         const int rr = threadIdx.x / d4, col = (threadIdx.x - rr * d4) * 4;
                         float mm = -INFINITY, ll = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1139,7 +1165,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         *reinterpret_cast<uint2 *>(p.o + row * p.o_tok + hd * p.o_head + col) =
                             make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
                         if (p.lse && col == 0)
-                            p.lse[row * p.heads + hd] = ll == 0.f ? -INFINITY : (mm * c + log2f(ll)) * 0.6931471805599453f;
+                            p.lse[row * p.heads + hd] = ll == 0.f ? -INFINITY : (mm * c + log2_sum<kF16>(ll)) * 0.6931471805599453f;
                     }
                     if (threadIdx.x == 0) p.counters[ACNT_GROUP + w.unit0] = 0;
                 }
@@ -1174,7 +1200,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int DP, bool kPaged, bool kTwo>
+template <int DP, bool kPaged, bool kTwo, bool kF16 = false>
 static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_t stream)
 {
     static int configured[64] = {0};
@@ -1183,7 +1209,7 @@ static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_
     constexpr int bytes = AttnSmem<DP>::kBytes;
     if (dev >= 64 || !configured[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(attn_kernel<DP, kPaged, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaFuncSetAttribute(attn_kernel<DP, kPaged, kTwo, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = 1;
     }
@@ -1194,7 +1220,7 @@ static cudaError_t launch(const AttnMaps &maps, const AttnParams &p, cudaStream_
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     pdl_attribute(cfg, at);
-    return cudaLaunchKernelEx(&cfg, attn_kernel<DP, kPaged, kTwo>, maps, p);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<DP, kPaged, kTwo, kF16>, maps, p);
 }
 
 cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
@@ -1234,6 +1260,7 @@ cudaError_t launch_attn(AttnParams &p, cudaStream_t stream)
             return cudaErrorInvalidValue;
     }
     if (!p.paged) return p.head_dim <= 64 ? launch<64, false, false>(m, p, stream) : launch<128, false, false>(m, p, stream);
+    if (p.f16) return p.head_dim <= 64 ? launch<64, true, false, true>(m, p, stream) : launch<128, true, false, true>(m, p, stream);
     if (p.two) return p.head_dim <= 64 ? launch<64, true, true>(m, p, stream) : launch<128, true, true>(m, p, stream);
     return p.head_dim <= 64 ? launch<64, true, false>(m, p, stream) : launch<128, true, false>(m, p, stream);
 }

@@ -123,6 +123,7 @@ struct AttnParams {
     int32_t table_width, num_pages, page_shift;
     int64_t page_stride, head_stride, slot_stride;
     int32_t paged;
+    int32_t f16;             // paged: the values are fp16, and p is rounded to it (the unpacked keys and values of a 4-bit cache)
     int32_t box_rows;        // keys of one TMA box
     int32_t o_wide;          // every row of o starts on a 32-byte boundary
     int64_t T;
@@ -158,6 +159,11 @@ cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
 cudaError_t launch_kv_store(const KvStoreParams &p, cudaStream_t stream);
 cudaError_t launch_attn_schedule(const AttnSchedParams &p, cudaStream_t stream);
 cudaError_t launch_attn(AttnParams &p, cudaStream_t stream);   // fills in box_rows
+
+// lora_attn_paged; f16: over values in fp16 instead of bf16 (batches of single tokens, two_heads, have no such kernel)
+int attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *cache, const int32_t *block_table, int32_t table_width,
+               int64_t table_stride, const int32_t *kv_len, const lora_attn_sched_t *sched, bool f16, void *ws,
+               size_t ws_bytes, cudaStream_t stream);
 
 // Launch attribute of a programmatic dependent launch: the kernel may start
 // its prologue while the one ahead finishes (every kernel here waits for it

@@ -164,6 +164,40 @@ static int prepare_attn(const lora_attn_t *a, const int32_t *kv_len, int64_t max
     return LORA_OK;
 }
 
+int attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *cache, const int32_t *block_table, int32_t table_width,
+               int64_t table_stride, const int32_t *kv_len, const lora_attn_sched_t *sched, bool f16, void *ws,
+               size_t ws_bytes, cudaStream_t stream)
+{
+    int rc = check_attn(attn);
+    if (rc) return rc;
+    rc = check_cache(cache);
+    if (rc) return rc;
+    if (cache->kv_heads != attn->kv_heads || cache->head_dim != attn->head_dim) return LORA_ERR_SHAPE;
+    if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > kMaxTokens) return LORA_ERR_SHAPE;
+    if (attn->num_requests > 1 && table_stride < table_width) return LORA_ERR_SHAPE;
+    if (attn->num_tokens == 0 || attn->num_requests == 0) return LORA_OK;
+    if (!kv_len || (table_width > 0 && !block_table)) return LORA_ERR_NULL;
+    if (!ints_aligned({kv_len, block_table})) return LORA_ERR_ALIGN;
+    AttnParams p;
+    rc = prepare_attn(attn, kv_len, static_cast<int64_t>(table_width) * cache->page_size, sched, ws, ws_bytes,
+                      stream, &p);
+    if (rc) return rc;
+    if (f16 && p.two) return LORA_ERR_SHAPE;
+    p.k = cache->k;
+    p.v = cache->v;
+    p.paged = 1;
+    p.f16 = f16;
+    p.block_table = block_table;
+    p.table_stride = table_stride;
+    p.table_width = table_width;
+    p.num_pages = cache->num_pages;
+    p.page_shift = page_shift(cache->page_size);
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.slot_stride = cache->slot_stride;
+    return launch_attn(p, stream) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
 }  // namespace lora
 
 using namespace lora;
@@ -273,32 +307,8 @@ extern "C" int lora_attn_paged(const lora_attn_t *attn, const lora_kv_cache_t *c
                                int32_t table_width, int64_t table_stride, const int32_t *kv_len,
                                const lora_attn_sched_t *sched, void *ws, size_t ws_bytes, lora_stream_t stream)
 {
-    int rc = check_attn(attn);
-    if (rc) return rc;
-    rc = check_cache(cache);
-    if (rc) return rc;
-    if (cache->kv_heads != attn->kv_heads || cache->head_dim != attn->head_dim) return LORA_ERR_SHAPE;
-    if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > kMaxTokens) return LORA_ERR_SHAPE;
-    if (attn->num_requests > 1 && table_stride < table_width) return LORA_ERR_SHAPE;
-    if (attn->num_tokens == 0 || attn->num_requests == 0) return LORA_OK;
-    if (!kv_len || (table_width > 0 && !block_table)) return LORA_ERR_NULL;
-    if (!ints_aligned({kv_len, block_table})) return LORA_ERR_ALIGN;
-    AttnParams p;
-    rc = prepare_attn(attn, kv_len, static_cast<int64_t>(table_width) * cache->page_size, sched, ws, ws_bytes,
-                      static_cast<cudaStream_t>(stream), &p);
-    if (rc) return rc;
-    p.k = cache->k;
-    p.v = cache->v;
-    p.paged = 1;
-    p.block_table = block_table;
-    p.table_stride = table_stride;
-    p.table_width = table_width;
-    p.num_pages = cache->num_pages;
-    p.page_shift = page_shift(cache->page_size);
-    p.page_stride = cache->page_stride;
-    p.head_stride = cache->head_stride;
-    p.slot_stride = cache->slot_stride;
-    return launch_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+    return attn_paged(attn, cache, block_table, table_width, table_stride, kv_len, sched, false, ws, ws_bytes,
+                      static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int lora_attn_prompt(const lora_attn_t *attn, const lora_bf16_t *k, int64_t k_token_stride,

@@ -78,6 +78,11 @@ __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xfffff
 // Instruction descriptor as umma_idesc_bf16, with B stored N-major (its N
 // elements contiguous).
 __device__ __forceinline__ uint32_t umma_idesc_bf16_bn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
+// The same with A and B in fp16 (format 0 where bf16 is 1).
+__device__ __forceinline__ uint32_t umma_idesc_f16_bn(int M, int N)
+{
+    return umma_idesc_bf16_bn(M, N) & ~((1u << 7) | (1u << 10));
+}
 
 // Tiled loads for the lanes with `on` set (one); dst and bar: shared addresses.
 __device__ __forceinline__ void tma_load_3d_if(uint32_t on, uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y,

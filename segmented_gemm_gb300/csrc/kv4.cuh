@@ -36,17 +36,24 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t v)
     return __byte_perm(v, 0u, I | 0x40 | (J << 8) | 0x4000) << 7;
 }
 
-// 8 codes and their scale -> 8 bf16 values (exact: 6 significant bits).
-__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale)
+// 8 codes and their scale -> 8 fp16 values (exact).
+__device__ __forceinline__ uint4 kv4_values_f16(uint32_t codes, uint32_t scale)
 {
     uint32_t f[4];
     e2m1x8_to_f16(codes, f);
     const uint32_t s = scale_pair<0, 0>(scale);
+    return make_uint4(mul_f16x2(f[0], s), mul_f16x2(f[1], s), mul_f16x2(f[2], s), mul_f16x2(f[3], s));
+}
+
+// 8 codes and their scale -> 8 bf16 values (exact: 6 significant bits).
+__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale)
+{
+    const uint4 v = kv4_values_f16(codes, scale);
+    const uint32_t two[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t two = mul_f16x2(f[i], s);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&two[i]));
         o[i] = pack_bf16x2(x.x, x.y);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);

@@ -74,13 +74,6 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t transposed(uint32_t v)
 {
     uint32_t r;

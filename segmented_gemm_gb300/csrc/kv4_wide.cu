@@ -1,7 +1,7 @@
 // The wide requests of a step over the 4-bit cache (lora_kv4_attn): chunks of
 // prompts, whose many rows share each key, so that the tensor cores bound them and
-// not the cache's bytes.  Their keys and values are unpacked to bf16 once (exactly),
-// and the attention over a bf16 cache (attn.cu) runs over that: 8 chunks of 64 tokens over
+// not the cache's bytes.  Their keys are unpacked to bf16 and their values to fp16 once (exactly), and the attention over a
+// bf16 cache (attn.cu) runs over that, with p in fp16 as in the kernel for the other requests: 8 chunks of 64 tokens over
 // 1000 to 8000 take 113 us so and 224 by blocks of 8 columns, one of 512 over 8000 102 us (87 of them that
 // kernel, 9 its list, 4 the plan).
 #include <cuda_runtime.h>
@@ -144,12 +144,12 @@ __global__ void __launch_bounds__(kUnpackThreads) kv4_unpack_kernel(const Kv4Wid
                 const int d = g * (DP / 8);
                 const uint32_t scale = vs >> (8 * (2 * e + o)) & 0xFF;
                 uint16_t *to = w.v + row + (8 * e + 2 * c + o) * p.head_dim + d;
-                const uint4 lo = kv4_values(v[e][o], scale);
+                const uint4 lo = kv4_values_f16(v[e][o], scale);
                 if (DP == 64) {
                     if (d < p.head_dim) *reinterpret_cast<uint4 *>(to) = lo;
                     continue;
                 }
-                const uint4 hi = kv4_values(v[e][DP == 64 ? o : o + 2], scale);
+                const uint4 hi = kv4_values_f16(v[e][DP == 64 ? o : o + 2], scale);
                 if (sectors) {
                     if (d < p.head_dim) store32(to, lo, hi);
                 } else {

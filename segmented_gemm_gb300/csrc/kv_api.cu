@@ -353,7 +353,8 @@ extern "C" int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *ca
                                 a.kv_heads, a.head_dim, &list, at<void>(ws, L.attn), L.attn_bytes, stream);
         if (rc) return rc;
         if (launch_kv4_unpack(w, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LORA_ERR_CUDA;
-        rc = lora_attn_paged(&a, &c, w.table, w.pages, w.pages, w.kv_len, &list, at<void>(ws, L.attn), L.attn_bytes, stream);
+        rc = attn_paged(&a, &c, w.table, w.pages, w.pages, w.kv_len, &list, true, at<void>(ws, L.attn), L.attn_bytes,
+                        static_cast<cudaStream_t>(stream));
         if (rc) return rc;
         p.wide = w.wide;
         p.wide_status = at<int32_t>(ws, L.attn) + CNT_STATUS;

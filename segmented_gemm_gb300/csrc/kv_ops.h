@@ -101,7 +101,7 @@ struct Kv4WideParams {
     int4 *pages_of;                             // [pages] request, page of the request, its keys
     int32_t *used;                              // unpacked pages
     int32_t *table;                             // [2 max_wide + 1][pages]
-    uint16_t *k, *v;                            // [pages][kv_heads][kKv4WidePage][head_dim]
+    uint16_t *k, *v;                            // [pages][kv_heads][kKv4WidePage][head_dim], bf16 and fp16
     int32_t max_wide, pages;
 };
 

@@ -348,6 +348,13 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16])
 // ---------------------------------------------------------------------------
 // bf16 packing (round to nearest even, NaN kept quiet)
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
     uint32_t r;

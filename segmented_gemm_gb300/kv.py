@@ -237,7 +237,7 @@ class Kv4Workspace(_Workspace):
     """A zero-initialised device workspace for lora_kv4_attn over steps of up to T
     packed tokens and R requests; serves the small calls (lora_qk_rope, lora_kv4_store,
     lora_kv4_load) too.  unpack_tokens: how many cached tokens of chunks of
-    prompts it has room for in bf16; by default what 256 MiB hold if a step of T tokens of any number of
+    prompts it has room for in 16 bits; by default what 256 MiB hold if a step of T tokens of any number of
     requests may have chunks that take them, else none.  0 for steps of single tokens saves that."""
 
     def __init__(self, T: int, R: int, heads: int, kv_heads: int, head_dim: int, unpack_tokens: Optional[int] = None,

@@ -1,5 +1,6 @@
 """Attention over the 4-bit cache (include/lora_kv.h) against fp64 to within what
 each of its paths rounds, at the places where its shares, rings and joins change."""
+import math
 import os
 import sys
 
@@ -13,6 +14,8 @@ sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 from test_gpu_kv4_attn import Step  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+U = 2.0 ** -8
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -41,3 +44,59 @@ def test_a_workspace_of_the_largest_step_unpacks_the_chunks_of_smaller_ones(H, H
     assert torch.equal(o, want) and torch.equal(lse2, lse) and L.lora_get_status(server) == 0
     s.ws = KV.Kv4Workspace(512, 1, H, Hk, D, unpack_tokens=0)
     assert not torch.equal(s.check()[0], want)
+
+
+def check_exactly(s, what=""):
+    """Within what either path rounds.  o goes to bf16 once (U of it).  p goes to fp16: 2^-11 of sum_j p_j |v_j|, and where p is
+    below 2^-14, 2^-25 absolutely; a row's largest p is at least 2^7, so its sum is, and the latter is at most 2^-32 max |v|
+    a key.  A score's fp32 sum of up to 128 exact products loses at most 2^-20 of the sum of their magnitudes, below 100 (in
+    powers of two) at these sizes, and sums of p and of products some 2^-20 of themselves: 2e-4 in all."""
+    o, lse = s.run()
+    assert L.lora_get_status(s.ws) == 0, what
+    ref_o, ref_lse, mass = s.reference()
+    vmax = max([float(v.abs().max()) for v in s.values if v.numel()] + [0.0])
+    err = (o.double().cpu() - ref_o).abs()
+    tol = U * ref_o.abs() + (2.0 ** -11 + 2e-4) * mass + max(s.kv) * 2.0 ** -32 * vmax
+    assert torch.isfinite(o).all() and (err <= tol).all(), f"{what}: worst {(err / tol).max():.2f} x tol"
+    empty = torch.isinf(ref_lse)
+    lse = lse.double().cpu()
+    assert torch.equal(lse == -math.inf, empty), what
+    assert empty.all() or float((lse - ref_lse)[~empty].abs().max()) <= 2e-4, what
+
+
+@pytest.mark.parametrize("sharp", [1.0, 8.0])   # 8: scores some 30 above and below a row's first one
+@pytest.mark.parametrize("unpack", [0, None])
+@pytest.mark.parametrize("H,Hk,D,page", [(32, 8, 128, 16), (16, 2, 64, 32), (24, 3, 96, 64), (32, 4, 40, 16), (128, 1, 80, 128)])
+def test_chunks_and_single_tokens_to_what_is_rounded(H, Hk, D, page, unpack, sharp):
+    s = Step([1, 200, 0, 5, 33, 1, 130, 2, 64, 90], [300, 450, 77, 5, 33, 1, 600, 129, 64, 20], H, Hk, D, page, seed=H, unpack=unpack)
+    s.scale *= sharp
+    check_exactly(s)
+
+
+@pytest.mark.parametrize("sharp", [1.0, 8.0])
+@pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (16, 1, 80), (10, 2, 8), (128, 1, 64)])
+def test_few_tokens_to_what_is_rounded(H, Hk, D, sharp):
+    s = Step([1, 1, 2, 1, 3, 1, 1, 5, 1, 1], [1, 2, 15, 16, 17, 127, 128, 129, 3000, 33], H, Hk, D, 16, seed=H + D)
+    s.scale *= sharp
+    check_exactly(s)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,unpack", [(100, None), (100, 0), (1, None)])
+def test_weights_keep_eleven_bits(n, unpack, D):
+    """Every other key has a weight that rounding to bf16's 8 bits takes down by nearly 2^-8 of it, and the values cancel:
+    the outputs are far smaller than what they are sums of, and such a rounding would be most of them."""
+    s = Step([n], [n + 901], 64, 8, D, 16, seed=1, unpack=unpack)
+    w = 1 + 2.0 ** -8 - 2.0 ** -12
+    odd = torch.arange(n + 901) % 2 == 1
+    k, v = torch.zeros(2, n + 901, 8, D).to(BF)
+    k[odd, :, 0] = 6.0
+    v[~odd], v[odd] = -6.0, 6.0
+    t = torch.arange(n + 901)
+    KV.lora_kv4_store(k.cuda(), v.cuda(), s.cache, (s.table[0].cpu()[t // 16] * 16 + t % 16).int().cuda(), s.ws)
+    s.keys, s.values = [k.double()], [v.double()]
+    s.q.zero_()
+    s.q[..., 0] = 1.0
+    s.q_cpu = s.q.double().cpu()
+    s.scale = math.log(w) / 6.0
+    check_exactly(s)
