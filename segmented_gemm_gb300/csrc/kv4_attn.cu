@@ -81,14 +81,24 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
     return r;
 }
 
-// mbar_wait, with what it does when the barrier is not there yet out of line.
+// Bounded wait, with what it does when the barrier is not there yet out of line.  A try may suspend for longer than the
+// load that it waits for takes, whatever the budget: short budgets are waited out without.
 __device__ __noinline__ bool wait_loop(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status, int64_t budget)
 {
-    return mbar_wait(bar, parity, abort, status, LORA_DEV_TIMEOUT, budget);
+    const uint32_t at = smem_u32(bar);
+    const long long most = wait_budget(abort, budget), t0 = clock64();
+    while (!(budget < kWaitShort ? mbar_test_wait(at, parity) : mbar_try_wait(at, parity))) {
+        if (clock64() - t0 > most) {
+            *abort = 1;
+            atomicOr(status, LORA_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
 }
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status, int64_t budget)
 {
-    return mbar_try_wait(smem_u32(bar), parity) || wait_loop(bar, parity, abort, status, budget);
+    return mbar_test_wait(smem_u32(bar), parity) || wait_loop(bar, parity, abort, status, budget);
 }
 
 // a / b; most quotients here fit 32 bits, where a division takes a quarter of the time.

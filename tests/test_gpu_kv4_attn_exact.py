@@ -100,3 +100,21 @@ def test_weights_keep_eleven_bits(n, unpack, D):
     s.q_cpu = s.q.double().cpu()
     s.scale = math.log(w) / 6.0
     check_exactly(s)
+
+
+def test_waits_that_give_up_do_so_and_the_next_call_is_right():
+    """A budget that no first load can meet.  (Not every call has to run out: one try of a barrier may itself
+    suspend for longer than the load takes.)"""
+    s = Step([1] * 40, [4000 - 90 * i for i in range(40)], 32, 8, 128, 16, seed=5)
+    want, _ = s.run()
+    seen = 0
+    L.lora_set_wait_budget(1)
+    try:
+        for _ in range(20):
+            s.run()
+            seen |= L.lora_get_status(s.ws)
+    finally:
+        L.lora_set_wait_budget(0)
+    assert seen == L.LORA_DEV_TIMEOUT
+    o, _ = s.run()
+    assert L.lora_get_status(s.ws) == 0 and torch.equal(o, want)
