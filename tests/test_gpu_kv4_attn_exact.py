@@ -11,6 +11,7 @@ from segmented_gemm_gb300 import kv as KV
 from segmented_gemm_gb300 import lora as L
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import test_gpu_kv4_attn as beside  # noqa: E402
 from test_gpu_kv4_attn import Step  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -102,6 +103,18 @@ def test_weights_keep_eleven_bits(n, unpack, D):
     check_exactly(s)
 
 
+@pytest.mark.parametrize("H,D,new,kv", [(4, 128, 1, 90000), (4, 64, 1, 90000), (8, 64, 2, 90000), (1, 128, 1, 60005),
+                                        (3, 72, 2, 38917), (8, 128, 1, 78000), (4, 128, 1, 9000)])
+def test_one_group_over_the_whole_gpu(H, D, new, kv):
+    """One key head of one request, in pieces over every CTA there is (from some 78000 keys on; two tiles are the
+    least share of a warp), or over some of them, of which the last one has a few warps at work."""
+    s = Step([new], [kv], H, 1, D, 16, seed=kv, spare=2)
+    check_exactly(s)
+    o, lse = s.run()
+    again, lse2 = s.run()
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
 def test_waits_that_give_up_do_so_and_the_next_call_is_right():
     """A budget that no first load can meet.  (Not every call has to run out: one try of a barrier may itself
     suspend for longer than the load takes.)"""
@@ -118,3 +131,23 @@ def test_waits_that_give_up_do_so_and_the_next_call_is_right():
     assert seen == L.LORA_DEV_TIMEOUT
     o, _ = s.run()
     assert L.lora_get_status(s.ws) == 0 and torch.equal(o, want)
+
+
+def test_the_operators_in_use_over_the_4_bit_cache(monkeypatch):
+    """The serving steps of the test beside this one, its attention held to what fp16 p rounds."""
+    def exactly(o, lse, ref_o, ref_lse, mass, vmax, wide, what=""):
+        err = (o.double().cpu() - ref_o).abs()
+        tol = U * ref_o.abs() + (2.0 ** -11 + 2e-4) * mass + 200 * 2.0 ** -32 * vmax
+        assert (err <= tol).all(), f"{what}: worst {(err / tol).max():.2f} x tol"
+        assert float((lse.double().cpu() - ref_lse).abs().max()) <= 1e-4, what
+    monkeypatch.setattr(beside, "assert_attn4", exactly)
+    beside.test_the_operators_in_use(4)
+
+
+@pytest.mark.parametrize("cfg", [dict(requests=6, layers=1, steps=10), dict(requests=5, layers=2, steps=6, head_dim=128, kv_heads=1)])
+def test_serving_example_with_rotation(cfg):
+    """Norms and rotation round queries and keys to bf16 (u = 2^-8) once more, so a score moves by up to 4 u times its
+    magnitude (4 covers these) and p with it, 16 u; with p, o, QKV, the output projection and the sum 21 u a layer."""
+    from test_gpu_attn_serving import _example
+    status, errors = _example().serve(rope=True, **cfg)
+    assert status == 0 and max(errors) <= 21 * U * cfg["layers"], errors
