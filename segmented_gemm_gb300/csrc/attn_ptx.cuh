@@ -84,6 +84,13 @@ __device__ __forceinline__ uint32_t umma_idesc_f16_bn(int M, int N)
     return umma_idesc_bf16_bn(M, N) & ~((1u << 7) | (1u << 10));
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Tiled loads for the lanes with `on` set (one); dst and bar: shared addresses.
 __device__ __forceinline__ void tma_load_3d_if(uint32_t on, uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y,
                                                int z)

@@ -41,6 +41,7 @@
 // but 15 us for one token), more units for the CTA that runs ahead (200 to 224).
 #include <cuda_runtime.h>
 
+#include "attn_ptx.cuh"
 #include "block_scan.cuh"
 #include "kv4.cuh"
 #include "kv4_request.cuh"
@@ -79,6 +80,20 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+
+// mbar_try_wait without suspending: whether the phase is over now.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Bounded wait, with what it does when the barrier is not there yet out of line.  A try may suspend for longer than the

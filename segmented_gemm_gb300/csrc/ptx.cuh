@@ -121,20 +121,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// The same without suspending: whether the phase is over now.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Cycle budgets of the bounded waits: a healthy wait ends in microseconds;
 // the long budget (~1 s at 2 GHz) only runs out when something is broken,
 // after which every later wait of the CTA uses the short budget so the
@@ -362,13 +348,6 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16])
 // ---------------------------------------------------------------------------
 // bf16 packing (round to nearest even, NaN kept quiet)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
     uint32_t r;
