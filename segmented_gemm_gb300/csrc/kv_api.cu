@@ -94,7 +94,7 @@ static Kv4Layout kv4_layout(int64_t T, int32_t R, int32_t heads, int32_t kv_head
 
 static size_t pages_workspace(int32_t num_pages)
 {
-    return kStatusBytes + (static_cast<size_t>(num_pages) + kPageChunk - 1) / kPageChunk * kPagesBlock;
+    return kStatusBytes + (static_cast<size_t>(num_pages) + kBlockPages - 1) / kBlockPages * kPagesBlock;
 }
 
 static bool num_pages_ok(int32_t n) { return n > 0 && n < (1 << 28); }

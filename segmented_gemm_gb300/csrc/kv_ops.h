@@ -105,19 +105,21 @@ struct Kv4WideParams {
     int32_t max_wide, pages;
 };
 
-// Workspace of the calls on pages: the status and the counters, then a block for every kPageChunk pages with what is
-// kept of them: their marks (used, free), the chunk's counts and the map.  A page's place
+// Workspace of the calls on pages: the status and the counters, then a block for every kBlockPages pages with what is
+// kept of them: the counts of its chunks, the pages' marks (used, free) and the map.  A page's place
 // does not depend on how many there are, so a workspace may serve caches of different sizes in turn: the
-// marks are zero at rest, counts and map are written before they are read.
+// marks are zero at rest, counts and map are written before they are read.  (Blocks of one chunk: a million pages
+// compacted in 49 us instead of 45, as every CTA reads all counts.)
 constexpr int kPagesArrived = 2;                // counter: CTAs done with their reading
 constexpr int kPageChunk = 1024;                // pages that one CTA counts and lists
-constexpr int kPagesFree = kPageChunk, kPagesCounts = 2 * kPageChunk, kPagesMap = kPagesCounts + 256;   // in a block
-constexpr int kPagesBlock = kPagesMap + 4 * kPageChunk;
+constexpr int kBlockChunks = 16, kBlockPages = kBlockChunks * kPageChunk;
+constexpr int kPagesUsed = kBlockChunks * 16, kPagesFree = kPagesUsed + kBlockPages, kPagesMap = kPagesFree + kBlockPages;   // in a block
+constexpr int kPagesBlock = kPagesMap + 4 * kBlockPages;
 
 struct KvPagesParams {
     lora_kv_pages_t a;
     int32_t *counters;
-    uint8_t *blocks;                            // [chunks][kPagesBlock]
+    uint8_t *blocks;                            // [blocks][kPagesBlock]
     // release: rows; fork: parent and child
     const int32_t *rows, *parent, *child;
     int32_t num;
@@ -126,14 +128,17 @@ struct KvPagesParams {
     int32_t limit, max_copies;
     int32_t *table_out, *ref_out, *free_out, *head_out;
 
-    __host__ __device__ uint8_t *block(int64_t chunk) const { return blocks + chunk * kPagesBlock; }
-    __host__ __device__ uint8_t *used(int64_t page) const { return block(page / kPageChunk) + page % kPageChunk; }
-    __host__ __device__ uint8_t *free(int64_t page) const { return used(page) + kPagesFree; }
-    __host__ __device__ int4 *counts(int64_t chunk) const { return reinterpret_cast<int4 *>(block(chunk) + kPagesCounts); }
-    // place + 1 of a page that moves, or 0
-    __host__ __device__ int32_t *map(int64_t page) const
+    __host__ __device__ uint8_t *block(uint32_t i) const { return blocks + static_cast<int64_t>(i) * kPagesBlock; }
+    __host__ __device__ uint8_t *used(uint32_t page) const { return block(page / kBlockPages) + kPagesUsed + page % kBlockPages; }
+    __host__ __device__ uint8_t *free(uint32_t page) const { return used(page) + kBlockPages; }
+    __host__ __device__ int4 *counts(uint32_t chunk) const
     {
-        return reinterpret_cast<int32_t *>(block(page / kPageChunk) + kPagesMap) + page % kPageChunk;
+        return reinterpret_cast<int4 *>(block(chunk / kBlockChunks)) + chunk % kBlockChunks;
+    }
+    // place + 1 of a page that moves, or 0
+    __host__ __device__ int32_t *map(uint32_t page) const
+    {
+        return reinterpret_cast<int32_t *>(block(page / kBlockPages) + kPagesMap) + page % kBlockPages;
     }
 };
 

@@ -341,12 +341,11 @@ __global__ void __launch_bounds__(kThreads) compact_mark_kernel(const KvPagesPar
     if (flags) atomicOr(p.counters, flags);
 }
 
-// What a page is: bit 0 a hole, bit 8 a mover, bit 16 free from the limit on (so that 16 of a thread add up without carries).
-__device__ __forceinline__ uint32_t kind_of(const KvPagesParams &p, int64_t page, int *both)
+// What a page is, of its marks: bit 0 a hole, bit 8 a mover, bit 16 free from the limit on (so that 16 of a thread add up without carries).
+__device__ __forceinline__ uint32_t kind_of(bool held, bool listed, bool high, int *both)
 {
-    const bool held = *p.used(page), listed = *p.free(page), free = listed && !held;
     *both |= held && listed;
-    return held ? (page >= p.limit ? 1u << 8 : 0u) : free ? (page < p.limit ? 1u : 1u << 16) : 0u;
+    return held ? (high ? 1u << 8 : 0u) : listed ? (high ? 1u << 16 : 1u) : 0u;
 }
 
 __global__ void __launch_bounds__(kThreads) compact_count_kernel(const KvPagesParams p)
@@ -357,12 +356,13 @@ __global__ void __launch_bounds__(kThreads) compact_count_kernel(const KvPagesPa
     __syncthreads();
     pdl_wait();
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x;
+    const uint8_t *used = p.used(base), *free = p.free(base);   // a chunk's marks are consecutive
     uint32_t n = 0;
     int both = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int64_t page = base + i * kThreads;
-        if (page < p.a.num_pages) n += kind_of(p, page, &both);
+        if (page < p.a.num_pages) n += kind_of(used[i * kThreads], free[i * kThreads], page >= p.limit, &both);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
@@ -386,11 +386,13 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
     const int moved = min(min(all.x, all.y), p.max_copies);
     const int first = a.num_free - (all.x + all.z);          // the new head: as many are free as before
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPerThread;
+    uint8_t *used = p.used(base), *free = p.free(base);
+    int32_t *map = p.map(base);
     uint32_t kind[kPerThread], n = 0;
     int both = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-        kind[i] = base + i < a.num_pages ? kind_of(p, base + i, &both) : 0u;
+        kind[i] = base + i < a.num_pages ? kind_of(used[i], free[i], base + i >= p.limit, &both) : 0u;
         n += kind[i];
     }
     int64_t total;
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
         const int64_t page = base + i;
         if (page >= a.num_pages) break;
         const int32_t id = static_cast<int32_t>(page);
-        int32_t map = 0;
+        int32_t to = 0;
         bool pair = false;                                   // its count is the other one's, or 0
         if (kind[i] & 1) {
             pair = hole < moved;
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
             pair = mover < moved;
             if (pair) {
                 p.src[mover] = id;
-                map = mover + 1;
+                to = mover + 1;
                 p.free_out[first + (all.x - moved) + high + mover] = id;
             }
             ++mover;
@@ -422,9 +424,9 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const KvPagesPar
             p.free_out[first + (all.x - moved) + high + min(mover, moved)] = id;
             ++high;
         }
-        *p.map(page) = map;
+        map[i] = to;
         if (!pair && p.ref_out != a.ref) p.ref_out[page] = a.ref[page];
-        *p.used(page) = *p.free(page) = 0;
+        used[i] = free[i] = 0;
     }
     for (int64_t i = moved + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < p.max_copies;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
