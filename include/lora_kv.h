@@ -154,7 +154,12 @@ size_t lora_kv4_workspace_size(int64_t num_tokens, int32_t num_requests, int32_t
  * heads / kv_heads; 160 for a head_dim up to 64), in order as long as they fit, are
  * unpacked there, exactly, and go through lora_attn_paged's kernel in a form with p in fp16 (8 chunks of 64 tokens over
  * 1000 to 8000, 32/8 heads of 128: 113 us so, 224 without).  Up to 2^24, in units of 128 (others are
- * rounded down); each such request needs its cached tokens, rounded up to 128.
+ * rounded down); each such request needs its cached tokens, rounded up to 128.  The host tells such steps by their
+ * sizes: more rows of a key head than 96 (160) a request, or 1536 (2560) beyond one token a request.
+ *
+ * Faster than lora_attn_paged over a bf16 cache wherever the cache's bytes count; slower for one request
+ * over some 1000 tokens (12 us, 9 there with a schedule made) and for few long chunks (one of
+ * 512 over 8000: 102 to 104 us, 87 there).
  */
 int lora_kv4_attn(const lora_attn_t *attn, const lora_kv4_cache_t *cache, const int32_t *block_table,
                   int32_t table_width, int64_t table_stride, const int32_t *kv_len, int64_t unpack_tokens, void *ws,

@@ -17,7 +17,8 @@
 //     the keys, one for each half of the values, the conversion instruction
 //     (two codes to a pair of fp16) and one product with the scale pair;
 //   - fp16 operands: code times scale is exact, q is scaled by a power of two a
-//     column, p of at most 2^kSlack has three bits more than in bf16;
+//     column, p of at most 2^kSlack has three bits more than in bf16 (as it has where keys and
+//     values are unpacked first, kv4_wide.cu);
 //   - a warp is on its own: it takes tiles of 16 keys from its own ring of bulk
 //     copies, so nothing but the ends of pieces is synchronised.
 //
@@ -54,8 +55,8 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kGap = 4;             // what a group costs beside its tiles, in tiles (48 requests of up to 5 tokens: 53 us, 55 with 2)
-constexpr int kMinShare = 2;        // least share of a warp, in tiles (one token over 1000: 14 us, 16 with 4, 20 with 8)
+constexpr int kGap = 4;             // what a group costs beside its tiles, in tiles (512 requests over 50 to 300: 38.1 us, 39.1 with 2)
+constexpr int kMinShare = 2;        // least share of a warp, in tiles (one token over 1000: 11.9 us, 13.4 with 4, 15.9 with 8)
 constexpr int kBatch = 2;           // most tiles of a stage of a warp's ring
 constexpr float kLift = 7.f;        // m is this far below the largest score where it is set: fp16 has p down to 2^-31 of the largest
 constexpr float kSlack = 15.f;      // log2 of the largest p; m is set again past it
@@ -822,11 +823,18 @@ cudaError_t launch_variant(const Kv4AttnParams &p, cudaStream_t stream)
 
 }  // namespace
 
-// Blocks of 8 columns: a request of more rows has several, which read its tiles again (from L2)
-// and unpack them again, but 8 more columns of a block would take as long on the matrix
-// units as that, and the registers of a second CTA an SM: 48 requests of up to 5 tokens of 28/4 heads
-// over 300 to 6000 take 52 us so, 61 with 16 columns, 87 with 32; 64 requests of 16 rows 118 and
-// 106.  With a head dimension of 64 the registers are there: 8 requests of 64 rows 65 us, 53 with 16.
+// Blocks of 8 columns for heads of more than 64: a request of more rows has several, which read its tiles again (from
+// L2) and unpack them again.  The registers of 16 columns cost the second CTA of an SM (with both, they
+// spill and every case is slower), and which is faster depends on the rows:
+//                                                             8 columns   16
+//   32 requests of one token, 32/8 heads, over 100 to 8000       40 us     54
+//   48 of up to 5 tokens, 28/4 heads, over 300 to 6000           52        56
+//   64 over 1000 to 8000, 16 rows: one token, 32/2 heads         39        37
+//                                  2 tokens, 32/4 heads          65        58
+//                                  4 tokens, 32/8 heads         113        98
+//   8 of 16 tokens, 32/8 heads, over 1000 to 8000                68        60
+// So 8 throughout gives up 6 to 14 % from 16 rows on, for one kernel less.  Heads up to 64 have the registers for
+// both, and take 16 where requests have more than 8 rows: 8 requests of 64 rows over 1000 to 8000 45 us with 8, 35 with 16.
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, cudaStream_t stream)
 {
     if (p.head_dim > 64) return launch_variant<128, 1>(p, stream);

@@ -2,7 +2,7 @@
 // prompts, whose many rows share each key, so that the tensor cores bound them and
 // not the cache's bytes.  Their keys are unpacked to bf16 and their values to fp16 once (exactly), and the attention over a
 // bf16 cache (attn.cu) runs over that, with p in fp16 as in the kernel for the other requests: 8 chunks of 64 tokens over
-// 1000 to 8000 take 113 us so and 224 by blocks of 8 columns, one of 512 over 8000 102 us (87 of them that
+// 1000 to 8000 take 113 us so and 224 by blocks of 8 columns, one of 512 over 8000 102 to 104 us (about 88 of them that
 // kernel, 9 its list, 4 the plan).
 #include <cuda_runtime.h>
 

@@ -67,8 +67,17 @@ constexpr int kKv4WidePage = 128;               // keys of a page of the unpacke
 // Most rows (tokens times a group's heads) of a request that is not wide.  8 requests over 1000 to 8000 take, 32/8
 // heads of 128, with 64, 96 and 128 rows each 68, 93 and 119 us by blocks of 8 columns, 79, 83 and 87
 // unpacked; with heads of 64, 64, 128 and 256 rows: 36, 58 and 102, and 50, 54 and 71.
+// Least rows of all heads of a step with wide requests.  Microseconds by blocks and unpacked, one request:
+//   heads       rows    over 1000        over 8000
+//   8/1 of 128  1600    19 and 34        51 and 121
+//               3200    26 and 36        89 and 85
+//               6400    46 and 41       172 and 81
+//   32/32       6400    37 and 37       164 and 106
+//   32/4 of 64  3200    17 and 30        43 and 56
+//               6400    23 and 31        74 and 55
+//              12800    35 and 32       137 and 65
 constexpr int kv4_wide_rows(int head_dim) { return head_dim <= 64 ? 160 : 96; }
-constexpr int kKv4WideTotal = 6400;             // least rows of all heads of a step with wide requests
+constexpr int kKv4WideTotal = 6400;
 
 struct Kv4AttnParams {
     const uint16_t *q;
@@ -108,8 +117,8 @@ struct Kv4WideParams {
 // Workspace of the calls on pages: the status and the counters, then a block for every kBlockPages pages with what is
 // kept of them: the counts of its chunks, the pages' marks (used, free) and the map.  A page's place
 // does not depend on how many there are, so a workspace may serve caches of different sizes in turn: the
-// marks are zero at rest, counts and map are written before they are read.  (Blocks of one chunk: a million pages
-// compacted in 49 us instead of 45, as every CTA reads all counts.)
+// marks are zero at rest, counts and map are written before they are read.  (Every CTA reads all counts: a million
+// pages are compacted in 44 us, 49 with blocks of one chunk.)
 constexpr int kPagesArrived = 2;                // counter: CTAs done with their reading
 constexpr int kPageChunk = 1024;                // pages that one CTA counts and lists
 constexpr int kBlockChunks = 16, kBlockPages = kBlockChunks * kPageChunk;
